@@ -419,6 +419,93 @@ ce_status ce_log_softmax_bwd(const void* grad_output, const void* output, void* 
                              int dtype, int64_t rows, int64_t C, ce_stream_t stream);
 
 /*
+ * ce_dropout - y = residual + keep * x / (1 - p), elementwise. The method has
+ * no counterpart: it is the dropout between the layers whose output the
+ * fused linear cross-entropy takes.
+ *
+ * x, residual, y   [n] contiguous, dtype CE_F32, CE_BF16 or CE_F16; residual
+ *              may be NULL; y may be x or residual. fp32 arithmetic, one
+ *              rounding into dtype.
+ * p            in [0, 1]: element i is kept when its random word is at least
+ *              floor(p 2^32). A dropped element contributes exactly 0
+ *              whatever it holds; p = 0 keeps every element, p = 1 none.
+ * seed, offset element i takes word i mod 4 of the Philox 4x32-10 block with
+ *              key `seed` and 128-bit counter (i div 4) + offset 2^64. The
+ *              same (p, seed, offset) on the gradient is the backward: no
+ *              mask is stored.
+ * state        device pointer to two int64 {seed, offset}, or NULL. It is
+ *              read when the kernel runs, replaces `seed` and is added to
+ *              `offset` (modulo 2^64), so that a captured graph draws new
+ *              words when the caller updates it.
+ * used         device pointer to two int64 that receive the {seed, offset}
+ *              the call drew from, or NULL. It must not be `state`.
+ * Asynchronous on `stream`; uses no library scratch.
+ */
+ce_status ce_dropout(const void* x, const void* residual, void* y, int dtype, int64_t n, double p,
+                     uint64_t seed, uint64_t offset, const int64_t* state, int64_t* used,
+                     ce_stream_t stream);
+
+/*
+ * ce_beam_select - one step of beam search: the M best continuations of each
+ * batch entry's K beams. The method has no counterpart: it continues
+ * _log_softmax over the same logits.
+ *
+ * logits       [B, K, V] row-major, dtype CE_F32, CE_BF16 or CE_F16.
+ * scores       [B, K] fp32: the beams' log-probabilities so far. A beam whose
+ *              score is not finite is dead: it has no candidates and its
+ *              logits are not read.
+ * finished     [B, K] bytes, or NULL. A finished beam (non-zero, with a
+ *              finite score) has one candidate, pad_token at its own score;
+ *              its logits are not read.
+ * pad_token    in [0, V).
+ * M            candidates a batch entry, 1..64; K at most 32
+ *              (CE_ERR_UNSUPPORTED above).
+ * out_scores, out_beams, out_tokens   [B, M]: candidate (k, v) has the score
+ *              scores[k] + logits[k, v] - log sum_j exp(logits[k, j]), formed
+ *              in 64 bits and rounded to fp32 for the output; descending,
+ *              equal ones by the lowest k V + v. Within a beam the order is
+ *              that of the logits. Tokens with a logit of -inf or NaN are no
+ *              candidates (and add nothing to the sum); a beam with no other
+ *              token, or with a logit of +inf, has none. Places without a
+ *              candidate hold the score -inf, beam -1 and pad_token.
+ * workspace    at least ce_beam_workspace_bytes(...) bytes, 256-byte
+ *              aligned, owned by the caller; nothing in it needs to be set.
+ * Asynchronous on `stream`; uses no library scratch. Results do not depend on
+ * the order in which CTAs run.
+ */
+size_t ce_beam_workspace_bytes(int dtype, int64_t B, int64_t K, int64_t V, int64_t M);
+
+ce_status ce_beam_select(const void* logits, int dtype, int64_t B, int64_t K, int64_t V,
+                         const float* scores, const uint8_t* finished, int64_t pad_token,
+                         int64_t M, float* out_scores, int64_t* out_beams, int64_t* out_tokens,
+                         void* workspace, size_t workspace_bytes, ce_stream_t stream);
+
+/* A tensor of beams' states for ce_beam_reorder: B K rows, each of `blocks`
+ * blocks of block_bytes contiguous bytes; row and block strides in bytes. */
+typedef struct {
+    const void* src;
+    void* dst; /* src itself, with the same strides, to reorder in place */
+    int64_t src_row, src_block, dst_row, dst_block;
+    int64_t blocks, block_bytes;
+} ce_beam_state;
+
+/*
+ * ce_beam_reorder - dst[b K + j] = src[b K + beams[b, j]] for each of n
+ * states (a host array; read before the call returns).
+ *
+ * beams        [B, K] int64 on the device. A value outside [0, K) (such as
+ *              the -1 of a place without a candidate) stands for j: that row
+ *              keeps its own state.
+ * In place, rows that keep their state are neither read nor written. Either
+ * all states are reordered in place or none; a dst that overlaps a src
+ * otherwise is the caller's error. Bytes between blocks and rows are left as
+ * they were. K at most 32 (CE_ERR_UNSUPPORTED above). Asynchronous on
+ * `stream`; uses no library scratch.
+ */
+ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* beams, int64_t B,
+                          int64_t K, ce_stream_t stream);
+
+/*
  * ce_bwd - backward (§Backward Pass: the stored gradient times
  * grad_output): dlogits *= grad_output, in place.
  *

@@ -20,6 +20,15 @@ CE_FLAG_GRAD, CE_FLAG_Z_LOSS, CE_FLAG_ACC, CE_FLAG_PRED, CE_FLAG_TARGET_I64 = 1,
 # (name, restype, argtypes) for every symbol include/gbce.h declares
 _P, _I, _I64, _U32, _F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32,
                           ctypes.c_float)
+_D, _U64, _SZ = ctypes.c_double, ctypes.c_uint64, ctypes.c_size_t
+
+
+class BeamState(ctypes.Structure):
+    """ce_beam_state."""
+    _fields_ = [("src", _P), ("dst", _P), ("src_row", _I64), ("src_block", _I64),
+                ("dst_row", _I64), ("dst_block", _I64), ("blocks", _I64), ("block_bytes", _I64)]
+
+
 SIGNATURES = {
     "ce_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P, _P, _P, _P]),
     "ce_fwd_noalloc": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P, _P, _P,
@@ -36,6 +45,11 @@ SIGNATURES = {
     "ce_gemm": (_I, [_P, _I, _P, _I, _I, _I64, _I64, _I64, _P, _I, _P, _P]),
     "ce_flce": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P,
                      _P, _P, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P]),
+    "ce_dropout": (_I, [_P, _P, _P, _I, _I64, _D, _U64, _U64, _P, _P, _P]),
+    "ce_beam_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I64]),
+    "ce_beam_select": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,
+                            _P]),
+    "ce_beam_reorder": (_I, [ctypes.POINTER(BeamState), _I, _P, _I64, _I64, _P]),
     "ce_bwd": (_I, [_P, _I, _P, _I, _I64, _I64, _P]),
     "ce_log_softmax": (_I, [_P, _P, _I, _I64, _I64, _P]),
     "ce_nll_loss_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _I, _U32, _P, _P, _P]),
@@ -167,6 +181,25 @@ def ce_nll_loss_bwd(grad_output, total_weight, grad_input, dtype, rows, C, targe
 
 def ce_log_softmax_bwd(grad_output, output, grad_input, dtype, rows, C, stream):
     return load().ce_log_softmax_bwd(grad_output, output, grad_input, dtype, rows, C, stream)
+
+
+def ce_dropout(x, residual, y, dtype, n, p, seed, offset, state, used, stream):
+    return load().ce_dropout(x, residual, y, dtype, n, p, seed, offset, state, used, stream)
+
+
+def ce_beam_workspace_bytes(dtype, B, K, V, M):
+    return load().ce_beam_workspace_bytes(dtype, B, K, V, M)
+
+
+def ce_beam_select(logits, dtype, B, K, V, scores, finished, pad_token, M, out_scores, out_beams,
+                   out_tokens, workspace, workspace_bytes, stream):
+    return load().ce_beam_select(logits, dtype, B, K, V, scores, finished, pad_token, M,
+                                 out_scores, out_beams, out_tokens, workspace, workspace_bytes,
+                                 stream)
+
+
+def ce_beam_reorder(states, n, beams, B, K, stream):
+    return load().ce_beam_reorder(states, n, beams, B, K, stream)
 
 
 def ce_device_status(stream):

@@ -1,0 +1,36 @@
+"""What the wrappers of single calls share: data types, pointers, the stream
+and device of a call, and the error of a status."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _lib
+from ._lib import CEError
+
+DTYPES = {torch.float32: _lib.CE_F32, torch.bfloat16: _lib.CE_BF16, torch.float16: _lib.CE_F16}
+_HERE = contextlib.nullcontext()
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def on(device):
+    """A context in which `device` is the current one (free where it is already)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def check(rc, where):
+    if rc != _lib.CE_OK:
+        raise CEError(rc, where)
+
+
+def require_cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
