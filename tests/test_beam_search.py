@@ -158,10 +158,12 @@ def test_ties_and_orders(dtype, V, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-def test_equal_beams_take_the_lowest_first(dtype):
+@pytest.mark.parametrize("V", [4096, 4097, 65001, 65003])
+def test_equal_beams_take_the_lowest_first(dtype, V):
+    # odd V: the equal rows start at different places of a 16-byte vector
     import softmax_cross_entropy_gb300 as gbce
-    x, _ = inputs(2, 1, 4096, dtype)
-    x = x.expand(2, 6, 4096).contiguous()
+    x, _ = inputs(2, 1, V, dtype)
+    x = x.expand(2, 6, V).contiguous()
     s = torch.full((2, 6), -1.5, device="cuda")
     compare(gbce.beam_search_step(x, s, num_candidates=12), reference(x, s, 12))
 
