@@ -445,6 +445,68 @@ ce_status ce_dropout(const void* x, const void* residual, void* y, int dtype, in
                      uint64_t seed, uint64_t offset, const int64_t* state, int64_t* used,
                      ce_stream_t stream);
 
+/* Activations of the gated feed-forward block. */
+enum {
+    CE_ACT_SILU = 0,     /* g / (1 + exp(-g)) */
+    CE_ACT_GELU = 1,     /* g Phi(g), Phi the normal distribution function */
+    CE_ACT_GELU_TANH = 2 /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+};
+
+/*
+ * ce_ffn_fwd - the gated feed-forward block
+ *     y = residual + dropout(h @ w_down^T),  h = act(x @ w_gate^T) * (x @ w_up^T)
+ * on the tensor cores. The method has no counterpart: it is the block whose
+ * output the fused linear cross-entropy takes as its hidden states.
+ *
+ * x [rows, H], w_gate and w_up [I, H], w_down [O, I], residual [rows, O] or
+ * NULL, y [rows, O]: row-major, all in dtype CE_BF16 or CE_F16, with 16-byte
+ * aligned bases and H, I and O multiples of 8 (CE_ERR_UNSUPPORTED
+ * otherwise, and for CE_F32). rows may be 0.
+ * act          a CE_ACT_* value.
+ * p, seed, offset, state   the dropout, as for ce_dropout over the [rows, O]
+ *              elements; p = 0 applies none.
+ * h            [rows, I] in dtype, written: act(g) u rounded once.
+ * g, u         [rows, I] in dtype, written (x @ w_gate^T and x @ w_up^T, what
+ *              ce_ffn_bwd needs besides h), or both NULL.
+ * workspace    device memory of at least ce_ffn_fwd_workspace_bytes(rows, H,
+ *              I, O) bytes, 256-byte aligned, owned by the caller (NULL where
+ *              that is 0); nothing in it needs to be set.
+ * Products accumulate in fp32; y is rounded once, after the dropout and the
+ * residual sum. Asynchronous on `stream`; a bounded wait that gives up
+ * records CE_ERR_TIMEOUT for ce_device_status (the call's outputs are then
+ * invalid). Deterministic.
+ */
+size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O);
+
+ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                     const void* residual, int dtype, int64_t rows, int64_t H, int64_t I,
+                     int64_t O, int act, double p, uint64_t seed, uint64_t offset,
+                     const int64_t* state, void* y, void* h, void* g, void* u, void* workspace,
+                     size_t workspace_bytes, ce_stream_t stream);
+
+/*
+ * ce_ffn_bwd - the gradients of ce_ffn_fwd: with dz = dropout(dy), dh = dz @
+ * w_down, dg = dh u act'(g) and du = dh act(g):
+ *     dx = dg @ w_gate + du @ w_up,  dw_gate = dg^T @ x,  dw_up = du^T @ x,
+ *     dw_down = dz^T @ h             (the residual's gradient is dy)
+ * dy [rows, O]; h, g, u as ce_ffn_fwd wrote them; sizes, types, alignment
+ * and dropout arguments as there (pass the same p, seed and offset, and the
+ * state it drew from).
+ * dx [rows, H], dw_gate and dw_up [I, H], dw_down [O, I] in dtype, written;
+ * dx, dw_down, or both dw_gate and dw_up may be NULL (not computed).
+ * workspace    at least ce_ffn_bwd_workspace_bytes(rows, I, O, p) bytes,
+ *              256-byte aligned, owned by the caller: dg and du (and dz).
+ * dg, du and dz are rounded to dtype once; products accumulate in fp32.
+ */
+size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t I, int64_t O, double p);
+
+ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up,
+                     const void* w_down, const void* h, const void* g, const void* u, int dtype,
+                     int64_t rows, int64_t H, int64_t I, int64_t O, int act, double p,
+                     uint64_t seed, uint64_t offset, const int64_t* state, void* dx,
+                     void* dw_gate, void* dw_up, void* dw_down, void* workspace,
+                     size_t workspace_bytes, ce_stream_t stream);
+
 /*
  * ce_beam_select - one step of beam search: the M best continuations of each
  * batch entry's K beams. The method has no counterpart: it continues

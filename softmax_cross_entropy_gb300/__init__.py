@@ -31,6 +31,7 @@ from ._lib import (CEError, ce_bwd, ce_bwd_nd, ce_count, ce_device_status, ce_fl
                    ce_flce_workspace_bytes, ce_fwd, ce_fwd_nd, ce_fwd_shard, ce_last_error,
                    ce_scale_round, ce_status_string)
 from .beam_search import BeamCandidates, beam_reorder, beam_search_step
+from .feed_forward import GatedFeedForward, GatedFeedForwardFunction, gated_feed_forward
 from .philox_dropout import DropoutFunction, dropout
 
 __all__ = ["cross_entropy", "CrossEntropyLoss", "CrossEntropyFunction", "CrossEntropyOutput",
@@ -38,7 +39,8 @@ __all__ = ["cross_entropy", "CrossEntropyLoss", "CrossEntropyFunction", "CrossEn
            "ce_bwd", "ce_fwd_nd", "ce_bwd_nd", "ce_flce", "ce_flce_workspace_bytes",
            "ce_scale_round", "ce_device_status", "ce_status_string", "ce_last_error",
            "fused_linear_cross_entropy", "FusedLinearCrossEntropyFunction", "dropout",
-           "DropoutFunction", "beam_search_step", "beam_reorder", "BeamCandidates"]
+           "DropoutFunction", "beam_search_step", "beam_reorder", "BeamCandidates",
+           "gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
 
 CrossEntropyOutput = namedtuple("CrossEntropyOutput",
                                 ["loss", "z_loss", "token_accuracy", "predicted_tokens"])

@@ -46,6 +46,12 @@ SIGNATURES = {
     "ce_flce": (_I, [_P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P,
                      _P, _P, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P]),
     "ce_dropout": (_I, [_P, _P, _P, _I, _I64, _D, _U64, _U64, _P, _P, _P]),
+    "ce_ffn_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "ce_ffn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64, _U64, _P, _P,
+                        _P, _P, _P, _P, _SZ, _P]),
+    "ce_ffn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _D]),
+    "ce_ffn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64,
+                        _U64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "ce_beam_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I64]),
     "ce_beam_select": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,
                             _P]),
@@ -185,6 +191,30 @@ def ce_log_softmax_bwd(grad_output, output, grad_input, dtype, rows, C, stream):
 
 def ce_dropout(x, residual, y, dtype, n, p, seed, offset, state, used, stream):
     return load().ce_dropout(x, residual, y, dtype, n, p, seed, offset, state, used, stream)
+
+
+CE_ACT_SILU, CE_ACT_GELU, CE_ACT_GELU_TANH = 0, 1, 2
+
+
+def ce_ffn_fwd_workspace_bytes(rows, H, I, O):
+    return load().ce_ffn_fwd_workspace_bytes(rows, H, I, O)
+
+
+def ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, seed, offset,
+               state, y, h, g, u, workspace, workspace_bytes, stream):
+    return load().ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, seed,
+                             offset, state, y, h, g, u, workspace, workspace_bytes, stream)
+
+
+def ce_ffn_bwd_workspace_bytes(rows, I, O, p):
+    return load().ce_ffn_bwd_workspace_bytes(rows, I, O, p)
+
+
+def ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, g, u, dtype, rows, H, I, O, act, p, seed, offset,
+               state, dx, dw_gate, dw_up, dw_down, workspace, workspace_bytes, stream):
+    return load().ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, g, u, dtype, rows, H, I, O, act, p,
+                             seed, offset, state, dx, dw_gate, dw_up, dw_down, workspace,
+                             workspace_bytes, stream)
 
 
 def ce_beam_workspace_bytes(dtype, B, K, V, M):

@@ -119,6 +119,30 @@ ce_status device_info(int dev, DeviceInfo* out) {
     return CE_OK;
 }
 
+// Scratch for a stream whose first call is captured: allocated and zeroed
+// apart from the capture (on a stream of its own, waited for), so that the
+// zeroing does not become part of the graph.
+cudaError_t scratch_while_capturing(void** out) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    void* p = nullptr;
+    cudaStream_t own = nullptr;
+    e = cudaMalloc(&p, kScratchBytes);
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kScratchBytes, own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    if (own) cudaStreamDestroy(own);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) e = back;
+    if (e != cudaSuccess) {
+        if (p) cudaFree(p);
+        return e;
+    }
+    *out = p;
+    return cudaSuccess;
+}
+
 // Scratch for (device, stream): allocated and zeroed on first use, on the
 // caller's stream so the zeroing is ordered before the first kernel.
 ce_status scratch_for(int dev, cudaStream_t st, Scratch** out) {
@@ -129,7 +153,17 @@ ce_status scratch_for(int dev, cudaStream_t st, Scratch** out) {
         return CE_OK;
     }
     void* p = nullptr;
-    cudaError_t e = cudaMalloc(&p, kScratchBytes);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &capture);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaStreamIsCapturing");
+    if (capture != cudaStreamCaptureStatusNone) {
+        e = scratch_while_capturing(&p);
+        if (e != cudaSuccess) return cuda_failure(e, "scratch of a capturing stream");
+        g_scratch[key] = static_cast<Scratch*>(p);
+        *out = static_cast<Scratch*>(p);
+        return CE_OK;
+    }
+    e = cudaMalloc(&p, kScratchBytes);
     if (e != cudaSuccess) return cuda_failure(e, "cudaMalloc(scratch)");
     e = cudaMemsetAsync(p, 0, kScratchBytes, st);
     if (e != cudaSuccess) {

@@ -1,0 +1,653 @@
+// The gated feed-forward block y = residual + dropout(h Wd^T), h = act(x
+// Wg^T) * (x Wu^T), forward and backward, on the fifth-generation tensor
+// cores. x [rows, H], Wg and Wu [I, H], Wd [O, I], all bf16 or fp16 with
+// fp32 accumulation.
+//
+// One kernel, the pipeline of the GEMM in ce_gemm_tc.cu (a TMA producer
+// warp, an MMA-issuing warp, four epilogue warps; persistent, one CTA an
+// SM), in five forms (FfnMode) that differ in what a tile's K blocks are
+// made of and in the epilogue:
+//  * kGateUp: a tile's 256 accumulator columns are 128 columns of x Wg^T and
+//    the same 128 of x Wu^T (the B tile is 128 rows of each weight), so the
+//    epilogue has both and writes act(g) * u: g and u never leave the chip
+//    unless a backward needs them;
+//  * kDown: y = h Wd^T with dropout and the residual sum in the epilogue;
+//  * kDact: dh = dz Wd; the epilogue reads g and u and writes dg = dh u
+//    act'(g) and du = dh act(g), dh itself is never stored;
+//  * kDx: dx = dg Wg + du Wu as one product whose K runs over dg, then du;
+//  * kDw: dWg = dg^T x, dWu = du^T x and dWd = dz^T h as one launch over the
+//    tiles of all three (one tail for the SMs instead of three).
+// Roundings to 16 bits: h, g, u, dg and du, which feed tensor-core products
+// (or are kept for the backward), once each from fp32; dropout and the
+// residual are applied in fp32 before y's only rounding.
+//
+// Bound by the tensor cores from about 600 rows on (6 rows H I operations on
+// 6 H I bytes of weights); ce_ffn_rows.cu takes few rows.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstdlib>
+#include <string>
+
+#include "ce_ffn.cuh"
+#include "ce_philox.cuh"
+#include "ce_tc.cuh"
+#include "gbce.h"
+
+namespace gbce {
+ce_status record_cuda_failure(cudaError_t e, const char* what);
+void record_message(const std::string& msg);
+ce_status library_status_word(cudaStream_t st, unsigned** out);
+bool drop_spec(double p, uint64_t seed, uint64_t offset, const int64_t* state, DropSpec* out);
+
+namespace {
+
+enum FfnMode : int { kGateUp, kDown, kDact, kDx, kDw };
+
+struct FfnMaps {
+    CUtensorMap a[3], b[3], c[3];
+};
+
+struct FfnGemm {
+    // problems (kDw), whose tiles follow one another
+    int64_t M[3], N[3], tiles_m[3], tiles_n[3], tile_end[3];
+    int64_t K;      // of one segment
+    int segs;       // segments of K (kDx: 2)
+    int m_first;    // a problem's tiles run along M first
+    int outs;       // kGateUp: 3 with g and u, else 1
+    int act;
+    const void* g;  // kDact: [M, N]
+    const void* u;
+    const void* res;  // kDown: [M, N] or nullptr
+    DropSpec drop;    // kDown
+    uint64_t timeout_ns;
+    unsigned* status;
+};
+
+template <uint32_t AB>
+struct FfnType {
+    using T = __nv_bfloat16;
+};
+template <>
+struct FfnType<0u> {
+    using T = __half;
+};
+
+// 32 columns of 16-bit elements from column n of row `row` of [M, N] (N a
+// multiple of 8); zeros outside.
+template <typename T>
+__device__ __forceinline__ void load_row32(const void* p, int64_t row, int64_t n, int64_t M,
+                                           int64_t N, float (&f)[32]) {
+    const T* q = static_cast<const T*>(p) + row * N + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (row < M && n + 8 * j < N)
+            Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(q + 8 * j)), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
+    }
+}
+
+// 32 16-bit columns, half h of a 32-row x 128-byte staging box in the TMA's
+// 128-byte swizzle (16-byte chunk j of row r at chunk j ^ (r mod 8)).
+template <typename T>
+__device__ __forceinline__ void stage32(uint32_t buf, int r, int h, const float (&v)[32]) {
+    const uint32_t row = buf + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float f[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
+                            v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+        const uint4 p = Vec<T>::pack(f);
+        const uint32_t at = row + (static_cast<uint32_t>((4 * h + j) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(p.x), "r"(p.y),
+                     "r"(p.z), "r"(p.w)
+                     : "memory");
+    }
+}
+
+// The problem of tile t, and t within it.
+__device__ __forceinline__ int ffn_problem(const FfnGemm& a, int64_t* t) {
+    if (*t < a.tile_end[0]) return 0;
+    const int p = *t < a.tile_end[1] ? 1 : 2;
+    *t -= a.tile_end[p - 1];
+    return p;
+}
+__device__ __forceinline__ int64_t ffn_tile_m(const FfnGemm& a, int p, int64_t t) {
+    return a.m_first ? t % a.tiles_m[p] : t / a.tiles_n[p];
+}
+__device__ __forceinline__ int64_t ffn_tile_n(const FfnGemm& a, int p, int64_t t) {
+    return a.m_first ? t / a.tiles_m[p] : t % a.tiles_n[p];
+}
+
+template <uint32_t AB, int MODE, int BM>
+__global__ void __launch_bounds__(kTcThreads, 1)
+ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a) {
+    using T = typename FfnType<AB>::T;
+    using TT = TcTile<BM>;
+    constexpr bool A_MN = MODE == kDw;
+    constexpr bool B_MN = MODE == kDact || MODE == kDx || MODE == kDw;
+    constexpr int kCols = MODE == kGateUp ? kBN / 2 : kBN;  // output columns of a tile
+    constexpr int kStages = TT::kStages;
+    constexpr uint32_t kABytes = TT::kABytes;
+    constexpr uint32_t kStageBytes = TT::kStageBytes;
+    constexpr int NACC = TT::kAccBufs;
+    constexpr int H = TT::kHalves;
+    extern __shared__ unsigned char ffn_smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[kTcMaxStages];
+    __shared__ __align__(8) uint64_t empty_bar[kTcMaxStages];
+    __shared__ __align__(8) uint64_t acc_full[2];
+    __shared__ __align__(8) uint64_t acc_empty[2];
+    __shared__ __align__(8) uint64_t done_bar;  // every MMA of the CTA completed
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ uint32_t s_issued[kTcMaxStages];  // 0, or 2 + parity of the last copy into the stage
+    __shared__ int s_fail;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t smem0 = (smem_u32(ffn_smem_raw) + 1023u) & ~1023u;  // 1024-byte aligned
+    const int nk = static_cast<int>((a.K + kBK - 1) / kBK);
+    const int64_t ntiles = a.tile_end[2];
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+            s_issued[s] = 0;
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 128);
+        }
+        mbar_init(smem_u32(&done_bar), 1);
+        s_fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile(
+            "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                smem_u32(&tmem_base_sh)),
+            "r"(kTmemCols)
+            : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- TMA producer: every K block of every tile of this CTA
+            int it = 0;  // K blocks issued so far (ring position)
+            bool fail = false;
+            for (int64_t t = blockIdx.x; t < ntiles && !fail; t += gridDim.x) {
+                int64_t tl = t;
+                const int p = ffn_problem(a, &tl);
+                const int m0 = static_cast<int>(ffn_tile_m(a, p, tl) * BM);
+                const int n0 = static_cast<int>(ffn_tile_n(a, p, tl) * kCols);
+                for (int kb = 0; kb < nk * a.segs; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
+                    if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
+                        fail = true;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full_bar[s]);
+                    mbar_arrive_expect_tx(fb, kStageBytes);
+                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * kStageBytes;
+                    // the operands' maps: of the problem, or of the segment
+                    const int seg = kb >= nk ? 1 : 0;
+                    const int i = MODE == kDx ? seg : p;
+                    const int k0 = (kb - seg * nk) * kBK;
+                    if constexpr (A_MN) {
+                        for (int j = 0; j < BM / 64; ++j)
+                            tma_load_2d(sa + j * kMnBox, &maps.a[i], m0 + 64 * j, k0, fb);
+                    } else {
+                        tma_load_2d(sa, &maps.a[i], k0, m0, fb);
+                    }
+                    if constexpr (MODE == kGateUp) {
+                        tma_load_2d(sa + kABytes, &maps.b[0], k0, n0, fb);
+                        tma_load_2d(sa + kABytes + kBBytes / 2, &maps.b[1], k0, n0, fb);
+                    } else if constexpr (B_MN) {
+                        for (int j = 0; j < kBN / 64; ++j)
+                            tma_load_2d(sa + kABytes + j * kMnBox, &maps.b[i], n0 + 64 * j, k0, fb);
+                    } else {
+                        tma_load_2d(sa + kABytes, &maps.b[i], k0, n0, fb);
+                    }
+                    s_issued[s] = 2u + ph;
+                }
+            }
+            if (fail) s_fail = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMA issuer: tile i into accumulator buffer i mod NACC
+            constexpr uint32_t idesc = tc_idesc(AB, A_MN ? 1u : 0u, B_MN ? 1u : 0u);
+            int it = 0;
+            int i = 0;  // tiles of this CTA so far
+            bool fail = false;
+            for (int64_t t = blockIdx.x; t < ntiles && !fail; t += gridDim.x, ++i) {
+                const int b = i % NACC;
+                // the epilogue has drained this buffer's previous tile
+                if (!tc_wait(smem_u32(&acc_empty[b]),
+                             (static_cast<uint32_t>(i / NACC) & 1u) ^ 1u, a.timeout_ns)) {
+                    fail = true;
+                    break;
+                }
+                tc_fence_after();
+                // half h of the tile (rows 128 h ...) in columns (b H + h) 256
+                const uint32_t acc = tmem + static_cast<uint32_t>(b * H * kBN);
+                for (int kb = 0; kb < nk * a.segs; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
+                    if (!tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)) {
+                        fail = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * kStageBytes;
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k) {
+                        const uint64_t db = B_MN ? tc_smem_desc_mn(sa + kABytes + 2048u * k)
+                                                 : tc_smem_desc(sa + kABytes + 32u * k);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t ah = sa + static_cast<uint32_t>(h) * kHalfA;
+                            const uint64_t da = A_MN ? tc_smem_desc_mn(ah + 2048u * k)
+                                                     : tc_smem_desc(ah + 32u * k);
+                            tc_mma(acc + static_cast<uint32_t>(h * kBN), da, db, idesc,
+                                   (kb > 0 || k > 0) ? 1u : 0u);
+                        }
+                    }
+                    tc_commit(smem_u32(&empty_bar[s]));
+                }
+                // every MMA of the tile issued: the epilogue may read it once
+                // they complete (also after a failure, so that nothing waits)
+                tc_commit(smem_u32(&acc_full[b]));
+            }
+            if (fail) s_fail = 1;
+            tc_commit(smem_u32(&done_bar));  // after every MMA this thread issued
+        }
+    } else {
+        // ---- epilogue: warp w reads accumulator lanes 32 (w mod 4) of
+        // each 128-row half of the tile
+        const int q = warp & 3;
+        // this warp's two staging boxes, used in turn
+        const uint32_t stg = smem0 + kRingBytes + static_cast<uint32_t>(q) * 2u * kStageOut;
+        uint32_t nst = 0;  // boxes this warp has handed to the TMA
+        PhiloxKey key{};
+        if constexpr (MODE == kDown) key = philox_key(a.drop);
+        const int outs = MODE == kGateUp ? a.outs : MODE == kDact ? 2 : 1;
+        int i = 0;
+        for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, ++i) {
+            const int b = i % NACC;
+            const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
+                                              static_cast<uint32_t>(i / NACC) & 1u, a.timeout_ns);
+            if (!ok || *reinterpret_cast<volatile int*>(&s_fail)) {
+                if (lane == 0) s_fail = 1;
+                break;
+            }
+            tc_fence_after();
+            int64_t tl = t;
+            const int p = ffn_problem(a, &tl);
+            const int64_t M = a.M[p], N = a.N[p];
+            const int64_t n0 = ffn_tile_n(a, p, tl) * kCols;
+#pragma unroll 1
+            for (int hh = 0; hh < H; ++hh) {
+                const int64_t m0 = ffn_tile_m(a, p, tl) * BM + hh * kMmaM;
+                const int64_t row = m0 + q * 32 + lane;
+                const bool rows_in = m0 + q * 32 < M;  // the same for the whole warp
+                const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                                      static_cast<uint32_t>((b * H + hh) * kBN);
+                if (!rows_in) continue;
+#pragma unroll 1
+                for (int c = 0; c < kCols / 64; ++c) {
+                    const int64_t n = n0 + c * 64;
+                    if (n >= N) break;  // the same for every thread of the warp
+#pragma unroll 1
+                    for (int o = 0; o < outs; ++o) {
+                        const uint32_t buf = stg + (nst & 1u) * kStageOut;
+                        // the box written two turns ago has been read out of this buffer
+                        if (lane == 0) bulk_wait_read_1();
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t col = static_cast<uint32_t>(c * 64 + h * 32);
+                            const int64_t nb = n + h * 32;
+                            float v[32];
+                            if constexpr (MODE == kGateUp) {
+                                tc_ld32(trow + (o == 2 ? 128u + col : col), v);
+                                if (o == 0) {
+                                    float w[32];
+                                    tc_ld32(trow + 128u + col, w);
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] = ffn_act(a.act, v[j]) * w[j];
+                                }
+                            } else if constexpr (MODE == kDact) {
+                                tc_ld32(trow + col, v);
+                                float g[32];
+                                load_row32<T>(a.g, row, nb, M, N, g);
+                                if (o == 0) {
+                                    float w[32];
+                                    load_row32<T>(a.u, row, nb, M, N, w);
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j)
+                                        v[j] = v[j] * w[j] * ffn_slope(a.act, g[j]);
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] *= ffn_act(a.act, g[j]);
+                                }
+                            } else {
+                                tc_ld32(trow + col, v);
+                            }
+                            if constexpr (MODE == kDown) {
+                                if (a.drop.mode == kDropSome) {
+                                    const uint64_t at = static_cast<uint64_t>(row * N + nb) / 4;
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) drop4(a.drop, key, at + j, v + 4 * j);
+                                } else if (a.drop.mode == kDropAll) {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                                }
+                                if (a.res) {
+                                    float w[32];
+                                    load_row32<T>(a.res, row, nb, M, N, w);
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] += w[j];
+                                }
+                            }
+                            stage32<T>(buf, lane, h, v);
+                        }
+                        fence_proxy_async_smem();  // the writes, seen by the TMA
+                        __syncwarp();
+                        if (lane == 0) {
+                            // rows past M and columns past N are clipped by the TMA
+                            tma_store_2d(&maps.c[MODE == kDw ? p : o], buf, static_cast<int>(n),
+                                         static_cast<int>(m0 + q * 32));
+                            bulk_commit();
+                        }
+                        ++nst;
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&acc_empty[b]));
+        }
+        // every box written out before the shared memory goes
+        if (lane == 0) bulk_wait_all();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // every MMA completes before the tensor memory is freed
+        const bool done = mbar_wait_bounded(smem_u32(&done_bar), 0u, a.timeout_ns);
+        if (s_fail || !done) {
+            atomicOr(a.status, kDevErrTimeout);
+            // copies still in flight land before the shared memory is released
+            for (int s = 0; s < kStages; ++s)
+                if (s_issued[s])
+                    (void)mbar_wait_bounded(smem_u32(&full_bar[s]), s_issued[s] & 1u,
+                                            a.timeout_ns);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+}
+
+template <uint32_t AB, int MODE>
+const void* ffn_fn(int bm) {
+    return bm == 256 ? (const void*)&ffn_gemm<AB, MODE, 256> : (const void*)&ffn_gemm<AB, MODE, 128>;
+}
+const void* ffn_fn(int dtype, int mode, int bm) {
+    const bool bf = dtype == CE_BF16;
+    switch (mode) {
+    case kGateUp: return bf ? ffn_fn<1u, kGateUp>(bm) : ffn_fn<0u, kGateUp>(bm);
+    case kDown: return bf ? ffn_fn<1u, kDown>(bm) : ffn_fn<0u, kDown>(bm);
+    case kDact: return bf ? ffn_fn<1u, kDact>(bm) : ffn_fn<0u, kDact>(bm);
+    case kDx: return bf ? ffn_fn<1u, kDx>(bm) : ffn_fn<0u, kDx>(bm);
+    default: return bf ? ffn_fn<1u, kDw>(bm) : ffn_fn<0u, kDw>(bm);
+    }
+}
+
+// A call's device, its status word and its wait limit.
+struct FfnDevice {
+    int sms;
+    unsigned* status;
+    uint64_t timeout_ns;
+};
+
+ce_status ffn_device(cudaStream_t st, FfnDevice* d) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    // makes the device's context this thread's (an autograd thread has none
+    // yet), which encoding a tensor map needs
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward device");
+    d->sms = std::max(d->sms, 1);
+    const char* env = std::getenv("GBCE_WAIT_TIMEOUT_MS");
+    d->timeout_ns = ((env && *env) ? static_cast<uint64_t>(std::atoll(env)) : 2000ull) * 1000000ull;
+    return library_status_word(st, &d->status);
+}
+
+// An operand of a launch: a row-major [outer, inner] matrix, as A or B.
+struct FfnMatrix {
+    const void* p;
+    int64_t outer, inner;
+};
+
+// One launch of form `mode`: problems or segments A[i] x B[i], outputs C[i].
+ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatrix (&A)[3],
+                     const FfnMatrix (&B)[3], const FfnMatrix (&C)[3], const FfnDevice& d,
+                     cudaStream_t st) {
+    const int64_t cols = mode == kGateUp ? kBN / 2 : kBN;
+    g.timeout_ns = d.timeout_ns;
+    g.status = d.status;
+    // the tile height with the fewer rounds of tiles over the SMs, as the
+    // GEMM chooses it (a round of 256-row tiles counts as 1.6 of 128-row ones)
+    int64_t tiles[2] = {0, 0};
+    for (int p = 0; p < problems; ++p)
+        for (int h = 0; h < 2; ++h)
+            tiles[h] += (g.M[p] + (h ? 255 : 127)) / (h ? 256 : 128) * ((g.N[p] + cols - 1) / cols);
+    const int64_t r128 = (tiles[0] + d.sms - 1) / d.sms, r256 = (tiles[1] + d.sms - 1) / d.sms;
+    const int bm = 16 * r256 < 10 * r128 ? 256 : 128;
+    int64_t end = 0;
+    for (int p = 0; p < 3; ++p) {
+        if (p < problems) {
+            g.tiles_m[p] = (g.M[p] + bm - 1) / bm;
+            g.tiles_n[p] = (g.N[p] + cols - 1) / cols;
+            end += g.tiles_m[p] * g.tiles_n[p];
+        }
+        g.tile_end[p] = end;
+    }
+    // consecutive tiles share a tile of the larger operand
+    g.m_first = g.N[0] >= g.M[0] ? 1 : 0;
+    FfnMaps maps = {};
+    const bool a_mn = mode == kDw, b_mn = mode == kDact || mode == kDx || mode == kDw;
+    for (int i = 0; i < 3; ++i) {
+        ce_status rc = CE_OK;
+        if (A[i].p) rc = tc_map_16bit(&maps.a[i], A[i].p, dtype, A[i].outer, A[i].inner, a_mn ? 64 : bm);
+        if (rc == CE_OK && B[i].p)
+            rc = tc_map_16bit(&maps.b[i], B[i].p, dtype, B[i].outer, B[i].inner,
+                              b_mn ? 64 : mode == kGateUp ? kBN / 2 : kBN);
+        if (rc == CE_OK && C[i].p)
+            rc = tc_map_16bit(&maps.c[i], C[i].p, dtype, C[i].outer, C[i].inner, 32);
+        if (rc != CE_OK) return rc;
+    }
+    const void* fn = ffn_fn(dtype, mode, bm);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kTcSmem));
+    if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward attributes");
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(end, d.sms));
+    void* args[] = {&maps, &g};
+    e = cudaLaunchKernel(fn, dim3(grid), dim3(kTcThreads), args, kTcSmem, st);
+    return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "feed-forward launch");
+}
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
+
+ce_status check_ffn(int dtype, int64_t rows, int64_t H, int64_t I, int64_t O, int act) {
+    if (dtype != CE_BF16 && dtype != CE_F16) return dtype == CE_F32 ? CE_ERR_UNSUPPORTED : CE_ERR_INVALID_ARG;
+    if (rows < 0 || H <= 0 || I <= 0 || O <= 0) return CE_ERR_INVALID_ARG;
+    if (act < CE_ACT_SILU || act > CE_ACT_GELU_TANH) return CE_ERR_INVALID_ARG;
+    if (H % 8 || I % 8 || O % 8 || rows > INT32_MAX || H > INT32_MAX || I > INT32_MAX || O > INT32_MAX) {
+        record_message("the feed-forward block takes H, I and O that are multiples of 8, below 2^31");
+        return CE_ERR_UNSUPPORTED;
+    }
+    return CE_OK;
+}
+
+}  // namespace
+}  // namespace gbce
+
+using namespace gbce;
+
+extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up,
+                                const void* w_down, const void* residual, int dtype, int64_t rows,
+                                int64_t H, int64_t I, int64_t O, int act, double p, uint64_t seed,
+                                uint64_t offset, const int64_t* state, void* y, void* h, void* g,
+                                void* u, void* workspace, size_t workspace_bytes,
+                                ce_stream_t stream) {
+    ce_status rc = check_ffn(dtype, rows, H, I, O, act);
+    if (rc != CE_OK) return rc;
+    FfnGemm a = {};
+    if (!drop_spec(p, seed, offset, state, &a.drop)) return CE_ERR_INVALID_ARG;
+    if (!w_gate || !w_up || !w_down || (g == nullptr) != (u == nullptr)) return CE_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !y || !h)) return CE_ERR_INVALID_ARG;
+    for (const void* q : {x, w_gate, w_up, w_down, residual, static_cast<const void*>(y),
+                          static_cast<const void*>(h), static_cast<const void*>(g),
+                          static_cast<const void*>(u)})
+        if (!aligned(q)) return CE_ERR_UNSUPPORTED;
+    if (rows == 0) return CE_OK;
+    (void)workspace;
+    (void)workspace_bytes;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    FfnDevice d;
+    rc = ffn_device(st, &d);
+    if (rc != CE_OK) return rc;
+    a.segs = 1;
+    a.act = act;
+    FfnGemm up = a;
+    up.M[0] = rows;
+    up.N[0] = I;
+    up.K = H;
+    up.outs = g ? 3 : 1;
+    rc = ffn_launch(kGateUp, dtype, up, 1, {{x, rows, H}}, {{w_gate, I, H}, {w_up, I, H}},
+                    {{h, rows, I}, {g, rows, I}, {u, rows, I}}, d, st);
+    if (rc != CE_OK) return rc;
+    FfnGemm down = a;
+    down.M[0] = rows;
+    down.N[0] = O;
+    down.K = I;
+    down.res = residual;
+    return ffn_launch(kDown, dtype, down, 1, {{h, rows, I}}, {{w_down, O, I}}, {{y, rows, O}}, d, st);
+}
+
+extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t I, int64_t O, double p) {
+    if (rows < 0 || I <= 0 || O <= 0) return 0;
+    return static_cast<size_t>(2 * up256(rows * I * 2) + (p > 0.0 ? up256(rows * O * 2) : 0));
+}
+
+extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate,
+                                const void* w_up, const void* w_down, const void* h,
+                                const void* g, const void* u, int dtype, int64_t rows, int64_t H,
+                                int64_t I, int64_t O, int act, double p, uint64_t seed,
+                                uint64_t offset, const int64_t* state, void* dx, void* dw_gate,
+                                void* dw_up, void* dw_down, void* workspace,
+                                size_t workspace_bytes, ce_stream_t stream) {
+    ce_status rc = check_ffn(dtype, rows, H, I, O, act);
+    if (rc != CE_OK) return rc;
+    FfnGemm a = {};
+    if (!drop_spec(p, seed, offset, state, &a.drop)) return CE_ERR_INVALID_ARG;
+    if ((dw_gate == nullptr) != (dw_up == nullptr)) return CE_ERR_INVALID_ARG;
+    if (!w_gate || !w_up || !w_down) return CE_ERR_INVALID_ARG;
+    if (rows > 0 && (!dy || !x || !h || !g || !u)) return CE_ERR_INVALID_ARG;
+    for (const void* q : {dy, x, w_gate, w_up, w_down, h, g, u, static_cast<const void*>(dx),
+                          static_cast<const void*>(dw_gate), static_cast<const void*>(dw_up),
+                          static_cast<const void*>(dw_down)})
+        if (!aligned(q)) return CE_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // no rows: zero gradients of the weights
+        cudaError_t e = cudaSuccess;
+        if (dw_gate) e = cudaMemsetAsync(dw_gate, 0, static_cast<size_t>(I * H * 2), st);
+        if (e == cudaSuccess && dw_up) e = cudaMemsetAsync(dw_up, 0, static_cast<size_t>(I * H * 2), st);
+        if (e == cudaSuccess && dw_down)
+            e = cudaMemsetAsync(dw_down, 0, static_cast<size_t>(O * I * 2), st);
+        return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "cudaMemsetAsync(weight gradients)");
+    }
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < ce_ffn_bwd_workspace_bytes(rows, I, O, p))
+        return CE_ERR_INVALID_ARG;
+    FfnDevice d;
+    rc = ffn_device(st, &d);
+    if (rc != CE_OK) return rc;
+    char* ws = static_cast<char*>(workspace);
+    void* dg = ws;
+    void* du = ws + up256(rows * I * 2);
+    const void* dz = dy;
+    if (a.drop.mode != kDropNone) {
+        void* masked = ws + 2 * up256(rows * I * 2);
+        rc = ce_dropout(dy, nullptr, masked, dtype, rows * O, p, seed, offset, state, nullptr, stream);
+        if (rc != CE_OK) return rc;
+        dz = masked;
+    }
+    a.segs = 1;
+    a.act = act;
+    if (dx || dw_gate) {
+        FfnGemm t = a;
+        t.M[0] = rows;
+        t.N[0] = I;
+        t.K = O;
+        t.g = g;
+        t.u = u;
+        rc = ffn_launch(kDact, dtype, t, 1, {{dz, rows, O}}, {{w_down, O, I}},
+                        {{dg, rows, I}, {du, rows, I}}, d, st);
+        if (rc != CE_OK) return rc;
+    }
+    if (dx) {
+        FfnGemm t = a;
+        t.M[0] = rows;
+        t.N[0] = H;
+        t.K = I;
+        t.segs = 2;
+        rc = ffn_launch(kDx, dtype, t, 1, {{dg, rows, I}, {du, rows, I}}, {{w_gate, I, H}, {w_up, I, H}},
+                        {{dx, rows, H}}, d, st);
+        if (rc != CE_OK) return rc;
+    }
+    if (dw_gate || dw_down) {
+        FfnGemm t = a;
+        t.K = rows;
+        FfnMatrix A[3] = {}, B[3] = {}, C[3] = {};
+        int n = 0;
+        const auto add = [&](const void* left, int64_t m, const void* right, int64_t cols, void* out) {
+            t.M[n] = m;
+            t.N[n] = cols;
+            A[n] = FfnMatrix{left, rows, m};
+            B[n] = FfnMatrix{right, rows, cols};
+            C[n] = FfnMatrix{out, m, cols};
+            ++n;
+        };
+        if (dw_gate) {
+            add(dg, I, x, H, dw_gate);
+            add(du, I, x, H, dw_up);
+        }
+        if (dw_down) add(dz, O, h, I, dw_down);
+        rc = ffn_launch(kDw, dtype, t, n, A, B, C, d, st);
+        if (rc != CE_OK) return rc;
+    }
+    return CE_OK;
+}
+
+extern "C" size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O) {
+    (void)rows;
+    (void)H;
+    (void)I;
+    (void)O;
+    return 0;
+}

@@ -1,0 +1,166 @@
+"""The gated feed-forward block on the tensor cores.
+
+    y = gated_feed_forward(x, gate_weight, up_weight, down_weight,
+                           activation="silu", dropout_p=0.0, seed=None,
+                           residual=None)
+
+y = residual + dropout(h @ down_weight^T) with h = act(x @ gate_weight^T) *
+(x @ up_weight^T): both projections, the activation and the product in one
+kernel, dropout and the residual sum in the second's epilogue, and the whole
+backward pass (ce_ffn_fwd and ce_ffn_bwd in include/gbce.h). Runs in
+libgbce.so; there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._tensors import DTYPES, check, on, ptr, require_cuda, stream
+from .philox_dropout import check_rng, dropout
+
+__all__ = ["gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
+
+_ACTIVATIONS = {"silu": _lib.CE_ACT_SILU, "gelu": _lib.CE_ACT_GELU,
+                "gelu_tanh": _lib.CE_ACT_GELU_TANH}
+
+
+class GatedFeedForwardFunction(torch.autograd.Function):
+    """Autograd wrapper of ce_ffn_fwd and ce_ffn_bwd on [rows, H] inputs. The
+    forward keeps x, g, u and h (the last three [rows, I]) for the backward."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, residual, act, p, seed, offset, state):
+        rows, H = x.shape
+        O, I = w_down.shape
+        dev, dt = x.device, x.dtype
+        grad = any(ctx.needs_input_grad[:4])
+        empty = lambda *shape: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+        y, h = empty(rows, O), empty(rows, I)
+        g, u = (empty(rows, I), empty(rows, I)) if grad else (None, None)
+        if grad and state is not None and p > 0.0:
+            state = state.clone()  # the caller may change it before the backward runs
+        nbytes = _lib.ce_ffn_fwd_workspace_bytes(rows, H, I, O)
+        with on(dev):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+            check(_lib.ce_ffn_fwd(ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(residual),
+                                  DTYPES[dt], rows, H, I, O, act, p, seed, offset, ptr(state),
+                                  ptr(y), ptr(h), ptr(g), ptr(u), ptr(ws), nbytes, stream(dev)),
+                  "ce_ffn_fwd")
+        if grad:
+            ctx.save_for_backward(x, w_gate, w_up, w_down, h, g, u, state)
+        ctx.args = (act, p, seed, offset)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need = ctx.needs_input_grad
+        dx = dwg = dwu = dwd = None
+        if any(need[:4]):
+            x, w_gate, w_up, w_down, h, g, u, state = ctx.saved_tensors
+            act, p, seed, offset = ctx.args
+            rows, H = x.shape
+            O, I = w_down.shape
+            dev, dt = x.device, x.dtype
+            grad_out, dy = dy, dy.contiguous()
+            if dy.data_ptr() % 16:
+                dy = dy.clone()
+            dx = torch.empty_like(x) if need[0] else None
+            if need[1] or need[2]:
+                dwg, dwu = torch.empty_like(w_gate), torch.empty_like(w_up)
+            dwd = torch.empty_like(w_down) if need[3] else None
+            nbytes = _lib.ce_ffn_bwd_workspace_bytes(rows, I, O, p)
+            with on(dev):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                check(_lib.ce_ffn_bwd(ptr(dy), ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(h),
+                                      ptr(g), ptr(u), DTYPES[dt], rows, H, I, O, act, p, seed,
+                                      offset, ptr(state), ptr(dx), ptr(dwg), ptr(dwu), ptr(dwd),
+                                      ptr(ws), nbytes, stream(dev)), "ce_ffn_bwd")
+            dy = grad_out
+        return (dx, dwg if need[1] else None, dwu if need[2] else None, dwd,
+                dy if need[4] else None, None, None, None, None, None)
+
+
+def _padded(t, rows, cols):
+    """t [r, c] with zeros up to multiples of `rows` and `cols`."""
+    r, c = -t.shape[0] % rows, -t.shape[1] % cols
+    return torch.nn.functional.pad(t, (0, c, 0, r)) if r or c else t
+
+
+def _aligned(t):
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu", dropout_p=0.0,
+                       seed=None, offset=0, residual=None):
+    """residual + dropout((act(x @ gate_weight^T) * (x @ up_weight^T)) @ down_weight^T).
+
+    x [..., H], gate_weight and up_weight [I, H], down_weight [O, I], residual
+    None or [..., O], all bfloat16 or float16 on one CUDA device; activation
+    "silu", "gelu" or "gelu_tanh". dropout_p, seed and offset as for dropout()
+    over the [..., O] elements. Differentiable in x, the weights and residual;
+    for that the forward keeps x and three [..., I] tensors.
+
+    H, I and O that are not multiples of 8 are padded with zeros on each call
+    (a copy of what they concern), and the dropout and residual then follow as
+    a call of their own, on an output rounded once before."""
+    for name, t in (("x", x), ("gate_weight", gate_weight), ("up_weight", up_weight),
+                    ("down_weight", down_weight)) + \
+            ((("residual", residual),) if residual is not None else ()):
+        require_cuda(t, name)
+        if t.dtype not in (torch.bfloat16, torch.float16) or t.dtype != x.dtype:
+            raise TypeError("the block takes bfloat16 or float16, the same for every tensor")
+        if t.device != x.device:
+            raise ValueError("the tensors must be on one device")
+    if gate_weight.dim() != 2 or down_weight.dim() != 2 or gate_weight.shape != up_weight.shape:
+        raise ValueError("gate_weight and up_weight must be [I, H], down_weight [O, I]")
+    I, H = gate_weight.shape
+    O = down_weight.shape[0]
+    if x.dim() < 1 or x.shape[-1] != H or down_weight.shape[1] != I or min(H, I, O) < 1:
+        raise ValueError("x must be [..., H], down_weight [O, I]")
+    shape = (*x.shape[:-1], O)
+    if residual is not None and tuple(residual.shape) != shape:
+        raise ValueError("residual must have the shape of the output")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    act = _ACTIVATIONS[activation]
+    p, seed_, offset_, state = check_rng(dropout_p, seed, offset, x.device)
+    x2 = x.reshape(-1, H)
+    if H % 8 or I % 8 or O % 8:
+        y = GatedFeedForwardFunction.apply(
+            _aligned(_padded(x2, 1, 8)), _aligned(_padded(gate_weight, 8, 8)),
+            _aligned(_padded(up_weight, 8, 8)), _aligned(_padded(down_weight, 8, 8)), None, act,
+            0.0, 0, 0, None)[:, :O].reshape(shape)
+        if p == 0.0 and residual is None:
+            return y
+        return dropout(y, p, seed, offset, residual=residual)
+    res = None if residual is None else _aligned(residual.reshape(-1, O))
+    return GatedFeedForwardFunction.apply(
+        _aligned(x2), _aligned(gate_weight), _aligned(up_weight), _aligned(down_weight), res, act,
+        p, seed_, offset_, state).reshape(shape)
+
+
+class GatedFeedForward(torch.nn.Module):
+    """Module form of gated_feed_forward, with its three weights. Its dropout
+    (in training mode) takes the seed of each call."""
+
+    def __init__(self, hidden_size, intermediate_size, activation="silu", dropout_p=0.0,
+                 device=None, dtype=torch.bfloat16):
+        super().__init__()
+        f = dict(device=device, dtype=dtype)
+        self.gate = torch.nn.Parameter(torch.empty(intermediate_size, hidden_size, **f))
+        self.up = torch.nn.Parameter(torch.empty(intermediate_size, hidden_size, **f))
+        self.down = torch.nn.Parameter(torch.empty(hidden_size, intermediate_size, **f))
+        self.activation = activation
+        self.dropout_p = dropout_p
+        self.reset_parameters()
+
+    def reset_parameters(self):
+        for w in (self.gate, self.up, self.down):
+            torch.nn.init.normal_(w, std=w.shape[1] ** -0.5)
+
+    def forward(self, x, residual=None, seed=None, offset=0):
+        p = self.dropout_p if self.training else 0.0
+        return gated_feed_forward(x, self.gate, self.up, self.down, self.activation, p, seed,
+                                  offset, residual)

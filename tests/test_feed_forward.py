@@ -1,0 +1,399 @@
+"""The gated feed-forward block: refusals (CPU), and the kernels against the
+formulas in 64 bits (GPU)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from philox_ref import keep
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def act64(g, name):
+    """(act, slope) in 64 bits."""
+    if name == "silu":
+        q = torch.sigmoid(g)
+        return g * q, q + g * q * (1 - q)
+    if name == "gelu":
+        c = 0.5 * torch.erfc(-g / math.sqrt(2))
+        return g * c, c + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    k = math.sqrt(2 / math.pi)
+    t = torch.tanh(k * (g + 0.044715 * g ** 3))
+    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 0.134145 * g * g)
+
+
+def mask64(rows, O, p, seed, offset=0):
+    if p == 0.0:
+        return torch.ones(rows, O, dtype=torch.float64, device="cuda")
+    kept = torch.from_numpy(keep(rows * O, p, seed, offset)).cuda().reshape(rows, O)
+    return kept.double() * (0.0 if p == 1.0 else 1.0 / (1.0 - p))
+
+
+def reference(x, wg, wu, wd, act, f, res=None, dy=None):
+    """Outputs and gradients in 64 bits, and for each the sum of the absolute
+    values that its last product adds (what a relative error of its factors is
+    scaled by)."""
+    x, wg, wu, wd = (t.detach().double() for t in (x, wg, wu, wd))
+    g, u = x @ wg.T, x @ wu.T
+    a, s = act64(g, act)
+    h = a * u
+    y = (h @ wd.T) * f
+    size = {"y": (h.abs() @ wd.abs().T) * f}
+    if res is not None:
+        y = y + res.detach().double()
+    out = {"y": y}
+    if dy is None:
+        return out, size
+    dz = dy.double() * f
+    dh = dz @ wd
+    dg, du = dh * u * s, dh * a
+    # dh's factors: what an error of g and u (and of dh, from dz rounded) does to dg and du
+    adh = dz.abs() @ wd.abs()
+    out.update(dx=dg @ wg + du @ wu, dw_gate=dg.T @ x, dw_up=du.T @ x, dw_down=dz.T @ h)
+    # |act'| is at most 1.13 (gelu) and changes by at most 1.6 |g| 2^-8 where g does; sizes that
+    # bound both: adh |u| 1.13 (1 + |g|) and adh (|a| + 1.13 |g|)
+    bg, bu = adh * u.abs() * 1.13 * (1 + 1.5 * g.abs()), adh * (a.abs() + 1.13 * g.abs())
+    size.update(dx=bg @ wg.abs() + bu @ wu.abs(), dw_gate=bg.T @ x.abs(), dw_up=bu.T @ x.abs(),
+                dw_down=dz.abs().T @ h.abs())
+    return out, size
+
+
+# The kernel rounds h once before y's product, and g, u, dz, then dg and du before the gradients':
+# half a step (eps / 2) of each factor, at most five of them in a gradient's term (g, u, dz, the
+# slope's change counted in its size, dg or du), and products that accumulate in fp32: n terms are
+# added with at most n 2^-24 of their sizes. The result's own rounding is half a step of the value.
+def check(got, want, size, dt, roundings, terms):
+    eps = torch.finfo(dt).eps
+    bound = size * (roundings * eps / 2 * 1.02 + terms * 2.0 ** -24) + \
+        want.abs() * eps / 2 * 1.02 + torch.finfo(dt).smallest_normal
+    err = (got.detach().double() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    # what the bound leaves room for, a systematic error, would show in the norm: the roundings are
+    # independent, so the error is of the order of one of them (2^-8 of the norm, or eps)
+    norm = want.norm()
+    if norm > 0 and want.numel() >= 64:
+        assert float(err.norm() / norm) <= 3 * eps
+
+
+def make(rows, H, I, O, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + rows + 3 * H + 5 * I + 7 * O)
+    n = lambda *s, k=1.0: (torch.randn(*s, generator=g, device="cuda") * k).to(DT[dtype])  # noqa: E731
+    return (n(rows, H), n(I, H, k=H ** -0.5), n(I, H, k=H ** -0.5), n(O, I, k=I ** -0.5),
+            n(rows, O), n(rows, O))
+
+
+# ---------------------------------------------------------------- CPU
+
+def fwd(**over):
+    from softmax_cross_entropy_gb300 import _lib
+    a = dict(x=256, w_gate=256, w_up=256, w_down=256, residual=None, dtype=_lib.CE_BF16, rows=4,
+             H=64, I=64, O=64, act=0, p=0.0, seed=0, offset=0, state=None, y=256, h=256, g=None,
+             u=None, workspace=None, workspace_bytes=0, stream=None)
+    a.update(over)
+    return _lib.ce_ffn_fwd(**a)
+
+
+def bwd(**over):
+    from softmax_cross_entropy_gb300 import _lib
+    a = dict(dy=256, x=256, w_gate=256, w_up=256, w_down=256, h=256, g=256, u=256,
+             dtype=_lib.CE_F16, rows=4, H=64, I=64, O=64, act=1, p=0.1, seed=0, offset=0,
+             state=None, dx=256, dw_gate=256, dw_up=256, dw_down=256, workspace=256,
+             workspace_bytes=1 << 20, stream=None)
+    a.update(over)
+    return _lib.ce_ffn_bwd(**a)
+
+
+BAD = [dict(dtype=3), dict(rows=-1), dict(H=0), dict(I=-8), dict(O=0), dict(act=3), dict(act=-1),
+       dict(p=-0.5), dict(p=2.0), dict(p=float("nan")), dict(x=None), dict(w_gate=None),
+       dict(w_up=None), dict(w_down=None)]
+
+
+@pytest.mark.parametrize("over", BAD + [dict(y=None), dict(h=None), dict(g=256)])
+def test_forward_refuses(over):
+    from softmax_cross_entropy_gb300 import _lib
+    assert fwd(**over) == _lib.CE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", BAD + [dict(dy=None), dict(h=None), dict(g=None), dict(u=None),
+                                        dict(dw_up=None), dict(workspace=None),
+                                        dict(workspace=264), dict(workspace_bytes=100)])
+def test_backward_refuses(over):
+    from softmax_cross_entropy_gb300 import _lib
+    assert bwd(**over) == _lib.CE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(dtype=0), dict(H=60), dict(I=63), dict(O=66), dict(x=264),
+                                  dict(w_down=258), dict(rows=2 ** 31)])
+def test_sizes_and_types_it_does_not_take(over):
+    from softmax_cross_entropy_gb300 import _lib
+    assert fwd(**over) == _lib.CE_ERR_UNSUPPORTED
+    assert bwd(**over) == _lib.CE_ERR_UNSUPPORTED
+
+
+def test_wrapper_refuses_cpu_tensors():
+    import softmax_cross_entropy_gb300 as gbce
+    t = torch.zeros(8, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        gbce.gated_feed_forward(t, t, t, t)
+
+
+# ---------------------------------------------------------------- GPU
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("rows,H,I,O", [
+    (1, 8, 8, 8), (2, 64, 128, 64), (3, 200, 72, 40), (16, 256, 512, 256), (17, 1000, 24, 136),
+    (33, 72, 1000, 264), (64, 512, 640, 512), (129, 136, 264, 8), (300, 384, 320, 640),
+    (515, 256, 1032, 256)])
+def test_forward(dtype, act, rows, H, I, O):
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, _, _ = make(rows, H, I, O, dtype)
+    y = gbce.gated_feed_forward(x, wg, wu, wd, activation=act)
+    want, size = reference(x, wg, wu, wd, act, mask64(rows, O, 0.0, 0))
+    check(y, want["y"], size["y"], DT[dtype], 1, H + I)
+    assert gbce.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("rows,H,I,O,p,residual", [
+    (1, 8, 8, 8, 0.0, False), (5, 64, 128, 72, 0.3, True), (70, 264, 136, 264, 0.0, True),
+    (130, 128, 256, 128, 0.1, False), (257, 520, 392, 520, 0.1, True), (512, 512, 1024, 512, 0.5, True),
+    (64, 64, 64, 64, 1.0, True)])
+def test_training_step(dtype, act, rows, H, I, O, p, residual):
+    import softmax_cross_entropy_gb300 as gbce
+    dt = DT[dtype]
+    x, wg, wu, wd, res, dy = make(rows, H, I, O, dtype)
+    leaves = [t.requires_grad_() for t in (x, wg, wu, wd)] + ([res.requires_grad_()] if residual else [])
+    y = gbce.gated_feed_forward(x, wg, wu, wd, activation=act, dropout_p=p, seed=99, offset=7,
+                                residual=res if residual else None)
+    grads = torch.autograd.grad(y, leaves, dy)
+    want, size = reference(x, wg, wu, wd, act, mask64(rows, O, p, 99, 7), res if residual else None, dy)
+    check(y, want["y"], size["y"], dt, 1, H + I)
+    for name, got, n in zip(("dx", "dw_gate", "dw_up", "dw_down"), grads, (O + 2 * I, O + rows, O + rows, rows)):
+        check(got, want[name], size[name], dt, 5, n + H)
+    if residual:
+        assert torch.equal(grads[4], dy)
+    assert gbce.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gradients_against_differences(act):
+    # (f(t + d) - f(t - d)) / 2 of the 64-bit formulas along the kernel's own gradient direction
+    import softmax_cross_entropy_gb300 as gbce
+    args = [t.requires_grad_() for t in make(40, 64, 96, 64, "f16")[:4]]
+    dy = make(40, 64, 96, 64, "f16", 1)[5]
+    grads = torch.autograd.grad(gbce.gated_feed_forward(*args, activation=act), args, dy)
+
+    def loss(step):
+        x, wg, wu, wd = (t.detach().double() + step * d.double() for t, d in zip(args, grads))
+        return float((((act64(x @ wg.T, act)[0] * (x @ wu.T)) @ wd.T) * dy.double()).sum())
+
+    total = sum(float(d.double().square().sum()) for d in grads)
+    step = 1e-4 / math.sqrt(total)
+    diff = (loss(step) - loss(-step)) / (2 * step)
+    # the direction is the gradient itself: the derivative along it is its squared norm, up to the
+    # gradients' own relative error (a few eps) and the difference's second order
+    assert abs(diff / total - 1.0) <= 4 * torch.finfo(torch.float16).eps
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,H,I,O", [(1, 7, 9, 5), (37, 33, 65, 33), (130, 1001, 131, 77)])
+@pytest.mark.parametrize("p,residual", [(0.0, False), (0.25, True)])
+def test_odd_sizes_are_padded(rows, H, I, O, p, residual):
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, dy = make(rows, H, I, O, "bf16")
+    leaves = [t.requires_grad_() for t in (x, wg, wu, wd)] + ([res.requires_grad_()] if residual else [])
+    y = gbce.gated_feed_forward(x, wg, wu, wd, dropout_p=p, seed=5, residual=res if residual else None)
+    want, size = reference(x, wg, wu, wd, "silu", mask64(rows, O, p, 5), res if residual else None, dy)
+    check(y, want["y"], size["y"], torch.bfloat16, 2, H + I)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "dw_down"), torch.autograd.grad(y, leaves, dy)):
+        assert got.shape == want[name].shape
+        check(got, want[name], size[name], torch.bfloat16, 5, H + 2 * I + O + rows)
+
+
+@pytest.mark.gpu
+def test_leading_dimensions_strides_and_no_rows():
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, _ = make(24, 64, 128, 64, "bf16")
+    y = gbce.gated_feed_forward(x, wg, wu, wd, residual=res)
+    y3 = gbce.gated_feed_forward(x.view(2, 3, 4, 64), wg, wu, wd, residual=res.view(2, 3, 4, 64))
+    assert torch.equal(y3.view(24, 64), y)
+    yt = gbce.gated_feed_forward(x.t().contiguous().t(), wg.t().contiguous().t(), wu, wd, residual=res)
+    assert torch.equal(yt, y)
+    odd = torch.empty(24 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(24, 64).copy_(x)
+    assert torch.equal(gbce.gated_feed_forward(odd, wg, wu, wd, residual=res), y)
+    one = gbce.gated_feed_forward(x[3], wg, wu, wd)
+    assert one.shape == (64,)
+    e = x[:0].requires_grad_()
+    w = wg.detach().requires_grad_()
+    ye = gbce.gated_feed_forward(e, w, wu, wd)
+    assert ye.shape == (0, 64)
+    ge, gw = torch.autograd.grad(ye.sum(), [e, w])
+    assert ge.shape == (0, 64) and torch.equal(gw, torch.zeros_like(w))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", [(0,), (1,), (2, 3), (3,), (0, 3), (4,)])
+def test_some_gradients_only(which):
+    import softmax_cross_entropy_gb300 as gbce
+    args = list(make(72, 64, 136, 64, "bf16")[:5])
+    dy = make(72, 64, 136, 64, "bf16", 2)[5]
+
+    def grads(idx):
+        a = [t.detach().clone().requires_grad_(i in idx) for i, t in enumerate(args)]
+        y = gbce.gated_feed_forward(*a[:4], residual=a[4], dropout_p=0.2, seed=1)
+        return torch.autograd.grad(y, [a[i] for i in idx], dy)
+
+    every = grads((0, 1, 2, 3, 4))
+    for i, g in zip(which, grads(which)):
+        assert torch.equal(g, every[i])
+
+
+@pytest.mark.gpu
+def test_rows_do_not_touch_each_other_and_results_repeat():
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, _ = make(200, 128, 256, 128, "bf16")
+    y = gbce.gated_feed_forward(x, wg, wu, wd, residual=res)
+    assert torch.equal(gbce.gated_feed_forward(x, wg, wu, wd, residual=res), y)
+    x2 = x.clone()
+    x2[100] = float("nan")
+    y2 = gbce.gated_feed_forward(x2, wg, wu, wd, residual=res)
+    rest = torch.arange(200, device="cuda") != 100
+    assert torch.equal(y2[rest], y[rest]) and bool(y2[100].isnan().all())
+
+
+@pytest.mark.gpu
+def test_large_gates_saturate():
+    import softmax_cross_entropy_gb300 as gbce
+    # g = +-3008: act(g) is g or 0, its slope 1 or 0
+    x = torch.full((8, 64), 1.0, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    sign = torch.tensor([1.0, -1.0], device="cuda").repeat(32)[:, None]
+    wg = (sign * 47.0).expand(64, 64).bfloat16().contiguous()
+    wu = torch.full((64, 64), 1 / 64, device="cuda", dtype=torch.bfloat16)
+    wd = torch.full((64, 64), 1 / 64, device="cuda", dtype=torch.bfloat16)
+    for act in ("silu", "gelu", "gelu_tanh"):
+        y = gbce.gated_feed_forward(x, wg, wu, wd, activation=act)
+        # 32 gates of 3008, the others 0
+        assert torch.equal(y.detach().float(), torch.full_like(y, 1504.0).float())
+        (dx,) = torch.autograd.grad(y.sum(), [x])
+        assert bool(dx.isfinite().all())
+
+
+@pytest.mark.gpu
+def test_seed_tensor_changed_before_the_backward_and_captured_step():
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, dy = make(40, 64, 128, 64, "bf16")
+    leaves = [t.requires_grad_() for t in (x, wg, wu, wd)]
+    state = torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+
+    def step(seed, offset=0):
+        y = gbce.gated_feed_forward(x, wg, wu, wd, dropout_p=0.5, seed=seed, offset=offset, residual=res)
+        if isinstance(seed, torch.Tensor):
+            seed += 1
+        return [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+
+    want = [step(s, s + 1) for s in range(3, 7)]
+    for a, b in zip(step(state), want[0]):
+        assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            outs = step(state)
+    torch.cuda.synchronize()
+    for w in want[1:]:
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, w):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    import softmax_cross_entropy_gb300 as gbce
+    sets = [make(96, 256, 512, 256, "f16", i) for i in range(3)]
+    want = [gbce.gated_feed_forward(*s[:4], residual=s[4]) for s in sets]
+    few = [gbce.gated_feed_forward(s[0][:4], *s[1:4]) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append((gbce.gated_feed_forward(*s[:4], residual=s[4]),
+                            gbce.gated_feed_forward(s[0][:4], *s[1:4])))
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(got):
+        assert torch.equal(a, want[i % 3]) and torch.equal(b, few[i % 3])
+
+
+@pytest.mark.gpu
+def test_block_then_loss_then_beams():
+    """Together as they would be used: a training step of block + fused linear cross-entropy, whose
+    gradients reach the block's weights, then beams over the same model's logits."""
+    import softmax_cross_entropy_gb300 as gbce
+    torch.manual_seed(0)
+    H, V, rows = 64, 512, 48
+    block = gbce.GatedFeedForward(H, 128, dropout_p=0.1, device="cuda")
+    emb = (torch.randn(V, H, device="cuda") * 0.5).bfloat16().requires_grad_()
+    tokens = torch.randint(0, V, (rows,), device="cuda")
+    target = torch.randint(0, V, (rows,), device="cuda")
+    x = emb[tokens]
+    hidden = block(x, residual=x, seed=11)
+    loss = gbce.fused_linear_cross_entropy(hidden, emb, target)
+    loss.backward()
+    # the same in 64 bits
+    p64 = [t.detach().double().requires_grad_() for t in (emb, block.gate, block.up, block.down)]
+    e, wg, wu, wd = p64
+    x64 = e[tokens]
+    g = x64 @ wg.T
+    y = ((g * torch.sigmoid(g) * (x64 @ wu.T)) @ wd.T) * mask64(rows, H, 0.1, 11) + x64
+    ref = torch.nn.functional.cross_entropy(y @ e.T, target)
+    ref.backward()
+    assert abs(float(loss) - float(ref)) <= 2e-3 * float(ref)
+    for got, want in zip((emb, block.gate, block.up, block.down), p64):
+        assert float((got.grad.double() - want.grad).norm() / want.grad.norm()) <= 0.02
+    # generating: 2 sequences x 4 beams, the token form of the block, a step of beam search
+    block.eval()
+    B, K = 2, 4
+    last = torch.randint(0, V, (B, K), device="cuda")
+    scores = torch.zeros(B, K, device="cuda")
+    history = torch.zeros(B * K, 4, dtype=torch.int64, device="cuda")
+    for step in range(4):
+        x = emb.detach()[last]
+        logits = block(x, residual=x) @ emb.detach().T
+        best = gbce.beam_search_step(logits, scores, finished=None)
+        total = (scores[..., None].double() + torch.log_softmax(logits.double(), 2)).reshape(B, -1)
+        assert torch.allclose(best.scores.double(), total.topk(K, 1).values, atol=1e-4)
+        gbce.beam_reorder(history, best.beams, inplace=True)
+        last, scores = best.tokens, best.scores
+        history[:, step] = last.reshape(-1)
+    assert bool((scores[:, :-1] >= scores[:, 1:]).all())
+
+
+@pytest.mark.gpu
+def test_wrapper_refuses():
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, _ = make(8, 64, 128, 64, "bf16")
+    f = gbce.gated_feed_forward
+    with pytest.raises(TypeError):
+        f(x.float(), wg.float(), wu.float(), wd.float())
+    with pytest.raises(TypeError):
+        f(x, wg.half(), wu, wd)
+    with pytest.raises(ValueError):
+        f(x, wg, wu[:64], wd)
+    with pytest.raises(ValueError):
+        f(x, wg, wu, wd.t())
+    with pytest.raises(ValueError):
+        f(x, wg, wu, wd, residual=res[:4])
+    with pytest.raises(ValueError):
+        f(x, wg, wu, wd, activation="tanh")
+    with pytest.raises(ValueError):
+        f(x, wg, wu, wd, dropout_p=0.5)
