@@ -459,15 +459,19 @@ enum {
  * output the fused linear cross-entropy takes as its hidden states.
  *
  * x [rows, H], w_gate and w_up [I, H], w_down [O, I], residual [rows, O] or
- * NULL, y [rows, O]: row-major, all in dtype CE_BF16 or CE_F16, with 16-byte
- * aligned bases and H, I and O multiples of 8 (CE_ERR_UNSUPPORTED
- * otherwise, and for CE_F32). rows may be 0.
+ * NULL, y [rows, O]: row-major, all in dtype CE_BF16 or CE_F16
+ * (CE_ERR_UNSUPPORTED for CE_F32). Any sizes; rows may be 0. A matrix whose
+ * rows are whole 16-byte vectors (its last dimension a multiple of 8) needs a
+ * 16-byte aligned base (CE_ERR_UNSUPPORTED otherwise; y and residual need
+ * none); others are packed into the workspace first, which costs a copy.
  * act          a CE_ACT_* value.
  * p, seed, offset, state   the dropout, as for ce_dropout over the [rows, O]
  *              elements; p = 0 applies none.
- * h            [rows, I] in dtype, written: act(g) u rounded once.
- * g, u         [rows, I] in dtype, written (x @ w_gate^T and x @ w_up^T, what
- *              ce_ffn_bwd needs besides h), or both NULL.
+ * h            [rows, I8] in dtype, 16-byte aligned, written: act(g) u with
+ *              g = x @ w_gate^T and u = x @ w_up^T, rounded once. I8 is I
+ *              rounded up to a multiple of 8; the columns behind I get 0.
+ * s, a         [rows, I8] like h, written: u act'(g) and act(g), what
+ *              ce_ffn_bwd needs besides h; or both NULL.
  * workspace    device memory of at least ce_ffn_fwd_workspace_bytes(rows, H,
  *              I, O) bytes, 256-byte aligned, owned by the caller (NULL where
  *              that is 0); nothing in it needs to be set.
@@ -481,27 +485,29 @@ size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O)
 ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                      const void* residual, int dtype, int64_t rows, int64_t H, int64_t I,
                      int64_t O, int act, double p, uint64_t seed, uint64_t offset,
-                     const int64_t* state, void* y, void* h, void* g, void* u, void* workspace,
+                     const int64_t* state, void* y, void* h, void* s, void* a, void* workspace,
                      size_t workspace_bytes, ce_stream_t stream);
 
 /*
  * ce_ffn_bwd - the gradients of ce_ffn_fwd: with dz = dropout(dy), dh = dz @
- * w_down, dg = dh u act'(g) and du = dh act(g):
+ * w_down, dg = dh s and du = dh a:
  *     dx = dg @ w_gate + du @ w_up,  dw_gate = dg^T @ x,  dw_up = du^T @ x,
  *     dw_down = dz^T @ h             (the residual's gradient is dy)
- * dy [rows, O]; h, g, u as ce_ffn_fwd wrote them; sizes, types, alignment
+ * dy [rows, O]; h, s, a as ce_ffn_fwd wrote them; sizes, types, alignment
  * and dropout arguments as there (pass the same p, seed and offset, and the
  * state it drew from).
  * dx [rows, H], dw_gate and dw_up [I, H], dw_down [O, I] in dtype, written;
  * dx, dw_down, or both dw_gate and dw_up may be NULL (not computed).
- * workspace    at least ce_ffn_bwd_workspace_bytes(rows, I, O, p) bytes,
- *              256-byte aligned, owned by the caller: dg and du (and dz).
- * dg, du and dz are rounded to dtype once; products accumulate in fp32.
+ * workspace    at least ce_ffn_bwd_workspace_bytes(rows, H, I, O, p) bytes,
+ *              256-byte aligned, owned by the caller: dg, du, dy where
+ *              dropped, and packed operands.
+ * dg and du are rounded to dtype once; the dropout's factor 1 / (1 - p) is
+ * applied in fp32; products accumulate in fp32.
  */
-size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t I, int64_t O, double p);
+size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O, double p);
 
 ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up,
-                     const void* w_down, const void* h, const void* g, const void* u, int dtype,
+                     const void* w_down, const void* h, const void* s, const void* a, int dtype,
                      int64_t rows, int64_t H, int64_t I, int64_t O, int act, double p,
                      uint64_t seed, uint64_t offset, const int64_t* state, void* dx,
                      void* dw_gate, void* dw_up, void* dw_down, void* workspace,

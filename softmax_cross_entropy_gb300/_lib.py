@@ -49,7 +49,7 @@ SIGNATURES = {
     "ce_ffn_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "ce_ffn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64, _U64, _P, _P,
                         _P, _P, _P, _P, _SZ, _P]),
-    "ce_ffn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _D]),
+    "ce_ffn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _D]),
     "ce_ffn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64,
                         _U64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "ce_beam_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I64]),
@@ -201,18 +201,18 @@ def ce_ffn_fwd_workspace_bytes(rows, H, I, O):
 
 
 def ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, seed, offset,
-               state, y, h, g, u, workspace, workspace_bytes, stream):
+               state, y, h, s, a, workspace, workspace_bytes, stream):
     return load().ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, seed,
-                             offset, state, y, h, g, u, workspace, workspace_bytes, stream)
+                             offset, state, y, h, s, a, workspace, workspace_bytes, stream)
 
 
-def ce_ffn_bwd_workspace_bytes(rows, I, O, p):
-    return load().ce_ffn_bwd_workspace_bytes(rows, I, O, p)
+def ce_ffn_bwd_workspace_bytes(rows, H, I, O, p):
+    return load().ce_ffn_bwd_workspace_bytes(rows, H, I, O, p)
 
 
-def ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, g, u, dtype, rows, H, I, O, act, p, seed, offset,
+def ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, s, a, dtype, rows, H, I, O, act, p, seed, offset,
                state, dx, dw_gate, dw_up, dw_down, workspace, workspace_bytes, stream):
-    return load().ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, g, u, dtype, rows, H, I, O, act, p,
+    return load().ce_ffn_bwd(dy, x, w_gate, w_up, w_down, h, s, a, dtype, rows, H, I, O, act, p,
                              seed, offset, state, dx, dw_gate, dw_up, dw_down, workspace,
                              workspace_bytes, stream)
 

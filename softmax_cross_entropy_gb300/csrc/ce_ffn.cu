@@ -12,14 +12,22 @@
 //    epilogue has both and writes act(g) * u: g and u never leave the chip
 //    unless a backward needs them;
 //  * kDown: y = h Wd^T with dropout and the residual sum in the epilogue;
-//  * kDact: dh = dz Wd; the epilogue reads g and u and writes dg = dh u
-//    act'(g) and du = dh act(g), dh itself is never stored;
+//  * kDact: dh = dz Wd; the epilogue multiplies by what the forward kept of
+//    each element, s = u act'(g) and a = act(g), and writes dg = dh s and du =
+//    dh a; dh itself is never stored;
 //  * kDx: dx = dg Wg + du Wu as one product whose K runs over dg, then du;
 //  * kDw: dWg = dg^T x, dWu = du^T x and dWd = dz^T h as one launch over the
 //    tiles of all three (one tail for the SMs instead of three).
-// Roundings to 16 bits: h, g, u, dg and du, which feed tensor-core products
-// (or are kept for the backward), once each from fp32; dropout and the
-// residual are applied in fp32 before y's only rounding.
+// Roundings to 16 bits: h, s, a, dg and du, once each from fp32 (h, dg and du
+// feed tensor-core products; s and a instead of g and u, so that the backward
+// forms no activation and the rounding of g does not enter act'(g)); dropout
+// and the residual are applied in fp32 before y's only rounding; dz is dy
+// with zeros, its factor 1 / (1 - p) is applied to the products in fp32.
+//
+// The TMA wants rows of whole 16 bytes. Operands that have others (H, I or O
+// not a multiple of 8, or an unaligned base) are packed into rows of such a
+// length by a kernel of their own first, and outputs that have others leave
+// by plain stores.
 //
 // Bound by the tensor cores from about 600 rows on (6 rows H I operations on
 // 6 H I bytes of weights); ce_ffn_rows.cu takes few rows.
@@ -52,13 +60,18 @@ struct FfnGemm {
     // problems (kDw), whose tiles follow one another
     int64_t M[3], N[3], tiles_m[3], tiles_n[3], tile_end[3];
     int64_t K;      // of one segment
+    // outputs by plain stores: [M, ncols] with pitch ncols, or nullptr
+    void* plain[3];
+    int64_t ncols[3];
+    float scale[3];  // kDact, kDw: of the products
     int segs;       // segments of K (kDx: 2)
     int m_first;    // a problem's tiles run along M first
-    int outs;       // kGateUp: 3 with g and u, else 1
+    int outs;       // kGateUp: 3 with s and a, else 1
     int act;
-    const void* g;  // kDact: [M, N]
-    const void* u;
-    const void* res;  // kDown: [M, N] or nullptr
+    const void* s;  // kDact: u act'(g), [M, N]
+    const void* a;  // kDact: act(g), [M, N]
+    const void* res;  // kDown: [M, ncols] or nullptr
+    int res_vec;      // 1: its rows are whole 16-byte vectors
     DropSpec drop;    // kDown
     uint64_t timeout_ns;
     unsigned* status;
@@ -103,6 +116,47 @@ __device__ __forceinline__ void stage32(uint32_t buf, int r, int h, const float 
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(p.x), "r"(p.y),
                      "r"(p.z), "r"(p.w)
                      : "memory");
+    }
+}
+
+// Whether element `i` is kept.
+__device__ __noinline__ bool ffn_kept(const DropSpec& d, PhiloxKey key, uint64_t i) {
+    const uint4 w = philox4x32(key, i >> 2);
+    const uint32_t l = static_cast<uint32_t>(i) & 3u;
+    return (l == 0 ? w.x : l == 1 ? w.y : l == 2 ? w.z : w.w) >= d.threshold;
+}
+
+// Dropout of 32 columns from column n of row `row` of y, and the residual.
+template <typename T>
+__device__ __forceinline__ void ffn_drop_res(const FfnGemm& a, const PhiloxKey& key, int64_t row,
+                                             int64_t n, float (&v)[32]) {
+    const int64_t M = a.M[0], N = a.ncols[0];
+    if (a.drop.mode == kDropSome) {
+        const uint64_t at = static_cast<uint64_t>(row * N + n);
+        if ((N & 3) == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) drop4(a.drop, key, at / 4 + j, v + 4 * j);
+        } else {  // rows that start inside a block of four words
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = ffn_kept(a.drop, key, at + j) ? v[j] * a.drop.scale : 0.f;
+        }
+    } else if (a.drop.mode == kDropAll) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+    }
+    if (a.res) {
+        if (a.res_vec) {
+            float w[32];
+            load_row32<T>(a.res, row, n, M, N, w);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += w[j];
+        } else if (row < M) {
+            const T* q = static_cast<const T*>(a.res) + row * N + n;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j < N) v[j] += Vec<T>::load1(q, j);
+        }
     }
 }
 
@@ -316,49 +370,45 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                             const uint32_t col = static_cast<uint32_t>(c * 64 + h * 32);
                             const int64_t nb = n + h * 32;
                             float v[32];
+                            tc_ld32(trow + col, v);
                             if constexpr (MODE == kGateUp) {
-                                tc_ld32(trow + (o == 2 ? 128u + col : col), v);
-                                if (o == 0) {
+                                if (o == 2) {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] = ffn_act(a.act, v[j]);
+                                } else {
                                     float w[32];
                                     tc_ld32(trow + 128u + col, w);
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = ffn_act(a.act, v[j]) * w[j];
+                                    for (int j = 0; j < 32; ++j)
+                                        v[j] = w[j] * (o == 0 ? ffn_act(a.act, v[j])
+                                                              : ffn_slope(a.act, v[j]));
                                 }
                             } else if constexpr (MODE == kDact) {
-                                tc_ld32(trow + col, v);
-                                float g[32];
-                                load_row32<T>(a.g, row, nb, M, N, g);
-                                if (o == 0) {
-                                    float w[32];
-                                    load_row32<T>(a.u, row, nb, M, N, w);
+                                float w[32];
+                                load_row32<T>(o == 0 ? a.s : a.a, row, nb, M, N, w);
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        v[j] = v[j] * w[j] * ffn_slope(a.act, g[j]);
-                                } else {
+                                for (int j = 0; j < 32; ++j) v[j] *= w[j] * a.scale[0];
+                            } else if constexpr (MODE == kDw) {
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] *= ffn_act(a.act, g[j]);
-                                }
-                            } else {
-                                tc_ld32(trow + col, v);
+                                for (int j = 0; j < 32; ++j) v[j] *= a.scale[p];
+                            } else if constexpr (MODE == kDown) {
+                                ffn_drop_res<T>(a, key, row, nb, v);
                             }
-                            if constexpr (MODE == kDown) {
-                                if (a.drop.mode == kDropSome) {
-                                    const uint64_t at = static_cast<uint64_t>(row * N + nb) / 4;
+                            if constexpr (MODE == kDown || MODE == kDx || MODE == kDw) {
+                                const int pi = MODE == kDw ? p : 0;
+                                if (a.plain[pi]) {
+                                    if (row < M) {
+                                        T* out = static_cast<T*>(a.plain[pi]) + row * a.ncols[pi] + nb;
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) drop4(a.drop, key, at + j, v + 4 * j);
-                                } else if (a.drop.mode == kDropAll) {
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                                }
-                                if (a.res) {
-                                    float w[32];
-                                    load_row32<T>(a.res, row, nb, M, N, w);
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] += w[j];
+                                        for (int j = 0; j < 32; ++j)
+                                            if (nb + j < a.ncols[pi]) Vec<T>::store1(out, j, v[j]);
+                                    }
+                                    continue;
                                 }
                             }
                             stage32<T>(buf, lane, h, v);
                         }
+                        if (MODE != kGateUp && MODE != kDact && a.plain[MODE == kDw ? p : 0]) continue;
                         fence_proxy_async_smem();  // the writes, seen by the TMA
                         __syncwarp();
                         if (lane == 0) {
@@ -396,6 +446,65 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
+}
+
+// Packs matrices [rows, cols] into rows of `pitch` elements (a multiple of 8,
+// zeros behind the columns); `mask`: elements that the dropout drops are
+// zeros too. A thread an output vector of 8 elements.
+constexpr int kPackMats = 5;
+struct PackArgs {
+    struct {
+        const void* src;
+        void* dst;
+        int64_t rows, cols, pitch;
+        int64_t end;  // vectors of this matrix and those before it
+        int vec;      // 1: the source's rows are whole 16-byte vectors
+        int mask;
+    } m[kPackMats];
+    int n;
+    DropSpec drop;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) ffn_pack(const __grid_constant__ PackArgs a) {
+    const PhiloxKey key = philox_key(a.drop);
+    const int64_t all = a.m[a.n - 1].end;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        int k = 0;
+        while (i >= a.m[k].end) ++k;
+        const auto& m = a.m[k];
+        const int64_t v = i - (k ? a.m[k - 1].end : 0);
+        const int64_t r = v / (m.pitch / 8), c = (v - r * (m.pitch / 8)) * 8;
+        const T* src = static_cast<const T*>(m.src) + r * m.cols + c;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (m.vec) {
+            w = *reinterpret_cast<const uint4*>(src);
+            Vec<T>::unpack(w, f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < m.cols) f[j] = Vec<T>::load1(src, j);
+        }
+        if (m.mask && a.drop.mode != kDropNone) {
+            const uint64_t at = static_cast<uint64_t>(r * m.cols + c);
+            if (a.drop.mode == kDropAll) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = 0.f;
+            } else if ((m.cols & 3) == 0) {
+                DropSpec d = a.drop;
+                d.scale = 1.f;
+                drop4(d, key, at / 4, f);
+                drop4(d, key, at / 4 + 1, f + 4);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = ffn_kept(a.drop, key, at + j) ? f[j] : 0.f;
+            }
+        }
+        // (16-bit values pass through fp32 unchanged)
+        reinterpret_cast<uint4*>(m.dst)[v] = Vec<T>::pack(f);
+    }
 }
 
 template <uint32_t AB, int MODE>
@@ -489,89 +598,170 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
 }
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
 ce_status check_ffn(int dtype, int64_t rows, int64_t H, int64_t I, int64_t O, int act) {
     if (dtype != CE_BF16 && dtype != CE_F16) return dtype == CE_F32 ? CE_ERR_UNSUPPORTED : CE_ERR_INVALID_ARG;
     if (rows < 0 || H <= 0 || I <= 0 || O <= 0) return CE_ERR_INVALID_ARG;
     if (act < CE_ACT_SILU || act > CE_ACT_GELU_TANH) return CE_ERR_INVALID_ARG;
-    if (H % 8 || I % 8 || O % 8 || rows > INT32_MAX || H > INT32_MAX || I > INT32_MAX || O > INT32_MAX) {
-        record_message("the feed-forward block takes H, I and O that are multiples of 8, below 2^31");
+    constexpr int64_t kMost = INT32_MAX - 512;  // tile coordinates are 32-bit
+    if (rows > kMost || H > kMost || I > kMost || O > kMost) {
+        record_message("the feed-forward block takes rows, H, I and O below 2^31 - 512");
         return CE_ERR_UNSUPPORTED;
     }
     return CE_OK;
 }
+
+// Hands out a caller's workspace, and collects the matrices that one launch
+// of ffn_pack fills there.
+struct FfnPacker {
+    char* ws;
+    PackArgs args = {};
+
+    void* take(int64_t rows, int64_t cols) {
+        void* p = ws;
+        ws += up256(rows * up8(cols) * 2);
+        return p;
+    }
+    // `src` itself where the TMA can read it, else its packed copy
+    const void* operand(const void* src, int64_t rows, int64_t cols, bool mask = false) {
+        const bool whole = cols % 8 == 0 && aligned(src);
+        if (whole && !mask) return src;
+        void* dst = take(rows, cols);
+        auto& m = args.m[args.n];
+        m.src = src;
+        m.dst = dst;
+        m.rows = rows;
+        m.cols = cols;
+        m.pitch = up8(cols);
+        m.end = (args.n ? args.m[args.n - 1].end : 0) + rows * (m.pitch / 8);
+        m.vec = whole ? 1 : 0;
+        m.mask = mask ? 1 : 0;
+        ++args.n;
+        return dst;
+    }
+    ce_status run(int dtype, const DropSpec& drop, const FfnDevice& d, cudaStream_t st) {
+        if (!args.n) return CE_OK;
+        args.drop = drop;
+        const int64_t grid = std::min<int64_t>((args.m[args.n - 1].end + 255) / 256, 16L * d.sms);
+        void* p[] = {&args};
+        const void* fn = dtype == CE_BF16 ? (const void*)&ffn_pack<__nv_bfloat16>
+                                          : (const void*)&ffn_pack<__half>;
+        const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(256), p, 0, st);
+        return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "feed-forward pack launch");
+    }
+};
+
+// Output matrix i of a launch: through the TMA where it can write it.
+void ffn_output(FfnGemm* g, FfnMatrix (&C)[3], int i, void* p, int64_t rows, int64_t cols) {
+    g->ncols[i] = cols;
+    if (cols % 8 == 0 && aligned(p)) C[i] = FfnMatrix{p, rows, cols};
+    else g->plain[i] = p;
+}
+
+// What a packed copy of [rows, cols] takes; 0 where the TMA reads the
+// original, if its base is aligned.
+int64_t pack_bytes(int64_t rows, int64_t cols) { return up256(rows * up8(cols) * 2); }
 
 }  // namespace
 }  // namespace gbce
 
 using namespace gbce;
 
+extern "C" size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O) {
+    if (rows < 0 || H <= 0 || I <= 0 || O <= 0) return 0;
+    const int64_t x = H % 8 ? pack_bytes(rows, H) + 2 * pack_bytes(I, H) : 0;
+    return static_cast<size_t>(x + (I % 8 ? pack_bytes(O, I) : 0));
+}
+
 extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up,
                                 const void* w_down, const void* residual, int dtype, int64_t rows,
                                 int64_t H, int64_t I, int64_t O, int act, double p, uint64_t seed,
-                                uint64_t offset, const int64_t* state, void* y, void* h, void* g,
-                                void* u, void* workspace, size_t workspace_bytes,
+                                uint64_t offset, const int64_t* state, void* y, void* h, void* s,
+                                void* a, void* workspace, size_t workspace_bytes,
                                 ce_stream_t stream) {
     ce_status rc = check_ffn(dtype, rows, H, I, O, act);
     if (rc != CE_OK) return rc;
-    FfnGemm a = {};
-    if (!drop_spec(p, seed, offset, state, &a.drop)) return CE_ERR_INVALID_ARG;
-    if (!w_gate || !w_up || !w_down || (g == nullptr) != (u == nullptr)) return CE_ERR_INVALID_ARG;
+    FfnGemm base = {};
+    if (!drop_spec(p, seed, offset, state, &base.drop)) return CE_ERR_INVALID_ARG;
+    if (!w_gate || !w_up || !w_down || (s == nullptr) != (a == nullptr)) return CE_ERR_INVALID_ARG;
     if (rows > 0 && (!x || !y || !h)) return CE_ERR_INVALID_ARG;
-    for (const void* q : {x, w_gate, w_up, w_down, residual, static_cast<const void*>(y),
-                          static_cast<const void*>(h), static_cast<const void*>(g),
-                          static_cast<const void*>(u)})
-        if (!aligned(q)) return CE_ERR_UNSUPPORTED;
+    if (!aligned(h) || !aligned(s) || !aligned(a)) return CE_ERR_INVALID_ARG;
+    for (const void* q : {x, w_gate, w_up, w_down})
+        if (reinterpret_cast<uintptr_t>(q) & 1u) return CE_ERR_INVALID_ARG;
+    if ((H % 8 == 0 && !(aligned(x) && aligned(w_gate) && aligned(w_up))) ||
+        (I % 8 == 0 && !aligned(w_down))) {
+        record_message("rows of whole 16-byte vectors need a 16-byte aligned base");
+        return CE_ERR_UNSUPPORTED;
+    }
+    const size_t need = ce_ffn_fwd_workspace_bytes(rows, H, I, O);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
+        return CE_ERR_INVALID_ARG;
     if (rows == 0) return CE_OK;
-    (void)workspace;
-    (void)workspace_bytes;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     FfnDevice d;
     rc = ffn_device(st, &d);
     if (rc != CE_OK) return rc;
-    a.segs = 1;
-    a.act = act;
-    FfnGemm up = a;
-    up.M[0] = rows;
-    up.N[0] = I;
-    up.K = H;
-    up.outs = g ? 3 : 1;
-    rc = ffn_launch(kGateUp, dtype, up, 1, {{x, rows, H}}, {{w_gate, I, H}, {w_up, I, H}},
-                    {{h, rows, I}, {g, rows, I}, {u, rows, I}}, d, st);
+    const int64_t H8 = up8(H), I8 = up8(I);
+    FfnPacker pack{static_cast<char*>(workspace)};
+    x = pack.operand(x, rows, H);
+    w_gate = pack.operand(w_gate, I, H);
+    w_up = pack.operand(w_up, I, H);
+    w_down = pack.operand(w_down, O, I);
+    rc = pack.run(dtype, base.drop, d, st);
     if (rc != CE_OK) return rc;
-    FfnGemm down = a;
+    base.segs = 1;
+    base.act = act;
+    FfnGemm up = base;
+    up.M[0] = rows;
+    up.N[0] = I8;
+    up.K = H8;
+    up.outs = s ? 3 : 1;
+    rc = ffn_launch(kGateUp, dtype, up, 1, {{x, rows, H8}}, {{w_gate, I, H8}, {w_up, I, H8}},
+                    {{h, rows, I8}, {s, rows, I8}, {a, rows, I8}}, d, st);
+    if (rc != CE_OK) return rc;
+    FfnGemm down = base;
     down.M[0] = rows;
     down.N[0] = O;
-    down.K = I;
+    down.K = I8;
     down.res = residual;
-    return ffn_launch(kDown, dtype, down, 1, {{h, rows, I}}, {{w_down, O, I}}, {{y, rows, O}}, d, st);
+    down.res_vec = O % 8 == 0 && aligned(residual) ? 1 : 0;
+    FfnMatrix C[3] = {};
+    ffn_output(&down, C, 0, y, rows, O);
+    return ffn_launch(kDown, dtype, down, 1, {{h, rows, I8}}, {{w_down, O, I8}}, C, d, st);
 }
 
-extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t I, int64_t O, double p) {
-    if (rows < 0 || I <= 0 || O <= 0) return 0;
-    return static_cast<size_t>(2 * up256(rows * I * 2) + (p > 0.0 ? up256(rows * O * 2) : 0));
+extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O, double p) {
+    if (rows < 0 || H <= 0 || I <= 0 || O <= 0) return 0;
+    const int64_t x = H % 8 ? pack_bytes(rows, H) + 2 * pack_bytes(I, H) : 0;
+    const int64_t wd = I % 8 ? pack_bytes(O, I) : 0;
+    const int64_t dz = O % 8 || p > 0.0 ? pack_bytes(rows, O) : 0;
+    return static_cast<size_t>(2 * pack_bytes(rows, I) + x + wd + dz);
 }
 
 extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate,
                                 const void* w_up, const void* w_down, const void* h,
-                                const void* g, const void* u, int dtype, int64_t rows, int64_t H,
+                                const void* s, const void* a, int dtype, int64_t rows, int64_t H,
                                 int64_t I, int64_t O, int act, double p, uint64_t seed,
                                 uint64_t offset, const int64_t* state, void* dx, void* dw_gate,
                                 void* dw_up, void* dw_down, void* workspace,
                                 size_t workspace_bytes, ce_stream_t stream) {
     ce_status rc = check_ffn(dtype, rows, H, I, O, act);
     if (rc != CE_OK) return rc;
-    FfnGemm a = {};
-    if (!drop_spec(p, seed, offset, state, &a.drop)) return CE_ERR_INVALID_ARG;
+    FfnGemm base = {};
+    if (!drop_spec(p, seed, offset, state, &base.drop)) return CE_ERR_INVALID_ARG;
     if ((dw_gate == nullptr) != (dw_up == nullptr)) return CE_ERR_INVALID_ARG;
     if (!w_gate || !w_up || !w_down) return CE_ERR_INVALID_ARG;
-    if (rows > 0 && (!dy || !x || !h || !g || !u)) return CE_ERR_INVALID_ARG;
-    for (const void* q : {dy, x, w_gate, w_up, w_down, h, g, u, static_cast<const void*>(dx),
-                          static_cast<const void*>(dw_gate), static_cast<const void*>(dw_up),
-                          static_cast<const void*>(dw_down)})
-        if (!aligned(q)) return CE_ERR_UNSUPPORTED;
+    if (rows > 0 && (!dy || !x || !h || !s || !a)) return CE_ERR_INVALID_ARG;
+    if (!aligned(h) || !aligned(s) || !aligned(a)) return CE_ERR_INVALID_ARG;
+    for (const void* q : {dy, x, w_gate, w_up, w_down})
+        if (reinterpret_cast<uintptr_t>(q) & 1u) return CE_ERR_INVALID_ARG;
+    if ((H % 8 == 0 && !(aligned(x) && aligned(w_gate) && aligned(w_up))) ||
+        (I % 8 == 0 && !aligned(w_down)) || (O % 8 == 0 && !aligned(dy))) {
+        record_message("rows of whole 16-byte vectors need a 16-byte aligned base");
+        return CE_ERR_UNSUPPORTED;
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (rows == 0) {  // no rows: zero gradients of the weights
         cudaError_t e = cudaSuccess;
@@ -582,72 +772,75 @@ extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gat
         return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "cudaMemsetAsync(weight gradients)");
     }
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        workspace_bytes < ce_ffn_bwd_workspace_bytes(rows, I, O, p))
+        workspace_bytes < ce_ffn_bwd_workspace_bytes(rows, H, I, O, p))
         return CE_ERR_INVALID_ARG;
+    if (!dx && !dw_gate && !dw_down) return CE_OK;
     FfnDevice d;
     rc = ffn_device(st, &d);
     if (rc != CE_OK) return rc;
-    char* ws = static_cast<char*>(workspace);
-    void* dg = ws;
-    void* du = ws + up256(rows * I * 2);
-    const void* dz = dy;
-    if (a.drop.mode != kDropNone) {
-        void* masked = ws + 2 * up256(rows * I * 2);
-        rc = ce_dropout(dy, nullptr, masked, dtype, rows * O, p, seed, offset, state, nullptr, stream);
-        if (rc != CE_OK) return rc;
-        dz = masked;
+    const int64_t H8 = up8(H), I8 = up8(I), O8 = up8(O);
+    FfnPacker pack{static_cast<char*>(workspace)};
+    void* dg = pack.take(rows, I);
+    void* du = pack.take(rows, I);
+    const void* dz = pack.operand(dy, rows, O, base.drop.mode != kDropNone);
+    const float scale = base.drop.mode == kDropNone ? 1.f : base.drop.scale;
+    if (dx || dw_gate) w_down = pack.operand(w_down, O, I);
+    if (dw_gate) x = pack.operand(x, rows, H);
+    if (dx) {
+        w_gate = pack.operand(w_gate, I, H);
+        w_up = pack.operand(w_up, I, H);
     }
-    a.segs = 1;
-    a.act = act;
+    rc = pack.run(dtype, base.drop, d, st);
+    if (rc != CE_OK) return rc;
+    base.segs = 1;
+    base.act = act;
     if (dx || dw_gate) {
-        FfnGemm t = a;
+        FfnGemm t = base;
         t.M[0] = rows;
-        t.N[0] = I;
-        t.K = O;
-        t.g = g;
-        t.u = u;
-        rc = ffn_launch(kDact, dtype, t, 1, {{dz, rows, O}}, {{w_down, O, I}},
-                        {{dg, rows, I}, {du, rows, I}}, d, st);
+        t.N[0] = I8;
+        t.K = O8;
+        t.s = s;
+        t.a = a;
+        t.scale[0] = scale;
+        rc = ffn_launch(kDact, dtype, t, 1, {{dz, rows, O8}}, {{w_down, O, I8}},
+                        {{dg, rows, I8}, {du, rows, I8}}, d, st);
         if (rc != CE_OK) return rc;
     }
     if (dx) {
-        FfnGemm t = a;
+        FfnGemm t = base;
         t.M[0] = rows;
         t.N[0] = H;
-        t.K = I;
+        t.K = I8;
         t.segs = 2;
-        rc = ffn_launch(kDx, dtype, t, 1, {{dg, rows, I}, {du, rows, I}}, {{w_gate, I, H}, {w_up, I, H}},
-                        {{dx, rows, H}}, d, st);
+        FfnMatrix C[3] = {};
+        ffn_output(&t, C, 0, dx, rows, H);
+        rc = ffn_launch(kDx, dtype, t, 1, {{dg, rows, I8}, {du, rows, I8}}, {{w_gate, I, H8}, {w_up, I, H8}},
+                        C, d, st);
         if (rc != CE_OK) return rc;
     }
     if (dw_gate || dw_down) {
-        FfnGemm t = a;
+        FfnGemm t = base;
         t.K = rows;
         FfnMatrix A[3] = {}, B[3] = {}, C[3] = {};
         int n = 0;
-        const auto add = [&](const void* left, int64_t m, const void* right, int64_t cols, void* out) {
+        // left^T right: [rows, m] and [rows, cols], their rows of m8 and cols8 elements
+        const auto add = [&](const void* left, int64_t m, const void* right, int64_t cols, void* out,
+                             float factor) {
             t.M[n] = m;
             t.N[n] = cols;
-            A[n] = FfnMatrix{left, rows, m};
-            B[n] = FfnMatrix{right, rows, cols};
-            C[n] = FfnMatrix{out, m, cols};
+            t.scale[n] = factor;
+            A[n] = FfnMatrix{left, rows, up8(m)};
+            B[n] = FfnMatrix{right, rows, up8(cols)};
+            ffn_output(&t, C, n, out, m, cols);
             ++n;
         };
         if (dw_gate) {
-            add(dg, I, x, H, dw_gate);
-            add(du, I, x, H, dw_up);
+            add(dg, I, x, H, dw_gate, 1.f);
+            add(du, I, x, H, dw_up, 1.f);
         }
-        if (dw_down) add(dz, O, h, I, dw_down);
+        if (dw_down) add(dz, O, h, I, dw_down, scale);
         rc = ffn_launch(kDw, dtype, t, n, A, B, C, d, st);
         if (rc != CE_OK) return rc;
     }
     return CE_OK;
-}
-
-extern "C" size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O) {
-    (void)rows;
-    (void)H;
-    (void)I;
-    (void)O;
-    return 0;
 }

@@ -16,7 +16,7 @@ import torch
 
 from . import _lib
 from ._tensors import DTYPES, check, on, ptr, require_cuda, stream
-from .philox_dropout import check_rng, dropout
+from .philox_dropout import check_rng
 
 __all__ = ["gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
 
@@ -26,7 +26,7 @@ _ACTIVATIONS = {"silu": _lib.CE_ACT_SILU, "gelu": _lib.CE_ACT_GELU,
 
 class GatedFeedForwardFunction(torch.autograd.Function):
     """Autograd wrapper of ce_ffn_fwd and ce_ffn_bwd on [rows, H] inputs. The
-    forward keeps x, g, u and h (the last three [rows, I]) for the backward."""
+    forward keeps x and three [rows, I] tensors (h, u act'(g) and act(g))."""
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, residual, act, p, seed, offset, state):
@@ -34,9 +34,13 @@ class GatedFeedForwardFunction(torch.autograd.Function):
         O, I = w_down.shape
         dev, dt = x.device, x.dtype
         grad = any(ctx.needs_input_grad[:4])
-        empty = lambda *shape: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
-        y, h = empty(rows, O), empty(rows, I)
-        g, u = (empty(rows, I), empty(rows, I)) if grad else (None, None)
+        I8 = (I + 7) // 8 * 8
+        y = torch.empty((rows, O), dtype=dt, device=dev)
+        # one allocation for h, s and a (their rows are whole 16-byte vectors)
+        kept = torch.empty((3 if grad else 1, rows, I8), dtype=dt, device=dev)
+        step = rows * I8 * 2
+        h = kept.data_ptr()
+        s, a = (h + step, h + 2 * step) if grad else (None, None)
         if grad and state is not None and p > 0.0:
             state = state.clone()  # the caller may change it before the backward runs
         nbytes = _lib.ce_ffn_fwd_workspace_bytes(rows, H, I, O)
@@ -44,10 +48,9 @@ class GatedFeedForwardFunction(torch.autograd.Function):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
             check(_lib.ce_ffn_fwd(ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(residual),
                                   DTYPES[dt], rows, H, I, O, act, p, seed, offset, ptr(state),
-                                  ptr(y), ptr(h), ptr(g), ptr(u), ptr(ws), nbytes, stream(dev)),
-                  "ce_ffn_fwd")
+                                  ptr(y), h, s, a, ptr(ws), nbytes, stream(dev)), "ce_ffn_fwd")
         if grad:
-            ctx.save_for_backward(x, w_gate, w_up, w_down, h, g, u, state)
+            ctx.save_for_backward(x, w_gate, w_up, w_down, kept, state)
         ctx.args = (act, p, seed, offset)
         return y
 
@@ -57,39 +60,33 @@ class GatedFeedForwardFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx = dwg = dwu = dwd = None
         if any(need[:4]):
-            x, w_gate, w_up, w_down, h, g, u, state = ctx.saved_tensors
+            x, w_gate, w_up, w_down, kept, state = ctx.saved_tensors
             act, p, seed, offset = ctx.args
             rows, H = x.shape
             O, I = w_down.shape
             dev, dt = x.device, x.dtype
-            grad_out, dy = dy, dy.contiguous()
-            if dy.data_ptr() % 16:
-                dy = dy.clone()
+            g = aligned(dy)
             dx = torch.empty_like(x) if need[0] else None
             if need[1] or need[2]:
                 dwg, dwu = torch.empty_like(w_gate), torch.empty_like(w_up)
             dwd = torch.empty_like(w_down) if need[3] else None
-            nbytes = _lib.ce_ffn_bwd_workspace_bytes(rows, I, O, p)
+            nbytes = _lib.ce_ffn_bwd_workspace_bytes(rows, H, I, O, p)
+            h, step = kept.data_ptr(), kept.stride(0) * 2
             with on(dev):
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-                check(_lib.ce_ffn_bwd(ptr(dy), ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(h),
-                                      ptr(g), ptr(u), DTYPES[dt], rows, H, I, O, act, p, seed,
-                                      offset, ptr(state), ptr(dx), ptr(dwg), ptr(dwu), ptr(dwd),
-                                      ptr(ws), nbytes, stream(dev)), "ce_ffn_bwd")
-            dy = grad_out
+                check(_lib.ce_ffn_bwd(ptr(g), ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), h,
+                                      h + step, h + 2 * step, DTYPES[dt], rows, H, I, O, act, p,
+                                      seed, offset, ptr(state), ptr(dx), ptr(dwg), ptr(dwu),
+                                      ptr(dwd), ptr(ws), nbytes, stream(dev)), "ce_ffn_bwd")
         return (dx, dwg if need[1] else None, dwu if need[2] else None, dwd,
                 dy if need[4] else None, None, None, None, None, None)
 
 
-def _padded(t, rows, cols):
-    """t [r, c] with zeros up to multiples of `rows` and `cols`."""
-    r, c = -t.shape[0] % rows, -t.shape[1] % cols
-    return torch.nn.functional.pad(t, (0, c, 0, r)) if r or c else t
-
-
-def _aligned(t):
+def aligned(t):
+    """t as a contiguous tensor whose base the kernels take: 16-byte aligned
+    where its rows are whole 16-byte vectors."""
     t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return t.clone() if t.data_ptr() % 16 and t.shape[-1] % 8 == 0 else t
 
 
 def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu", dropout_p=0.0,
@@ -102,9 +99,8 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
     over the [..., O] elements. Differentiable in x, the weights and residual;
     for that the forward keeps x and three [..., I] tensors.
 
-    H, I and O that are not multiples of 8 are padded with zeros on each call
-    (a copy of what they concern), and the dropout and residual then follow as
-    a call of their own, on an output rounded once before."""
+    H, I and O that are not multiples of 8 cost a packed copy of what they
+    concern (x and the projections for H, down_weight for I) on each call."""
     for name, t in (("x", x), ("gate_weight", gate_weight), ("up_weight", up_weight),
                     ("down_weight", down_weight)) + \
             ((("residual", residual),) if residual is not None else ()):
@@ -125,20 +121,11 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
     act = _ACTIVATIONS[activation]
-    p, seed_, offset_, state = check_rng(dropout_p, seed, offset, x.device)
-    x2 = x.reshape(-1, H)
-    if H % 8 or I % 8 or O % 8:
-        y = GatedFeedForwardFunction.apply(
-            _aligned(_padded(x2, 1, 8)), _aligned(_padded(gate_weight, 8, 8)),
-            _aligned(_padded(up_weight, 8, 8)), _aligned(_padded(down_weight, 8, 8)), None, act,
-            0.0, 0, 0, None)[:, :O].reshape(shape)
-        if p == 0.0 and residual is None:
-            return y
-        return dropout(y, p, seed, offset, residual=residual)
-    res = None if residual is None else _aligned(residual.reshape(-1, O))
+    p, seed, offset, state = check_rng(dropout_p, seed, offset, x.device)
+    res = None if residual is None else residual.reshape(-1, O).contiguous()
     return GatedFeedForwardFunction.apply(
-        _aligned(x2), _aligned(gate_weight), _aligned(up_weight), _aligned(down_weight), res, act,
-        p, seed_, offset_, state).reshape(shape)
+        aligned(x.reshape(-1, H)), aligned(gate_weight), aligned(up_weight), aligned(down_weight),
+        res, act, p, seed, offset, state).reshape(shape)
 
 
 class GatedFeedForward(torch.nn.Module):
