@@ -1,0 +1,436 @@
+// The gated feed-forward block for few rows (the tokens of a batch that is
+// being generated): the weights are the large operand, so they are the rows
+// of the tensor-core products and the tokens their columns.
+//
+// Bound by HBM: every weight is read once, 6 H I bytes. Two products,
+// each split so that every SM reads the same number of weight bytes:
+//  * ffn_rows: tiles of 128 weight rows (of Wg, then Wu; or of Wd) x K blocks
+//    of 64 are units of 16 KB, dealt out in equal runs to one CTA an SM. A
+//    TMA producer keeps a ring of up to 11 units in flight (176 KB an SM); an
+//    MMA thread multiplies each by the tokens' block of x (or h), N = rows
+//    rounded up to 16; four epilogue warps write the sums of a tile's part,
+//    fp32, to the workspace. A run may start and end inside a tile, so a
+//    tile has a few parts.
+//  * ffn_rows_act and ffn_rows_out add a tile's parts in order (results do
+//    not depend on which SM finishes first) and apply the activation and
+//    product, or the dropout and residual, in fp32, rounding once.
+// The four launches overlap at their ends (programmatic dependent launch):
+// the second product fills its ring with weights, which no launch of this
+// call writes, while the first's sums are still being added.
+#include <algorithm>
+#include <cstdint>
+#include <string>
+
+#include "ce_ffn.cuh"
+#include "ce_philox.cuh"
+#include "ce_tc.cuh"
+#include "gbce.h"
+
+namespace gbce {
+ce_status record_cuda_failure(cudaError_t e, const char* what);
+
+namespace {
+
+constexpr int kRowsThreads = 192;  // producer, MMA issuer, 4 epilogue warps
+constexpr int kRowsTile = 128;     // weight rows of a tile
+constexpr uint32_t kRowsA = kRowsTile * kBK * 2;  // 16 KB
+constexpr int kRowsStages = 11;
+constexpr uint32_t kRowsSmem = 200 * 1024;  // of the ring
+
+struct RowsArgs {
+    int64_t units, per;  // tiles x K blocks; of a CTA
+    int64_t tiles0;      // tiles of the first weight matrix
+    int nk;              // K blocks of a tile
+    int rows, nt;        // tokens; rounded up to a multiple of 16
+    int stages, parts;   // ring slots; parts of a tile at most
+    uint32_t stage_bytes;
+    float* sums;  // [tiles, parts, rows, 128]
+    uint64_t timeout_ns;
+    unsigned* status;
+};
+
+// The first CTA of tile t, and the CTAs that share it.
+__host__ __device__ inline int64_t rows_first(int64_t t, int nk, int64_t per) { return t * nk / per; }
+__host__ __device__ inline int rows_parts(int64_t t, int nk, int64_t per) {
+    return static_cast<int>(((t + 1) * nk - 1) / per - t * nk / per) + 1;
+}
+
+template <uint32_t AB>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+         const __grid_constant__ CUtensorMap mapx, const __grid_constant__ RowsArgs a) {
+    extern __shared__ unsigned char rows_smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[kRowsStages];
+    __shared__ __align__(8) uint64_t empty_bar[kRowsStages];
+    __shared__ __align__(8) uint64_t acc_full[2];
+    __shared__ __align__(8) uint64_t acc_empty[2];
+    __shared__ __align__(8) uint64_t done_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ uint32_t s_issued[kRowsStages];  // 0, or 2 + parity of the last copy into the stage
+    __shared__ int s_fail;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t smem0 = (smem_u32(rows_smem_raw) + 1023u) & ~1023u;
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * a.per;
+    const int64_t u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+            s_issued[s] = 0;
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 128);
+        }
+        mbar_init(smem_u32(&done_bar), 1);
+        s_fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile(
+            "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                smem_u32(&tmem_base_sh)),
+            "r"(kTmemCols)
+            : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = tmem_base_sh;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const auto load_a = [&](int64_t u, uint32_t slot, uint32_t bar) {
+                const int64_t t = u / a.nk;
+                const int k0 = static_cast<int>(u - t * a.nk) * kBK;
+                const bool second = t >= a.tiles0;
+                tma_load_2d(slot, second ? &map1 : &map0, k0,
+                            static_cast<int>((second ? t - a.tiles0 : t) * kRowsTile), bar);
+            };
+            const auto load_x = [&](int64_t u, uint32_t slot, uint32_t bar) {
+                tma_load_2d(slot + kRowsA, &mapx, static_cast<int>(u % a.nk) * kBK, 0, bar);
+            };
+            // the ring's first round: the weights, then (once the launch that
+            // writes them is done) the tokens
+            const int pre = static_cast<int>(u1 - u0 < a.stages ? u1 - u0 : a.stages);
+            for (int s = 0; s < pre; ++s) {
+                const uint32_t fb = smem_u32(&full_bar[s]);
+                mbar_arrive_expect_tx(fb, a.stage_bytes);
+                load_a(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, fb);
+                s_issued[s] = 2u;
+            }
+            pdl_wait();
+            for (int s = 0; s < pre; ++s)
+                load_x(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, smem_u32(&full_bar[s]));
+            int s = 0;
+            uint32_t ph = 1;
+            bool fail = false;
+            for (int64_t u = u0 + pre; u < u1; ++u) {
+                if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
+                    fail = true;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&full_bar[s]);
+                const uint32_t slot = smem0 + static_cast<uint32_t>(s) * a.stage_bytes;
+                mbar_arrive_expect_tx(fb, a.stage_bytes);
+                load_a(u, slot, fb);
+                load_x(u, slot, fb);
+                s_issued[s] = 2u + ph;
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (fail) s_fail = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (AB << 7) | (AB << 10) |
+                                   (static_cast<uint32_t>(a.nt >> 3) << 17) |
+                                   (static_cast<uint32_t>(kRowsTile >> 4) << 24);
+            int s = 0, run = 0;
+            uint32_t ph = 0;
+            bool fail = false;
+            int64_t kb = u0 % a.nk;
+            for (int64_t u = u0; u < u1; ++u) {
+                const int b = run & 1;
+                const uint32_t acc = tmem + static_cast<uint32_t>(b * 256);
+                const bool start = u == u0 || kb == 0;
+                if (start && !tc_wait(smem_u32(&acc_empty[b]),
+                                      (static_cast<uint32_t>(run >> 1) & 1u) ^ 1u, a.timeout_ns)) {
+                    fail = true;
+                    break;
+                }
+                if (!tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)) {
+                    fail = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t slot = smem0 + static_cast<uint32_t>(s) * a.stage_bytes;
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    tc_mma(acc, tc_smem_desc(slot + 32u * k), tc_smem_desc(slot + kRowsA + 32u * k),
+                           idesc, (start && k == 0) ? 0u : 1u);
+                tc_commit(smem_u32(&empty_bar[s]));
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++kb == a.nk) kb = 0;
+                if (kb == 0 || u + 1 == u1) {
+                    tc_commit(smem_u32(&acc_full[b]));
+                    ++run;
+                }
+            }
+            if (fail) {
+                s_fail = 1;
+                tc_commit(smem_u32(&acc_full[run & 1]));  // so that nothing waits
+            }
+            tc_commit(smem_u32(&done_bar));
+        }
+    } else {
+        const int q = warp & 3;
+        int run = 0;
+        for (int64_t u = u0; u < u1; ++run) {
+            const int64_t t = u / a.nk;
+            const int b = run & 1;
+            const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
+                                              static_cast<uint32_t>(run >> 1) & 1u, a.timeout_ns);
+            if (!ok || *reinterpret_cast<volatile int*>(&s_fail)) {
+                if (lane == 0) s_fail = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * 256);
+            const int64_t part = blockIdx.x - rows_first(t, a.nk, a.per);
+            float* out = a.sums + ((t * a.parts + part) * a.rows) * kRowsTile + q * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < a.rows; c += 32) {
+                float v[32];
+                tc_ld32(trow + static_cast<uint32_t>(c), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j < a.rows) out[static_cast<int64_t>(c + j) * kRowsTile] = v[j];
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&acc_empty[b]));
+            u = (t + 1) * a.nk;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool done = mbar_wait_bounded(smem_u32(&done_bar), 0u, a.timeout_ns);
+        if (s_fail || !done) {
+            atomicOr(a.status, kDevErrTimeout);
+            for (int s = 0; s < a.stages; ++s)
+                if (s_issued[s])
+                    (void)mbar_wait_bounded(smem_u32(&full_bar[s]), s_issued[s] & 1u, a.timeout_ns);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+}
+
+struct RowsJoin {
+    const float* sums;
+    int64_t per, tiles0;
+    int nk, parts, rows;
+    int64_t cols, pitch;  // I and I8, or O and O
+    int act;
+    void* out;  // h or y
+    void* s;    // or nullptr
+    void* a;
+    const void* res;
+    DropSpec drop;
+};
+
+__device__ __forceinline__ float join_parts(const RowsJoin& j, int64_t t, int row) {
+    const int n = rows_parts(t, j.nk, j.per);
+    const float* p = j.sums + ((t * j.parts) * j.rows + row) * kRowsTile + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(j.rows) * kRowsTile;
+    float v = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) v += p[i * step];
+    return v;
+}
+
+// h = act(g) u (and s, a) of one token and 128 columns.
+template <typename T>
+__global__ void __launch_bounds__(kRowsTile) ffn_rows_act(const __grid_constant__ RowsJoin j) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowsTile + threadIdx.x;
+    const int row = blockIdx.y;
+    if (c >= j.pitch) return;
+    float h = 0.f, s = 0.f, a = 0.f;
+    if (c < j.cols) {
+        const float g = join_parts(j, blockIdx.x, row);
+        const float u = join_parts(j, j.tiles0 + blockIdx.x, row);
+        a = ffn_act(j.act, g);
+        h = a * u;
+        if (j.s) s = u * ffn_slope(j.act, g);
+    }
+    const int64_t at = row * j.pitch + c;
+    Vec<T>::store1(j.out, at, h);
+    if (j.s) {
+        Vec<T>::store1(j.s, at, s);
+        Vec<T>::store1(j.a, at, a);
+    }
+}
+
+// y = residual + dropout(z) of one token and 128 columns.
+template <typename T>
+__global__ void __launch_bounds__(kRowsTile) ffn_rows_out(const __grid_constant__ RowsJoin j) {
+    pdl_wait();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowsTile + threadIdx.x;
+    const int row = blockIdx.y;
+    if (c >= j.cols) return;
+    float v = join_parts(j, blockIdx.x, row);
+    const int64_t at = row * j.cols + c;
+    if (j.drop.mode == kDropSome) {
+        const PhiloxKey key = philox_key(j.drop);
+        const uint4 w = philox4x32(key, static_cast<uint64_t>(at) >> 2);
+        const uint32_t l = static_cast<uint32_t>(at) & 3u;
+        const uint32_t word = l == 0 ? w.x : l == 1 ? w.y : l == 2 ? w.z : w.w;
+        v = word >= j.drop.threshold ? v * j.drop.scale : 0.f;
+    } else if (j.drop.mode == kDropAll) {
+        v = 0.f;
+    }
+    if (j.res) v += Vec<T>::load1(j.res, at);
+    Vec<T>::store1(j.out, at, v);
+}
+
+int64_t up256r(int64_t b) { return (b + 255) / 256 * 256; }
+
+// How a product of `tiles` weight tiles and K columns is dealt out to `sms`.
+struct RowsPlan {
+    int64_t units, per, grid;
+    int nk, parts;
+    int64_t bytes;  // of the sums
+};
+RowsPlan rows_plan(int64_t tiles, int64_t K, int64_t rows, int sms) {
+    RowsPlan p;
+    p.nk = static_cast<int>((K + kBK - 1) / kBK);
+    p.units = tiles * p.nk;
+    p.per = (p.units + sms - 1) / sms;
+    p.grid = (p.units + p.per - 1) / p.per;
+    p.parts = static_cast<int>((p.nk + p.per - 1) / p.per + 1);
+    p.bytes = up256r(tiles * p.parts * rows * kRowsTile * 4);
+    return p;
+}
+
+ce_status rows_pdl(const void* fn, dim3 grid, int threads, size_t smem, bool pdl, void** args,
+                   cudaStream_t st, const char* what) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = &attr;
+    lc.numAttrs = pdl ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+    return e == cudaSuccess ? CE_OK : record_cuda_failure(e, what);
+}
+
+// sums = [W0; W1] x^T
+ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void* w1, int64_t wrows,
+                       const void* x, int64_t rows, int64_t K, float* sums, bool pdl,
+                       uint64_t timeout_ns, unsigned* status, cudaStream_t st) {
+    RowsArgs a = {};
+    a.units = p.units;
+    a.per = p.per;
+    a.tiles0 = (wrows + kRowsTile - 1) / kRowsTile;
+    a.nk = p.nk;
+    a.rows = static_cast<int>(rows);
+    a.nt = static_cast<int>((rows + 15) / 16 * 16);
+    a.stage_bytes = kRowsA + static_cast<uint32_t>(a.nt) * kBK * 2;
+    a.stages = std::min<int>(kRowsStages, static_cast<int>(kRowsSmem / a.stage_bytes));
+    a.parts = p.parts;
+    a.sums = sums;
+    a.timeout_ns = timeout_ns;
+    a.status = status;
+    CUtensorMap m0, m1, mx;
+    ce_status rc = tc_map_16bit(&m0, w0, dtype, wrows, K, kRowsTile);
+    if (rc == CE_OK) rc = tc_map_16bit(&m1, w1 ? w1 : w0, dtype, wrows, K, kRowsTile);
+    if (rc == CE_OK) rc = tc_map_16bit(&mx, x, dtype, rows, K, static_cast<uint32_t>(a.nt));
+    if (rc != CE_OK) return rc;
+    const void* fn = dtype == CE_BF16 ? (const void*)&ffn_rows<1u> : (const void*)&ffn_rows<0u>;
+    const size_t smem = kRowsSmem + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward rows attributes");
+    void* args[] = {&m0, &m1, &mx, &a};
+    return rows_pdl(fn, dim3(static_cast<unsigned>(p.grid)), kRowsThreads, smem, pdl, args, st,
+                    "feed-forward rows launch");
+}
+
+}  // namespace
+
+int64_t ffn_rows_workspace(int64_t rows, int64_t H8, int64_t I8, int64_t O, int sms) {
+    const int64_t ti = (I8 + kRowsTile - 1) / kRowsTile, to = (O + kRowsTile - 1) / kRowsTile;
+    return rows_plan(2 * ti, H8, rows, sms).bytes + rows_plan(to, I8, rows, sms).bytes;
+}
+
+// The block's forward for at most 256 rows: operands as ce_ffn_fwd has
+// packed them (x [rows, H8], Wg and Wu [I, H8], Wd [O, I8], h, s, a [rows,
+// I8]); y and residual [rows, O].
+ce_status ffn_rows_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                       const void* residual, int dtype, int64_t rows, int64_t H8, int64_t I,
+                       int64_t I8, int64_t O, int act, const DropSpec& drop, void* y, void* h,
+                       void* s, void* a, void* workspace, int sms, uint64_t timeout_ns,
+                       unsigned* status, cudaStream_t st) {
+    const int64_t ti = (I8 + kRowsTile - 1) / kRowsTile, to = (O + kRowsTile - 1) / kRowsTile;
+    const RowsPlan up = rows_plan(2 * ti, H8, rows, sms), down = rows_plan(to, I8, rows, sms);
+    float* sums_up = static_cast<float*>(workspace);
+    float* sums_down = reinterpret_cast<float*>(static_cast<char*>(workspace) + up.bytes);
+    // the first launch waits for all work before it: what the others read
+    // early (the weights) is then written
+    ce_status rc = rows_product(up, dtype, w_gate, w_up, I, x, rows, H8, sums_up, false, timeout_ns,
+                                status, st);
+    if (rc != CE_OK) return rc;
+    const bool bf = dtype == CE_BF16;
+    RowsJoin j = {};
+    j.sums = sums_up;
+    j.per = up.per;
+    j.nk = up.nk;
+    j.parts = up.parts;
+    j.tiles0 = ti;
+    j.rows = static_cast<int>(rows);
+    j.cols = I;
+    j.pitch = I8;
+    j.act = act;
+    j.out = h;
+    j.s = s;
+    j.a = a;
+    void* args[] = {&j};
+    rc = rows_pdl(bf ? (const void*)&ffn_rows_act<__nv_bfloat16> : (const void*)&ffn_rows_act<__half>,
+                  dim3(static_cast<unsigned>(ti), static_cast<unsigned>(rows)), kRowsTile, 0, true,
+                  args, st, "feed-forward activation launch");
+    if (rc != CE_OK) return rc;
+    rc = rows_product(down, dtype, w_down, nullptr, O, h, rows, I8, sums_down, true, timeout_ns,
+                      status, st);
+    if (rc != CE_OK) return rc;
+    j.sums = sums_down;
+    j.per = down.per;
+    j.nk = down.nk;
+    j.parts = down.parts;
+    j.cols = j.pitch = O;
+    j.out = y;
+    j.res = residual;
+    j.drop = drop;
+    return rows_pdl(bf ? (const void*)&ffn_rows_out<__nv_bfloat16> : (const void*)&ffn_rows_out<__half>,
+                    dim3(static_cast<unsigned>(to), static_cast<unsigned>(rows)), kRowsTile, 0, true,
+                    args, st, "feed-forward output launch");
+}
+
+}  // namespace gbce

@@ -113,7 +113,8 @@ BAD = [dict(dtype=3), dict(rows=-1), dict(H=0), dict(I=-8), dict(O=0), dict(act=
 @pytest.mark.parametrize("over", BAD + [dict(y=None), dict(h=None), dict(s=256), dict(h=264), dict(H=60, workspace=None)])
 def test_forward_refuses(over):
     from softmax_cross_entropy_gb300 import _lib
-    assert fwd(**over) == _lib.CE_ERR_INVALID_ARG
+    ws = dict(workspace=4096, workspace_bytes=1 << 30) if "workspace" not in over else {}
+    assert fwd(**{**ws, **over}) == _lib.CE_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("over", BAD + [dict(dy=None), dict(h=None), dict(s=None), dict(a=None), dict(x=257),
@@ -146,6 +147,7 @@ def test_wrapper_refuses_cpu_tensors():
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("rows,H,I,O", [
     (1, 8, 8, 8), (2, 64, 128, 64), (3, 200, 72, 40), (16, 256, 512, 256), (17, 1000, 24, 136),
+    (1, 2048, 4096, 2048), (40, 1024, 2048, 1000), (63, 4096, 640, 264),
     (33, 72, 1000, 264), (64, 512, 640, 512), (129, 136, 264, 8), (300, 384, 320, 640),
     (515, 256, 1032, 256)])
 def test_forward(dtype, act, rows, H, I, O):
