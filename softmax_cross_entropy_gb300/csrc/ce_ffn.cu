@@ -4,7 +4,7 @@
 // fp32 accumulation.
 //
 // One kernel, the pipeline of the GEMM in ce_gemm_tc.cu (a TMA producer
-// warp, an MMA-issuing warp, four epilogue warps; persistent, one CTA an
+// warp, an MMA-issuing warp, eight epilogue warps; persistent, one CTA an
 // SM), in five forms (FfnMode) that differ in what a tile's K blocks are
 // made of and in the epilogue:
 //  * kGateUp: a tile's 256 accumulator columns are 128 columns of x Wg^T and
@@ -93,38 +93,92 @@ struct FfnType<0u> {
     using T = __half;
 };
 
+constexpr int kFfnThreads = 320;  // producer, MMA issuer, 8 epilogue warps
+constexpr int kFfnEpiThreads = 256;
+// epilogue staging: two boxes of 32 x 32 16-bit elements a warp
+constexpr uint32_t kFfnBox = 2048;
+static_assert(8 * 2 * kFfnBox == kOutBytes, "the staging area of the GEMM");
+
 // 32 columns of 16-bit elements from column n of row `row` of [M, N] (N a
-// multiple of 8); zeros outside.
+// multiple of 8) as they are; zeros outside.
 template <typename T>
 __device__ __forceinline__ void load_row32(const void* p, int64_t row, int64_t n, int64_t M,
-                                           int64_t N, float (&f)[32]) {
+                                           int64_t N, uint4 (&w)[4]) {
     const T* q = static_cast<const T*>(p) + row * N + n;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (row < M && n + 8 * j < N)
-            Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(q + 8 * j)), t);
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < M && n + 8 * j < N) w[j] = __ldg(reinterpret_cast<const uint4*>(q + 8 * j));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void unpack32(const uint4 (&w)[4], float (&f)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float t[8];
+        Vec<T>::unpack(w[j], t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
     }
 }
-
-// 32 16-bit columns, half h of a 32-row x 128-byte staging box in the TMA's
-// 128-byte swizzle (16-byte chunk j of row r at chunk j ^ (r mod 8)).
 template <typename T>
-__device__ __forceinline__ void stage32(uint32_t buf, int r, int h, const float (&v)[32]) {
-    const uint32_t row = buf + static_cast<uint32_t>(r) * 128u;
+__device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&w)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float f[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
-                            v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
-        const uint4 p = Vec<T>::pack(f);
-        const uint32_t at = row + (static_cast<uint32_t>((4 * h + j) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(p.x), "r"(p.y),
-                     "r"(p.z), "r"(p.w)
-                     : "memory");
+        const float t[8] = {f[8 * j],     f[8 * j + 1], f[8 * j + 2], f[8 * j + 3],
+                            f[8 * j + 4], f[8 * j + 5], f[8 * j + 6], f[8 * j + 7]};
+        w[j] = Vec<T>::pack(t);
     }
 }
+
+// An epilogue warp's way out for boxes of 32 x 32 elements: through shared
+// memory (64-byte swizzle, conflict-free) to the TMA, or, for an output whose
+// rows are not whole 16-byte vectors, a row a store instruction.
+struct FfnStore {
+    uint32_t stage;  // two boxes, used in turn
+    uint32_t boxes;  // handed to the TMA so far
+    int lane;
+
+    __device__ __forceinline__ uint32_t at(uint32_t buf, int r, int j) const {
+        return buf + static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(j ^ ((r >> 1) & 3)) << 4);
+    }
+    __device__ __forceinline__ uint32_t put(const uint4 (&w)[4]) {
+        const uint32_t buf = stage + (boxes & 1u) * kFfnBox;
+        ++boxes;
+        // the box written two turns ago has been read out of this buffer
+        if (lane == 0) bulk_wait_read_1();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(buf, lane, j)),
+                         "r"(w[j].x), "r"(w[j].y), "r"(w[j].z), "r"(w[j].w)
+                         : "memory");
+        return buf;
+    }
+    // the box at column n, row m; the TMA clips what lies outside
+    __device__ __forceinline__ void tma(const CUtensorMap* map, int64_t n, int64_t m, const uint4 (&w)[4]) {
+        const uint32_t buf = put(w);
+        fence_proxy_async_smem();  // the writes, seen by the TMA
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, buf, static_cast<int>(n), static_cast<int>(m));
+            bulk_commit();
+        }
+    }
+    __device__ __forceinline__ void plain(void* out, int64_t n, int64_t m, int64_t M, int64_t cols,
+                                          const uint4 (&w)[4]) {
+        const uint32_t buf = put(w);
+        __syncwarp();
+        uint16_t* to = static_cast<uint16_t*>(out) + m * cols + n + lane;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at(buf, r, lane >> 3) + 2u * (lane & 7)));
+            if (m + r < M && n + lane < cols) to[r * cols] = v;
+        }
+        __syncwarp();
+    }
+};
 
 // Whether element `i` is kept.
 __device__ __noinline__ bool ffn_kept(const DropSpec& d, PhiloxKey key, uint64_t i) {
@@ -154,8 +208,10 @@ __device__ __forceinline__ void ffn_drop_res(const FfnGemm& a, const PhiloxKey& 
     }
     if (a.res) {
         if (a.res_vec) {
+            uint4 raw[4];
+            load_row32<T>(a.res, row, n, M, N, raw);
             float w[32];
-            load_row32<T>(a.res, row, n, M, N, w);
+            unpack32<T>(raw, w);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += w[j];
         } else if (row < M) {
@@ -182,7 +238,7 @@ __device__ __forceinline__ int64_t ffn_tile_n(const FfnGemm& a, int p, int64_t t
 }
 
 template <uint32_t AB, int MODE, int BM>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kFfnThreads, 1)
 ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a) {
     using T = typename FfnType<AB>::T;
     using TT = TcTile<BM>;
@@ -218,7 +274,7 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), 128);
+            mbar_init(smem_u32(&acc_empty[b]), kFfnEpiThreads);
         }
         mbar_init(smem_u32(&done_bar), 1);
         s_fail = 0;
@@ -331,18 +387,27 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
             tc_commit(smem_u32(&done_bar));  // after every MMA this thread issued
         }
     } else {
-        // ---- epilogue: warp w reads accumulator lanes 32 (w mod 4) of
-        // each 128-row half of the tile
-        const int q = warp & 3;
-        // this warp's two staging boxes, used in turn
-        const uint32_t stg = smem0 + kRingBytes + static_cast<uint32_t>(q) * 2u * kStageOut;
-        uint32_t nst = 0;  // boxes this warp has handed to the TMA
+        // ---- epilogue: warp w reads accumulator lanes 32 (w mod 4) of each
+        // 128-row half of the tile; of its columns warps 2-5 take the first
+        // half, warps 6-9 the second
+        const int q = warp & 3, side = (warp - 2) >> 2;
+        FfnStore store{smem0 + kRingBytes + static_cast<uint32_t>(warp - 2) * 2u * kFfnBox, 0u, lane};
         PhiloxKey key{};
         if constexpr (MODE == kDown) key = philox_key(a.drop);
-        const int outs = MODE == kGateUp ? a.outs : MODE == kDact ? 2 : 1;
         int i = 0;
         for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, ++i) {
             const int b = i % NACC;
+            int64_t tl = t;
+            const int p = ffn_problem(a, &tl);
+            const int64_t M = a.M[p], N = a.N[p];
+            const int64_t n0 = ffn_tile_n(a, p, tl) * kCols + side * (kCols / 2);
+            const int64_t mt = ffn_tile_m(a, p, tl) * BM + q * 32;  // + 128 hh
+            constexpr int kUnits = kCols / 64;  // units of 32 columns of this warp's half
+            uint4 ns[4], na[4];  // kDact: s and a of the next unit
+            if constexpr (MODE == kDact) {  // the tile's first, while its products run
+                load_row32<T>(a.s, mt + lane, n0, M, N, ns);
+                load_row32<T>(a.a, mt + lane, n0, M, N, na);
+            }
             const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
                                               static_cast<uint32_t>(i / NACC) & 1u, a.timeout_ns);
             if (!ok || *reinterpret_cast<volatile int*>(&s_fail)) {
@@ -350,82 +415,79 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 break;
             }
             tc_fence_after();
-            int64_t tl = t;
-            const int p = ffn_problem(a, &tl);
-            const int64_t M = a.M[p], N = a.N[p];
-            const int64_t n0 = ffn_tile_n(a, p, tl) * kCols;
 #pragma unroll 1
-            for (int hh = 0; hh < H; ++hh) {
-                const int64_t m0 = ffn_tile_m(a, p, tl) * BM + hh * kMmaM;
-                const int64_t row = m0 + q * 32 + lane;
-                const bool rows_in = m0 + q * 32 < M;  // the same for the whole warp
-                const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                                      static_cast<uint32_t>((b * H + hh) * kBN);
-                if (!rows_in) continue;
-#pragma unroll 1
-                for (int c = 0; c < kCols / 64; ++c) {
-                    const int64_t n = n0 + c * 64;
-                    if (n >= N) break;  // the same for every thread of the warp
-#pragma unroll 1
-                    for (int o = 0; o < outs; ++o) {
-                        const uint32_t buf = stg + (nst & 1u) * kStageOut;
-                        // the box written two turns ago has been read out of this buffer
-                        if (lane == 0) bulk_wait_read_1();
-                        __syncwarp();
+            for (int x = 0; x < H * kUnits; ++x) {
+                const int hh = x / kUnits, c = x % kUnits;
+                const int64_t m = mt + hh * kMmaM, row = m + lane, n = n0 + c * 32;
+                // the accumulator's column of this unit
+                const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                                     static_cast<uint32_t>((b * H + hh) * kBN + side * (kCols / 2) + c * 32);
+                uint4 cs[4], ca[4];
+                if constexpr (MODE == kDact) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t col = static_cast<uint32_t>(c * 64 + h * 32);
-                            const int64_t nb = n + h * 32;
-                            float v[32];
-                            tc_ld32(trow + col, v);
-                            if constexpr (MODE == kGateUp) {
-                                if (o == 2) {
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = ffn_act(a.act, v[j]);
-                                } else {
-                                    float w[32];
-                                    tc_ld32(trow + 128u + col, w);
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        v[j] = w[j] * (o == 0 ? ffn_act(a.act, v[j])
-                                                              : ffn_slope(a.act, v[j]));
-                                }
-                            } else if constexpr (MODE == kDact) {
-                                float w[32];
-                                load_row32<T>(o == 0 ? a.s : a.a, row, nb, M, N, w);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] *= w[j] * a.scale[0];
-                            } else if constexpr (MODE == kDw) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] *= a.scale[p];
-                            } else if constexpr (MODE == kDown) {
-                                ffn_drop_res<T>(a, key, row, nb, v);
-                            }
-                            if constexpr (MODE == kDown || MODE == kDx || MODE == kDw) {
-                                const int pi = MODE == kDw ? p : 0;
-                                if (a.plain[pi]) {
-                                    if (row < M) {
-                                        T* out = static_cast<T*>(a.plain[pi]) + row * a.ncols[pi] + nb;
-#pragma unroll
-                                        for (int j = 0; j < 32; ++j)
-                                            if (nb + j < a.ncols[pi]) Vec<T>::store1(out, j, v[j]);
-                                    }
-                                    continue;
-                                }
-                            }
-                            stage32<T>(buf, lane, h, v);
-                        }
-                        if (MODE != kGateUp && MODE != kDact && a.plain[MODE == kDw ? p : 0]) continue;
-                        fence_proxy_async_smem();  // the writes, seen by the TMA
-                        __syncwarp();
-                        if (lane == 0) {
-                            // rows past M and columns past N are clipped by the TMA
-                            tma_store_2d(&maps.c[MODE == kDw ? p : o], buf, static_cast<int>(n),
-                                         static_cast<int>(m0 + q * 32));
-                            bulk_commit();
-                        }
-                        ++nst;
+                    for (int j = 0; j < 4; ++j) {
+                        cs[j] = ns[j];
+                        ca[j] = na[j];
                     }
+                    const int y = x + 1 < H * kUnits ? x + 1 : x;
+                    const int64_t nr = mt + (y / kUnits) * kMmaM + lane, nn = n0 + (y % kUnits) * 32;
+                    load_row32<T>(a.s, nr, nn, M, N, ns);
+                    load_row32<T>(a.a, nr, nn, M, N, na);
+                }
+                if (m >= M || n >= N) continue;  // the same for the whole warp
+                float v[32];
+                tc_ld32(acc, v);
+                uint4 w[4];
+                if constexpr (MODE == kGateUp) {
+                    float u[32];
+                    tc_ld32(acc + kBN / 2, u);
+                    if (a.outs == 1) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = ffn_gate<false>(a.act, v[j]).act * u[j];
+                        pack32<T>(v, w);
+                        store.tma(&maps.c[0], n, m, w);
+                    } else {
+                        uint4 ws[4], wa[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float fh[8], fs[8], fa[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const FfnGate r = ffn_gate<true>(a.act, v[8 * j + e]);
+                                fa[e] = r.act;
+                                fs[e] = u[8 * j + e] * r.slope;
+                                fh[e] = r.act * u[8 * j + e];
+                            }
+                            w[j] = Vec<T>::pack(fh);
+                            ws[j] = Vec<T>::pack(fs);
+                            wa[j] = Vec<T>::pack(fa);
+                        }
+                        store.tma(&maps.c[0], n, m, w);
+                        store.tma(&maps.c[1], n, m, ws);
+                        store.tma(&maps.c[2], n, m, wa);
+                    }
+                } else if constexpr (MODE == kDact) {
+                    float f[32], o[32];
+                    unpack32<T>(cs, f);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
+                    pack32<T>(o, w);
+                    store.tma(&maps.c[0], n, m, w);
+                    unpack32<T>(ca, f);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
+                    pack32<T>(o, w);
+                    store.tma(&maps.c[1], n, m, w);
+                } else {
+                    if constexpr (MODE == kDw) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= a.scale[p];
+                    }
+                    if constexpr (MODE == kDown) ffn_drop_res<T>(a, key, row, n, v);
+                    pack32<T>(v, w);
+                    const int pi = MODE == kDw ? p : 0;
+                    if (a.plain[pi]) store.plain(a.plain[pi], n, m, M, a.ncols[pi], w);
+                    else store.tma(&maps.c[pi], n, m, w);
                 }
             }
             tc_fence_before();
@@ -591,7 +653,7 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
             rc = tc_map_16bit(&maps.b[i], B[i].p, dtype, B[i].outer, B[i].inner,
                               b_mn ? 64 : mode == kGateUp ? kBN / 2 : kBN);
         if (rc == CE_OK && C[i].p)
-            rc = tc_map_16bit(&maps.c[i], C[i].p, dtype, C[i].outer, C[i].inner, 32);
+            rc = tc_map_16bit_out(&maps.c[i], const_cast<void*>(C[i].p), dtype, C[i].outer, C[i].inner);
         if (rc != CE_OK) return rc;
     }
     const void* fn = ffn_fn(dtype, mode, bm);
@@ -600,7 +662,7 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
     if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward attributes");
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(end, d.sms));
     void* args[] = {&maps, &g};
-    e = cudaLaunchKernel(fn, dim3(grid), dim3(kTcThreads), args, kTcSmem, st);
+    e = cudaLaunchKernel(fn, dim3(grid), dim3(kFfnThreads), args, kTcSmem, st);
     return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "feed-forward launch");
 }
 

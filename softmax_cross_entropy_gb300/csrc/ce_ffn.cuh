@@ -18,22 +18,25 @@ __device__ __forceinline__ float ffn_logistic(float z) {
 constexpr float kGelu2k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
-__device__ __forceinline__ float ffn_act(int act, float g) {
-    if (act == CE_ACT_SILU) return g * ffn_logistic(g);
-    if (act == CE_ACT_GELU) return g * (0.5f * erfcf(-0.70710678f * g));
-    return g * ffn_logistic(kGelu2k * g * (1.f + kGeluC * g * g));
-}
-
-// d act / d g
-__device__ __forceinline__ float ffn_slope(int act, float g) {
-    if (act == CE_ACT_SILU) {
-        const float q = ffn_logistic(g);
-        return q * (1.f + g * (1.f - q));
+// What the block needs of a gate g: act(g), and its derivative where SLOPE.
+struct FfnGate {
+    float act, slope;
+};
+template <bool SLOPE>
+__device__ __forceinline__ FfnGate ffn_gate(int act, float g) {
+    FfnGate r{0.f, 0.f};
+    if (act == CE_ACT_GELU) {
+        const float phi = 0.5f * erfcf(-0.70710678f * g);
+        r.act = g * phi;
+        if (SLOPE) r.slope = phi + g * 0.39894228f * ex2(-0.5f * kLog2e * g * g);
+    } else {
+        const bool silu = act == CE_ACT_SILU;
+        const float q = ffn_logistic(silu ? g : kGelu2k * g * (1.f + kGeluC * g * g));
+        r.act = g * q;
+        if (SLOPE)
+            r.slope = q + g * q * (1.f - q) * (silu ? 1.f : kGelu2k * (1.f + 3.f * kGeluC * g * g));
     }
-    if (act == CE_ACT_GELU)
-        return 0.5f * erfcf(-0.70710678f * g) + g * 0.39894228f * ex2(-0.5f * kLog2e * g * g);
-    const float q = ffn_logistic(kGelu2k * g * (1.f + kGeluC * g * g));
-    return q + g * q * (1.f - q) * kGelu2k * (1.f + 3.f * kGeluC * g * g);
+    return r;
 }
 
 }  // namespace gbce

@@ -273,9 +273,10 @@ __global__ void __launch_bounds__(kRowsTile) ffn_rows_act(const __grid_constant_
     if (c < j.cols) {
         const float g = join_parts(j, blockIdx.x, row);
         const float u = join_parts(j, j.tiles0 + blockIdx.x, row);
-        a = ffn_act(j.act, g);
+        const FfnGate r = ffn_gate<true>(j.act, g);
+        a = r.act;
         h = a * u;
-        if (j.s) s = u * ffn_slope(j.act, g);
+        s = u * r.slope;
     }
     const int64_t at = row * j.pitch + c;
     Vec<T>::store1(j.out, at, h);

@@ -179,9 +179,12 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
 // A 2-D map of a row-major [outer, inner] matrix of 16-bit elements, boxes of
 // box_outer x 64 elements (128 bytes: the swizzle width), 128-byte swizzle,
 // zeros outside the matrix (ce_gemm_tc.cu). A K-major operand is [MN, K] with
-// boxes of 128 or 256 rows, an MN-major one [K, MN] with boxes of 64 K rows,
-// a 16-bit output [M, N] with boxes of 32 rows.
+// boxes of 128 or 256 rows, an MN-major one [K, MN] with boxes of 64 K rows.
 ce_status tc_map_16bit(CUtensorMap* map, const void* p, int dtype, int64_t outer, int64_t inner,
                        uint32_t box_outer);
+// The same of an output [rows, cols], stored in boxes of 32 x 32 elements
+// (64 bytes a row) with 64-byte swizzle: 16-byte chunk j of row r at chunk j
+// ^ (r / 2 mod 4).
+ce_status tc_map_16bit_out(CUtensorMap* map, void* p, int dtype, int64_t rows, int64_t cols);
 
 }  // namespace gbce
