@@ -25,9 +25,8 @@
 // with zeros, its factor 1 / (1 - p) is applied to the products in fp32.
 //
 // The TMA wants rows of whole 16 bytes. Operands that have others (H, I or O
-// not a multiple of 8, or an unaligned base) are packed into rows of such a
-// length by a kernel of their own first, and outputs that have others leave
-// by plain stores.
+// not a multiple of 8) are packed into rows of such a length by a kernel of
+// their own first.
 //
 // Bound by the tensor cores from about 600 rows on (6 rows H I operations on
 // 6 H I bytes of weights); ce_ffn_rows.cu takes few rows.
@@ -59,17 +58,42 @@ namespace {
 
 enum FfnMode : int { kGateUp, kDown, kDact, kDx, kDw };
 
+// Tile shapes, all 256 accumulator columns wide:
+//  * 128: 128 rows on one SM, 4 stages of 48 KB, two accumulators;
+//  * 256: 256 rows on one SM, 3 stages of 64 KB, its two halves in all of
+//    the tensor memory: the epilogue does not overlap the next tile;
+//  * kPair: 256 rows on a pair of SMs (a cluster of two CTAs whose tensor
+//    cores work as one: each holds 128 rows of A, half of B's 256 columns and
+//    128 rows of the accumulator), 6 stages of 32 KB a CTA, two accumulators.
+//    Each byte staged feeds twice the multiplications of the 128-row tile,
+//    and the epilogue of a tile overlaps the next tile's products.
+constexpr int kPair = 2;
+template <int SHAPE>
+struct FfnTile {
+    static constexpr bool kTwo = SHAPE == kPair;
+    static constexpr int kRows = kTwo ? 256 : SHAPE;
+    static constexpr int kStages = kTwo ? 6 : SHAPE == 256 ? 3 : 4;
+    static constexpr int kHalves = SHAPE == 256 ? 2 : 1;  // 128-row MMAs a K step
+    static constexpr int kAccBufs = SHAPE == 256 ? 1 : 2;
+    static constexpr uint32_t kA = (SHAPE == 256 ? 2u : 1u) * kHalfA;  // bytes of a stage, this CTA
+    static constexpr uint32_t kB = kTwo ? kBBytes / 2 : kBBytes;
+    static constexpr uint32_t kStage = kA + kB;
+    static_assert(kStages * kStage == kRingBytes, "one ring for every shape");
+};
+constexpr int kFfnStages = 6;
+
 struct FfnMaps {
-    CUtensorMap a[3], b[3], c[3];
+    CUtensorMap a[3], b[3];
 };
 
 struct FfnGemm {
     // problems (kDw), whose tiles follow one another
     int64_t M[3], N[3], tiles_m[3], tiles_n[3], tile_end[3];
     int64_t K;      // of one segment
-    // outputs by plain stores: [M, ncols] with pitch ncols, or nullptr
-    void* plain[3];
-    int64_t ncols[3];
+    // outputs: of the problems (kDx, kDown: one), or of one problem (kGateUp:
+    // h, s, a; kDact: dg, du); odd: its rows are not whole 16-byte vectors
+    void* out[3];
+    int odd[3];
     float scale[3];  // kDact, kDw: of the products
     int segs;       // segments of K (kDx: 2)
     int m_first;    // a problem's tiles run along M first
@@ -77,12 +101,66 @@ struct FfnGemm {
     int act;
     const void* s;  // kDact: u act'(g), [M, N]
     const void* a;  // kDact: act(g), [M, N]
-    const void* res;  // kDown: [M, ncols] or nullptr
+    const void* res;  // kDown: [M, N] or nullptr
     int res_vec;      // 1: its rows are whole 16-byte vectors
     DropSpec drop;    // kDown
     uint64_t timeout_ns;
     unsigned* status;
 };
+
+// The pair's forms of the copies, products and barriers: a copy that signals
+// a barrier of the pair's first CTA, a product over both CTAs' operands and
+// accumulators (issued by the first), a commit that arrives in both.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    const uint16_t both = 3;
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(both)
+        : "memory");
+}
+__device__ __forceinline__ void pair_arrive(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool pair_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// tc_wait for a barrier that the other CTA of the pair arrives on
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+    if (pair_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (pair_try_wait(bar, parity)) return true;
+        if ((i & 1023u) == 0 && global_timer_ns() - t0 > timeout_ns) return false;
+    }
+}
 
 template <uint32_t AB>
 struct FfnType {
@@ -94,10 +172,10 @@ struct FfnType<0u> {
 };
 
 constexpr int kFfnThreads = 320;  // producer, MMA issuer, 8 epilogue warps
-constexpr int kFfnEpiThreads = 256;
+constexpr int kFfnEpiWarps = 8;
 // epilogue staging: two boxes of 32 x 32 16-bit elements a warp
 constexpr uint32_t kFfnBox = 2048;
-static_assert(8 * 2 * kFfnBox == kOutBytes, "the staging area of the GEMM");
+static_assert(kFfnEpiWarps * 2 * kFfnBox == kOutBytes, "the staging area of the GEMM");
 
 // 32 columns of 16-bit elements from column n of row `row` of [M, N] (N a
 // multiple of 8) as they are; zeros outside.
@@ -110,6 +188,9 @@ __device__ __forceinline__ void load_row32(const void* p, int64_t row, int64_t n
         w[j] = make_uint4(0u, 0u, 0u, 0u);
         if (row < M && n + 8 * j < N) w[j] = __ldg(reinterpret_cast<const uint4*>(q + 8 * j));
     }
+}
+__device__ __forceinline__ void ffn_prefetch(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 template <typename T>
 __device__ __forceinline__ void unpack32(const uint4 (&w)[4], float (&f)[32]) {
@@ -131,44 +212,53 @@ __device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&w)[4]) {
     }
 }
 
-// An epilogue warp's way out for boxes of 32 x 32 elements: through shared
-// memory (64-byte swizzle, conflict-free) to the TMA, or, for an output whose
-// rows are not whole 16-byte vectors, a row a store instruction.
+// An epilogue warp's way out for boxes of 32 x 32 elements, which each lane
+// holds a row of: through shared memory (16-byte chunk j of row r at chunk j ^
+// (r / 2 mod 4), conflict-free) to stores of 64 bytes a row, eight rows an
+// instruction. (A TMA store of the box, whose read of the staging area waits
+// behind the ring's loads in the copy engine, took 346 instead of 327 us for
+// kDact at 4096 x 12288 x 4096 and 496 instead of 483 for kGateUp.)
 struct FfnStore {
     uint32_t stage;  // two boxes, used in turn
-    uint32_t boxes;  // handed to the TMA so far
+    uint32_t boxes;  // so far
     int lane;
 
     __device__ __forceinline__ uint32_t at(uint32_t buf, int r, int j) const {
         return buf + static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(j ^ ((r >> 1) & 3)) << 4);
     }
+    // (a buffer's last reads lie before the barrier of the box between)
     __device__ __forceinline__ uint32_t put(const uint4 (&w)[4]) {
         const uint32_t buf = stage + (boxes & 1u) * kFfnBox;
         ++boxes;
-        // the box written two turns ago has been read out of this buffer
-        if (lane == 0) bulk_wait_read_1();
-        __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(buf, lane, j)),
                          "r"(w[j].x), "r"(w[j].y), "r"(w[j].z), "r"(w[j].w)
                          : "memory");
+        __syncwarp();
         return buf;
     }
-    // the box at column n, row m; the TMA clips what lies outside
-    __device__ __forceinline__ void tma(const CUtensorMap* map, int64_t n, int64_t m, const uint4 (&w)[4]) {
-        const uint32_t buf = put(w);
-        fence_proxy_async_smem();  // the writes, seen by the TMA
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, buf, static_cast<int>(n), static_cast<int>(m));
-            bulk_commit();
-        }
-    }
-    __device__ __forceinline__ void plain(void* out, int64_t n, int64_t m, int64_t M, int64_t cols,
+    // the box at column n, row m of [M, cols], whose rows are whole 16-byte
+    // vectors
+    __device__ __forceinline__ void whole(void* out, int64_t n, int64_t m, int64_t M, int64_t cols,
                                           const uint4 (&w)[4]) {
         const uint32_t buf = put(w);
-        __syncwarp();
+        const int r0 = lane >> 2, ch = lane & 3;
+        uint16_t* to = static_cast<uint16_t*>(out) + (m + r0) * cols + n + 8 * ch;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + r0;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(at(buf, r, ch)));
+            if (m + r < M && n + 8 * ch < cols) *reinterpret_cast<uint4*>(to + 8 * j * cols) = v;
+        }
+    }
+    // the same of rows that are not: a row an instruction
+    __device__ __forceinline__ void odd(void* out, int64_t n, int64_t m, int64_t M, int64_t cols,
+                                        const uint4 (&w)[4]) {
+        const uint32_t buf = put(w);
         uint16_t* to = static_cast<uint16_t*>(out) + m * cols + n + lane;
 #pragma unroll 8
         for (int r = 0; r < 32; ++r) {
@@ -176,7 +266,6 @@ struct FfnStore {
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at(buf, r, lane >> 3) + 2u * (lane & 7)));
             if (m + r < M && n + lane < cols) to[r * cols] = v;
         }
-        __syncwarp();
     }
 };
 
@@ -191,7 +280,7 @@ __device__ __noinline__ bool ffn_kept(const DropSpec& d, PhiloxKey key, uint64_t
 template <typename T>
 __device__ __forceinline__ void ffn_drop_res(const FfnGemm& a, const PhiloxKey& key, int64_t row,
                                              int64_t n, float (&v)[32]) {
-    const int64_t M = a.M[0], N = a.ncols[0];
+    const int64_t M = a.M[0], N = a.N[0];
     if (a.drop.mode == kDropSome) {
         const uint64_t at = static_cast<uint64_t>(row * N + n);
         if ((N & 3) == 0) {
@@ -237,31 +326,35 @@ __device__ __forceinline__ int64_t ffn_tile_n(const FfnGemm& a, int p, int64_t t
     return a.m_first ? t / a.tiles_m[p] : t % a.tiles_n[p];
 }
 
-template <uint32_t AB, int MODE, int BM>
+template <uint32_t AB, int MODE, int SHAPE>
 __global__ void __launch_bounds__(kFfnThreads, 1)
 ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a) {
     using T = typename FfnType<AB>::T;
-    using TT = TcTile<BM>;
+    using TT = FfnTile<SHAPE>;
+    constexpr bool PAIR = TT::kTwo;
     constexpr bool A_MN = MODE == kDw;
     constexpr bool B_MN = MODE == kDact || MODE == kDx || MODE == kDw;
     constexpr int kCols = MODE == kGateUp ? kBN / 2 : kBN;  // output columns of a tile
+    constexpr int BM = TT::kRows;
     constexpr int kStages = TT::kStages;
-    constexpr uint32_t kABytes = TT::kABytes;
-    constexpr uint32_t kStageBytes = TT::kStageBytes;
     constexpr int NACC = TT::kAccBufs;
     constexpr int H = TT::kHalves;
     extern __shared__ unsigned char ffn_smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[kTcMaxStages];
-    __shared__ __align__(8) uint64_t empty_bar[kTcMaxStages];
+    __shared__ __align__(8) uint64_t full_bar[kFfnStages];
+    __shared__ __align__(8) uint64_t empty_bar[kFfnStages];
     __shared__ __align__(8) uint64_t acc_full[2];
     __shared__ __align__(8) uint64_t acc_empty[2];
     __shared__ __align__(8) uint64_t done_bar;  // every MMA of the CTA completed
     __shared__ uint32_t tmem_base_sh;
-    __shared__ uint32_t s_issued[kTcMaxStages];  // 0, or 2 + parity of the last copy into the stage
+    __shared__ uint32_t s_issued[kFfnStages];  // 0, or 2 + parity of the last copy into the stage
     __shared__ int s_fail;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    // a pair's CTAs work on the same tiles; the first issues the products
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
+    const int64_t tile_step = PAIR ? gridDim.x / 2 : gridDim.x;
     const uint32_t smem0 = (smem_u32(ffn_smem_raw) + 1023u) & ~1023u;  // 1024-byte aligned
     const int nk = static_cast<int>((a.K + kBK - 1) / kBK);
     const int64_t ntiles = a.tile_end[2];
@@ -274,117 +367,157 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
-            mbar_init(smem_u32(&acc_empty[b]), kFfnEpiThreads);
+            mbar_init(smem_u32(&acc_empty[b]), (PAIR ? 2 : 1) * kFfnEpiWarps);
         }
         mbar_init(smem_u32(&done_bar), 1);
         s_fail = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile(
-            "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                smem_u32(&tmem_base_sh)),
-            "r"(kTmemCols)
-            : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile(
+                "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                    smem_u32(&tmem_base_sh)),
+                "r"(kTmemCols)
+                : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile(
+                "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                    smem_u32(&tmem_base_sh)),
+                "r"(kTmemCols)
+                : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // both CTAs' barriers and tensor memory
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
 
     if (warp == 0) {
         if (lane == 0) {
             // ---- TMA producer: every K block of every tile of this CTA
-            int it = 0;  // K blocks issued so far (ring position)
+            const auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+                if constexpr (PAIR) pair_load_2d(dst, map, x, y, bar);
+                else tma_load_2d(dst, map, x, y, bar);
+            };
+            int s = 0;
+            uint32_t ph = 0;
             bool fail = false;
-            for (int64_t t = blockIdx.x; t < ntiles && !fail; t += gridDim.x) {
+            for (int64_t t = tile0; t < ntiles && !fail; t += tile_step) {
                 int64_t tl = t;
                 const int p = ffn_problem(a, &tl);
-                const int m0 = static_cast<int>(ffn_tile_m(a, p, tl) * BM);
-                const int n0 = static_cast<int>(ffn_tile_n(a, p, tl) * kCols);
-                for (int kb = 0; kb < nk * a.segs; ++kb, ++it) {
-                    const int s = it % kStages;
-                    const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
+                // this CTA's rows of A, and its columns of B
+                const int m0 = static_cast<int>(ffn_tile_m(a, p, tl) * BM + rank * kMmaM);
+                const int nt = static_cast<int>(ffn_tile_n(a, p, tl) * kCols);
+                const int n0 = MODE == kGateUp ? nt : nt + static_cast<int>(rank) * (kBN / 2);
+                for (int kb = 0; kb < nk * a.segs; ++kb) {
                     if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
                         fail = true;
                         break;
                     }
-                    const uint32_t fb = smem_u32(&full_bar[s]);
-                    mbar_arrive_expect_tx(fb, kStageBytes);
-                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * kStageBytes;
+                    // the pair's copies signal its first CTA's barrier, which
+                    // expects the bytes of both
+                    uint32_t fb = smem_u32(&full_bar[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(fb, (PAIR ? 2u : 1u) * TT::kStage);
+                    if constexpr (PAIR) fb = map_to_rank(fb, 0);
+                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage;
                     // the operands' maps: of the problem, or of the segment
                     const int seg = kb >= nk ? 1 : 0;
                     const int i = MODE == kDx ? seg : p;
                     const int k0 = (kb - seg * nk) * kBK;
                     if constexpr (A_MN) {
-                        for (int j = 0; j < BM / 64; ++j)
-                            tma_load_2d(sa + j * kMnBox, &maps.a[i], m0 + 64 * j, k0, fb);
+                        for (uint32_t j = 0; j < TT::kA / kMnBox; ++j)
+                            load(sa + j * kMnBox, &maps.a[i], m0 + 64 * j, k0, fb);
                     } else {
-                        tma_load_2d(sa, &maps.a[i], k0, m0, fb);
+                        load(sa, &maps.a[i], k0, m0, fb);
                     }
+                    const uint32_t sb = sa + TT::kA;
                     if constexpr (MODE == kGateUp) {
-                        tma_load_2d(sa + kABytes, &maps.b[0], k0, n0, fb);
-                        tma_load_2d(sa + kABytes + kBBytes / 2, &maps.b[1], k0, n0, fb);
+                        if constexpr (PAIR) {
+                            load(sb, &maps.b[rank], k0, n0, fb);
+                        } else {
+                            load(sb, &maps.b[0], k0, n0, fb);
+                            load(sb + kBBytes / 2, &maps.b[1], k0, n0, fb);
+                        }
                     } else if constexpr (B_MN) {
-                        for (int j = 0; j < kBN / 64; ++j)
-                            tma_load_2d(sa + kABytes + j * kMnBox, &maps.b[i], n0 + 64 * j, k0, fb);
+                        for (uint32_t j = 0; j < TT::kB / kMnBox; ++j)
+                            load(sb + j * kMnBox, &maps.b[i], n0 + 64 * j, k0, fb);
                     } else {
-                        tma_load_2d(sa + kABytes, &maps.b[i], k0, n0, fb);
+                        load(sb, &maps.b[i], k0, n0, fb);
                     }
                     s_issued[s] = 2u + ph;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
             if (fail) s_fail = 1;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             // ---- MMA issuer: tile i into accumulator buffer i mod NACC
-            constexpr uint32_t idesc = tc_idesc(AB, A_MN ? 1u : 0u, B_MN ? 1u : 0u);
-            int it = 0;
+            const auto commit = [](uint32_t bar) {
+                if constexpr (PAIR) pair_commit(bar);
+                else tc_commit(bar);
+            };
+            constexpr uint32_t idesc =
+                (tc_idesc(AB, A_MN ? 1u : 0u, B_MN ? 1u : 0u) & ~(31u << 24)) |
+                (static_cast<uint32_t>((PAIR ? 256 : 128) >> 4) << 24);
+            int s = 0;
+            uint32_t ph = 0;
             int i = 0;  // tiles of this CTA so far
             bool fail = false;
-            for (int64_t t = blockIdx.x; t < ntiles && !fail; t += gridDim.x, ++i) {
+            for (int64_t t = tile0; t < ntiles && !fail; t += tile_step, ++i) {
                 const int b = i % NACC;
                 // the epilogue has drained this buffer's previous tile
-                if (!tc_wait(smem_u32(&acc_empty[b]),
-                             (static_cast<uint32_t>(i / NACC) & 1u) ^ 1u, a.timeout_ns)) {
+                const uint32_t drained = (static_cast<uint32_t>(i / NACC) & 1u) ^ 1u;
+                if (!(PAIR ? pair_wait(smem_u32(&acc_empty[b]), drained, a.timeout_ns)
+                           : tc_wait(smem_u32(&acc_empty[b]), drained, a.timeout_ns))) {
                     fail = true;
                     break;
                 }
                 tc_fence_after();
                 // half h of the tile (rows 128 h ...) in columns (b H + h) 256
                 const uint32_t acc = tmem + static_cast<uint32_t>(b * H * kBN);
-                for (int kb = 0; kb < nk * a.segs; ++kb, ++it) {
-                    const int s = it % kStages;
-                    const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
-                    if (!tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)) {
+                for (int kb = 0; kb < nk * a.segs; ++kb) {
+                    if (!(PAIR ? pair_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)
+                               : tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns))) {
                         fail = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * kStageBytes;
+                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage;
+                    const uint32_t sb = sa + TT::kA;
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k) {
-                        const uint64_t db = B_MN ? tc_smem_desc_mn(sa + kABytes + 2048u * k)
-                                                 : tc_smem_desc(sa + kABytes + 32u * k);
+                        const uint64_t db = B_MN ? tc_smem_desc_mn(sb + 2048u * k)
+                                                 : tc_smem_desc(sb + 32u * k);
 #pragma unroll
                         for (int h = 0; h < H; ++h) {
                             const uint32_t ah = sa + static_cast<uint32_t>(h) * kHalfA;
                             const uint64_t da = A_MN ? tc_smem_desc_mn(ah + 2048u * k)
                                                      : tc_smem_desc(ah + 32u * k);
-                            tc_mma(acc + static_cast<uint32_t>(h * kBN), da, db, idesc,
-                                   (kb > 0 || k > 0) ? 1u : 0u);
+                            const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+                            if constexpr (PAIR) pair_mma(acc, da, db, idesc, add);
+                            else tc_mma(acc + static_cast<uint32_t>(h * kBN), da, db, idesc, add);
                         }
                     }
-                    tc_commit(smem_u32(&empty_bar[s]));
+                    commit(smem_u32(&empty_bar[s]));
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
                 // every MMA of the tile issued: the epilogue may read it once
                 // they complete (also after a failure, so that nothing waits)
-                tc_commit(smem_u32(&acc_full[b]));
+                commit(smem_u32(&acc_full[b]));
             }
             if (fail) s_fail = 1;
-            tc_commit(smem_u32(&done_bar));  // after every MMA this thread issued
+            commit(smem_u32(&done_bar));  // after every MMA this thread issued
         }
     } else {
         // ---- epilogue: warp w reads accumulator lanes 32 (w mod 4) of each
@@ -395,16 +528,25 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
         PhiloxKey key{};
         if constexpr (MODE == kDown) key = philox_key(a.drop);
         int i = 0;
-        for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x, ++i) {
+        for (int64_t t = tile0; t < ntiles; t += tile_step, ++i) {
             const int b = i % NACC;
             int64_t tl = t;
             const int p = ffn_problem(a, &tl);
             const int64_t M = a.M[p], N = a.N[p];
             const int64_t n0 = ffn_tile_n(a, p, tl) * kCols + side * (kCols / 2);
-            const int64_t mt = ffn_tile_m(a, p, tl) * BM + q * 32;  // + 128 hh
+            const int64_t mt = ffn_tile_m(a, p, tl) * BM + rank * kMmaM + q * 32;  // + 128 hh
             constexpr int kUnits = kCols / 64;  // units of 32 columns of this warp's half
             uint4 ns[4], na[4];  // kDact: s and a of the next unit
-            if constexpr (MODE == kDact) {  // the tile's first, while its products run
+            if constexpr (MODE == kDact) {
+                // while the tile's products run: the others into L2, the first here
+                for (int hh = 0; hh < H; ++hh) {
+                    const int64_t row = mt + hh * kMmaM + lane;
+                    for (int c = 0; c < kCols / 2; c += 64) {
+                        if (row >= M || n0 + c >= N) break;
+                        ffn_prefetch(static_cast<const T*>(a.s) + row * N + n0 + c);
+                        ffn_prefetch(static_cast<const T*>(a.a) + row * N + n0 + c);
+                    }
+                }
                 load_row32<T>(a.s, mt + lane, n0, M, N, ns);
                 load_row32<T>(a.a, mt + lane, n0, M, N, na);
             }
@@ -445,7 +587,7 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = ffn_gate<false>(a.act, v[j]).act * u[j];
                         pack32<T>(v, w);
-                        store.tma(&maps.c[0], n, m, w);
+                        store.whole(a.out[0], n, m, M, N, w);
                     } else {
                         uint4 ws[4], wa[4];
 #pragma unroll
@@ -462,9 +604,9 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                             ws[j] = Vec<T>::pack(fs);
                             wa[j] = Vec<T>::pack(fa);
                         }
-                        store.tma(&maps.c[0], n, m, w);
-                        store.tma(&maps.c[1], n, m, ws);
-                        store.tma(&maps.c[2], n, m, wa);
+                        store.whole(a.out[0], n, m, M, N, w);
+                        store.whole(a.out[1], n, m, M, N, ws);
+                        store.whole(a.out[2], n, m, M, N, wa);
                     }
                 } else if constexpr (MODE == kDact) {
                     float f[32], o[32];
@@ -472,12 +614,12 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
                     pack32<T>(o, w);
-                    store.tma(&maps.c[0], n, m, w);
+                    store.whole(a.out[0], n, m, M, N, w);
                     unpack32<T>(ca, f);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
                     pack32<T>(o, w);
-                    store.tma(&maps.c[1], n, m, w);
+                    store.whole(a.out[1], n, m, M, N, w);
                 } else {
                     if constexpr (MODE == kDw) {
 #pragma unroll
@@ -486,15 +628,18 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                     if constexpr (MODE == kDown) ffn_drop_res<T>(a, key, row, n, v);
                     pack32<T>(v, w);
                     const int pi = MODE == kDw ? p : 0;
-                    if (a.plain[pi]) store.plain(a.plain[pi], n, m, M, a.ncols[pi], w);
-                    else store.tma(&maps.c[pi], n, m, w);
+                    if (a.odd[pi]) store.odd(a.out[pi], n, m, M, N, w);
+                    else store.whole(a.out[pi], n, m, M, N, w);
                 }
             }
+            // the warp's loads of the accumulator are done
             tc_fence_before();
-            mbar_arrive(smem_u32(&acc_empty[b]));
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) pair_arrive(map_to_rank(smem_u32(&acc_empty[b]), 0));
+                else mbar_arrive(smem_u32(&acc_empty[b]));
+            }
         }
-        // every box written out before the shared memory goes
-        if (lane == 0) bulk_wait_all();
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -503,18 +648,27 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
         if (s_fail || !done) {
             atomicOr(a.status, kDevErrTimeout);
             // copies still in flight land before the shared memory is released
-            for (int s = 0; s < kStages; ++s)
-                if (s_issued[s])
-                    (void)mbar_wait_bounded(smem_u32(&full_bar[s]), s_issued[s] & 1u,
-                                            a.timeout_ns);
+            // (a pair's are counted by its first CTA)
+            if (rank == 0)
+                for (int s = 0; s < kStages; ++s)
+                    if (s_issued[s])
+                        (void)mbar_wait_bounded(smem_u32(&full_bar[s]), s_issued[s] & 1u,
+                                                a.timeout_ns);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1)
+    if constexpr (PAIR) {
+        cluster_sync();  // neither CTA leaves while the other may still use its memory
+        if (warp == 1)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kTmemCols)
+                         : "memory");
+    } else if (warp == 1) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
+    }
 }
 
 // Packs matrices [rows, cols] into rows of `pitch` elements (a multiple of 8,
@@ -578,7 +732,8 @@ __global__ void __launch_bounds__(256) ffn_pack(const __grid_constant__ PackArgs
 
 template <uint32_t AB, int MODE>
 const void* ffn_fn(int bm) {
-    return bm == 256 ? (const void*)&ffn_gemm<AB, MODE, 256> : (const void*)&ffn_gemm<AB, MODE, 128>;
+    return bm == kPair ? (const void*)&ffn_gemm<AB, MODE, kPair>
+           : bm == 256 ? (const void*)&ffn_gemm<AB, MODE, 256> : (const void*)&ffn_gemm<AB, MODE, 128>;
 }
 const void* ffn_fn(int dtype, int mode, int bm) {
     const bool bf = dtype == CE_BF16;
@@ -618,21 +773,36 @@ struct FfnMatrix {
     int64_t outer, inner;
 };
 
-// One launch of form `mode`: problems or segments A[i] x B[i], outputs C[i].
+// One launch of form `mode`: problems or segments A[i] x B[i].
 ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatrix (&A)[3],
-                     const FfnMatrix (&B)[3], const FfnMatrix (&C)[3], const FfnDevice& d,
-                     cudaStream_t st) {
+                     const FfnMatrix (&B)[3], const FfnDevice& d, cudaStream_t st) {
     const int64_t cols = mode == kGateUp ? kBN / 2 : kBN;
     g.timeout_ns = d.timeout_ns;
     g.status = d.status;
-    // the tile height with the fewer rounds of tiles over the SMs, as the
-    // GEMM chooses it (a round of 256-row tiles counts as 1.6 of 128-row ones)
-    int64_t tiles[2] = {0, 0};
-    for (int p = 0; p < problems; ++p)
-        for (int h = 0; h < 2; ++h)
-            tiles[h] += (g.M[p] + (h ? 255 : 127)) / (h ? 256 : 128) * ((g.N[p] + cols - 1) / cols);
-    const int64_t r128 = (tiles[0] + d.sms - 1) / d.sms, r256 = (tiles[1] + d.sms - 1) / d.sms;
-    const int bm = 16 * r256 < 10 * r128 ? 256 : 128;
+    // The tile shape by its rounds of tiles over the SMs (or pairs of SMs)
+    // and what a round was measured to take, that of pairs being 100 (per 4096
+    // of K, bf16: 23 us): 256 rows an SM 190 (4096 x 4096 x 24576 468 against
+    // 516 us for pairs), 210 where the epilogue, which it does not overlap,
+    // writes or reads much (512 against 483, 377 against 327 us), 128 rows 107
+    // (1023 x 4096 x 12288 75 against 67 us).
+    const bool heavy = mode == kGateUp || mode == kDact;
+    const int shapes[3] = {kPair, 256, 128};
+    const int64_t round[3] = {100, heavy ? 210 : 190, 107};
+    int shape = kPair;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t rows = shapes[i] == 128 ? 128 : 256;
+        const int64_t ctas = shapes[i] == kPair ? std::max(d.sms / 2, 1) : d.sms;
+        int64_t tiles = 0;
+        for (int p = 0; p < problems; ++p)
+            tiles += (g.M[p] + rows - 1) / rows * ((g.N[p] + cols - 1) / cols);
+        const int64_t cost = (tiles + ctas - 1) / ctas * round[i];
+        if (cost < least) {
+            least = cost;
+            shape = shapes[i];
+        }
+    }
+    const int bm = shape == 128 ? 128 : 256;
     int64_t end = 0;
     for (int p = 0; p < 3; ++p) {
         if (p < problems) {
@@ -648,21 +818,35 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
     const bool a_mn = mode == kDw, b_mn = mode == kDact || mode == kDx || mode == kDw;
     for (int i = 0; i < 3; ++i) {
         ce_status rc = CE_OK;
-        if (A[i].p) rc = tc_map_16bit(&maps.a[i], A[i].p, dtype, A[i].outer, A[i].inner, a_mn ? 64 : bm);
+        if (A[i].p) rc = tc_map_16bit(&maps.a[i], A[i].p, dtype, A[i].outer, A[i].inner,
+                                     a_mn ? 64 : shape == kPair ? 128 : bm);
         if (rc == CE_OK && B[i].p)
             rc = tc_map_16bit(&maps.b[i], B[i].p, dtype, B[i].outer, B[i].inner,
-                              b_mn ? 64 : mode == kGateUp ? kBN / 2 : kBN);
-        if (rc == CE_OK && C[i].p)
-            rc = tc_map_16bit_out(&maps.c[i], const_cast<void*>(C[i].p), dtype, C[i].outer, C[i].inner);
+                              b_mn ? 64 : mode == kGateUp || shape == kPair ? kBN / 2 : kBN);
         if (rc != CE_OK) return rc;
     }
-    const void* fn = ffn_fn(dtype, mode, bm);
+    const void* fn = ffn_fn(dtype, mode, shape);
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kTcSmem));
     if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward attributes");
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(end, d.sms));
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    if (shape == kPair) {
+        lc.gridDim = dim3(2u * static_cast<unsigned>(std::min<int64_t>(end, std::max(d.sms / 2, 1))));
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        lc.attrs = &attr;
+        lc.numAttrs = 1;
+    } else {
+        lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(end, d.sms)));
+    }
+    lc.blockDim = dim3(kFfnThreads);
+    lc.dynamicSmemBytes = kTcSmem;
+    lc.stream = st;
     void* args[] = {&maps, &g};
-    e = cudaLaunchKernel(fn, dim3(grid), dim3(kFfnThreads), args, kTcSmem, st);
+    e = cudaLaunchKernelExC(&lc, fn, args);
     return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "feed-forward launch");
 }
 
@@ -728,11 +912,10 @@ struct FfnPacker {
 // 1024, I 4096: 16 / 36, 20 / 37 and 35 / 38.
 constexpr int64_t kFewRows = 256;
 
-// Output matrix i of a launch: through the TMA where it can write it.
-void ffn_output(FfnGemm* g, FfnMatrix (&C)[3], int i, void* p, int64_t rows, int64_t cols) {
-    g->ncols[i] = cols;
-    if (cols % 8 == 0 && aligned(p)) C[i] = FfnMatrix{p, rows, cols};
-    else g->plain[i] = p;
+// Output i of a launch, with rows of `cols` elements.
+void ffn_output(FfnGemm* g, int i, void* p, int64_t cols) {
+    g->out[i] = p;
+    g->odd[i] = cols % 8 == 0 && aligned(p) ? 0 : 1;
 }
 
 // What a packed copy of [rows, cols] takes; 0 where the TMA reads the
@@ -801,8 +984,10 @@ extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w
     up.N[0] = I8;
     up.K = H8;
     up.outs = s ? 3 : 1;
-    rc = ffn_launch(kGateUp, dtype, up, 1, {{x, rows, H8}}, {{w_gate, I, H8}, {w_up, I, H8}},
-                    {{h, rows, I8}, {s, rows, I8}, {a, rows, I8}}, d, st);
+    up.out[0] = h;
+    up.out[1] = s;
+    up.out[2] = a;
+    rc = ffn_launch(kGateUp, dtype, up, 1, {{x, rows, H8}}, {{w_gate, I, H8}, {w_up, I, H8}}, d, st);
     if (rc != CE_OK) return rc;
     FfnGemm down = base;
     down.M[0] = rows;
@@ -810,9 +995,8 @@ extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w
     down.K = I8;
     down.res = residual;
     down.res_vec = O % 8 == 0 && aligned(residual) ? 1 : 0;
-    FfnMatrix C[3] = {};
-    ffn_output(&down, C, 0, y, rows, O);
-    return ffn_launch(kDown, dtype, down, 1, {{h, rows, I8}}, {{w_down, O, I8}}, C, d, st);
+    ffn_output(&down, 0, y, O);
+    return ffn_launch(kDown, dtype, down, 1, {{h, rows, I8}}, {{w_down, O, I8}}, d, st);
 }
 
 extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O, double p) {
@@ -885,8 +1069,9 @@ extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gat
         t.s = s;
         t.a = a;
         t.scale[0] = scale;
-        rc = ffn_launch(kDact, dtype, t, 1, {{dz, rows, O8}}, {{w_down, O, I8}},
-                        {{dg, rows, I8}, {du, rows, I8}}, d, st);
+        t.out[0] = dg;
+        t.out[1] = du;
+        rc = ffn_launch(kDact, dtype, t, 1, {{dz, rows, O8}}, {{w_down, O, I8}}, d, st);
         if (rc != CE_OK) return rc;
     }
     if (dx) {
@@ -895,16 +1080,15 @@ extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gat
         t.N[0] = H;
         t.K = I8;
         t.segs = 2;
-        FfnMatrix C[3] = {};
-        ffn_output(&t, C, 0, dx, rows, H);
+        ffn_output(&t, 0, dx, H);
         rc = ffn_launch(kDx, dtype, t, 1, {{dg, rows, I8}, {du, rows, I8}}, {{w_gate, I, H8}, {w_up, I, H8}},
-                        C, d, st);
+                        d, st);
         if (rc != CE_OK) return rc;
     }
     if (dw_gate || dw_down) {
         FfnGemm t = base;
         t.K = rows;
-        FfnMatrix A[3] = {}, B[3] = {}, C[3] = {};
+        FfnMatrix A[3] = {}, B[3] = {};
         int n = 0;
         // left^T right: [rows, m] and [rows, cols], their rows of m8 and cols8 elements
         const auto add = [&](const void* left, int64_t m, const void* right, int64_t cols, void* out,
@@ -914,7 +1098,7 @@ extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gat
             t.scale[n] = factor;
             A[n] = FfnMatrix{left, rows, up8(m)};
             B[n] = FfnMatrix{right, rows, up8(cols)};
-            ffn_output(&t, C, n, out, m, cols);
+            ffn_output(&t, n, out, cols);
             ++n;
         };
         if (dw_gate) {
@@ -922,7 +1106,7 @@ extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gat
             add(du, I, x, H, dw_up, 1.f);
         }
         if (dw_down) add(dz, O, h, I, dw_down, scale);
-        rc = ffn_launch(kDw, dtype, t, n, A, B, C, d, st);
+        rc = ffn_launch(kDw, dtype, t, n, A, B, d, st);
         if (rc != CE_OK) return rc;
     }
     return CE_OK;
