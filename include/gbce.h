@@ -561,7 +561,8 @@ typedef struct {
  * ce_beam_reorder - dst[b K + j] = src[b K + beams[b, j]] for each of n
  * states (a host array; read before the call returns).
  *
- * beams        [B, K] int64 on the device. A value outside [0, K) (such as
+ * beams        [B, K] int64 on the device, its rows beams_row (at least K)
+ *              elements apart. A value outside [0, K) (such as
  *              the -1 of a place without a candidate) stands for j: that row
  *              keeps its own state.
  * In place, rows that keep their state are neither read nor written. Either
@@ -570,8 +571,8 @@ typedef struct {
  * they were. K at most 32 (CE_ERR_UNSUPPORTED above). Asynchronous on
  * `stream`; uses no library scratch.
  */
-ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* beams, int64_t B,
-                          int64_t K, ce_stream_t stream);
+ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* beams,
+                          int64_t beams_row, int64_t B, int64_t K, ce_stream_t stream);
 
 /*
  * ce_bwd - backward (§Backward Pass: the stored gradient times

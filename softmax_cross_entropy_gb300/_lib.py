@@ -55,7 +55,7 @@ SIGNATURES = {
     "ce_beam_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64, _I64]),
     "ce_beam_select": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,
                             _P]),
-    "ce_beam_reorder": (_I, [ctypes.POINTER(BeamState), _I, _P, _I64, _I64, _P]),
+    "ce_beam_reorder": (_I, [ctypes.POINTER(BeamState), _I, _P, _I64, _I64, _I64, _P]),
     "ce_bwd": (_I, [_P, _I, _P, _I, _I64, _I64, _P]),
     "ce_log_softmax": (_I, [_P, _P, _I, _I64, _I64, _P]),
     "ce_nll_loss_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _I, _U32, _P, _P, _P]),
@@ -228,8 +228,8 @@ def ce_beam_select(logits, dtype, B, K, V, scores, finished, pad_token, M, out_s
                                  stream)
 
 
-def ce_beam_reorder(states, n, beams, B, K, stream):
-    return load().ce_beam_reorder(states, n, beams, B, K, stream)
+def ce_beam_reorder(states, n, beams, beams_row, B, K, stream):
+    return load().ce_beam_reorder(states, n, beams, beams_row, B, K, stream)
 
 
 def ce_device_status(stream):

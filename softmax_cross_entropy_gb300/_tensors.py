@@ -17,8 +17,21 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream as an integer; the plain call builds a Stream object
+# first (some microseconds, as much as the rest of a short call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def stream(device):
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def once(name):
+    """Refuses a backward that is itself to be differentiated."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} is differentiable once: its backward has no graph")
 
 
 def on(device):

@@ -21,7 +21,6 @@ __all__ = ["beam_search_step", "beam_reorder", "BeamCandidates"]
 BeamCandidates = namedtuple("BeamCandidates", ["scores", "beams", "tokens"])
 
 
-@torch.no_grad()
 def beam_search_step(logits, scores, num_candidates=None, finished=None, pad_token=0):
     """The num_candidates (default K, at most 64) best continuations of each
     batch entry: BeamCandidates of scores (float32), beams and tokens (int64),
@@ -92,7 +91,6 @@ def _blocks(t, skip):
     return row, block_stride, blocks, inner
 
 
-@torch.no_grad()
 def beam_reorder(states, beams, inplace=False):
     """states[b, j] = states[b, beams[b, j]] for a tensor or a sequence of
     tensors of beams' states, each [B, K, ...] or [B * K, ...], of any dtype.
@@ -113,7 +111,8 @@ def beam_reorder(states, beams, inplace=False):
     if K < 1:
         raise ValueError("beams must hold at least one beam")
     dev = beams.device
-    beams = beams.contiguous()
+    if beams.stride(1) != 1 or beams.stride(0) < K:
+        beams = beams.contiguous()
     outs = []
     table = (_lib.BeamState * len(states))()
     for t, at in zip(states, table):
@@ -139,6 +138,6 @@ def beam_reorder(states, beams, inplace=False):
             (blocks * inner * b, inner * b)
         at.blocks, at.block_bytes = (blocks, inner * b) if t.numel() else (0, 0)
     with on(dev):
-        check(_lib.ce_beam_reorder(table, len(states), ptr(beams), B, K, stream(dev)),
+        check(_lib.ce_beam_reorder(table, len(states), ptr(beams), beams.stride(0), B, K, stream(dev)),
               "ce_beam_reorder")
     return outs[0] if one else outs

@@ -699,8 +699,8 @@ struct ReorderTensor {
 };
 struct ReorderArgs {
     ReorderTensor t[kReorderTensors];
-    const int64_t* beams;  // [B, K]
-    int64_t B;
+    const int64_t* beams;  // [B, K], rows beams_row apart
+    int64_t beams_row, B;
     int K, inplace;
 };
 
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder(const __grid_con
             const int k = threadIdx.x;
             int f = -1;
             if (k < a.K) {
-                const int64_t s = a.beams[b * a.K + k];
+                const int64_t s = a.beams[b * a.beams_row + k];
                 f = (s >= 0 && s < a.K) ? static_cast<int>(s) : k;  // anything else: stays
                 if (f == k && a.inplace) f = -1;
             }
@@ -857,7 +857,8 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     if (!logits || !scores || !out_scores || !out_beams || !out_tokens) return CE_ERR_INVALID_ARG;
     const uintptr_t b = dtype == CE_F32 ? 4 : 2;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        reinterpret_cast<uintptr_t>(logits) % b)
+        reinterpret_cast<uintptr_t>(logits) % b ||
+        workspace_bytes < static_cast<size_t>(B * K * M * 8))  // (of one part a row)
         return CE_ERR_INVALID_ARG;
     int sms = 0;
     rc = sm_count(&sms);
@@ -904,8 +905,8 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
 }
 
 extern "C" ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* beams,
-                                     int64_t B, int64_t K, ce_stream_t stream) {
-    if (n < 0 || B < 0 || K < 1) return CE_ERR_INVALID_ARG;
+                                     int64_t beams_row, int64_t B, int64_t K, ce_stream_t stream) {
+    if (n < 0 || B < 0 || K < 1 || beams_row < K) return CE_ERR_INVALID_ARG;
     if (K > kMaxBeams) {
         record_message("beam search takes at most 32 beams");
         return CE_ERR_UNSUPPORTED;
@@ -933,6 +934,7 @@ extern "C" ce_status ce_beam_reorder(const ce_beam_state* states, int n, const i
     for (int i = 0; i < n;) {
         ReorderArgs a = {};
         a.beams = beams;
+        a.beams_row = beams_row;
         a.B = B;
         a.K = static_cast<int>(K);
         a.inplace = inplace;

@@ -826,9 +826,8 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
         if (rc != CE_OK) return rc;
     }
     const void* fn = ffn_fn(dtype, mode, shape);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kTcSmem));
-    if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward attributes");
+    const ce_status rc = tc_smem_limit(fn, kTcSmem);
+    if (rc != CE_OK) return rc;
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr;
     if (shape == kPair) {
@@ -846,7 +845,7 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
     lc.dynamicSmemBytes = kTcSmem;
     lc.stream = st;
     void* args[] = {&maps, &g};
-    e = cudaLaunchKernelExC(&lc, fn, args);
+    const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
     return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "feed-forward launch");
 }
 

@@ -367,9 +367,8 @@ ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void*
     if (rc != CE_OK) return rc;
     const void* fn = dtype == CE_BF16 ? (const void*)&ffn_rows<1u> : (const void*)&ffn_rows<0u>;
     const size_t smem = kRowsSmem + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return record_cuda_failure(e, "feed-forward rows attributes");
+    rc = tc_smem_limit(fn, smem);
+    if (rc != CE_OK) return rc;
     void* args[] = {&m0, &m1, &mx, &a};
     return rows_pdl(fn, dim3(static_cast<unsigned>(p.grid)), kRowsThreads, smem, pdl, args, st,
                     "feed-forward rows launch");

@@ -37,7 +37,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <set>
 #include <string>
+#include <tuple>
 #include <type_traits>
 
 #include "ce_kernels.cuh"
@@ -517,6 +519,21 @@ int tile_rows(int64_t M, int64_t N, int sms, bool tmao) {
 }
 
 }  // namespace
+
+ce_status tc_smem_limit(const void* fn, size_t bytes) {
+    static std::mutex mu;
+    static std::set<std::tuple<int, const void*, size_t>> raised;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record_cuda_failure(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(dev, fn, bytes);
+    if (raised.count(key)) return CE_OK;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) return record_cuda_failure(e, "dynamic shared memory limit");
+    raised.insert(key);
+    return CE_OK;
+}
 
 ce_status tc_map_16bit(CUtensorMap* map, const void* p, int dtype, int64_t outer, int64_t inner,
                        uint32_t box_outer) {

@@ -176,6 +176,10 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Raises a kernel's limit of dynamic shared memory to `bytes`, once a device
+// (the current one).
+ce_status tc_smem_limit(const void* fn, size_t bytes);
+
 // A 2-D map of a row-major [outer, inner] matrix of 16-bit elements, boxes of
 // box_outer x 64 elements (128 bytes: the swizzle width), 128-byte swizzle,
 // zeros outside the matrix (ce_gemm_tc.cu). A K-major operand is [MN, K] with

@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, on, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, on, once, ptr, require_cuda, stream
 from .philox_dropout import check_rng
 
 __all__ = ["gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
@@ -24,39 +24,44 @@ _ACTIVATIONS = {"silu": _lib.CE_ACT_SILU, "gelu": _lib.CE_ACT_GELU,
                 "gelu_tanh": _lib.CE_ACT_GELU_TANH}
 
 
+def _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad):
+    """(y, what the backward needs of the block: h and, with grad, u act'(g)
+    and act(g), each [rows, I] in rows of whole 16-byte vectors)."""
+    rows, H = x.shape
+    O, I = w_down.shape
+    dev, dt = x.device, x.dtype
+    y = torch.empty((rows, O), dtype=dt, device=dev)
+    I8 = (I + 7) // 8 * 8
+    kept = torch.empty((3 if grad else 1, rows, I8), dtype=dt, device=dev)
+    h, step = kept.data_ptr(), rows * I8 * 2
+    s, a = (h + step, h + 2 * step) if grad else (None, None)
+    with on(dev):
+        nbytes = _lib.ce_ffn_fwd_workspace_bytes(rows, H, I, O)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        check(_lib.ce_ffn_fwd(ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(residual),
+                              DTYPES[dt], rows, H, I, O, act, p, seed, offset, ptr(state), ptr(y),
+                              h, s, a, ptr(ws), nbytes, stream(dev)), "ce_ffn_fwd")
+    return y, kept
+
+
 class GatedFeedForwardFunction(torch.autograd.Function):
     """Autograd wrapper of ce_ffn_fwd and ce_ffn_bwd on [rows, H] inputs. The
     forward keeps x and three [rows, I] tensors (h, u act'(g) and act(g))."""
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, residual, act, p, seed, offset, state):
-        rows, H = x.shape
-        O, I = w_down.shape
-        dev, dt = x.device, x.dtype
         grad = any(ctx.needs_input_grad[:4])
-        I8 = (I + 7) // 8 * 8
-        y = torch.empty((rows, O), dtype=dt, device=dev)
-        # one allocation for h, s and a (their rows are whole 16-byte vectors)
-        kept = torch.empty((3 if grad else 1, rows, I8), dtype=dt, device=dev)
-        step = rows * I8 * 2
-        h = kept.data_ptr()
-        s, a = (h + step, h + 2 * step) if grad else (None, None)
         if grad and state is not None and p > 0.0:
             state = state.clone()  # the caller may change it before the backward runs
-        nbytes = _lib.ce_ffn_fwd_workspace_bytes(rows, H, I, O)
-        with on(dev):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-            check(_lib.ce_ffn_fwd(ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(residual),
-                                  DTYPES[dt], rows, H, I, O, act, p, seed, offset, ptr(state),
-                                  ptr(y), h, s, a, ptr(ws), nbytes, stream(dev)), "ce_ffn_fwd")
+        y, kept = _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad)
         if grad:
             ctx.save_for_backward(x, w_gate, w_up, w_down, kept, state)
         ctx.args = (act, p, seed, offset)
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        once("gated_feed_forward")
         need = ctx.needs_input_grad
         dx = dwg = dwu = dwd = None
         if any(need[:4]):
@@ -123,9 +128,11 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
     act = _ACTIVATIONS[activation]
     p, seed, offset, state = check_rng(dropout_p, seed, offset, x.device)
     res = None if residual is None else residual.reshape(-1, O).contiguous()
-    return GatedFeedForwardFunction.apply(
-        aligned(x.reshape(-1, H)), aligned(gate_weight), aligned(up_weight), aligned(down_weight),
-        res, act, p, seed, offset, state).reshape(shape)
+    args = (aligned(x.reshape(-1, H)), aligned(gate_weight), aligned(up_weight),
+            aligned(down_weight), res, act, p, seed, offset, state)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args[:5]):
+        return GatedFeedForwardFunction.apply(*args).reshape(shape)
+    return _forward(*args, False)[0].reshape(shape)
 
 
 class GatedFeedForward(torch.nn.Module):

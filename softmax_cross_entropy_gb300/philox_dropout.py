@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, on, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, on, once, ptr, require_cuda, stream
 
 __all__ = ["dropout", "DropoutFunction"]
 
@@ -37,9 +37,10 @@ def check_rng(p, seed, offset, device):
 
 def _call(x, residual, p, seed, offset, state, used):
     y = torch.empty_like(x)
-    with on(x.device):
+    dev = x.device
+    with on(dev):
         check(_lib.ce_dropout(ptr(x), ptr(residual), ptr(y), DTYPES[x.dtype], x.numel(), p, seed,
-                              offset, ptr(state), ptr(used), stream(x.device)), "ce_dropout")
+                              offset, ptr(state), ptr(used), stream(dev)), "ce_dropout")
     return y
 
 
@@ -57,8 +58,8 @@ class DropoutFunction(torch.autograd.Function):
         return _call(x, residual, p, seed, offset, state, used)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        once("dropout")
         dx = None
         if ctx.needs_input_grad[0]:
             p, seed, offset = ctx.rng
@@ -88,4 +89,8 @@ def dropout(x, p, seed, offset=0, residual=None):
             raise ValueError("residual must have the shape, dtype and device of x")
         residual = residual.contiguous()
     p, seed, offset, state = check_rng(p, seed, offset, x.device)
-    return DropoutFunction.apply(x.contiguous(), residual, p, seed, offset, state)
+    x = x.contiguous()
+    if not (torch.is_grad_enabled() and (x.requires_grad or (residual is not None and
+                                                             residual.requires_grad))):
+        return _call(x, residual, p, seed, offset, state, None)
+    return DropoutFunction.apply(x, residual, p, seed, offset, state)

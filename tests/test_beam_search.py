@@ -84,7 +84,7 @@ def test_select_of_no_entries_is_a_no_op():
     assert select(B=0, logits=None, workspace=None) == _lib.CE_OK
 
 
-def reorder(n=1, beams=64, B=2, K=4, **over):
+def reorder(n=1, beams=64, row=None, B=2, K=4, **over):
     from softmax_cross_entropy_gb300 import _lib
     at = (_lib.BeamState * 1)()
     f = dict(src=256, dst=512, src_row=16, src_block=0, dst_row=16, dst_block=0, blocks=1,
@@ -92,11 +92,11 @@ def reorder(n=1, beams=64, B=2, K=4, **over):
     f.update(over)
     for k, v in f.items():
         setattr(at[0], k, v)
-    return _lib.ce_beam_reorder(at if n else None, n, beams, B, K, None)
+    return _lib.ce_beam_reorder(at if n else None, n, beams, K if row is None else row, B, K, None)
 
 
 @pytest.mark.parametrize("over", [
-    dict(n=-1), dict(B=-1), dict(K=0), dict(beams=None), dict(src=None), dict(dst=None),
+    dict(n=-1), dict(B=-1), dict(K=0), dict(row=3), dict(beams=None), dict(src=None), dict(dst=None),
     dict(blocks=-1), dict(block_bytes=-1), dict(dst=256, dst_row=32),
     dict(dst=256, dst_block=8)])
 def test_reorder_refuses(over):
@@ -274,6 +274,16 @@ def test_reorder_of_strided_states(inplace):
     assert torch.equal(cache[:, :, 19:], before[0][:, :, 19:])  # behind the last position
     if not inplace:
         assert torch.equal(cache, before[0]) and torch.equal(heads, before[1])
+
+
+@pytest.mark.gpu
+def test_reorder_by_a_part_of_the_candidates():
+    import softmax_cross_entropy_gb300 as gbce
+    g = torch.Generator(device="cuda").manual_seed(1)
+    every = torch.randint(-1, 4, (5, 8), generator=g, device="cuda")
+    state = torch.randn(20, 6, device="cuda")
+    for beams in (every[:, :4], every[:, 2:6], every.t()[:5, :4], every[:1, :4].expand(5, 4)):
+        assert torch.equal(gbce.beam_reorder(state, beams), plain_reorder(state, beams))
 
 
 @pytest.mark.gpu

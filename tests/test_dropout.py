@@ -106,13 +106,19 @@ def test_shapes_strides_and_empty():
 
 
 @pytest.mark.gpu
-def test_elements_past_32_bits():
+@pytest.mark.parametrize("bits,state", [(32, False), (33, True), (34, False), (34, True)])
+def test_elements_past_32_bits(bits, state):
+    # a launch's last element (2^33), the block counter's low word (2^34)
     import softmax_cross_entropy_gb300 as gbce
-    n = 2 ** 32 + 13
-    y = gbce.dropout(torch.ones(n, dtype=torch.bfloat16, device="cuda"), 0.5, 77)
-    first = 2 ** 32 - 64
-    kept = keep(n - first, 0.5, 77, 0, first)
-    assert np.array_equal(y[first:].float().cpu().numpy(), np.where(kept, 2.0, 0.0))
+    n = 2 ** bits + 13
+    seed = torch.tensor([77, 5], device="cuda") if state else 77
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    y = gbce.dropout(x, 0.5, seed)
+    for first in (2 ** bits - 64, 2 ** (bits - 1) - 32):
+        kept = keep(77, 0.5, 77, 5 if state else 0, first)
+        assert np.array_equal(y[first:first + 77].float().cpu().numpy(), np.where(kept, 2.0, 0.0))
+    del x, y
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.gpu
@@ -178,3 +184,11 @@ def test_wrapper_refuses():
         gbce.dropout(x, 0.5, 1, residual=torch.ones(8, device="cuda", dtype=torch.float16))
     with pytest.raises(TypeError):
         gbce.dropout(x.double(), 0.5, 1)
+
+
+@pytest.mark.gpu
+def test_second_derivatives_are_refused():
+    import softmax_cross_entropy_gb300 as gbce
+    x = torch.ones(8, device="cuda", requires_grad=True)
+    with pytest.raises(RuntimeError, match="once"):
+        torch.autograd.grad(gbce.dropout(x, 0.5, 1).sum(), [x], create_graph=True)
