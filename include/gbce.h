@@ -526,8 +526,8 @@ ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const vo
  *              finite score) has one candidate, pad_token at its own score;
  *              its logits are not read.
  * pad_token    in [0, V).
- * M            candidates a batch entry, 1..64; K at most 32
- *              (CE_ERR_UNSUPPORTED above).
+ * M            candidates a batch entry, 1..64; K at most 32, V and B at most
+ *              2^20 (CE_ERR_UNSUPPORTED above).
  * out_scores, out_beams, out_tokens   [B, M]: candidate (k, v) has the score
  *              scores[k] + logits[k, v] - log sum_j exp(logits[k, j]), formed
  *              in 64 bits and rounded to fp32 for the output; descending,

@@ -4,18 +4,19 @@
 //
 // Selection. With lse_k = log sum_v exp(x_kv), candidate (k, v) has the score
 // s_k + x_kv - lse_k, so within a beam the order is that of the logits:
-//  1. beam_scan reads every logit once. A row is split over CTAs and their
-//     warps; a lane keeps a running maximum and sum of the softmax, a warp
-//     its M best logits in a sorted list over its lanes. A logit that can
-//     still matter goes to a buffer in shared memory; 32 of them are sorted
-//     and merged into the list by a bitonic network. What can matter is
-//     bounded from the lanes' largest logits: with m = ceil(M / 8), each of
-//     the 8 warps has m lanes whose largest is at least the warp's m-th
-//     largest of those, so M logits of the CTA are at least the smallest of
-//     the 8 values. Formed after 1, 2, 4, ... blocks, it lets some 40
-//     logits of each doubling pass, where a list that starts empty would
-//     merge the first blocks whole. A CTA ranks what its warps hold by
-//     counting and writes M candidates and {max, sum}.
+//  1. beam_scan reads every logit once, in parts of a row of up to 40 KB that
+//     a CTA stages in shared memory (cp.async; four CTAs an SM, so that parts
+//     are on their way while others are worked on) and passes over twice.
+//     The first pass takes each thread's largest logit. From these come the
+//     part's maximum and a bound that M logits reach: for M up to 16 the M-th
+//     best of the 8 warps' 4 largest, else the smallest of the 8 warps'
+//     ceil(M / 8)-th largest (a thread counts once). The second pass
+//     sums exp(x - maximum) (one FFMA and one exp2 a logit) and lists the
+//     logits that reach the bound, about M of them, which are ranked by
+//     counting. The part's M best and {maximum, sum} go to the workspace.
+//     Where more logits reach the bound than the list holds (equal ones), the
+//     warps merge the part's logits into sorted lists instead, 32 at a time
+//     by a bitonic network.
 //  2. beam_pick, a CTA a batch entry, forms the K log-sum-exps from the
 //     {max, sum} in a fixed order, takes the M-th best of the lists' first
 //     candidates as a bound (no list that starts below it can contribute),
@@ -26,6 +27,7 @@
 // Bound by HBM: one read of the logits.
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <string>
 
 #include "ce_kernels.cuh"
@@ -34,18 +36,21 @@
 namespace gbce {
 ce_status record_cuda_failure(cudaError_t e, const char* what);
 void record_message(const std::string& msg);
+ce_status tc_smem_limit(const void* fn, size_t bytes);
 
 namespace {
 
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanCtas = 3;    // CTAs an SM
-constexpr int kScanVec = 4;     // 16-byte vectors a lane holds at a time
-constexpr int kScanBuf = 128;   // words of a warp's buffer (fewer than 32 at the start of a block)
+constexpr int kScanCtas = 4;        // CTAs an SM
+constexpr int kScanMost = 2560;     // 16-byte vectors of a part at most
+constexpr int kScanList = 512;      // logits of a part that may reach the bound
+constexpr int kScanBuf = 64;        // words of a warp's buffer when merging
 constexpr int kPickThreads = 256;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxCandidates = 64;
-constexpr int kMaxSplits = 64;  // CTAs a row
+constexpr int kMaxSplits = 128;     // parts a row
+constexpr int64_t kMaxVocab = 1 << 20;  // 103 parts of fp32
 constexpr float kLowest = -3.402823466e38f;
 
 // A candidate inside a row: the logit as an ordered integer above the
@@ -63,7 +68,7 @@ __device__ __forceinline__ uint64_t candidate(float x, int token) {
 }
 
 struct RowSum {  // of one split of a row
-    float m;     // maximum (kLowest with no token)
+    float m;     // maximum (-inf with no token)
     float s;     // sum of exp(x - m)
 };
 
@@ -76,6 +81,7 @@ struct BeamArgs {
     int K, M;
     int splits;        // parts of a row, the same of every row
     int part_vec;      // 16-byte vectors of a part
+    int row_step, part_step;  // a CTA's step of gridDim parts: rows and parts
     int64_t pad;
     RowSum* sums;        // [rows, splits]
     uint64_t* lists;     // [rows, splits, M]
@@ -95,12 +101,13 @@ __device__ __forceinline__ bool beam_lives(const BeamArgs& a, int64_t row) {
 }
 
 // Sorts a word a lane in descending order over the warp.
-__device__ __forceinline__ uint64_t warp_sort_desc(uint64_t v, int lane) {
+template <typename U>
+__device__ __forceinline__ U warp_sort_desc(U v, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
         for (int d = size >> 1; d > 0; d >>= 1) {
-            const uint64_t o = __shfl_xor_sync(~0u, v, d);
+            const U o = __shfl_xor_sync(~0u, v, d);
             const bool up = (lane & d) == 0;
             const bool desc = (lane & size) == 0 || size == 32;
             v = ((v > o) == (up == desc)) ? v : o;
@@ -117,7 +124,7 @@ struct WarpBest {
     uint64_t* buf;  // kScanBuf words of shared memory of this warp
     int count;
     uint64_t last;  // a candidate must lie above this to matter,
-    float bar;      // a logit above this: of last, or just below the bound
+    float bar;      // and this is its logit
     int lane, M;
 
     __device__ __forceinline__ void init(uint64_t* b, int l, int m) {
@@ -129,15 +136,6 @@ struct WarpBest {
         last = candidate(bar, 0);  // -inf is never a candidate
         lane = l;
         M = m;
-    }
-
-    // At least M logits of the CTA are `least` or more.
-    __device__ __forceinline__ void bound(float least) {
-        if (least > -INFINITY && (static_cast<uint64_t>(ordered(least)) << 32) - 1u > last) {
-            last = (static_cast<uint64_t>(ordered(least)) << 32) - 1u;
-            // the next value below it (below +0 that is not -0)
-            bar = least == 0.f ? -__uint_as_float(1u) : unordered(static_cast<uint32_t>(last >> 32));
-        }
     }
 
     // Merges up to 32 buffered words (0 on the lanes behind the last).
@@ -200,330 +198,284 @@ __device__ __forceinline__ uint32_t neg_inf_word<__nv_bfloat16>() { return 0xFF8
 template <>
 __device__ __forceinline__ uint32_t neg_inf_word<__half>() { return 0xFC00FC00u; }
 
-// A part of a row: vectors [j0, j1) of a warp, vector j being the elements
-// N j .. N j + N - 1 wherever the row starts in memory, so that equal rows
-// are summed alike (and equal beams tie exactly).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A part of a row: its 16-byte vectors [j0, j0 + len), vector j being the
+// elements N j .. N j + N - 1 wherever the row starts in memory, so that equal
+// rows are summed alike (and equal beams tie exactly).
 template <typename T>
 struct RowPart {
+    static constexpr int N = Vec<T>::N;
     const T* row;
-    int V, j0, j1;
-    int in0, in1;  // the vectors in [in0, in1) are loaded whole
-    int shift;     // bytes from the 16-byte boundary before the row to the row
-    bool live;
+    int V, j0, len;
+    int shift;  // bytes from the 16-byte boundary before the row to the row
 
-    // vector j by element, with -inf outside the row and the part
-    __device__ __forceinline__ uint4 edge(int j) const {
-        constexpr int N = Vec<T>::N;
+    // Copies the part's aligned vectors (one more where the row is not
+    // aligned) to shared memory; elements outside the row become -inf.
+    __device__ __forceinline__ void fetch(uint4* stage) const {
+        const int64_t bytes = static_cast<int64_t>(V) * sizeof(T) + shift;  // to the row's end
+        const int n = len + (shift ? 1 : 0);
+        const int lo = shift && j0 == 0 ? 1 : 0;  // vectors [lo, hi) lie in the row
+        const int hi = min(n, static_cast<int>(bytes / 16) - j0);
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) - shift) + j0;
+        uint32_t dst = smem_u32(stage + lo + threadIdx.x);
+        src += lo + threadIdx.x;
+#pragma unroll 4
+        for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += kScanThreads) {
+            cp_async16(dst, src);
+            dst += 16 * kScanThreads;
+            src += kScanThreads;
+        }
+        if (static_cast<int>(threadIdx.x) < lo) stage[threadIdx.x] = edge(j0);
+        for (int i = max(hi, lo) + static_cast<int>(threadIdx.x); i < n; i += kScanThreads) stage[i] = edge(j0 + i);
+    }
+    // aligned vector w, of which only some elements lie in the row
+    __device__ __forceinline__ uint4 edge(int w) const {
         const uint32_t none = neg_inf_word<T>();
-        uint32_t w[4] = {none, none, none, none};
-        if (j < j1) {
-            const int e = j * N;
+        uint32_t v[4] = {none, none, none, none};
+        const int64_t e0 = static_cast<int64_t>(w) * N - shift / static_cast<int>(sizeof(T));
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (e + i >= V) continue;
-                if constexpr (sizeof(T) == 4) {
-                    w[i] = reinterpret_cast<const uint32_t*>(row)[e + i];
-                } else {
-                    const uint32_t h = reinterpret_cast<const uint16_t*>(row)[e + i];
-                    w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | (h << 16) : (w[i / 2] & 0xFFFF0000u) | h;
-                }
+        for (int i = 0; i < N; ++i) {
+            const int64_t e = e0 + i;
+            if (e < 0 || e >= V) continue;
+            if constexpr (sizeof(T) == 4) {
+                v[i] = reinterpret_cast<const uint32_t*>(row)[e];
+            } else {
+                const uint32_t h = reinterpret_cast<const uint16_t*>(row)[e];
+                v[i / 2] = (i & 1) ? (v[i / 2] & 0xFFFFu) | (h << 16) : (v[i / 2] & 0xFFFF0000u) | h;
             }
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(v[0], v[1], v[2], v[3]);
     }
-
-    // vector j of a row that is not 16-byte aligned, from the two aligned
-    // vectors that it lies in (both inside the row)
-    __device__ __forceinline__ uint4 apart(int j) const {
-        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) - shift) + j;
-        const uint4 a = p[0], b = p[1];
+    // vector j0 + i, from the staged aligned ones that it lies in (FLAT: of a
+    // row that is aligned)
+    template <bool FLAT>
+    __device__ __forceinline__ uint4 get(const uint4* stage, int i) const {
+        const uint4 a = stage[i];
+        if constexpr (FLAT) return a;
+        const uint4 b = stage[i + 1];
         uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = (shift & 8) ? w[i + 2] : w[i];
+        for (int k = 0; k < 6; ++k) w[k] = (shift & 8) ? w[k + 2] : w[k];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = (shift & 4) ? w[i + 1] : w[i];
+        for (int k = 0; k < 5; ++k) w[k] = (shift & 4) ? w[k + 1] : w[k];
         const int bits = 8 * (shift & 3);
         return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                           __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
     }
-
-    // this lane's vectors j + lane, j + 32 + lane, ...
-    template <int NV>
-    __device__ __forceinline__ void load(int j, uint4 (&v)[NV]) const {
-        const int lane = threadIdx.x & 31;
-        if (j >= in0 && j + 32 * NV <= in1) {
-            if (shift) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k) v[k] = apart(j + 32 * k + lane);
-            } else {
-                const uint4* p = reinterpret_cast<const uint4*>(row) + (j + lane);
-#pragma unroll
-                for (int k = 0; k < NV; ++k) v[k] = __ldcs(p + 32 * k);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) v[k] = edge(j + 32 * k + lane);
-        }
-    }
 };
 
-// A lane's part of a log-sum-exp: sum of exp2(log2e x - c) with c = log2e m
-// rounded to fp32, m the running maximum: one FFMA and one exp2 a logit. The
-// rounding of c is taken back when the sum is brought to another maximum.
-// Logits of a size at which c overflows (kHuge) do not raise m: below it
-// they add 0, as they should next to any other logit, and a warp that has no
-// other, or one above it, sums again by sum_apart.
+template <int E>
+struct ScanShared {
+    uint64_t list[kScanWarps * (32 * E + 32) > kScanList ? kScanWarps * (32 * E + 32) : kScanList];
+    uint64_t buf[kScanWarps][kScanBuf];
+    uint64_t lasts[kScanWarps];
+    uint32_t tops[kScanWarps * 8];  // the warps' t largest threads, as ordered integers
+    float sums[kScanWarps];
+    int found;
+};
+
+// The first pass: this thread's largest logit of the part.
+template <bool FLAT, typename T>
+__device__ __forceinline__ float part_max(const RowPart<T>& part, const uint4* stage) {
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < part.len; i += kScanThreads)
+        m = fmaxf(m, Vec<T>::vmax(part.template get<FLAT>(stage, i)));
+    return m;
+}
+
+// log2 e m overflows from here on: such parts take part_sum.
 constexpr float kHuge = 2e38f;
-struct LaneSum {
-    float m, c, s;
 
-    __device__ __forceinline__ void raise(float to) {
-        if (to > m && to > -kHuge) {
-            const float nc = to * kLog2e;
-            s *= ex2(c - nc);
-            m = to;
-            c = nc;
+// The second pass: the thread's share of the sum of exp(x - m), and its
+// logits from `bar` on into the list (what does not fit is counted only).
+template <bool FLAT, typename T, int E>
+__device__ __forceinline__ float part_scan(const RowPart<T>& part, const uint4* stage, float m,
+                                           float bar, ScanShared<E>& sh) {
+    constexpr int N = Vec<T>::N;
+    const float c = m * kLog2e;
+    const float2 scale = make_float2(kLog2e, kLog2e), minus = make_float2(-c, -c);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < part.len; i += kScanThreads) {
+        const uint4 v = part.template get<FLAT>(stage, i);
+        float f[N];
+        Vec<T>::unpack(v, f);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const float2 e = ffma2(make_float2(f[k], f[k + 1]), scale, minus);
+            s = fadd2(s, make_float2(ex2(e.x), ex2(e.y)));
+        }
+        if (Vec<T>::vmax(v) >= bar) {  // few
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (f[k] >= bar && f[k] > -INFINITY) {
+                    const int to = atomicAdd(&sh.found, 1);
+                    if (to < kScanList) sh.list[to] = candidate(f[k], (part.j0 + i) * N + k);
+                }
+            }
         }
     }
-    template <int N>
-    __device__ __forceinline__ void add(const float (&f)[N]) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < N; ++i) p[i & 3] += ex2(fmaf(f[i], kLog2e, -c));
-        s += (p[0] + p[1]) + (p[2] + p[3]);
-    }
-    // the sum relative to a maximum `to` that is finite
-    __device__ __forceinline__ float relative(float to) const { return s * ex2(-fmaf(to, kLog2e, -c)); }
-};
+    // the rounding of c is taken back
+    return (s.x + s.y) * ex2(-fmaf(m, kLog2e, -c));
+}
 
-// A lane's sum of exp(x - m) over its vectors of a part, without NaN logits
-// and for any finite m.
+// The sum alone, without NaN logits and for any finite m.
 template <typename T>
-__device__ __noinline__ float sum_apart(const RowPart<T>& part, float m) {
+__device__ __noinline__ float part_sum(const RowPart<T>& part, const uint4* stage, float m) {
     float s = 0.f;
-    for (int j = part.j0; j < part.j1; j += 32) {
-        uint4 v[1];
-        part.load(j, v);
+    for (int i = threadIdx.x; i < part.len; i += kScanThreads) {
         float f[Vec<T>::N];
-        Vec<T>::unpack(v[0], f);
+        Vec<T>::unpack(part.template get<false>(stage, i), f);
 #pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) s += ex2((fmaxf(f[i], -INFINITY) - m) * kLog2e);
+        for (int k = 0; k < Vec<T>::N; ++k) s += ex2((fmaxf(f[k], -INFINITY) - m) * kLog2e);
     }
     return s;
 }
 
-// Part `item` mod splits of row item / splits, as this warp takes it.
-template <typename T>
-__device__ __forceinline__ RowPart<T> row_part(const BeamArgs& a, int64_t item) {
-    constexpr int N = Vec<T>::N;
-    RowPart<T> p;
-    p.V = static_cast<int>(a.V);
-    p.live = item < a.rows * a.splits;
-    const int64_t r = p.live ? item / a.splits : 0;
-    const int off = static_cast<int>(item - r * a.splits) * a.part_vec;
-    p.row = static_cast<const T*>(a.logits) + r * a.V;
-    p.shift = static_cast<int>(reinterpret_cast<uintptr_t>(p.row) & 15u);
-    const int nv = (p.V - 1) / N + 1;
-    const int end = min(off + a.part_vec, nv);
-    const int per = (a.part_vec + kScanWarps - 1) / kScanWarps;
-    p.j0 = off + static_cast<int>(threadIdx.x >> 5) * per;
-    p.j1 = min(p.j0 + per, end);
-    // an unaligned vector j lies in the aligned ones j and j + 1
-    p.in0 = p.shift ? 1 : 0;
-    const int whole = p.shift ? static_cast<int>((a.V * static_cast<int64_t>(sizeof(T)) + p.shift) / 16) - 1
-                              : p.V / N;
-    p.in1 = min(whole, p.j1);
-    if (p.live) p.live = beam_lives(a, r);
-    return p;
-}
-
-template <int E>
-struct ScanShared {
-    uint64_t buf[kScanWarps][kScanBuf];
-    int count[kScanWarps];  // words in buf
-    uint64_t lists[kScanWarps * (32 * E + 32)];
-    uint64_t lasts[kScanWarps];
-    RowSum sums[kScanWarps];
-    float least[kScanWarps];
-    int found;
-};
-
-// One part of a row. `next` holds its first block on entry, and that of
-// `after` on return.
+// The part's best by merging, where the list overflows: each warp merges its
+// own run of vectors. Leaves all that can be among the M best in sh.list.
 template <typename T, int E>
-__device__ __forceinline__ void scan_part(const BeamArgs& a, const RowPart<T>& part,
-                                          const RowPart<T>& after, int64_t item,
-                                          uint4 (&v)[kScanVec], uint4 (&next)[kScanVec],
-                                          ScanShared<E>& sh) {
-    using VT = Vec<T>;
-    constexpr int N = VT::N;
+__device__ __noinline__ void scan_merge(const RowPart<T>& part, const uint4* stage, int M,
+                                        ScanShared<E>& sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();  // the shared arrays have been read by the part before
-    if (lane == 0) sh.count[warp] = 0;  // (block 1 synchronises)
     WarpBest<E> top;
-    top.init(sh.buf[warp], lane, a.M);
-    LaneSum sum{-INFINITY, kLowest, 0.f};
-    float lm = -INFINITY;  // the lane's maximum
-    unsigned block = 1;
-    for (int j = part.j0; block == 1 || j < part.j1; j += 32 * kScanVec, ++block) {
-#pragma unroll
-        for (int k = 0; k < kScanVec; ++k) v[k] = next[k];
-        if (j + 32 * kScanVec < part.j1) part.load(j + 32 * kScanVec, next);
-        else if (after.live) after.load(after.j0, next);
-        float vm[kScanVec];
-#pragma unroll
-        for (int k = 0; k < kScanVec; ++k) vm[k] = VT::vmax(v[k]);
-        const float bm = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
-        static_assert(kScanVec == 4, "four vectors a lane");
-        lm = fmaxf(lm, bm);
-        if ((block & (block - 1)) == 0) {
-            // the m-th largest of the lanes' largest so far
-            uint32_t mine = lm > -INFINITY ? ordered(lm) : 0u;
-            uint32_t best = 0;
-            for (int i = 0; i < (a.M + kScanWarps - 1) / kScanWarps; ++i) {
-                best = __reduce_max_sync(~0u, mine);
-                if (__ffs(__ballot_sync(~0u, mine == best)) - 1 == lane) mine = 0u;
-            }
-            volatile float* known = sh.least;
-            if (lane == 0) known[warp] = best ? unordered(best) : -INFINITY;
-            // every warp's first value; later ones only rise, so that an
-            // older one is a bound as well
-            if (block == 1) __syncthreads();
-            else __syncwarp();
-            float l = known[0];
-#pragma unroll
-            for (int w = 1; w < kScanWarps; ++w) l = fminf(l, known[w]);
-            top.bound(l);
-        }
-        sum.raise(bm);
-#pragma unroll
-        for (int k = 0; k < kScanVec; ++k) {
-            float f[N];
-            VT::unpack(v[k], f);
-            sum.add(f);
-        }
-        // tokens of later blocks are larger: an equal logit does not matter
-        if (__any_sync(~0u, bm > top.bar)) {
-#pragma unroll
-            for (int k = 0; k < kScanVec; ++k) {
-                if (vm[k] > top.bar) {  // few lanes
-                    float f[N];
-                    VT::unpack(v[k], f);
-                    const int t0 = (j + 32 * k + lane) * N;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        if (f[i] > top.bar) {
-                            const int to = atomicAdd(&sh.count[warp], 1);
-                            if (to < kScanBuf) sh.buf[warp][to] = candidate(f[i], t0 + i);
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-            const int before = top.count;
-            top.count = sh.count[warp];
-            if (top.count > kScanBuf) {
-                // more than the buffer holds (equal or ascending logits): the
-                // block once more, a logit a lane at a time
-                top.count = before;
+    top.init(sh.buf[warp], lane, M);
+    const int per = (part.len + kScanWarps - 1) / kScanWarps;
+    const int i1 = min(part.len, (warp + 1) * per);
 #pragma unroll 1
-                for (int k = 0; k < kScanVec; ++k) {
-                    const uint4 again = part.edge(j + 32 * k + lane);
-                    float f[N];
-                    VT::unpack(again, f);
-#pragma unroll 1
-                    for (int i = 0; i < N; ++i) {
-                        float x = f[0];
+    for (int i = warp * per; i < i1; i += 32) {
+        float f[Vec<T>::N];
 #pragma unroll
-                        for (int q = 1; q < N; ++q) x = q == i ? f[q] : x;
-                        top.offer(x, (j + 32 * k + lane) * N + i);
-                    }
-                }
-            }
-            top.drain();
-            if (lane == 0) sh.count[warp] = top.count;
-            __syncwarp();
-        }
+        for (int k = 0; k < Vec<T>::N; ++k) f[k] = -INFINITY;
+        if (i + lane < i1) Vec<T>::unpack(part.template get<false>(stage, i + lane), f);
+#pragma unroll
+        for (int k = 0; k < Vec<T>::N; ++k) top.offer(f[k], (part.j0 + i + lane) * Vec<T>::N + k);
     }
-    // the warp's sum, then the CTA's list and sum
-    float wm = lm;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) wm = fmaxf(wm, __shfl_xor_sync(~0u, wm, d));
-    float ws = 0.f;
-    if (wm == INFINITY) {
-        ws = wm;  // no log-sum-exp
-    } else if (wm > -INFINITY) {
-        // a NaN in a sum comes from a NaN logit, which counts as masked
-        if (__any_sync(~0u, isnan(sum.s)) || fabsf(wm) >= kHuge)
-            ws = sum_apart<T>(part, wm);
-        else
-            ws = sum.relative(wm);
-    }
-    wm = fmaxf(wm, kLowest);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ws += __shfl_xor_sync(~0u, ws, d);
-    if (lane == 0) sh.sums[warp] = RowSum{wm, ws};
     if (lane == 0) sh.lasts[warp] = top.last;
+    __syncthreads();  // every thread has read the overflowed count
     if (threadIdx.x == 0) sh.found = 0;
     __syncthreads();
-    if (warp == 0) {
-        RowSum t = lane < kScanWarps ? sh.sums[lane] : RowSum{kLowest, 0.f};
-        float tm = t.m;
-#pragma unroll
-        for (int d = kScanWarps / 2; d > 0; d >>= 1) tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, d));
-        float ts = t.s * ex2((t.m - tm) * kLog2e);
-#pragma unroll
-        for (int d = kScanWarps / 2; d > 0; d >>= 1) ts += __shfl_xor_sync(~0u, ts, d);
-        if (lane == 0) a.sums[item] = RowSum{tm, ts};
-    }
-    // The warps' lists and buffers as one: of what they hold, only words from
-    // the highest `last` on can be among the M best (M words of that warp, or
-    // of the CTA, are), so that about 2 M are ranked.
+    // of what the warps hold only words from the highest `last` on can be
+    // among the M best: M words of that warp are
     uint64_t bar = sh.lasts[0];
 #pragma unroll
     for (int w = 1; w < kScanWarps; ++w) bar = sh.lasts[w] > bar ? sh.lasts[w] : bar;
-    __syncwarp();
 #pragma unroll
     for (int e = 0; e <= E; ++e) {
-        const uint64_t w = e < E ? (32 * e + lane < a.M ? top.best[e < E ? e : 0] : 0)
+        const uint64_t w = e < E ? (32 * e + lane < M ? top.best[e < E ? e : 0] : 0)
                                  : (lane < top.count ? sh.buf[warp][lane] : 0);
         const unsigned who = __ballot_sync(~0u, w >= bar);
         int to = 0;
         if (lane == 0 && who) to = atomicAdd(&sh.found, __popc(who));
         to = __shfl_sync(~0u, to, 0);
-        if (w >= bar) sh.lists[to + __popc(who & ((1u << lane) - 1u))] = w;
+        if (w >= bar) sh.list[to + __popc(who & ((1u << lane) - 1u))] = w;
     }
     __syncthreads();
-    uint64_t* out = a.lists + item * a.M;
-    const int n = sh.found;
-    for (int i = threadIdx.x; i < n; i += kScanThreads) {
-        const uint64_t w = sh.lists[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < n; ++o) rank += sh.lists[o] > w;
-        if (rank < a.M) out[rank] = w;
-    }
-    // no candidate in the places behind the last
-    for (int i = n + threadIdx.x; i < a.M; i += kScanThreads) out[i] = 0;
 }
 
 template <typename T, int E>
 __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan(const __grid_constant__ BeamArgs a) {
+    using VT = Vec<T>;
+    constexpr int N = VT::N;
+    extern __shared__ uint4 scan_stage[];  // kScanMost + 1 vectors
     __shared__ ScanShared<E> sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
-    const int64_t items = a.rows * a.splits;
-    uint4 v[kScanVec], next[kScanVec];
-    RowPart<T> part = row_part<T>(a, blockIdx.x);
-    if (part.live) part.load(part.j0, next);
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        // the next part's first block is loaded before this one's end is worked off
-        const RowPart<T> after = row_part<T>(a, item + gridDim.x);
-        if (part.live) {
-            scan_part<T, E>(a, part, after, item, v, next, sh);
-        } else if (after.live) {
-            after.load(after.j0, next);
+    const int nv = (static_cast<int>(a.V) - 1) / N + 1;
+    // the parts of this CTA, in steps of the grid; those of dead beams are
+    // passed over
+    int64_t row = blockIdx.x / static_cast<unsigned>(a.splits);
+    int piece = blockIdx.x % static_cast<unsigned>(a.splits);
+    const auto step = [&] {
+        row += a.row_step;
+        piece += a.part_step;
+        if (piece >= a.splits) {
+            piece -= a.splits;
+            ++row;
         }
-        part = after;
+    };
+    const auto here = [&] {
+        RowPart<T> p;
+        p.row = static_cast<const T*>(a.logits) + row * a.V;
+        p.V = static_cast<int>(a.V);
+        p.j0 = piece * a.part_vec;
+        p.len = min(a.part_vec, nv - p.j0);
+        p.shift = static_cast<int>(reinterpret_cast<uintptr_t>(p.row) & 15u);
+        return p;
+    };
+    while (row < a.rows && !beam_lives(a, row)) step();
+    if (row < a.rows) here().fetch(scan_stage);
+    while (row < a.rows) {
+        const RowPart<T> part = here();
+        const bool flat = part.shift == 0;
+        const int64_t item = row * a.splits + piece;
+        do step();
+        while (row < a.rows && !beam_lives(a, row));
+        cp_async_wait();
+        __syncthreads();  // the part is staged, and the last one's list read
+        // ---- each thread's largest logit, and the warps' t largest of those
+        const float lm = flat ? part_max<true>(part, scan_stage) : part_max<false>(part, scan_stage);
+        const bool small = a.M <= 16;
+        const int t = small ? 4 : (a.M + kScanWarps - 1) / kScanWarps;
+        uint32_t mine = lm > -INFINITY ? ordered(lm) : 0u;
+        for (int i = 0; i < t; ++i) {
+            const uint32_t best = __reduce_max_sync(~0u, mine);
+            if (__ffs(__ballot_sync(~0u, mine == best)) - 1 == lane) mine = 0u;
+            if (lane == 0) sh.tops[warp * t + i] = best;
+        }
+        if (threadIdx.x == 0) sh.found = 0;
+        __syncthreads();
+        // ---- the maximum, and the bound (0: too few threads have a logit)
+        uint32_t top, bound;
+        if (small) {  // M of the 8 t = 32 values, sorted over the lanes
+            const uint32_t o = warp_sort_desc(sh.tops[lane], lane);
+            top = __shfl_sync(~0u, o, 0);
+            bound = __shfl_sync(~0u, o, a.M - 1);
+        } else {  // every warp has t such threads
+            top = __reduce_max_sync(~0u, lane < kScanWarps ? sh.tops[lane * t] : 0u);
+            bound = __reduce_min_sync(~0u, lane < kScanWarps ? sh.tops[lane * t + t - 1] : ~0u);
+        }
+        const float m = top ? unordered(top) : -INFINITY;
+        // (below +0 that is not -0: equal values)
+        const float bar = !bound ? -INFINITY : unordered(bound);
+        // ---- the sum, and the logits that reach the bound
+        float s = flat ? part_scan<true>(part, scan_stage, m, bar, sh)
+                       : part_scan<false>(part, scan_stage, m, bar, sh);
+        // a NaN in the sum comes from a NaN logit, which counts as masked
+        const bool usual = fabsf(m) < kHuge;
+        if (!usual) s = 0.f;
+        if (__syncthreads_or(isnan(s) || (!usual && fabsf(m) < INFINITY)))
+            s = part_sum<T>(part, scan_stage, m);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+        if (lane == 0) sh.sums[warp] = s;
+        if (sh.found > kScanList) scan_merge<T, E>(part, scan_stage, a.M, sh);
+        __syncthreads();  // the stage is free, the list and sums are whole
+        if (row < a.rows) here().fetch(scan_stage);
+        if (threadIdx.x == 0) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kScanWarps; ++w) sum += sh.sums[w];
+            a.sums[item] = RowSum{m, m == INFINITY ? INFINITY : sum};
+        }
+        uint64_t* out = a.lists + item * a.M;
+        const int n = sh.found;
+        for (int i = threadIdx.x; i < n; i += kScanThreads) {
+            const uint64_t w = sh.list[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int o = 0; o < n; ++o) rank += sh.list[o] > w;
+            if (rank < a.M) out[rank] = w;
+        }
+        // no candidate in the places behind the last
+        for (int i = n + threadIdx.x; i < a.M; i += kScanThreads) out[i] = 0;
     }
 }
 
@@ -597,16 +549,16 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
         const float score = a.scores[row];
         const bool done = a.finished && a.finished[row];
         // (a beam that was not scanned has left its sums as they were: not used)
-        RowSum t{kLowest, 0.f};
-        if (lane < a.splits) t = a.sums[row * a.splits + lane];
-        RowSum u{kLowest, 0.f};
-        if (lane + 32 < a.splits) u = a.sums[row * a.splits + 32 + lane];
-        static_assert(kMaxSplits <= 64, "two parts a lane");
-        float m = fmaxf(t.m, u.m);
+        const RowSum* sums = a.sums + row * a.splits;
+        float m = kLowest;
+        for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, sums[i].m);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        double s = static_cast<double>(t.s * exp2f((t.m - m) * kLog2e)) +
-                   static_cast<double>(u.s * exp2f((u.m - m) * kLog2e));
+        double s = 0.0;
+        for (int i = lane; i < a.splits; i += 32) {
+            const RowSum t = sums[i];  // (exp2(-inf) = 0 for a part with no token)
+            s += static_cast<double>(t.s * exp2f((t.m - m) * kLog2e));
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
         if (lane == 0) {
@@ -769,8 +721,8 @@ ce_status sm_count(int* sms) {
 
 // How the rows are dealt out: `splits` parts a row, all parts over one wave
 // of CTAs (kScanCtas an SM) in turn. A part costs its bytes and about as
-// much as another 24 KB (the first bound, the joining of the warps' lists);
-// the CTAs take ceil(parts / CTAs) parts each.
+// much as another 16 KB (the bound, the ranking); the CTAs take ceil(parts /
+// CTAs) parts each.
 constexpr int64_t kScanMin = 512;  // vectors of a part at least: 8 KB
 struct ScanPlan {
     int64_t part_vec, grid;
@@ -780,12 +732,15 @@ ScanPlan scan_plan(int64_t rows, int64_t V, int dtype, int sms) {
     const int64_t N = dtype == CE_F32 ? 4 : 8;
     const int64_t nv = (V + N - 1) / N;
     const int64_t ctas = int64_t{kScanCtas} * std::max(sms, 1);
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, nv / kScanMin));
+    const int64_t least = (nv + kScanMost - 1) / kScanMost;
+    const int64_t most = std::max(least, std::min<int64_t>(kMaxSplits, nv / kScanMin));
     ScanPlan p{nv, 0, 1};
     int64_t best = INT64_MAX;
-    for (int64_t s = 1; s <= most; ++s) {
+    const char* env = std::getenv("GBCE_BEAM_SPLITS");
+    for (int64_t s = least; s <= most; ++s) {
+        if (env && s != std::max(least, std::min<int64_t>(std::atoi(env), most))) continue;
         const int64_t vec = (nv + s - 1) / s;
-        const int64_t cost = (rows * s + ctas - 1) / ctas * (vec + 1536);
+        const int64_t cost = (rows * s + ctas - 1) / ctas * (vec + 1024);
         if (cost < best) {
             best = cost;
             p.part_vec = vec;
@@ -806,9 +761,9 @@ const void* scan_fn(int dtype) {
 ce_status check_beam(int dtype, int64_t B, int64_t K, int64_t V, int64_t M) {
     if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_ERR_INVALID_ARG;
     if (B < 0 || K < 1 || V < 1 || M < 1) return CE_ERR_INVALID_ARG;
-    if (K > kMaxBeams || M > kMaxCandidates || V > INT32_MAX - 64 || B > INT32_MAX / (kMaxBeams * kMaxSplits)) {
+    if (K > kMaxBeams || M > kMaxCandidates || V > kMaxVocab || B > kMaxVocab) {
         record_message("beam search takes at most 32 beams, 64 candidates, 2^20 batch entries "
-                       "and a vocabulary below 2^31 - 64");
+                       "and 2^20 tokens");
         return CE_ERR_UNSUPPORTED;
     }
     return CE_OK;
@@ -878,6 +833,8 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     a.M = static_cast<int>(M);
     a.splits = plan.splits;
     a.part_vec = static_cast<int>(plan.part_vec);
+    a.row_step = static_cast<int>(plan.grid / plan.splits);
+    a.part_step = static_cast<int>(plan.grid % plan.splits);
     a.pad = pad_token;
     a.sums = static_cast<RowSum*>(workspace);
     a.lists = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + sums_bytes);
@@ -886,9 +843,11 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     a.out_tokens = out_tokens;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* args[] = {&a};
-    cudaError_t e = cudaLaunchKernel(M <= 32 ? scan_fn<1>(dtype) : scan_fn<2>(dtype),
-                                     dim3(static_cast<unsigned>(plan.grid)),
-                                     dim3(kScanThreads), args, 0, st);
+    const void* scan = M <= 32 ? scan_fn<1>(dtype) : scan_fn<2>(dtype);
+    rc = tc_smem_limit(scan, 16 * (kScanMost + 1));
+    if (rc != CE_OK) return rc;
+    cudaError_t e = cudaLaunchKernel(scan, dim3(static_cast<unsigned>(plan.grid)), dim3(kScanThreads), args,
+                                     16 * static_cast<size_t>(plan.part_vec + 1), st);
     if (e != cudaSuccess) return record_cuda_failure(e, "beam scan launch");
     size_t smem = sizeof(Pick) * static_cast<size_t>(K * a.splits + M * M);
     const size_t words = 8 * static_cast<size_t>(K * a.splits * M);
@@ -896,9 +855,8 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     if (staged) smem += words;
     const void* pick = staged ? (const void*)&beam_pick<true> : (const void*)&beam_pick<false>;
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kPickSmem));
-        if (e != cudaSuccess) return record_cuda_failure(e, "beam pick attributes");
+        rc = tc_smem_limit(pick, kPickSmem);
+        if (rc != CE_OK) return rc;
     }
     return launch_pdl(pick, dim3(static_cast<unsigned>(B)), kPickThreads, smem, st, &a,
                       "beam pick launch");
