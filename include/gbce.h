@@ -530,12 +530,13 @@ ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const vo
  *              2^20 (CE_ERR_UNSUPPORTED above).
  * out_scores, out_beams, out_tokens   [B, M]: candidate (k, v) has the score
  *              scores[k] + logits[k, v] - log sum_j exp(logits[k, j]), formed
- *              in 64 bits and rounded to fp32 for the output; descending,
+ *              in pairs of fp32 (48 bits) and rounded to fp32 for the output;
+ *              descending,
  *              equal ones by the lowest k V + v. Within a beam the order is
  *              that of the logits. Tokens with a logit of -inf or NaN are no
  *              candidates (and add nothing to the sum); a beam with no other
- *              token, or with a logit of +inf, has none. Places without a
- *              candidate hold the score -inf, beam -1 and pad_token.
+ *              token, or with a logit of +inf, has none, nor has a token
+ *              whose score is not finite in fp32. Places without a candidate hold the score -inf, beam -1 and pad_token.
  * workspace    at least ce_beam_workspace_bytes(...) bytes, 256-byte
  *              aligned, owned by the caller; nothing in it needs to be set.
  * Asynchronous on `stream`; uses no library scratch. Results do not depend on

@@ -113,31 +113,37 @@ def beam_reorder(states, beams, inplace=False):
     dev = beams.device
     if beams.stride(1) != 1 or beams.stride(0) < K:
         beams = beams.contiguous()
-    outs = []
-    table = (_lib.BeamState * len(states))()
-    for t, at in zip(states, table):
+    outs, table = [], []
+    for t in states:
         require_cuda(t, "a state")
         if t.device != dev:
             raise ValueError("the states must be on the beams' device")
-        skip = 2 if t.dim() >= 2 and tuple(t.shape[:2]) == (B, K) else 1
-        if skip == 1 and (t.dim() < 1 or t.shape[0] != B * K):
+        shape = t.shape
+        skip = 2 if len(shape) >= 2 and shape[0] == B and shape[1] == K else 1
+        if skip == 1 and (len(shape) < 1 or shape[0] != B * K):
             raise ValueError("a state must be [B, K, ...] or [B * K, ...]")
         if inplace and t.requires_grad:
             raise ValueError("a state that requires a gradient cannot be reordered in place")
-        row, block_stride, blocks, inner = _blocks(t, skip)
-        apart = row >= (blocks - 1) * block_stride + inner or (
-            blocks > 1 and row >= inner and block_stride >= B * K * row)
-        if inplace and B * K > 1 and t.numel() and not apart:
-            raise ValueError("a state's rows must not overlap")
-        out = t if inplace else torch.empty(t.shape, dtype=t.dtype, device=dev)
+        n = t.numel()
+        if t.is_contiguous():
+            row = inner = n // (B * K) if n else 0
+            block_stride, blocks = 0, 1
+        else:
+            row, block_stride, blocks, inner = _blocks(t, skip)
+            apart = row >= (blocks - 1) * block_stride + inner or (
+                blocks > 1 and row >= inner and block_stride >= B * K * row)
+            if inplace and B * K > 1 and n and not apart:
+                raise ValueError("a state's rows must not overlap")
+        out = t if inplace else torch.empty(shape, dtype=t.dtype, device=dev)
         outs.append(out)
-        b = t.element_size()
-        at.src, at.dst = t.data_ptr(), out.data_ptr()
-        at.src_row, at.src_block = row * b, block_stride * b
-        at.dst_row, at.dst_block = (row * b, block_stride * b) if inplace else \
-            (blocks * inner * b, inner * b)
-        at.blocks, at.block_bytes = (blocks, inner * b) if t.numel() else (0, 0)
+        if n:
+            b = t.element_size()
+            to = (row * b, block_stride * b) if inplace else (blocks * inner * b, inner * b)
+            table.append((t.data_ptr(), out.data_ptr(), row * b, block_stride * b, *to, blocks,
+                          inner * b))
+    n = len(table)
+    table = (_lib.BeamState * n)(*table)
     with on(dev):
-        check(_lib.ce_beam_reorder(table, len(states), ptr(beams), beams.stride(0), B, K, stream(dev)),
+        check(_lib.ce_beam_reorder(table, n, ptr(beams), beams.stride(0), B, K, stream(dev)),
               "ce_beam_reorder")
     return outs[0] if one else outs

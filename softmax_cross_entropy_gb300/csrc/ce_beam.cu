@@ -21,13 +21,15 @@
 //     {max, sum} in a fixed order, takes the M-th best of the lists' first
 //     candidates as a bound (no list that starts below it can contribute),
 //     and ranks the candidates above it by counting.
-// Candidates are ordered by (score in 64 bits, then lowest k V + v), so ties
+// Candidates are ordered by (score in 48 bits, then lowest k V + v), so ties
 // and the order in which warps finish do not show in the result.
 //
-// Bound by HBM: one read of the logits.
+// One read of the logits; the scan is bound by the instructions of its two
+// passes (about 8 a logit of 16 bits and 20 a logit of 32, issue slots 55-60%
+// taken): 64 x 8 x 131072 fp32 72 us (3.7 TB/s), bf16 47 us (2.9 TB/s). The
+// reordering is bound by HBM: 2 x 134 MB of states in 67 us.
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <string>
 
 #include "ce_kernels.cuh"
@@ -479,7 +481,26 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan(const __gri
     }
 }
 
-// A candidate of a batch entry: its score in 64 bits as an ordered integer
+// Numbers held as the exact sum of two fp32 (48 bits and more): the scores
+// of candidates are formed and compared in them. (The same in fp64, which
+// this GPU issues at a sixteenth of a warp a cycle, made the pick of 16 x 8
+// beams 10 us instead of 4.)
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // exact (Knuth)
+    const float s = a + b;
+    const float t = s - a;
+    return Two{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two two_add(const Two& a, const Two& b) {
+    const Two s = two_sum(a.hi, b.hi);
+    const float e = s.lo + (a.lo + b.lo);
+    const float hi = s.hi + e;
+    return Two{hi, e - (hi - s.hi)};
+}
+
+// A candidate of a batch entry: its score as ordered integers, hi above lo
 // (0: none), then its beam above its token (the order of k V + v).
 struct Pick {
     uint64_t key;
@@ -489,13 +510,9 @@ constexpr uint64_t kNowhere = ~uint64_t{0};
 __device__ __forceinline__ bool better(const Pick& p, const Pick& q) {
     return p.key > q.key || (p.key == q.key && p.at < q.at);
 }
-__device__ __forceinline__ uint64_t ordered64(double x) {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-    return (b >> 63) ? ~b : b | (uint64_t{1} << 63);
-}
-__device__ __forceinline__ double unordered64(uint64_t u) {
-    return __longlong_as_double(
-        static_cast<long long>((u >> 63) ? u & ~(uint64_t{1} << 63) : ~u));
+// (a score that is not finite in fp32 is no candidate's)
+__device__ __forceinline__ uint64_t score_key(const Two& s) {
+    return isfinite(s.hi) ? (static_cast<uint64_t>(ordered(s.hi)) << 32) | ordered(s.lo) : 0u;
 }
 
 // What beam_pick knows of a beam. The log-sum-exp is m + logs: its parts are
@@ -503,7 +520,8 @@ __device__ __forceinline__ double unordered64(uint64_t u) {
 // sum loses logs.
 enum : int { kBeamDead = 0, kBeamAlive = 1, kBeamFinished = 2 };
 struct BeamInfo {
-    double m, logs, score;
+    Two minus_logs;
+    float m, score;
     int kind;
 };
 
@@ -513,13 +531,23 @@ __device__ __forceinline__ Pick word_pick(const BeamInfo& info, int k, uint64_t 
                                           int64_t pad) {
     const uint64_t beam = static_cast<uint64_t>(k) << 32;
     if (info.kind == kBeamAlive && w) {
-        const double x = static_cast<double>(unordered(static_cast<uint32_t>(w >> 32)));
-        return Pick{ordered64(((x - info.m) - info.logs) + info.score),
-                    beam | static_cast<uint32_t>(~static_cast<uint32_t>(w))};
+        const float x = unordered(static_cast<uint32_t>(w >> 32));
+        const Two s = two_add(two_add(two_sum(x, -info.m), info.minus_logs), Two{info.score, 0.f});
+        return Pick{score_key(s), beam | static_cast<uint32_t>(~static_cast<uint32_t>(w))};
     }
     if (info.kind == kBeamFinished && front)
-        return Pick{ordered64(info.score), beam | static_cast<uint64_t>(pad)};
+        return Pick{score_key(Two{info.score, 0.f}), beam | static_cast<uint64_t>(pad)};
     return Pick{0, kNowhere};
+}
+
+// How many of n picks are better than p, counted by the four lanes of a quad
+// (which all get the sum).
+__device__ __forceinline__ int quad_rank(const Pick* all, int n, const Pick& p) {
+    int rank = 0;
+#pragma unroll 4
+    for (int o = threadIdx.x & 3; o < n; o += 4) rank += better(all[o], p);
+    rank += __shfl_xor_sync(~0u, rank, 1);
+    return rank + __shfl_xor_sync(~0u, rank, 2);
 }
 
 // STAGED: the entry's lists are held in shared memory (all the loads at
@@ -554,29 +582,35 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
         for (int i = lane; i < a.splits; i += 32) m = fmaxf(m, sums[i].m);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        double s = 0.0;
+        Two s{0.f, 0.f};
         for (int i = lane; i < a.splits; i += 32) {
             const RowSum t = sums[i];  // (exp2(-inf) = 0 for a part with no token)
-            s += static_cast<double>(t.s * exp2f((t.m - m) * kLog2e));
+            s = two_add(s, Two{t.s * exp2f((t.m - m) * kLog2e), 0.f});
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+        for (int d = 16; d > 0; d >>= 1)
+            s = two_add(s, Two{__shfl_xor_sync(~0u, s.hi, d), __shfl_xor_sync(~0u, s.lo, d)});
         if (lane == 0) {
-            // log s from its binary exponent and a mantissa near 1: logf there
-            // is off by 2^-25 or less, the mantissa's rounding is put back
-            const long long bits = __double_as_longlong(s);
-            const int e = static_cast<int>((bits >> 52) & 0x7FF) - 1022;
-            const double f = __longlong_as_double((bits & 0x000FFFFFFFFFFFFFLL) | 0x3FE0000000000000LL) *
-                             1.4142135623730951;  // [0.7, 1.42)
-            const float f32 = static_cast<float>(f);
+            // log s = e ln 2 + log f, f in [0.7, 1.42): logf there is off by
+            // 2^-25 or less
+            const uint32_t bits = __float_as_uint(s.hi);
+            int e = static_cast<int>(bits >> 23) - 127;
+            float f = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+            if (f > 1.41421356f) {
+                f *= 0.5f;
+                ++e;
+            }
+            const float ef = static_cast<float>(e);
+            constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;  // ln 2 as two fp32
+            const float hi = ef * kLn2;
+            Two logs = two_add(Two{hi, fmaf(ef, kLn2, -hi) + ef * kLn2Lo}, two_sum(logf(f), s.lo / s.hi));
             BeamInfo w;
-            w.m = static_cast<double>(m);
-            w.logs = (e - 0.5) * 0.6931471805599453 +
-                     static_cast<double>(logf(f32) + static_cast<float>(f - f32) / f32);
-            w.score = static_cast<double>(score);
+            w.m = m;
+            w.minus_logs = Two{-logs.hi, -logs.lo};
+            w.score = score;
             w.kind = !isfinite(score) ? kBeamDead
                      : done           ? kBeamFinished
-                     : (isfinite(m) && s > 0.0 && isfinite(s)) ? kBeamAlive : kBeamDead;
+                     : (isfinite(m) && s.hi > 0.f && isfinite(s.hi)) ? kBeamAlive : kBeamDead;
             info[k] = w;
         }
     }
@@ -589,13 +623,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
     for (int l = threadIdx.x; l < nl; l += kPickThreads) heads[l] = at(l, 0);
     __syncthreads();
     // the M-th best of the lists' first candidates
-    for (int l = threadIdx.x; l < nl; l += kPickThreads) {
-        const Pick p = heads[l];
-        if (!p.key) continue;
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < nl; ++o) rank += better(heads[o], p);
-        if (rank == a.M - 1) bound = p;
+    for (int l0 = 0; l0 < nl; l0 += kPickThreads / 4) {
+        const int l = l0 + static_cast<int>(threadIdx.x >> 2);
+        const Pick p = l < nl ? heads[l] : Pick{0, kNowhere};
+        const int rank = quad_rank(heads, nl, p);
+        if (p.key && rank == a.M - 1) bound = p;
     }
     __syncthreads();
     const Pick bar = bound;
@@ -618,13 +650,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
     }
     __syncthreads();
     const int n = nsurv;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
-        const Pick p = surv[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < n; ++o) rank += better(surv[o], p);
-        if (rank < a.M) {
-            a.out_scores[b * a.M + rank] = static_cast<float>(unordered64(p.key));
+    for (int i0 = 0; i0 < n; i0 += kPickThreads / 4) {
+        const int i = i0 + static_cast<int>(threadIdx.x >> 2);
+        const Pick p = i < n ? surv[i] : Pick{0, kNowhere};
+        const int rank = quad_rank(surv, n, p);
+        if (i < n && rank < a.M && (threadIdx.x & 3) == 0) {
+            a.out_scores[b * a.M + rank] = unordered(static_cast<uint32_t>(p.key >> 32));
             a.out_beams[b * a.M + rank] = static_cast<int64_t>(p.at >> 32);
             a.out_tokens[b * a.M + rank] = static_cast<int64_t>(p.at & 0xFFFFFFFFu);
         }
@@ -719,11 +750,12 @@ ce_status sm_count(int* sms) {
     return e == cudaSuccess ? CE_OK : record_cuda_failure(e, "beam search device");
 }
 
-// How the rows are dealt out: `splits` parts a row, all parts over one wave
-// of CTAs (kScanCtas an SM) in turn. A part costs its bytes and about as
-// much as another 16 KB (the bound, the ranking); the CTAs take ceil(parts /
-// CTAs) parts each.
-constexpr int64_t kScanMin = 512;  // vectors of a part at least: 8 KB
+// How the rows are dealt out: `splits` parts a row, over one wave of CTAs
+// (kScanCtas an SM) in turn. As few parts as the stage allows, since each
+// costs a bound and a ranking (16 x 8 x 128256 bf16 in 7, 10 and 12 parts: 22,
+// 26 and 38 us), but, for few rows, up to two an SM of at least 1000 vectors
+// (4 x 32000 in 1 and 4 parts: 8.5 and 7.9 us).
+constexpr int64_t kScanMin = 1000;
 struct ScanPlan {
     int64_t part_vec, grid;
     int splits;
@@ -731,23 +763,13 @@ struct ScanPlan {
 ScanPlan scan_plan(int64_t rows, int64_t V, int dtype, int sms) {
     const int64_t N = dtype == CE_F32 ? 4 : 8;
     const int64_t nv = (V + N - 1) / N;
-    const int64_t ctas = int64_t{kScanCtas} * std::max(sms, 1);
     const int64_t least = (nv + kScanMost - 1) / kScanMost;
-    const int64_t most = std::max(least, std::min<int64_t>(kMaxSplits, nv / kScanMin));
-    ScanPlan p{nv, 0, 1};
-    int64_t best = INT64_MAX;
-    const char* env = std::getenv("GBCE_BEAM_SPLITS");
-    for (int64_t s = least; s <= most; ++s) {
-        if (env && s != std::max(least, std::min<int64_t>(std::atoi(env), most))) continue;
-        const int64_t vec = (nv + s - 1) / s;
-        const int64_t cost = (rows * s + ctas - 1) / ctas * (vec + 1024);
-        if (cost < best) {
-            best = cost;
-            p.part_vec = vec;
-            p.splits = static_cast<int>((nv + vec - 1) / vec);
-        }
-    }
-    p.grid = std::min<int64_t>(rows * p.splits, ctas);
+    const int64_t fill = (2L * std::max(sms, 1) + rows - 1) / std::max<int64_t>(rows, 1);
+    const int64_t s = std::max(least, std::min(fill, nv / kScanMin));
+    ScanPlan p;
+    p.part_vec = (nv + s - 1) / s;
+    p.splits = static_cast<int>((nv + p.part_vec - 1) / p.part_vec);
+    p.grid = std::min<int64_t>(rows * p.splits, int64_t{kScanCtas} * std::max(sms, 1));
     return p;
 }
 
