@@ -6,17 +6,17 @@
 // each split so that every SM reads the same number of weight bytes:
 //  * ffn_rows: tiles of 128 weight rows (of Wg, then Wu; or of Wd) x K blocks
 //    of 64 are units of 16 KB, dealt out in equal runs to one CTA an SM. A
-//    TMA producer keeps a ring of up to 11 units in flight (176 KB an SM); an
-//    MMA thread multiplies each by the tokens' block of x (or h), N = rows
+//    TMA producer keeps a ring of units in flight (about 100 KB an SM); an MMA
+//    thread multiplies each by the tokens' block of x (or h), N = rows
 //    rounded up to 16; four epilogue warps write the sums of a tile's part,
 //    fp32, to the workspace. A run may start and end inside a tile, so a
 //    tile has a few parts.
 //  * ffn_rows_act and ffn_rows_out add a tile's parts in order (results do
 //    not depend on which SM finishes first) and apply the activation and
 //    product, or the dropout and residual, in fp32, rounding once.
-// The four launches overlap at their ends (programmatic dependent launch):
-// the second product fills its ring with weights, which no launch of this
-// call writes, while the first's sums are still being added.
+// The four launches overlap (programmatic dependent launch): the second
+// product fills its ring with weights, which no launch of this call writes,
+// while the first still runs and its sums are added.
 #include <algorithm>
 #include <cstdint>
 #include <string>
@@ -35,7 +35,10 @@ constexpr int kRowsThreads = 192;  // producer, MMA issuer, 4 epilogue warps
 constexpr int kRowsTile = 128;     // weight rows of a tile
 constexpr uint32_t kRowsA = kRowsTile * kBK * 2;  // 16 KB
 constexpr int kRowsStages = 11;
-constexpr uint32_t kRowsSmem = 200 * 1024;  // of the ring
+// The ring: two CTAs an SM where that leaves it 4 units or more (up to 64
+// tokens), so that the second product's ring fills while the first product
+// still runs; else one.
+constexpr uint32_t kRowsSmemTwo = 110 * 1024, kRowsSmemOne = 200 * 1024;
 
 struct RowsArgs {
     int64_t units, per;  // tiles x K blocks; of a CTA
@@ -43,7 +46,7 @@ struct RowsArgs {
     int nk;              // K blocks of a tile
     int rows, nt;        // tokens; rounded up to a multiple of 16
     int stages, parts;   // ring slots; parts of a tile at most
-    uint32_t stage_bytes;
+    uint32_t stage_bytes, acc_cols, tmem_cols;  // of a unit; of an accumulator; of both
     float* sums;  // [tiles, parts, rows, 128]
     uint64_t timeout_ns;
     unsigned* status;
@@ -55,8 +58,12 @@ __host__ __device__ inline int rows_parts(int64_t t, int nk, int64_t per) {
     return static_cast<int>(((t + 1) * nk - 1) / per - t * nk / per) + 1;
 }
 
+__device__ __forceinline__ void rows_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 template <uint32_t AB>
-__global__ void __launch_bounds__(kRowsThreads, 1)
+__global__ void __launch_bounds__(kRowsThreads, 2)
 ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
          const __grid_constant__ CUtensorMap mapx, const __grid_constant__ RowsArgs a) {
     extern __shared__ unsigned char rows_smem_raw[];
@@ -74,6 +81,9 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * a.per;
     const int64_t u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
     if (threadIdx.x == 0) {
+        rows_prefetch_map(&map0);
+        rows_prefetch_map(&map1);
+        rows_prefetch_map(&mapx);
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
@@ -91,7 +101,7 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
         asm volatile(
             "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                 smem_u32(&tmem_base_sh)),
-            "r"(kTmemCols)
+            "r"(a.tmem_cols)
             : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -157,7 +167,7 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
             int64_t kb = u0 % a.nk;
             for (int64_t u = u0; u < u1; ++u) {
                 const int b = run & 1;
-                const uint32_t acc = tmem + static_cast<uint32_t>(b * 256);
+                const uint32_t acc = tmem + static_cast<uint32_t>(b) * a.acc_cols;
                 const bool start = u == u0 || kb == 0;
                 if (start && !tc_wait(smem_u32(&acc_empty[b]),
                                       (static_cast<uint32_t>(run >> 1) & 1u) ^ 1u, a.timeout_ns)) {
@@ -197,14 +207,14 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
         for (int64_t u = u0; u < u1; ++run) {
             const int64_t t = u / a.nk;
             const int b = run & 1;
-            const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
-                                              static_cast<uint32_t>(run >> 1) & 1u, a.timeout_ns);
+            const bool ok = tc_wait(smem_u32(&acc_full[b]), static_cast<uint32_t>(run >> 1) & 1u,
+                                    a.timeout_ns);
             if (!ok || *reinterpret_cast<volatile int*>(&s_fail)) {
                 if (lane == 0) s_fail = 1;
                 break;
             }
             tc_fence_after();
-            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * 256);
+            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b) * a.acc_cols;
             const int64_t part = blockIdx.x - rows_first(t, a.nk, a.per);
             float* out = a.sums + ((t * a.parts + part) * a.rows) * kRowsTile + q * 32 + lane;
 #pragma unroll 1
@@ -234,7 +244,7 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
     __syncthreads();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kTmemCols)
+                     "r"(a.tmem_cols)
                      : "memory");
 }
 
@@ -251,14 +261,20 @@ struct RowsJoin {
     DropSpec drop;
 };
 
+// The parts of tile t for one token, added in order; the loads of the first
+// eight are on their way together.
 __device__ __forceinline__ float join_parts(const RowsJoin& j, int64_t t, int row) {
     const int n = rows_parts(t, j.nk, j.per);
     const float* p = j.sums + ((t * j.parts) * j.rows + row) * kRowsTile + threadIdx.x;
     const int64_t step = static_cast<int64_t>(j.rows) * kRowsTile;
-    float v = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) v += p[i * step];
-    return v;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldcg(p + i * step) : 0.f;
+    float sum = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += v[i];
+    for (int i = 8; i < n; ++i) sum += __ldcg(p + i * step);
+    return sum;
 }
 
 // h = act(g) u (and s, a) of one token and 128 columns.
@@ -289,23 +305,23 @@ __global__ void __launch_bounds__(kRowsTile) ffn_rows_act(const __grid_constant_
 // y = residual + dropout(z) of one token and 128 columns.
 template <typename T>
 __global__ void __launch_bounds__(kRowsTile) ffn_rows_out(const __grid_constant__ RowsJoin j) {
-    pdl_wait();
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowsTile + threadIdx.x;
     const int row = blockIdx.y;
     if (c >= j.cols) return;
-    float v = join_parts(j, blockIdx.x, row);
     const int64_t at = row * j.cols + c;
+    // what no launch of this call writes, before the wait
+    const float res = j.res ? Vec<T>::load1(j.res, at) : 0.f;
+    float factor = j.drop.mode == kDropAll ? 0.f : 1.f;
     if (j.drop.mode == kDropSome) {
         const PhiloxKey key = philox_key(j.drop);
         const uint4 w = philox4x32(key, static_cast<uint64_t>(at) >> 2);
         const uint32_t l = static_cast<uint32_t>(at) & 3u;
         const uint32_t word = l == 0 ? w.x : l == 1 ? w.y : l == 2 ? w.z : w.w;
-        v = word >= j.drop.threshold ? v * j.drop.scale : 0.f;
-    } else if (j.drop.mode == kDropAll) {
-        v = 0.f;
+        factor = word >= j.drop.threshold ? j.drop.scale : 0.f;
     }
-    if (j.res) v += Vec<T>::load1(j.res, at);
-    Vec<T>::store1(j.out, at, v);
+    pdl_wait();
+    const float v = join_parts(j, blockIdx.x, row);
+    Vec<T>::store1(j.out, at, (factor != 0.f ? v * factor : 0.f) + res);
 }
 
 int64_t up256r(int64_t b) { return (b + 255) / 256 * 256; }
@@ -355,7 +371,11 @@ ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void*
     a.rows = static_cast<int>(rows);
     a.nt = static_cast<int>((rows + 15) / 16 * 16);
     a.stage_bytes = kRowsA + static_cast<uint32_t>(a.nt) * kBK * 2;
-    a.stages = std::min<int>(kRowsStages, static_cast<int>(kRowsSmem / a.stage_bytes));
+    const uint32_t ring = kRowsSmemTwo / a.stage_bytes >= 4 ? kRowsSmemTwo : kRowsSmemOne;
+    a.stages = std::min<int>(kRowsStages, static_cast<int>(ring / a.stage_bytes));
+    a.acc_cols = static_cast<uint32_t>(std::max(a.nt, 32));
+    a.tmem_cols = 64;  // a power of two
+    while (a.tmem_cols < 2 * a.acc_cols) a.tmem_cols *= 2;
     a.parts = p.parts;
     a.sums = sums;
     a.timeout_ns = timeout_ns;
@@ -366,8 +386,8 @@ ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void*
     if (rc == CE_OK) rc = tc_map_16bit(&mx, x, dtype, rows, K, static_cast<uint32_t>(a.nt));
     if (rc != CE_OK) return rc;
     const void* fn = dtype == CE_BF16 ? (const void*)&ffn_rows<1u> : (const void*)&ffn_rows<0u>;
-    const size_t smem = kRowsSmem + 1024;
-    rc = tc_smem_limit(fn, smem);
+    const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + 1024;
+    rc = tc_smem_limit(fn, kRowsSmemOne + 1024);
     if (rc != CE_OK) return rc;
     void* args[] = {&m0, &m1, &mx, &a};
     return rows_pdl(fn, dim3(static_cast<unsigned>(p.grid)), kRowsThreads, smem, pdl, args, st,
