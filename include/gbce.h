@@ -567,8 +567,9 @@ typedef struct {
  *              the -1 of a place without a candidate) stands for j: that row
  *              keeps its own state.
  * In place, rows that keep their state are neither read nor written. Either
- * all states are reordered in place or none; a dst that overlaps a src
- * otherwise is the caller's error. Bytes between blocks and rows are left as
+ * all states are reordered in place or none, and no dst is given twice
+ * (CE_ERR_INVALID_ARG); states that overlap one another otherwise, or a dst
+ * that overlaps a src, are the caller's error. Bytes between blocks and rows are left as
  * they were. K at most 32 (CE_ERR_UNSUPPORTED above). Asynchronous on
  * `stream`; uses no library scratch.
  */

@@ -26,7 +26,8 @@ def beam_search_step(logits, scores, num_candidates=None, finished=None, pad_tok
     batch entry: BeamCandidates of scores (float32), beams and tokens (int64),
     each [B, num_candidates], by descending score, equal ones by the lowest
     beam, then token. logits [B, K, V] in float32, bfloat16 or float16, K at
-    most 32; scores [B, K] float32, the beams' log-probabilities so far.
+    most 32, V at most 2^20; scores [B, K] float32, the beams'
+    log-probabilities so far. Gradients are not tracked.
 
     A candidate's score is scores[b, k] + log_softmax(logits[b, k])[v]. Tokens
     whose logit is -inf or NaN are left out; a beam whose score is not finite,
@@ -100,8 +101,9 @@ def beam_reorder(states, beams, inplace=False):
     Returns new tensors, or with inplace=True changes the states and returns
     them (rows that keep their state are not touched). Strided states, such as
     cache[:, :, :length], are taken when their rows are equally spaced blocks
-    of contiguous elements (ValueError otherwise). The states' gradients are
-    not tracked."""
+    of contiguous elements (ValueError otherwise). States that are changed in
+    place must not overlap one another. The states' gradients are not
+    tracked."""
     one = isinstance(states, torch.Tensor)
     states = [states] if one else list(states)
     require_cuda(beams, "beams")
@@ -142,6 +144,8 @@ def beam_reorder(states, beams, inplace=False):
             table.append((t.data_ptr(), out.data_ptr(), row * b, block_stride * b, *to, blocks,
                           inner * b))
     n = len(table)
+    if len({at[1] for at in table}) < n:
+        raise ValueError("a state is given twice")
     table = (_lib.BeamState * n)(*table)
     with on(dev):
         check(_lib.ce_beam_reorder(table, n, ptr(beams), beams.stride(0), B, K, stream(dev)),

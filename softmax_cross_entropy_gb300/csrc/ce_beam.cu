@@ -903,6 +903,9 @@ extern "C" ce_status ce_beam_reorder(const ce_beam_state* states, int n, const i
         if (in && (s.src_row != s.dst_row || s.src_block != s.dst_block)) return CE_ERR_INVALID_ARG;
         if (inplace < 0) inplace = in;
         if (inplace != in) return CE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)  // one state twice would be written by two
+            if (states[j].dst == s.dst && states[j].blocks && states[j].block_bytes)
+                return CE_ERR_INVALID_ARG;
     }
     int sms = 0;
     ce_status rc = sm_count(&sms);

@@ -33,8 +33,10 @@ __device__ __forceinline__ FfnGate ffn_gate(int act, float g) {
         const bool silu = act == CE_ACT_SILU;
         const float q = ffn_logistic(silu ? g : kGelu2k * g * (1.f + kGeluC * g * g));
         r.act = g * q;
-        if (SLOPE)
-            r.slope = q + g * q * (1.f - q) * (silu ? 1.f : kGelu2k * (1.f + 3.f * kGeluC * g * g));
+        if (SLOPE) {
+            const float d = q * (1.f - q);  // 0 where g g may overflow
+            r.slope = q + (d > 0.f ? g * d * (silu ? 1.f : kGelu2k * (1.f + 3.f * kGeluC * g * g)) : 0.f);
+        }
     }
     return r;
 }

@@ -110,6 +110,13 @@ def test_reorder_sizes():
     assert reorder(n=0) == _lib.CE_OK and reorder(B=0) == _lib.CE_OK
 
 
+def test_reorder_refuses_one_state_twice():
+    from softmax_cross_entropy_gb300 import _lib
+    one = (256, 512, 16, 0, 16, 0, 1, 16)
+    at = (_lib.BeamState * 2)(one, (256 + 64, *one[1:]))
+    assert _lib.ce_beam_reorder(at, 2, 64, 4, 2, 4, None) == _lib.CE_ERR_INVALID_ARG
+
+
 def test_wrapper_refuses_cpu_tensors():
     import softmax_cross_entropy_gb300 as gbce
     with pytest.raises(ValueError):
@@ -277,6 +284,51 @@ def test_reorder_of_strided_states(inplace):
 
 
 @pytest.mark.gpu
+def test_no_entries():
+    import softmax_cross_entropy_gb300 as gbce
+    best = gbce.beam_search_step(torch.empty(0, 3, 7, device="cuda"), torch.empty(0, 3, device="cuda"))
+    assert best.scores.shape == best.beams.shape == best.tokens.shape == (0, 3)
+    assert gbce.beam_reorder(torch.empty(0, 5, device="cuda"), best.beams).shape == (0, 5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(2 ** 20, "f32"), (2 ** 20 - 3, "bf16")])
+def test_the_largest_vocabulary(V, dtype):
+    import softmax_cross_entropy_gb300 as gbce
+    x, s = inputs(1, 3, V, dtype)
+    compare(gbce.beam_search_step(x, s, num_candidates=64), reference(x, s, 64))
+
+
+@pytest.mark.gpu
+def test_logits_past_32_bits():
+    import softmax_cross_entropy_gb300 as gbce
+    B, K, V = 66, 32, 2 ** 20 - 1
+    x = torch.empty(B, K, V, dtype=torch.bfloat16, device="cuda").normal_()
+    s = -torch.rand(B, K, device="cuda")
+    s[1:-1] = -math.inf  # entries whose logits are not read
+    got = gbce.beam_search_step(x, s, num_candidates=4)
+    last = gbce.BeamCandidates(*(t[-1:] for t in got))
+    compare(last, reference(x[-1:], s[-1:], 4))
+    assert bool((got.beams[1:-1] == -1).all())
+    del x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+def test_many_equal_logits_next_to_better_ones():
+    # more logits reach the bound than a part lists: equal ones, in several beams and parts
+    import softmax_cross_entropy_gb300 as gbce
+    x = torch.zeros(3, 4, 70001, device="cuda")
+    x[0, :, ::3] = 1.0
+    x[1, 2, 69990:] = 5.0
+    x[2, 1, 5] = x[2, 3, 70000] = 2.0
+    s = torch.tensor([[-1.0, -1.5, -1.25, -3.0]], device="cuda").expand(3, 4).contiguous()
+    for M in (3, 16, 40):
+        for t in (x, x.bfloat16()):
+            compare(gbce.beam_search_step(t, s, num_candidates=M), reference(t, s, M))
+
+
+@pytest.mark.gpu
 def test_reorder_by_a_part_of_the_candidates():
     import softmax_cross_entropy_gb300 as gbce
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -328,6 +380,9 @@ def test_wrapper_refuses():
             gbce.beam_reorder(state, beams, inplace=True)
     with pytest.raises(ValueError):
         gbce.beam_reorder(torch.zeros(6, 4, device="cuda"), beams.int())
+    twice = torch.zeros(6, 4, device="cuda")
+    with pytest.raises(ValueError):
+        gbce.beam_reorder([twice, twice], beams, inplace=True)
 
 
 @pytest.mark.gpu

@@ -284,7 +284,12 @@ def test_large_gates_saturate():
         # 32 gates of 3008, the others 0
         assert torch.equal(y.detach().float(), torch.full_like(y, 1504.0).float())
         (dx,) = torch.autograd.grad(y.sum(), [x])
-        assert bool(dx.isfinite().all())
+        # dh = 1: dg = 1 (u = act' = 1) or 0, du = 3008 or 0: 32 (47 + 3008 / 64)
+        assert torch.equal(dx.float(), torch.full_like(dx, 3008.0).float())
+    # gates of 1e20, whose squares overflow
+    y = gbce.gated_feed_forward(x * 1e20 / 47.0 / 64.0, wg, wu, wd, activation="gelu_tanh")
+    (dx,) = torch.autograd.grad(y.sum(), [x])
+    assert bool(y.isfinite().all()) and bool(dx.isfinite().all())
 
 
 @pytest.mark.gpu
