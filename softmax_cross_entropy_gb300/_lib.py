@@ -84,6 +84,8 @@ class CEError(RuntimeError):
 def load():
     """Loads libgbce.so once and declares its signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

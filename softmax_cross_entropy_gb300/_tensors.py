@@ -34,9 +34,13 @@ def once(name):
         raise RuntimeError(f"{name} is differentiable once: its backward has no graph")
 
 
+# (a CUDA tensor is at hand, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def on(device):
     """A context in which `device` is the current one (free where it is already)."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == _current_device() else torch.cuda.device(device)
 
 
 def check(rc, where):

@@ -382,7 +382,8 @@ ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void*
     a.status = status;
     CUtensorMap m0, m1, mx;
     ce_status rc = tc_map_16bit(&m0, w0, dtype, wrows, K, kRowsTile);
-    if (rc == CE_OK) rc = tc_map_16bit(&m1, w1 ? w1 : w0, dtype, wrows, K, kRowsTile);
+    m1 = m0;
+    if (rc == CE_OK && w1) rc = tc_map_16bit(&m1, w1, dtype, wrows, K, kRowsTile);
     if (rc == CE_OK) rc = tc_map_16bit(&mx, x, dtype, rows, K, static_cast<uint32_t>(a.nt));
     if (rc != CE_OK) return rc;
     const void* fn = dtype == CE_BF16 ? (const void*)&ffn_rows<1u> : (const void*)&ffn_rows<0u>;

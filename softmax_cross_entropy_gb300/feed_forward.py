@@ -94,6 +94,15 @@ def aligned(t):
     return t.clone() if t.data_ptr() % 16 and t.shape[-1] % 8 == 0 else t
 
 
+def _refuse(*tensors):
+    for t in tensors:
+        if t is not None:
+            require_cuda(t, "every tensor of the block")
+    if any(t is not None and t.device != tensors[0].device for t in tensors):
+        raise ValueError("the tensors must be on one device")
+    raise TypeError("the block takes bfloat16 or float16, the same for every tensor")
+
+
 def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu", dropout_p=0.0,
                        seed=None, offset=0, residual=None):
     """residual + dropout((act(x @ gate_weight^T) * (x @ up_weight^T)) @ down_weight^T).
@@ -106,33 +115,38 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
 
     H, I and O that are not multiples of 8 cost a packed copy of what they
     concern (x and the projections for H, down_weight for I) on each call."""
-    for name, t in (("x", x), ("gate_weight", gate_weight), ("up_weight", up_weight),
-                    ("down_weight", down_weight)) + \
-            ((("residual", residual),) if residual is not None else ()):
-        require_cuda(t, name)
-        if t.dtype not in (torch.bfloat16, torch.float16) or t.dtype != x.dtype:
-            raise TypeError("the block takes bfloat16 or float16, the same for every tensor")
-        if t.device != x.device:
-            raise ValueError("the tensors must be on one device")
+    dt, dev = x.dtype, x.device
+    if not x.is_cuda or (dt != torch.bfloat16 and dt != torch.float16) or \
+            gate_weight.dtype != dt or up_weight.dtype != dt or down_weight.dtype != dt or \
+            gate_weight.device != dev or up_weight.device != dev or down_weight.device != dev or \
+            (residual is not None and (residual.dtype != dt or residual.device != dev)):
+        _refuse(x, gate_weight, up_weight, down_weight, residual)
     if gate_weight.dim() != 2 or down_weight.dim() != 2 or gate_weight.shape != up_weight.shape:
         raise ValueError("gate_weight and up_weight must be [I, H], down_weight [O, I]")
     I, H = gate_weight.shape
     O = down_weight.shape[0]
     if x.dim() < 1 or x.shape[-1] != H or down_weight.shape[1] != I or min(H, I, O) < 1:
         raise ValueError("x must be [..., H], down_weight [O, I]")
+    flat = x.dim() == 2
     shape = (*x.shape[:-1], O)
-    if residual is not None and tuple(residual.shape) != shape:
+    if residual is not None and residual.shape != shape:
         raise ValueError("residual must have the shape of the output")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
     act = _ACTIVATIONS[activation]
-    p, seed, offset, state = check_rng(dropout_p, seed, offset, x.device)
-    res = None if residual is None else residual.reshape(-1, O).contiguous()
-    args = (aligned(x.reshape(-1, H)), aligned(gate_weight), aligned(up_weight),
-            aligned(down_weight), res, act, p, seed, offset, state)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args[:5]):
-        return GatedFeedForwardFunction.apply(*args).reshape(shape)
-    return _forward(*args, False)[0].reshape(shape)
+    p, seed, offset, state = check_rng(dropout_p, seed, offset, dev)
+    if not flat:
+        x = x.reshape(-1, H)
+        residual = None if residual is None else residual.reshape(-1, O)
+    args = (aligned(x), aligned(gate_weight), aligned(up_weight), aligned(down_weight),
+            None if residual is None else residual.contiguous(), act, p, seed, offset, state)
+    if torch.is_grad_enabled() and (
+            x.requires_grad or gate_weight.requires_grad or up_weight.requires_grad or
+            down_weight.requires_grad or (residual is not None and residual.requires_grad)):
+        y = GatedFeedForwardFunction.apply(*args)
+    else:
+        y = _forward(*args, False)[0]
+    return y if flat else y.reshape(shape)
 
 
 class GatedFeedForward(torch.nn.Module):
