@@ -470,8 +470,8 @@ enum {
  * h            [rows, I8] in dtype, 16-byte aligned, written: act(g) u with
  *              g = x @ w_gate^T and u = x @ w_up^T, rounded once. I8 is I
  *              rounded up to a multiple of 8; the columns behind I get 0.
- * s, a         [rows, I8] like h, written: u act'(g) and act(g), what
- *              ce_ffn_bwd needs besides h; or both NULL.
+ * s, a         [rows, I8] fp32, 16-byte aligned, written: u act'(g) and
+ *              act(g), what ce_ffn_bwd needs besides h; or both NULL.
  * workspace    device memory of at least ce_ffn_fwd_workspace_bytes(rows, H,
  *              I, O) bytes, 256-byte aligned, owned by the caller (NULL where
  *              that is 0); nothing in it needs to be set.
@@ -485,7 +485,7 @@ size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O)
 ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                      const void* residual, int dtype, int64_t rows, int64_t H, int64_t I,
                      int64_t O, int act, double p, uint64_t seed, uint64_t offset,
-                     const int64_t* state, void* y, void* h, void* s, void* a, void* workspace,
+                     const int64_t* state, void* y, void* h, float* s, float* a, void* workspace,
                      size_t workspace_bytes, ce_stream_t stream);
 
 /*
@@ -507,7 +507,7 @@ ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const 
 size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O, double p);
 
 ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const void* w_up,
-                     const void* w_down, const void* h, const void* s, const void* a, int dtype,
+                     const void* w_down, const void* h, const float* s, const float* a, int dtype,
                      int64_t rows, int64_t H, int64_t I, int64_t O, int act, double p,
                      uint64_t seed, uint64_t offset, const int64_t* state, void* dx,
                      void* dw_gate, void* dw_up, void* dw_down, void* workspace,

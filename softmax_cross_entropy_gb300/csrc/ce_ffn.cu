@@ -18,11 +18,12 @@
 //  * kDx: dx = dg Wg + du Wu as one product whose K runs over dg, then du;
 //  * kDw: dWg = dg^T x, dWu = du^T x and dWd = dz^T h as one launch over the
 //    tiles of all three (one tail for the SMs instead of three).
-// Roundings to 16 bits: h, s, a, dg and du, once each from fp32 (h, dg and du
-// feed tensor-core products; s and a instead of g and u, so that the backward
-// forms no activation and the rounding of g does not enter act'(g)); dropout
-// and the residual are applied in fp32 before y's only rounding; dz is dy
-// with zeros, its factor 1 / (1 - p) is applied to the products in fp32.
+// Roundings to 16 bits: h, dg and du, which feed tensor-core products, once
+// each from fp32. s and a stay in fp32 (kept in 16 bits they made the
+// gradients' errors 1.7 instead of 1.4 times that of one rounding, and saved
+// 60 of 2460 us of the 4096 x 4096 x 12288 training step); dropout and the residual
+// are applied in fp32 before y's only rounding; dz is dy with zeros, its
+// factor 1 / (1 - p) is applied to the products in fp32.
 //
 // The TMA wants rows of whole 16 bytes. Operands that have others (H, I or O
 // not a multiple of 8) are packed into rows of such a length by a kernel of
@@ -51,7 +52,7 @@ int64_t ffn_rows_workspace(int64_t rows, int64_t H8, int64_t I8, int64_t O, int 
 ce_status ffn_rows_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                        const void* residual, int dtype, int64_t rows, int64_t H8, int64_t I,
                        int64_t I8, int64_t O, int act, const DropSpec& drop, void* y, void* h,
-                       void* s, void* a, void* workspace, int sms, uint64_t timeout_ns,
+                       float* s, float* a, void* workspace, int sms, uint64_t timeout_ns,
                        unsigned* status, cudaStream_t st);
 
 namespace {
@@ -91,7 +92,8 @@ struct FfnGemm {
     int64_t M[3], N[3], tiles_m[3], tiles_n[3], tile_end[3];
     int64_t K;      // of one segment
     // outputs: of the problems (kDx, kDown: one), or of one problem (kGateUp:
-    // h, s, a; kDact: dg, du); odd: its rows are not whole 16-byte vectors
+    // h, and s, a in fp32; kDact: dg, du); odd: its rows are not whole
+    // 16-byte vectors
     void* out[3];
     int odd[3];
     float scale[3];  // kDact, kDw: of the products
@@ -99,8 +101,8 @@ struct FfnGemm {
     int m_first;    // a problem's tiles run along M first
     int outs;       // kGateUp: 3 with s and a, else 1
     int act;
-    const void* s;  // kDact: u act'(g), [M, N]
-    const void* a;  // kDact: act(g), [M, N]
+    const float* s;  // kDact: u act'(g), [M, N]
+    const float* a;  // kDact: act(g), [M, N]
     const void* res;  // kDown: [M, N] or nullptr
     int res_vec;      // 1: its rows are whole 16-byte vectors
     DropSpec drop;    // kDown
@@ -213,16 +215,17 @@ __device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&w)[4]) {
 }
 
 // An epilogue warp's way out for boxes of 32 x 32 elements, which each lane
-// holds a row of: through shared memory (16-byte chunk j of row r at chunk j ^
-// (r / 2 mod 4), conflict-free) to stores of 64 bytes a row, eight rows an
-// instruction. (A TMA store of the box, whose read of the staging area waits
-// behind the ring's loads in the copy engine, took 346 instead of 327 us for
-// kDact at 4096 x 12288 x 4096 and 496 instead of 483 for kGateUp.)
+// holds a row of: through shared memory, conflict-free, to stores of whole
+// 64- or 128-byte pieces of rows. (A TMA store of the box, whose read of the
+// staging area waits behind the ring's loads in the copy engine, took 346
+// instead of 327 us for kDact at 4096 x 12288 x 4096 and 496 instead of 483
+// for kGateUp.)
 struct FfnStore {
-    uint32_t stage;  // two boxes, used in turn
+    uint32_t stage;  // 4 KB: a box of fp32, or two of 16 bits used in turn
     uint32_t boxes;  // so far
     int lane;
 
+    // 16-bit boxes: 16-byte chunk j of row r at chunk j ^ (r / 2 mod 4)
     __device__ __forceinline__ uint32_t at(uint32_t buf, int r, int j) const {
         return buf + static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(j ^ ((r >> 1) & 3)) << 4);
     }
@@ -267,7 +270,58 @@ struct FfnStore {
             if (m + r < M && n + lane < cols) to[r * cols] = v;
         }
     }
+
+    // fp32 boxes: chunk j of row r at chunk j ^ (r mod 8). Piece i (of 8) of a
+    // lane is 4 elements: row 4 i + lane / 8, chunk lane mod 8.
+    __device__ __forceinline__ void put32(const float (&v)[32]) {
+        __syncwarp();  // what was staged before has been read
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stage + static_cast<uint32_t>(lane) * 128u +
+                             (static_cast<uint32_t>(j ^ (lane & 7)) << 4)),
+                         "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                         : "memory");
+        __syncwarp();
+    }
+    __device__ __forceinline__ int piece_row(int i) const { return 4 * i + (lane >> 3); }
+    __device__ __forceinline__ float4 piece(int i) const {
+        const int r = piece_row(i);
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(stage + static_cast<uint32_t>(r) * 128u +
+                           (static_cast<uint32_t>((lane & 7) ^ (r & 7)) << 4)));
+        return v;
+    }
+    // a box of fp32 at column n, row m of [M, cols], cols a multiple of 8
+    __device__ __forceinline__ void whole32(void* out, int64_t n, int64_t m, int64_t M, int64_t cols,
+                                            const float (&v)[32]) {
+        put32(v);
+        const int64_t c = n + 4 * (lane & 7);
+        float* to = static_cast<float*>(out) + m * cols + c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = piece_row(i);
+            const float4 p = piece(i);
+            if (m + r < M && c < cols) *reinterpret_cast<float4*>(to + r * cols) = p;
+        }
+        __syncwarp();
+    }
 };
+
+// kDact: this lane's pieces of a box of fp32 (FfnStore); zeros outside.
+__device__ __forceinline__ void load_pieces(const float* p, int64_t n, int64_t m, int64_t M, int64_t cols,
+                                            int lane, float4 (&w)[8]) {
+    const int64_t c = n + 4 * (lane & 7);
+    const float* q = p + m * cols + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m + r < M && c < cols) w[i] = __ldg(reinterpret_cast<const float4*>(q + r * cols));
+    }
+}
 
 // Whether element `i` is kept.
 __device__ __noinline__ bool ffn_kept(const DropSpec& d, PhiloxKey key, uint64_t i) {
@@ -536,19 +590,19 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
             const int64_t n0 = ffn_tile_n(a, p, tl) * kCols + side * (kCols / 2);
             const int64_t mt = ffn_tile_m(a, p, tl) * BM + rank * kMmaM + q * 32;  // + 128 hh
             constexpr int kUnits = kCols / 64;  // units of 32 columns of this warp's half
-            uint4 ns[4], na[4];  // kDact: s and a of the next unit
+            float4 ps[8], pa[8];  // kDact: pieces of s and a of the next unit
             if constexpr (MODE == kDact) {
                 // while the tile's products run: the others into L2, the first here
                 for (int hh = 0; hh < H; ++hh) {
                     const int64_t row = mt + hh * kMmaM + lane;
-                    for (int c = 0; c < kCols / 2; c += 64) {
+                    for (int c = 0; c < kCols / 2; c += 32) {
                         if (row >= M || n0 + c >= N) break;
-                        ffn_prefetch(static_cast<const T*>(a.s) + row * N + n0 + c);
-                        ffn_prefetch(static_cast<const T*>(a.a) + row * N + n0 + c);
+                        ffn_prefetch(a.s + row * N + n0 + c);
+                        ffn_prefetch(a.a + row * N + n0 + c);
                     }
                 }
-                load_row32<T>(a.s, mt + lane, n0, M, N, ns);
-                load_row32<T>(a.a, mt + lane, n0, M, N, na);
+                load_pieces(a.s, n0, mt, M, N, lane, ps);
+                load_pieces(a.a, n0, mt, M, N, lane, pa);
             }
             const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
                                               static_cast<uint32_t>(i / NACC) & 1u, a.timeout_ns);
@@ -560,23 +614,20 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
 #pragma unroll 1
             for (int x = 0; x < H * kUnits; ++x) {
                 const int hh = x / kUnits, c = x % kUnits;
-                const int64_t m = mt + hh * kMmaM, row = m + lane, n = n0 + c * 32;
+                const int64_t m = mt + hh * kMmaM, n = n0 + c * 32;
                 // the accumulator's column of this unit
                 const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                                      static_cast<uint32_t>((b * H + hh) * kBN + side * (kCols / 2) + c * 32);
-                uint4 cs[4], ca[4];
-                if constexpr (MODE == kDact) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        cs[j] = ns[j];
-                        ca[j] = na[j];
+                // the unit after this one
+                const int y = x + 1 < H * kUnits ? x + 1 : x;
+                const int64_t nm = mt + (y / kUnits) * kMmaM, nn = n0 + (y % kUnits) * 32;
+                if (m >= M || n >= N) {  // the same for the whole warp
+                    if constexpr (MODE == kDact) {
+                        load_pieces(a.s, nn, nm, M, N, lane, ps);
+                        load_pieces(a.a, nn, nm, M, N, lane, pa);
                     }
-                    const int y = x + 1 < H * kUnits ? x + 1 : x;
-                    const int64_t nr = mt + (y / kUnits) * kMmaM + lane, nn = n0 + (y % kUnits) * 32;
-                    load_row32<T>(a.s, nr, nn, M, N, ns);
-                    load_row32<T>(a.a, nr, nn, M, N, na);
+                    continue;
                 }
-                if (m >= M || n >= N) continue;  // the same for the whole warp
                 float v[32];
                 tc_ld32(acc, v);
                 uint4 w[4];
@@ -589,43 +640,51 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                         pack32<T>(v, w);
                         store.whole(a.out[0], n, m, M, N, w);
                     } else {
-                        uint4 ws[4], wa[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            float fh[8], fs[8], fa[8];
+                            float fh[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const FfnGate r = ffn_gate<true>(a.act, v[8 * j + e]);
-                                fa[e] = r.act;
-                                fs[e] = u[8 * j + e] * r.slope;
                                 fh[e] = r.act * u[8 * j + e];
+                                u[8 * j + e] *= r.slope;  // s
+                                v[8 * j + e] = r.act;     // a
                             }
                             w[j] = Vec<T>::pack(fh);
-                            ws[j] = Vec<T>::pack(fs);
-                            wa[j] = Vec<T>::pack(fa);
                         }
                         store.whole(a.out[0], n, m, M, N, w);
-                        store.whole(a.out[1], n, m, M, N, ws);
-                        store.whole(a.out[2], n, m, M, N, wa);
+                        store.whole32(a.out[1], n, m, M, N, u);
+                        store.whole32(a.out[2], n, m, M, N, v);
                     }
                 } else if constexpr (MODE == kDact) {
-                    float f[32], o[32];
-                    unpack32<T>(cs, f);
+                    store.put32(v);
+                    const int64_t col = n + 4 * (lane & 7);
+                    T* dg = static_cast<T*>(a.out[0]) + m * N + col;
+                    T* du = static_cast<T*>(a.out[1]) + m * N + col;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
-                    pack32<T>(o, w);
-                    store.whole(a.out[0], n, m, M, N, w);
-                    unpack32<T>(ca, f);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = v[j] * f[j] * a.scale[0];
-                    pack32<T>(o, w);
-                    store.whole(a.out[1], n, m, M, N, w);
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = store.piece_row(i);
+                        float4 d = store.piece(i);
+                        d.x *= a.scale[0];
+                        d.y *= a.scale[0];
+                        d.z *= a.scale[0];
+                        d.w *= a.scale[0];
+                        if (m + r < M && col < N) {
+                            const float f[8] = {d.x * ps[i].x, d.y * ps[i].y, d.z * ps[i].z, d.w * ps[i].w,
+                                                d.x * pa[i].x, d.y * pa[i].y, d.z * pa[i].z, d.w * pa[i].w};
+                            const uint4 o = Vec<T>::pack(f);
+                            *reinterpret_cast<uint2*>(dg + r * N) = make_uint2(o.x, o.y);
+                            *reinterpret_cast<uint2*>(du + r * N) = make_uint2(o.z, o.w);
+                        }
+                    }
+                    load_pieces(a.s, nn, nm, M, N, lane, ps);
+                    load_pieces(a.a, nn, nm, M, N, lane, pa);
                 } else {
                     if constexpr (MODE == kDw) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] *= a.scale[p];
                     }
-                    if constexpr (MODE == kDown) ffn_drop_res<T>(a, key, row, n, v);
+                    if constexpr (MODE == kDown) ffn_drop_res<T>(a, key, m + lane, n, v);
                     pack32<T>(v, w);
                     const int pi = MODE == kDw ? p : 0;
                     if (a.odd[pi]) store.odd(a.out[pi], n, m, M, N, w);
@@ -940,8 +999,8 @@ extern "C" size_t ce_ffn_fwd_workspace_bytes(int64_t rows, int64_t H, int64_t I,
 extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up,
                                 const void* w_down, const void* residual, int dtype, int64_t rows,
                                 int64_t H, int64_t I, int64_t O, int act, double p, uint64_t seed,
-                                uint64_t offset, const int64_t* state, void* y, void* h, void* s,
-                                void* a, void* workspace, size_t workspace_bytes,
+                                uint64_t offset, const int64_t* state, void* y, void* h, float* s,
+                                float* a, void* workspace, size_t workspace_bytes,
                                 ce_stream_t stream) {
     ce_status rc = check_ffn(dtype, rows, H, I, O, act);
     if (rc != CE_OK) return rc;
@@ -1008,7 +1067,7 @@ extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I,
 
 extern "C" ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate,
                                 const void* w_up, const void* w_down, const void* h,
-                                const void* s, const void* a, int dtype, int64_t rows, int64_t H,
+                                const float* s, const float* a, int dtype, int64_t rows, int64_t H,
                                 int64_t I, int64_t O, int act, double p, uint64_t seed,
                                 uint64_t offset, const int64_t* state, void* dx, void* dw_gate,
                                 void* dw_up, void* dw_down, void* workspace,

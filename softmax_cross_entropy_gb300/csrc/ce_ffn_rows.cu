@@ -266,8 +266,8 @@ struct RowsJoin {
     int64_t cols, pitch;  // I and I8, or O and O
     int act;
     void* out;  // h or y
-    void* s;    // or nullptr
-    void* a;
+    float* s;   // or nullptr
+    float* a;
     const void* res;
     DropSpec drop;
 };
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kRowsTile) ffn_rows_act(const __grid_constant_
     const int64_t at = row * j.pitch + c;
     Vec<T>::store1(j.out, at, h);
     if (j.s) {
-        Vec<T>::store1(j.s, at, s);
-        Vec<T>::store1(j.a, at, a);
+        j.s[at] = s;
+        j.a[at] = a;
     }
 }
 
@@ -419,7 +419,7 @@ int64_t ffn_rows_workspace(int64_t rows, int64_t H8, int64_t I8, int64_t O, int 
 ce_status ffn_rows_fwd(const void* x, const void* w_gate, const void* w_up, const void* w_down,
                        const void* residual, int dtype, int64_t rows, int64_t H8, int64_t I,
                        int64_t I8, int64_t O, int act, const DropSpec& drop, void* y, void* h,
-                       void* s, void* a, void* workspace, int sms, uint64_t timeout_ns,
+                       float* s, float* a, void* workspace, int sms, uint64_t timeout_ns,
                        unsigned* status, cudaStream_t st) {
     const int64_t ti = (I8 + kRowsTile - 1) / kRowsTile, to = (O + kRowsTile - 1) / kRowsTile;
     const RowsPlan up = rows_plan(2 * ti, H8, rows, sms), down = rows_plan(to, I8, rows, sms);

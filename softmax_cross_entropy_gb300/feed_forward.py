@@ -25,37 +25,38 @@ _ACTIVATIONS = {"silu": _lib.CE_ACT_SILU, "gelu": _lib.CE_ACT_GELU,
 
 
 def _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad):
-    """(y, what the backward needs of the block: h and, with grad, u act'(g)
-    and act(g), each [rows, I] in rows of whole 16-byte vectors)."""
+    """(y, h, sa): h [rows, I] in rows of whole 16-byte vectors and, with grad,
+    u act'(g) and act(g) in float32 [2, rows, I] likewise, for the backward."""
     rows, H = x.shape
     O, I = w_down.shape
     dev, dt = x.device, x.dtype
     y = torch.empty((rows, O), dtype=dt, device=dev)
     I8 = (I + 7) // 8 * 8
-    kept = torch.empty((3 if grad else 1, rows, I8), dtype=dt, device=dev)
-    h, step = kept.data_ptr(), rows * I8 * 2
-    s, a = (h + step, h + 2 * step) if grad else (None, None)
+    h = torch.empty((rows, I8), dtype=dt, device=dev)
+    sa = torch.empty((2, rows, I8), dtype=torch.float32, device=dev) if grad else None
+    s = sa.data_ptr() if grad else None
+    a = s + rows * I8 * 4 if grad else None
     with on(dev):
         nbytes = _lib.ce_ffn_fwd_workspace_bytes(rows, H, I, O)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         check(_lib.ce_ffn_fwd(ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(residual),
                               DTYPES[dt], rows, H, I, O, act, p, seed, offset, ptr(state), ptr(y),
-                              h, s, a, ptr(ws), nbytes, stream(dev)), "ce_ffn_fwd")
-    return y, kept
+                              ptr(h), s, a, ptr(ws), nbytes, stream(dev)), "ce_ffn_fwd")
+    return y, h, sa
 
 
 class GatedFeedForwardFunction(torch.autograd.Function):
     """Autograd wrapper of ce_ffn_fwd and ce_ffn_bwd on [rows, H] inputs. The
-    forward keeps x and three [rows, I] tensors (h, u act'(g) and act(g))."""
+    forward keeps x and, [rows, I] each, h and in float32 u act'(g) and act(g)."""
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, residual, act, p, seed, offset, state):
         grad = any(ctx.needs_input_grad[:4])
         if grad and state is not None and p > 0.0:
             state = state.clone()  # the caller may change it before the backward runs
-        y, kept = _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad)
+        y, h, sa = _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad)
         if grad:
-            ctx.save_for_backward(x, w_gate, w_up, w_down, kept, state)
+            ctx.save_for_backward(x, w_gate, w_up, w_down, h, sa, state)
         ctx.args = (act, p, seed, offset)
         return y
 
@@ -65,7 +66,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx = dwg = dwu = dwd = None
         if any(need[:4]):
-            x, w_gate, w_up, w_down, kept, state = ctx.saved_tensors
+            x, w_gate, w_up, w_down, h, sa, state = ctx.saved_tensors
             act, p, seed, offset = ctx.args
             rows, H = x.shape
             O, I = w_down.shape
@@ -76,11 +77,11 @@ class GatedFeedForwardFunction(torch.autograd.Function):
                 dwg, dwu = torch.empty_like(w_gate), torch.empty_like(w_up)
             dwd = torch.empty_like(w_down) if need[3] else None
             nbytes = _lib.ce_ffn_bwd_workspace_bytes(rows, H, I, O, p)
-            h, step = kept.data_ptr(), kept.stride(0) * 2
+            s = sa.data_ptr()
             with on(dev):
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-                check(_lib.ce_ffn_bwd(ptr(g), ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), h,
-                                      h + step, h + 2 * step, DTYPES[dt], rows, H, I, O, act, p,
+                check(_lib.ce_ffn_bwd(ptr(g), ptr(x), ptr(w_gate), ptr(w_up), ptr(w_down), ptr(h),
+                                      s, s + sa.stride(0) * 4, DTYPES[dt], rows, H, I, O, act, p,
                                       seed, offset, ptr(state), ptr(dx), ptr(dwg), ptr(dwu),
                                       ptr(dwd), ptr(ws), nbytes, stream(dev)), "ce_ffn_bwd")
         return (dx, dwg if need[1] else None, dwu if need[2] else None, dwd,
@@ -111,7 +112,7 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
     None or [..., O], all bfloat16 or float16 on one CUDA device; activation
     "silu", "gelu" or "gelu_tanh". dropout_p, seed and offset as for dropout()
     over the [..., O] elements. Differentiable in x, the weights and residual;
-    for that the forward keeps x and three [..., I] tensors.
+    for that the forward keeps x and 10 bytes for each of the [..., I] elements.
 
     H, I and O that are not multiples of 8 cost a packed copy of what they
     concern (x and the projections for H, down_weight for I) on each call."""
