@@ -18,9 +18,11 @@
 //     warps merge the part's logits into sorted lists instead, 32 at a time
 //     by a bitonic network.
 //  2. beam_pick, a CTA a batch entry, forms the K log-sum-exps from the
-//     {max, sum} in a fixed order, takes the M-th best of the lists' first
-//     candidates as a bound (no list that starts below it can contribute),
-//     and ranks the candidates above it by counting.
+//     {max, sum} in a fixed order and the scores of the lists' candidates, and
+//     merges the lists: a warp holds their first candidates and takes the best
+//     M times. (Where the lists are many, the M-th best of their first
+//     candidates bounds what can matter, and what reaches it is ranked by
+//     counting.)
 // Candidates are ordered by (score in 48 bits, then lowest k V + v), so ties
 // and the order in which warps finish do not show in the result.
 //
@@ -92,8 +94,8 @@ struct BeamArgs {
     int64_t* out_tokens;
 };
 
-// The most shared memory that beam_pick takes: 32 beams of 64 parts and 64
-// candidates squared, or staged lists below that.
+// The most shared memory that beam_pick takes: 32 beams of 128 parts and 64
+// candidates squared, or all lists' candidates below that.
 constexpr size_t kPickSmem = 16 * (kMaxBeams * kMaxSplits + kMaxCandidates * kMaxCandidates);
 
 // Whether beam `row` has candidates of its own (a finite score, not finished).
@@ -550,18 +552,76 @@ __device__ __forceinline__ int quad_rank(const Pick* all, int n, const Pick& p) 
     return rank + __shfl_xor_sync(~0u, rank, 2);
 }
 
-// STAGED: the entry's lists are held in shared memory (all the loads at
-// once); else they are read again where needed.
-template <bool STAGED>
+// Place i of entry b has no candidate.
+__device__ __forceinline__ void no_pick(const BeamArgs& a, int64_t b, int i) {
+    a.out_scores[b * a.M + i] = -INFINITY;
+    a.out_beams[b * a.M + i] = -1;
+    a.out_tokens[b * a.M + i] = a.pad;
+}
+
+// The M best of nl sorted lists of M picks, by one warp: lane i holds the
+// first of lists i, i + 32, ...
+constexpr int kMergeLists = 128;
+__device__ __forceinline__ int merge_lists(const BeamArgs& a, const Pick* all, int nl, int64_t b, int lane) {
+    constexpr int R = kMergeLists / 32;
+    Pick head[R];
+    int pos[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int l = lane + 32 * q;
+        pos[q] = 0;
+        head[q] = l < nl ? all[l * a.M] : Pick{0, kNowhere};
+    }
+    for (int r = 0; r < a.M; ++r) {
+        Pick best = head[0];
+#pragma unroll
+        for (int q = 1; q < R; ++q)
+            if (better(head[q], best)) best = head[q];
+        // the warp's best: by score, then (equal ones) by beam and token
+        const uint32_t hi = static_cast<uint32_t>(best.key >> 32);
+        const uint32_t top = __reduce_max_sync(~0u, hi);
+        if (!top) return r;  // no candidate left
+        bool mine = hi == top;
+        unsigned who = __ballot_sync(~0u, mine);
+        if (who & (who - 1)) {
+            // (every lane takes part in each reduction)
+            const uint32_t lo = static_cast<uint32_t>(best.key);
+            const uint32_t most = __reduce_max_sync(~0u, mine ? lo : 0u);
+            mine = mine && lo == most;
+            const uint32_t beam = mine ? static_cast<uint32_t>(best.at >> 32) : ~0u;
+            const uint32_t first = __reduce_min_sync(~0u, beam);
+            mine = mine && beam == first;
+            const uint32_t token = mine ? static_cast<uint32_t>(best.at) : ~0u;
+            const uint32_t least = __reduce_min_sync(~0u, token);
+            mine = mine && token == least;
+        }
+        if (mine) {
+            a.out_scores[b * a.M + r] = unordered(static_cast<uint32_t>(best.key >> 32));
+            a.out_beams[b * a.M + r] = static_cast<int64_t>(best.at >> 32);
+            a.out_tokens[b * a.M + r] = static_cast<int64_t>(best.at & 0xFFFFFFFFu);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (head[q].at != best.at) continue;
+                ++pos[q];
+                head[q] = pos[q] < a.M ? all[(lane + 32 * q) * a.M + pos[q]] : Pick{0, kNowhere};
+                break;
+            }
+        }
+    }
+    return a.M;
+}
+
+// MERGE: the entry has at most kMergeLists lists, whose candidates fit in
+// shared memory.
+template <bool MERGE>
 __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant__ BeamArgs a) {
     extern __shared__ Pick pick_smem[];
     __shared__ BeamInfo info[kMaxBeams];
     __shared__ Pick bound;
     __shared__ int nsurv;
     const int nl = a.K * a.splits;
-    Pick* heads = pick_smem;  // [nl]
+    Pick* heads = pick_smem;  // [nl], or MERGE: all candidates [nl, M]
     Pick* surv = heads + nl;  // [M M]
-    uint64_t* words = reinterpret_cast<uint64_t*>(surv + a.M * a.M);  // [nl, M], STAGED
     const int64_t b = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t* lists = a.lists + b * nl * a.M;
@@ -570,8 +630,16 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
         nsurv = 0;
     }
     pdl_wait();
-    if (STAGED)
-        for (int i = threadIdx.x; i < nl * a.M; i += kPickThreads) words[i] = lists[i];
+    // the lists' words, on their way while the log-sum-exps are formed
+    constexpr int kHold = 8;
+    uint64_t held[kHold];
+    if (MERGE) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int at = threadIdx.x + i * kPickThreads;
+            held[i] = at < nl * a.M ? lists[at] : 0;
+        }
+    }
     for (int k = warp; k < a.K; k += kPickThreads / 32) {
         const int64_t row = b * a.K + k;
         const float score = a.scores[row];
@@ -615,11 +683,26 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
         }
     }
     __syncthreads();
-    const auto at = [&](int l, int i) {
+    const auto pick_of = [&](int l, int i, uint64_t w) {
         const int k = l / a.splits;
-        const uint64_t w = STAGED ? words[l * a.M + i] : lists[static_cast<int64_t>(l) * a.M + i];
         return word_pick(info[k], k, w, i == 0 && l == k * a.splits, a.pad);
     };
+    if constexpr (MERGE) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int at = threadIdx.x + i * kPickThreads;
+            if (at < nl * a.M) heads[at] = pick_of(at / a.M, at % a.M, held[i]);
+        }
+        for (int at = threadIdx.x + kHold * kPickThreads; at < nl * a.M; at += kPickThreads)
+            heads[at] = pick_of(at / a.M, at % a.M, lists[at]);
+        __syncthreads();
+        if (warp == 0) {
+            const int n = merge_lists(a, heads, nl, b, lane);
+            for (int i = n + lane; i < a.M; i += 32) no_pick(a, b, i);
+        }
+        return;
+    }
+    const auto at = [&](int l, int i) { return pick_of(l, i, lists[static_cast<int64_t>(l) * a.M + i]); };
     for (int l = threadIdx.x; l < nl; l += kPickThreads) heads[l] = at(l, 0);
     __syncthreads();
     // the M-th best of the lists' first candidates
@@ -660,11 +743,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant_
             a.out_tokens[b * a.M + rank] = static_cast<int64_t>(p.at & 0xFFFFFFFFu);
         }
     }
-    for (int i = n + threadIdx.x; i < a.M; i += kPickThreads) {
-        a.out_scores[b * a.M + i] = -INFINITY;
-        a.out_beams[b * a.M + i] = -1;
-        a.out_tokens[b * a.M + i] = a.pad;
-    }
+    for (int i = n + threadIdx.x; i < a.M; i += kPickThreads) no_pick(a, b, i);
 }
 
 // ---------------------------------------------------------------- states
@@ -871,11 +950,10 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     cudaError_t e = cudaLaunchKernel(scan, dim3(static_cast<unsigned>(plan.grid)), dim3(kScanThreads), args,
                                      16 * static_cast<size_t>(plan.part_vec + 1), st);
     if (e != cudaSuccess) return record_cuda_failure(e, "beam scan launch");
-    size_t smem = sizeof(Pick) * static_cast<size_t>(K * a.splits + M * M);
-    const size_t words = 8 * static_cast<size_t>(K * a.splits * M);
-    const bool staged = smem + words <= kPickSmem;
-    if (staged) smem += words;
-    const void* pick = staged ? (const void*)&beam_pick<true> : (const void*)&beam_pick<false>;
+    const size_t lists_n = static_cast<size_t>(K * a.splits), all = sizeof(Pick) * lists_n * M;
+    const bool merge = lists_n <= kMergeLists && all <= kPickSmem;
+    const size_t smem = merge ? all : sizeof(Pick) * (lists_n + static_cast<size_t>(M * M));
+    const void* pick = merge ? (const void*)&beam_pick<true> : (const void*)&beam_pick<false>;
     if (smem > 48 * 1024) {
         rc = tc_smem_limit(pick, kPickSmem);
         if (rc != CE_OK) return rc;
