@@ -29,8 +29,11 @@
 // not a multiple of 8) are packed into rows of such a length by a kernel of
 // their own first.
 //
-// Bound by the tensor cores from about 600 rows on (6 rows H I operations on
-// 6 H I bytes of weights); ce_ffn_rows.cu takes few rows.
+// Bound by the tensor cores from about 300 rows on (6 rows H I operations on
+// 6 H I bytes of weights); ce_ffn_rows.cu takes few rows. (Starting a launch
+// early, by programmatic dependence, as the form for few rows does, gained
+// nothing at 1023 rows and cost 3% of a training step, whose waiting CTAs
+// draw power.)
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -966,8 +969,8 @@ struct FfnPacker {
 
 // The most rows that take the form for few rows, whose products have at most
 // 256 columns. Measured, bf16, forward with residual: H 4096, I 12288: 1 row
-// 64 against 124 us for the tiles, 64 rows 73 / 116, 256 rows 119 / 129; H
-// 1024, I 4096: 16 / 36, 20 / 37 and 35 / 38.
+// 61 against 124 us for the tiles, 64 rows 66 / 116, 256 rows 94 / 129; H
+// 1024, I 4096: 15 / 36, 17 / 37 and 27 / 38.
 constexpr int64_t kFewRows = 256;
 
 // Output i of a launch, with rows of `cols` elements.

@@ -90,6 +90,16 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
     const uint32_t smem0 = (smem_u32(rows_smem_raw) + 1023u) & ~1023u;
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * a.per;
     const int64_t u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
+    // the units of the ring's first round
+    const int pre = static_cast<int>(u1 - u0 < a.stages ? u1 - u0 : a.stages);
+    const uint64_t once = l2_evict_first_policy();
+    const auto load_a = [&](int64_t u, uint32_t slot, uint32_t bar) {
+        const int64_t t = u / a.nk;
+        const int k0 = static_cast<int>(u - t * a.nk) * kBK;
+        const bool second = t >= a.tiles0;
+        rows_load_once(slot, second ? &map1 : &map0, k0,
+                       static_cast<int>((second ? t - a.tiles0 : t) * kRowsTile), bar, once);
+    };
     if (threadIdx.x == 0) {
         rows_prefetch_map(&map0);
         rows_prefetch_map(&map1);
@@ -106,6 +116,13 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
         mbar_init(smem_u32(&done_bar), 1);
         s_fail = 0;
         fence_mbar_init();
+        // the first round's weights, before anything else is set up
+        for (int s = 0; s < pre; ++s) {
+            const uint32_t fb = smem_u32(&full_bar[s]);
+            mbar_arrive_expect_tx(fb, a.stage_bytes);
+            load_a(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, fb);
+            s_issued[s] = 2u;
+        }
     }
     if (warp == 1) {
         asm volatile(
@@ -123,26 +140,11 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t once = l2_evict_first_policy();
-            const auto load_a = [&](int64_t u, uint32_t slot, uint32_t bar) {
-                const int64_t t = u / a.nk;
-                const int k0 = static_cast<int>(u - t * a.nk) * kBK;
-                const bool second = t >= a.tiles0;
-                rows_load_once(slot, second ? &map1 : &map0, k0,
-                               static_cast<int>((second ? t - a.tiles0 : t) * kRowsTile), bar, once);
-            };
             const auto load_x = [&](int64_t u, uint32_t slot, uint32_t bar) {
                 tma_load_2d(slot + kRowsA, &mapx, static_cast<int>(u % a.nk) * kBK, 0, bar);
             };
-            // the ring's first round: the weights, then (once the launch that
-            // writes them is done) the tokens
-            const int pre = static_cast<int>(u1 - u0 < a.stages ? u1 - u0 : a.stages);
-            for (int s = 0; s < pre; ++s) {
-                const uint32_t fb = smem_u32(&full_bar[s]);
-                mbar_arrive_expect_tx(fb, a.stage_bytes);
-                load_a(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, fb);
-                s_issued[s] = 2u;
-            }
+            // the tokens of the ring's first round, once the launch that writes
+            // them is done
             pdl_wait();
             for (int s = 0; s < pre; ++s)
                 load_x(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, smem_u32(&full_bar[s]));
@@ -263,6 +265,7 @@ struct RowsJoin {
     const float* sums;
     int64_t per, tiles0;
     int nk, parts, rows;
+    int vec;  // y's rows are whole 8-byte vectors
     int64_t cols, pitch;  // I and I8, or O and O
     int act;
     void* out;  // h or y
@@ -272,70 +275,129 @@ struct RowsJoin {
     DropSpec drop;
 };
 
-// The parts of tile t for one token, added in order; the loads of the first
-// eight are on their way together.
-__device__ __forceinline__ float join_parts(const RowsJoin& j, int64_t t, int row) {
+// The parts of tile t for one token, added in order: this lane's four
+// columns. The loads of the first eight are on their way together.
+__device__ __forceinline__ void join_parts(const RowsJoin& j, int64_t t, int row, int lane, float (&sum)[4]) {
     const int n = rows_parts(t, j.nk, j.per);
-    const float* p = j.sums + ((t * j.parts) * j.rows + row) * kRowsTile + threadIdx.x;
-    const int64_t step = static_cast<int64_t>(j.rows) * kRowsTile;
-    float v[8];
+    const float4* p = reinterpret_cast<const float4*>(j.sums + ((t * j.parts) * j.rows + row) * kRowsTile) + lane;
+    const int64_t step = static_cast<int64_t>(j.rows) * (kRowsTile / 4);
+    float4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldcg(p + i * step) : 0.f;
-    float sum = v[0];
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldcg(p + i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = v[0];
+    const auto add = [&s](const float4& q) {
+        s.x += q.x;
+        s.y += q.y;
+        s.z += q.z;
+        s.w += q.w;
+    };
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += v[i];
-    for (int i = 8; i < n; ++i) sum += __ldcg(p + i * step);
-    return sum;
+    for (int i = 1; i < 8; ++i) add(v[i]);
+    for (int i = 8; i < n; ++i) add(__ldcg(p + i * step));
+    sum[0] = s.x;
+    sum[1] = s.y;
+    sum[2] = s.z;
+    sum[3] = s.w;
 }
 
-// h = act(g) u (and s, a) of one token and 128 columns.
+// Four values as 16 bits each.
 template <typename T>
-__global__ void __launch_bounds__(kRowsTile) ffn_rows_act(const __grid_constant__ RowsJoin j) {
+__device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
+    const float t[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+    const uint4 w = Vec<T>::pack(t);
+    return make_uint2(w.x, w.y);
+}
+
+// A warp a (token, 128 columns), a lane four columns.
+constexpr int kJoinThreads = 256;
+
+// h = act(g) u (and s, a).
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) ffn_rows_act(const __grid_constant__ RowsJoin j) {
     pdl_launch_dependents();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int row = static_cast<int>(i / j.tiles0);
+    const int64_t tile = i - row * j.tiles0;
+    const int64_t c = tile * kRowsTile + 4 * lane;
     pdl_wait();
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowsTile + threadIdx.x;
-    const int row = blockIdx.y;
-    if (c >= j.pitch) return;
-    float h = 0.f, s = 0.f, a = 0.f;
-    if (c < j.cols) {
-        const float g = join_parts(j, blockIdx.x, row);
-        const float u = join_parts(j, j.tiles0 + blockIdx.x, row);
-        const FfnGate r = ffn_gate<true>(j.act, g);
-        a = r.act;
-        h = a * u;
-        s = u * r.slope;
+    if (row >= j.rows || c >= j.pitch) return;
+    float g[4], u[4], h[4];
+    join_parts(j, tile, row, lane, g);
+    join_parts(j, j.tiles0 + tile, row, lane, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        // (columns behind the last: rows of weights that are not there, zeros)
+        const FfnGate r = ffn_gate<true>(j.act, g[e]);
+        const bool in = c + e < j.cols;
+        h[e] = in ? r.act * u[e] : 0.f;
+        u[e] = in ? u[e] * r.slope : 0.f;
+        g[e] = in ? r.act : 0.f;
     }
     const int64_t at = row * j.pitch + c;
-    Vec<T>::store1(j.out, at, h);
+    *reinterpret_cast<uint2*>(static_cast<T*>(j.out) + at) = pack4<T>(h);
     if (j.s) {
-        j.s[at] = s;
-        j.a[at] = a;
+        *reinterpret_cast<float4*>(j.s + at) = make_float4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<float4*>(j.a + at) = make_float4(g[0], g[1], g[2], g[3]);
     }
 }
 
-// y = residual + dropout(z) of one token and 128 columns.
+// y = residual + dropout(z).
 template <typename T>
-__global__ void __launch_bounds__(kRowsTile) ffn_rows_out(const __grid_constant__ RowsJoin j) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowsTile + threadIdx.x;
-    const int row = blockIdx.y;
-    if (c >= j.cols) return;
+__global__ void __launch_bounds__(kJoinThreads) ffn_rows_out(const __grid_constant__ RowsJoin j) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int row = static_cast<int>(i / j.tiles0);
+    const int64_t tile = i - row * j.tiles0;
+    const int64_t c = tile * kRowsTile + 4 * lane;
+    if (row >= j.rows || c >= j.cols) return;
     const int64_t at = row * j.cols + c;
+    const int n = j.cols - c < 4 ? static_cast<int>(j.cols - c) : 4;
     // what no launch of this call writes, before the wait
-    const float res = j.res ? Vec<T>::load1(j.res, at) : 0.f;
-    float factor = j.drop.mode == kDropAll ? 0.f : 1.f;
+    float res[4] = {0.f, 0.f, 0.f, 0.f}, factor[4];
+    const bool drop = j.drop.mode != kDropNone;
+    PhiloxKey key{};
+    if (j.drop.mode == kDropSome) key = philox_key(j.drop);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (j.res && e < n) res[e] = Vec<T>::load1(j.res, at + e);
+        factor[e] = j.drop.mode == kDropNone ? 1.f : 0.f;
+    }
     if (j.drop.mode == kDropSome) {
-        const PhiloxKey key = philox_key(j.drop);
-        const uint4 w = philox4x32(key, static_cast<uint64_t>(at) >> 2);
-        const uint32_t l = static_cast<uint32_t>(at) & 3u;
-        const uint32_t word = l == 0 ? w.x : l == 1 ? w.y : l == 2 ? w.z : w.w;
-        factor = word >= j.drop.threshold ? j.drop.scale : 0.f;
+        uint64_t block = static_cast<uint64_t>(at) >> 2;
+        uint4 w = philox4x32(key, block);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t k = static_cast<uint64_t>(at + e);
+            if (k >> 2 != block) {
+                block = k >> 2;
+                w = philox4x32(key, block);
+            }
+            const uint32_t l = static_cast<uint32_t>(k) & 3u;
+            const uint32_t word = l == 0 ? w.x : l == 1 ? w.y : l == 2 ? w.z : w.w;
+            factor[e] = word >= j.drop.threshold ? j.drop.scale : 0.f;
+        }
     }
     pdl_wait();
-    const float v = join_parts(j, blockIdx.x, row);
-    Vec<T>::store1(j.out, at, (factor != 0.f ? v * factor : 0.f) + res);
+    float z[4];
+    join_parts(j, tile, row, lane, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // (a dropped element leaves nothing, whatever it holds)
+        z[e] = (drop ? (factor[e] != 0.f ? z[e] * factor[e] : 0.f) : z[e]) + res[e];
+    if (j.vec && n == 4) {
+        *reinterpret_cast<uint2*>(static_cast<T*>(j.out) + at) = pack4<T>(z);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) Vec<T>::store1(j.out, at + e, z[e]);
+    }
 }
 
 int64_t up256r(int64_t b) { return (b + 255) / 256 * 256; }
+
+unsigned join_grid(int64_t tiles, int64_t rows) {
+    return static_cast<unsigned>((tiles * rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+}
 
 // How a product of `tiles` weight tiles and K columns is dealt out to `sms`.
 struct RowsPlan {
@@ -446,8 +508,8 @@ ce_status ffn_rows_fwd(const void* x, const void* w_gate, const void* w_up, cons
     j.a = a;
     void* args[] = {&j};
     rc = rows_pdl(bf ? (const void*)&ffn_rows_act<__nv_bfloat16> : (const void*)&ffn_rows_act<__half>,
-                  dim3(static_cast<unsigned>(ti), static_cast<unsigned>(rows)), kRowsTile, 0, true,
-                  args, st, "feed-forward activation launch");
+                  dim3(join_grid(ti, rows)), kJoinThreads, 0, true, args, st,
+                  "feed-forward activation launch");
     if (rc != CE_OK) return rc;
     rc = rows_product(down, dtype, w_down, nullptr, O, h, rows, I8, sums_down, true, timeout_ns,
                       status, st);
@@ -456,13 +518,15 @@ ce_status ffn_rows_fwd(const void* x, const void* w_gate, const void* w_up, cons
     j.per = down.per;
     j.nk = down.nk;
     j.parts = down.parts;
+    j.tiles0 = to;
     j.cols = j.pitch = O;
+    j.vec = O % 4 == 0 && reinterpret_cast<uintptr_t>(y) % 8 == 0 ? 1 : 0;
     j.out = y;
     j.res = residual;
     j.drop = drop;
     return rows_pdl(bf ? (const void*)&ffn_rows_out<__nv_bfloat16> : (const void*)&ffn_rows_out<__half>,
-                    dim3(static_cast<unsigned>(to), static_cast<unsigned>(rows)), kRowsTile, 0, true,
-                    args, st, "feed-forward output launch");
+                    dim3(join_grid(to, rows)), kJoinThreads, 0, true, args, st,
+                    "feed-forward output launch");
 }
 
 }  // namespace gbce
