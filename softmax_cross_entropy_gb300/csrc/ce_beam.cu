@@ -4,7 +4,7 @@
 //
 // Selection. With lse_k = log sum_v exp(x_kv), candidate (k, v) has the score
 // s_k + x_kv - lse_k, so within a beam the order is that of the logits:
-//  1. beam_scan reads every logit once, in parts of a row of up to 40 KB that
+//  1. beam_scan reads every logit once, in parts of a row of up to 44 KB that
 //     a CTA stages in shared memory (cp.async; four CTAs an SM, so that parts
 //     are on their way while others are worked on) and passes over twice.
 //     The first pass takes each thread's largest logit. From these come the
@@ -28,7 +28,7 @@
 //
 // One read of the logits; the scan is bound by the instructions of its two
 // passes (about 8 a logit of 16 bits and 20 a logit of 32, issue slots 55-60%
-// taken): 64 x 8 x 131072 fp32 72 us (3.7 TB/s), bf16 47 us (2.9 TB/s). The
+// taken): 64 x 8 x 131072 fp32 66 us (4.1 TB/s), bf16 45 us (3 TB/s). The
 // reordering is bound by HBM: 2 x 134 MB of states in 67 us.
 #include <algorithm>
 #include <cstdint>
@@ -47,14 +47,14 @@ namespace {
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kScanCtas = 4;        // CTAs an SM
-constexpr int kScanMost = 2560;     // 16-byte vectors of a part at most
+constexpr int kScanMost = 2816;     // 16-byte vectors of a part at most (44 KB)
 constexpr int kScanList = 512;      // logits of a part that may reach the bound
 constexpr int kScanBuf = 64;        // words of a warp's buffer when merging
 constexpr int kPickThreads = 256;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxCandidates = 64;
 constexpr int kMaxSplits = 128;     // parts a row
-constexpr int64_t kMaxVocab = 1 << 20;  // 103 parts of fp32
+constexpr int64_t kMaxVocab = 1 << 20;  // 94 parts of fp32
 constexpr float kLowest = -3.402823466e38f;
 
 // A candidate inside a row: the logit as an ordered integer above the
@@ -281,6 +281,7 @@ struct ScanShared {
     uint64_t lasts[kScanWarps];
     uint32_t tops[kScanWarps * 8];  // the warps' t largest threads, as ordered integers
     float sums[kScanWarps];
+    uint32_t top, bound;
     int found;
 };
 
@@ -438,10 +439,15 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan(const __gri
         __syncthreads();
         // ---- the maximum, and the bound (0: too few threads have a logit)
         uint32_t top, bound;
-        if (small) {  // M of the 8 t = 32 values, sorted over the lanes
-            const uint32_t o = warp_sort_desc(sh.tops[lane], lane);
-            top = __shfl_sync(~0u, o, 0);
-            bound = __shfl_sync(~0u, o, a.M - 1);
+        if (small) {  // M of the 8 t = 32 values, sorted over a warp's lanes
+            if (warp == 0) {
+                const uint32_t o = warp_sort_desc(sh.tops[lane], lane);
+                if (lane == 0) sh.top = o;
+                if (lane == a.M - 1) sh.bound = o;
+            }
+            __syncthreads();
+            top = sh.top;
+            bound = sh.bound;
         } else {  // every warp has t such threads
             top = __reduce_max_sync(~0u, lane < kScanWarps ? sh.tops[lane * t] : 0u);
             bound = __reduce_min_sync(~0u, lane < kScanWarps ? sh.tops[lane * t + t - 1] : ~0u);

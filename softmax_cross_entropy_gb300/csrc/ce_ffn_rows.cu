@@ -36,10 +36,11 @@ constexpr int kRowsThreads = 192;  // producer, MMA issuer, 4 epilogue warps
 constexpr int kRowsTile = 128;     // weight rows of a tile
 constexpr uint32_t kRowsA = kRowsTile * kBK * 2;  // 16 KB
 constexpr int kRowsStages = 11;
-// The ring: two CTAs an SM where that leaves it 4 units or more (up to 64
-// tokens), so that the second product's ring fills while the first product
-// still runs; else one.
-constexpr uint32_t kRowsSmemTwo = 110 * 1024, kRowsSmemOne = 200 * 1024;
+// The ring: where three units or more fit in the smaller (up to 96 tokens),
+// two CTAs an SM, so that the second product's ring fills while the first
+// product still runs; else one. (Rings of 110 KB each: 60 us for 1 token of
+// 4096 x 12288, 130 and 92 KB 59 us, 148 and 74 KB 60 us.)
+constexpr uint32_t kRowsSmemUp = 130 * 1024, kRowsSmemDown = 92 * 1024, kRowsSmemOne = 200 * 1024;
 
 struct RowsArgs {
     int64_t units, per;  // tiles x K blocks; of a CTA
@@ -90,14 +91,15 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
     const uint32_t smem0 = (smem_u32(rows_smem_raw) + 1023u) & ~1023u;
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * a.per;
     const int64_t u1 = u0 + a.per < a.units ? u0 + a.per : a.units;
-    // the units of the ring's first round
+    // the units of the ring's first round; a unit as its tile and K block,
+    // stepped without divisions (H 1024, I 4096: 13.4 instead of 14.7 us)
     const int pre = static_cast<int>(u1 - u0 < a.stages ? u1 - u0 : a.stages);
+    const int64_t tile_first = u0 / a.nk;
+    const int kb_first = static_cast<int>(u0 - tile_first * a.nk);
     const uint64_t once = l2_evict_first_policy();
-    const auto load_a = [&](int64_t u, uint32_t slot, uint32_t bar) {
-        const int64_t t = u / a.nk;
-        const int k0 = static_cast<int>(u - t * a.nk) * kBK;
+    const auto load_a = [&](int64_t t, int kb, uint32_t slot, uint32_t bar) {
         const bool second = t >= a.tiles0;
-        rows_load_once(slot, second ? &map1 : &map0, k0,
+        rows_load_once(slot, second ? &map1 : &map0, kb * kBK,
                        static_cast<int>((second ? t - a.tiles0 : t) * kRowsTile), bar, once);
     };
     if (threadIdx.x == 0) {
@@ -117,11 +119,16 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
         s_fail = 0;
         fence_mbar_init();
         // the first round's weights, before anything else is set up
-        for (int s = 0; s < pre; ++s) {
+        int64_t t = tile_first;
+        for (int s = 0, kb = kb_first; s < pre; ++s) {
             const uint32_t fb = smem_u32(&full_bar[s]);
             mbar_arrive_expect_tx(fb, a.stage_bytes);
-            load_a(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, fb);
+            load_a(t, kb, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, fb);
             s_issued[s] = 2u;
+            if (++kb == a.nk) {
+                kb = 0;
+                ++t;
+            }
         }
     }
     if (warp == 1) {
@@ -140,18 +147,26 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
 
     if (warp == 0) {
         if (lane == 0) {
-            const auto load_x = [&](int64_t u, uint32_t slot, uint32_t bar) {
-                tma_load_2d(slot + kRowsA, &mapx, static_cast<int>(u % a.nk) * kBK, 0, bar);
+            const auto load_x = [&](int kb, uint32_t slot, uint32_t bar) {
+                tma_load_2d(slot + kRowsA, &mapx, kb * kBK, 0, bar);
+            };
+            int64_t t = tile_first;
+            int kb = kb_first;
+            const auto step = [&] {
+                if (++kb == a.nk) {
+                    kb = 0;
+                    ++t;
+                }
             };
             // the tokens of the ring's first round, once the launch that writes
             // them is done
             pdl_wait();
-            for (int s = 0; s < pre; ++s)
-                load_x(u0 + s, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, smem_u32(&full_bar[s]));
+            for (int s = 0; s < pre; ++s, step())
+                load_x(kb, smem0 + static_cast<uint32_t>(s) * a.stage_bytes, smem_u32(&full_bar[s]));
             int s = 0;
             uint32_t ph = 1;
             bool fail = false;
-            for (int64_t u = u0 + pre; u < u1; ++u) {
+            for (int64_t u = u0 + pre; u < u1; ++u, step()) {
                 if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
                     fail = true;
                     break;
@@ -159,8 +174,8 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
                 const uint32_t fb = smem_u32(&full_bar[s]);
                 const uint32_t slot = smem0 + static_cast<uint32_t>(s) * a.stage_bytes;
                 mbar_arrive_expect_tx(fb, a.stage_bytes);
-                load_a(u, slot, fb);
-                load_x(u, slot, fb);
+                load_a(t, kb, slot, fb);
+                load_x(kb, slot, fb);
                 s_issued[s] = 2u + ph;
                 if (++s == a.stages) {
                     s = 0;
@@ -177,7 +192,7 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
             int s = 0, run = 0;
             uint32_t ph = 0;
             bool fail = false;
-            int64_t kb = u0 % a.nk;
+            int kb = kb_first;
             for (int64_t u = u0; u < u1; ++u) {
                 const int b = run & 1;
                 const uint32_t acc = tmem + static_cast<uint32_t>(b) * a.acc_cols;
@@ -217,8 +232,9 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
     } else {
         const int q = warp & 3;
         int run = 0;
-        for (int64_t u = u0; u < u1; ++run) {
-            const int64_t t = u / a.nk;
+        int64_t t = tile_first;
+        for (int64_t u = u0; u < u1; ++run, ++t) {
+            const int64_t part = blockIdx.x - rows_first(t, a.nk, a.per);
             const int b = run & 1;
             const bool ok = tc_wait(smem_u32(&acc_full[b]), static_cast<uint32_t>(run >> 1) & 1u,
                                     a.timeout_ns);
@@ -228,7 +244,6 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
             }
             tc_fence_after();
             const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b) * a.acc_cols;
-            const int64_t part = blockIdx.x - rows_first(t, a.nk, a.per);
             float* out = a.sums + ((t * a.parts + part) * a.rows) * kRowsTile + q * 32 + lane;
 #pragma unroll 1
             for (int c = 0; c < a.rows; c += 32) {
@@ -277,8 +292,8 @@ struct RowsJoin {
 
 // The parts of tile t for one token, added in order: this lane's four
 // columns. The loads of the first eight are on their way together.
-__device__ __forceinline__ void join_parts(const RowsJoin& j, int64_t t, int row, int lane, float (&sum)[4]) {
-    const int n = rows_parts(t, j.nk, j.per);
+__device__ __forceinline__ void join_parts(const RowsJoin& j, int64_t t, int n, int row, int lane,
+                                           float (&sum)[4]) {
     const float4* p = reinterpret_cast<const float4*>(j.sums + ((t * j.parts) * j.rows + row) * kRowsTile) + lane;
     const int64_t step = static_cast<int64_t>(j.rows) * (kRowsTile / 4);
     float4 v[8];
@@ -320,11 +335,12 @@ __global__ void __launch_bounds__(kJoinThreads) ffn_rows_act(const __grid_consta
     const int row = static_cast<int>(i / j.tiles0);
     const int64_t tile = i - row * j.tiles0;
     const int64_t c = tile * kRowsTile + 4 * lane;
+    const int ng = rows_parts(tile, j.nk, j.per), nu = rows_parts(j.tiles0 + tile, j.nk, j.per);
     pdl_wait();
     if (row >= j.rows || c >= j.pitch) return;
     float g[4], u[4], h[4];
-    join_parts(j, tile, row, lane, g);
-    join_parts(j, j.tiles0 + tile, row, lane, u);
+    join_parts(j, tile, ng, row, lane, g);
+    join_parts(j, j.tiles0 + tile, nu, row, lane, u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         // (columns behind the last: rows of weights that are not there, zeros)
@@ -378,9 +394,10 @@ __global__ void __launch_bounds__(kJoinThreads) ffn_rows_out(const __grid_consta
             factor[e] = word >= j.drop.threshold ? j.drop.scale : 0.f;
         }
     }
+    const int parts = rows_parts(tile, j.nk, j.per);
     pdl_wait();
     float z[4];
-    join_parts(j, tile, row, lane, z);
+    join_parts(j, tile, parts, row, lane, z);
 #pragma unroll
     for (int e = 0; e < 4; ++e)  // (a dropped element leaves nothing, whatever it holds)
         z[e] = (drop ? (factor[e] != 0.f ? z[e] * factor[e] : 0.f) : z[e]) + res[e];
@@ -444,7 +461,8 @@ ce_status rows_product(const RowsPlan& p, int dtype, const void* w0, const void*
     a.rows = static_cast<int>(rows);
     a.nt = static_cast<int>((rows + 15) / 16 * 16);
     a.stage_bytes = kRowsA + static_cast<uint32_t>(a.nt) * kBK * 2;
-    const uint32_t ring = kRowsSmemTwo / a.stage_bytes >= 4 ? kRowsSmemTwo : kRowsSmemOne;
+    const uint32_t two = pdl ? kRowsSmemDown : kRowsSmemUp;
+    const uint32_t ring = kRowsSmemDown / a.stage_bytes >= 3 ? two : kRowsSmemOne;
     a.stages = std::min<int>(kRowsStages, static_cast<int>(ring / a.stage_bytes));
     a.acc_cols = static_cast<uint32_t>(std::max(a.nt, 32));
     a.tmem_cols = 64;  // a power of two
