@@ -17,6 +17,10 @@ loss over ``logits`` itself (§Backward Pass: the gradient-in-forward trick),
 so the logits' values are gone after the call and backward only scales that
 buffer by grad_output. Every step runs in the CUDA kernels of libgbce.so
 (see include/gbce.h); PyTorch supplies device memory, streams and autograd.
+
+Around the loss: fused_linear_cross_entropy, gated_feed_forward (the block
+whose output it takes), dropout, and for generating beam_search_step and
+beam_reorder.
 """
 from __future__ import annotations
 
