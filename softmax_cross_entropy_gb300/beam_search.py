@@ -60,8 +60,8 @@ def beam_search_step(logits, scores, num_candidates=None, finished=None, pad_tok
                          torch.empty((B, M), dtype=torch.int64, device=dev),
                          torch.empty((B, M), dtype=torch.int64, device=dev))
     dt = DTYPES[logits.dtype]
-    nbytes = _lib.ce_beam_workspace_bytes(dt, B, K, V, M)
     with on(dev):
+        nbytes = _lib.ce_beam_workspace_bytes(dt, B, K, V, M)
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
         check(_lib.ce_beam_select(ptr(logits), dt, B, K, V, ptr(scores), ptr(finished),
                                   int(pad_token), M, ptr(out.scores), ptr(out.beams),

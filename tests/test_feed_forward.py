@@ -204,7 +204,9 @@ def test_gradients_against_differences(act):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,H,I,O", [(1, 7, 9, 5), (37, 33, 65, 33), (130, 1001, 131, 77)])
+@pytest.mark.parametrize("rows,H,I,O", [(1, 7, 9, 5), (37, 33, 65, 33), (130, 1001, 131, 77),
+                                        (300, 65, 131, 77), (513, 128, 203, 300),
+                                        (600, 200, 96, 130)])
 @pytest.mark.parametrize("p,residual", [(0.0, False), (0.25, True)])
 def test_odd_sizes(rows, H, I, O, p, residual):
     import softmax_cross_entropy_gb300 as gbce
@@ -237,6 +239,46 @@ def test_leading_dimensions_strides_and_no_rows():
     assert ye.shape == (0, 64)
     ge, gw = torch.autograd.grad(ye.sum(), [e, w])
     assert ge.shape == (0, 64) and torch.equal(gw, torch.zeros_like(w))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [40, 400])
+def test_unaligned_residual_and_gradient(rows):
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, dy = make(rows, 64, 128, 64, "f16")
+
+    def shifted(t):  # the same values on a base that is not 16-byte aligned
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
+
+    outs = []
+    for r, d in ((res, dy), (shifted(res), shifted(dy))):
+        a = [t.detach().requires_grad_() for t in (x, wg, wu, wd)]
+        y = gbce.gated_feed_forward(*a, residual=r, dropout_p=0.3, seed=2)
+        outs.append([y.detach(), *torch.autograd.grad(y, a, d)])
+    for p, q in zip(*outs):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.gpu
+def test_two_graphs_replayed_at_once():
+    # each graph has its own workspace: replays on two streams do not meet
+    import softmax_cross_entropy_gb300 as gbce
+    sets = [make(40, 256, 512, 256, "bf16", i) for i in range(2)]
+    want = [gbce.gated_feed_forward(*s[:4], residual=s[4]) for s in sets]
+    graphs, outs = [], []
+    for s in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(gbce.gated_feed_forward(*s[:4], residual=s[4]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
 
 
 @pytest.mark.gpu
