@@ -27,8 +27,8 @@
 // and the order in which warps finish do not show in the result.
 //
 // One read of the logits; the scan is bound by the instructions of its two
-// passes (about 8 a logit of 16 bits and 20 a logit of 32, issue slots 55-60%
-// taken): 64 x 8 x 131072 fp32 66 us (4.1 TB/s), bf16 45 us (3 TB/s). The
+// passes (32 logits take a warp 15 of them in 16 bits, 20 in 32; issue slots
+// 55-60% taken): 64 x 8 x 131072 fp32 66 us (4.1 TB/s), bf16 45 us (3 TB/s). The
 // reordering is bound by HBM: 2 x 134 MB of states in 67 us.
 #include <algorithm>
 #include <cstdint>

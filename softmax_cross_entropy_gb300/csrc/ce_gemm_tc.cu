@@ -436,20 +436,19 @@ ce_status encoder(EncodeTiled* out) {
 // swizzle, zeros outside the matrix. A K-major operand is [MN, K] with boxes
 // of 128 or 256 rows; an MN-major one is [K, MN] with boxes of 64 K rows.
 ce_status make_map(CUtensorMap* map, const void* p, int dtype, int64_t outer, int64_t inner,
-                   uint32_t box_outer, uint32_t box_inner = 64u,
-                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                   uint32_t box_outer) {
     EncodeTiled enc = nullptr;
     ce_status rc = encoder(&enc);
     if (rc != CE_OK) return rc;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
-    const cuuint32_t box[2] = {box_inner, box_outer};
+    const cuuint32_t box[2] = {64u, box_outer};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(map,
                            dtype == CE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                            2, const_cast<void*>(p), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         record_message("cuTensorMapEncodeTiled failed (" + std::to_string(static_cast<int>(r)) + ")");
@@ -538,10 +537,6 @@ ce_status tc_smem_limit(const void* fn, size_t bytes) {
 ce_status tc_map_16bit(CUtensorMap* map, const void* p, int dtype, int64_t outer, int64_t inner,
                        uint32_t box_outer) {
     return make_map(map, p, dtype, outer, inner, box_outer);
-}
-
-ce_status tc_map_16bit_out(CUtensorMap* map, void* p, int dtype, int64_t rows, int64_t cols) {
-    return make_map(map, p, dtype, rows, cols, 32u, 32u, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // A 2-D map of a row-major [outer, inner] matrix of `dtype` elements (pitch

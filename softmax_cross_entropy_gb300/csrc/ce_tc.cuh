@@ -1,4 +1,4 @@
-// The tensor-core GEMMs' common parts (ce_gemm_tc.cu, ce_ffn.cuh): tile
+// The tensor-core GEMMs' common parts (ce_gemm_tc.cu, ce_ffn.cu): tile
 // shapes, shared-memory and instruction descriptors, and the tcgen05, TMA and
 // bulk-group instructions as inline PTX.
 #pragma once
@@ -186,9 +186,5 @@ ce_status tc_smem_limit(const void* fn, size_t bytes);
 // boxes of 128 or 256 rows, an MN-major one [K, MN] with boxes of 64 K rows.
 ce_status tc_map_16bit(CUtensorMap* map, const void* p, int dtype, int64_t outer, int64_t inner,
                        uint32_t box_outer);
-// The same of an output [rows, cols], stored in boxes of 32 x 32 elements
-// (64 bytes a row) with 64-byte swizzle: 16-byte chunk j of row r at chunk j
-// ^ (r / 2 mod 4).
-ce_status tc_map_16bit_out(CUtensorMap* map, void* p, int dtype, int64_t rows, int64_t cols);
 
 }  // namespace gbce
