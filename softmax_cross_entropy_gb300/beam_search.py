@@ -84,7 +84,8 @@ def _blocks(t, skip):
             blocks *= n
         else:
             raise ValueError("a state's rows must be equally spaced blocks of contiguous elements")
-    row = t.stride(0) if skip == 1 else t.stride(1)
+    # (a dimension of one, such as the beams' at K = 1, has a stride that says nothing)
+    row = t.stride(0) if skip == 1 or t.shape[1] == 1 else t.stride(1)
     if skip == 2 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * row:
         raise ValueError("a state's batch and beam dimensions must be one evenly spaced dimension")
     if block_stride < 0 or row < 0 or (blocks > 1 and block_stride < inner):
@@ -150,4 +151,6 @@ def beam_reorder(states, beams, inplace=False):
     with on(dev):
         check(_lib.ce_beam_reorder(table, n, ptr(beams), beams.stride(0), B, K, stream(dev)),
               "ce_beam_reorder")
+    if inplace:  # a backward that saved a state then finds that it was changed
+        torch.autograd.graph.increment_version([t for t in outs if not t.is_inference()])
     return outs[0] if one else outs

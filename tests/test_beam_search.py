@@ -284,6 +284,34 @@ def test_reorder_of_strided_states(inplace):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("inplace", [False, True])
+def test_reorder_of_one_beam(inplace):
+    # the beams' dimension of one has a stride of its own (here 5 * 8, rows are 9 * 8 apart)
+    import softmax_cross_entropy_gb300 as gbce
+    cache = torch.randn(4, 9, 8, device="cuda")
+    state = cache[:, :5].unsqueeze(1)
+    want = state.clone()
+    got = gbce.beam_reorder(state, torch.tensor([[0], [-1], [0], [0]], device="cuda"), inplace=inplace)
+    assert got.shape == want.shape and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_reorder_in_place_is_seen_by_autograd():
+    import softmax_cross_entropy_gb300 as gbce
+    beams = torch.tensor([[1, 0, 2]], device="cuda")
+    state = torch.randn(3, 8, device="cuda")
+    w = torch.randn(3, 8, device="cuda", requires_grad=True)
+    y = (w * state).sum()
+    gbce.beam_reorder([state], beams, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        t = torch.randn(3, 8, device="cuda")
+        want = t[[1, 0, 2]]
+        assert torch.equal(gbce.beam_reorder(t, beams, inplace=True), want)
+
+
+@pytest.mark.gpu
 def test_no_entries():
     import softmax_cross_entropy_gb300 as gbce
     best = gbce.beam_search_step(torch.empty(0, 3, 7, device="cuda"), torch.empty(0, 3, device="cuda"))
