@@ -62,29 +62,35 @@ namespace {
 
 enum FfnMode : int { kGateUp, kDown, kDact, kDx, kDw };
 
-// Tile shapes, all 256 accumulator columns wide:
+// Tile shapes, 256 accumulator columns wide:
 //  * 128: 128 rows on one SM, 4 stages of 48 KB, two accumulators;
 //  * 256: 256 rows on one SM, 3 stages of 64 KB, its two halves in all of
 //    the tensor memory: the epilogue does not overlap the next tile;
 //  * kPair: 256 rows on a pair of SMs (a cluster of two CTAs whose tensor
 //    cores work as one: each holds 128 rows of A, half of B's 256 columns and
-//    128 rows of the accumulator), 6 stages of 32 KB a CTA, two accumulators.
+//    128 rows of the accumulator), 3 stages of 64 KB a CTA, two accumulators.
 //    Each byte staged feeds twice the multiplications of the 128-row tile,
-//    and the epilogue of a tile overlaps the next tile's products.
+//    and the epilogue of a tile overlaps the next tile's products. A stage
+//    holds two K blocks: with a wait and a commit for each block of 64 (6
+//    stages) a block took 650 cycles, of which its products are 512, whatever
+//    the tile's width; with one for two 600 (1023 rows of 4096 x 12288 211 ->
+//    196 us). Where B is K-major the tile may be 224 or 192 columns wide.
 constexpr int kPair = 2;
 template <int SHAPE>
 struct FfnTile {
     static constexpr bool kTwo = SHAPE == kPair;
     static constexpr int kRows = kTwo ? 256 : SHAPE;
-    static constexpr int kStages = kTwo ? 6 : SHAPE == 256 ? 3 : 4;
+    static constexpr int kSub = kTwo ? 2 : 1;  // K blocks of a stage
+    static constexpr int kStages = kTwo ? 3 : SHAPE == 256 ? 3 : 4;
     static constexpr int kHalves = SHAPE == 256 ? 2 : 1;  // 128-row MMAs a K step
     static constexpr int kAccBufs = SHAPE == 256 ? 1 : 2;
     static constexpr uint32_t kA = (SHAPE == 256 ? 2u : 1u) * kHalfA;  // bytes of a stage, this CTA
     static constexpr uint32_t kB = kTwo ? kBBytes / 2 : kBBytes;
-    static constexpr uint32_t kStage = kA + kB;
+    static constexpr uint32_t kBlock = kA + kB;
+    static constexpr uint32_t kStage = kSub * kBlock;
     static_assert(kStages * kStage == kRingBytes, "one ring for every shape");
 };
-constexpr int kFfnStages = 6;
+constexpr int kFfnStages = 4;
 
 struct FfnMaps {
     CUtensorMap a[3], b[3];
@@ -101,6 +107,7 @@ struct FfnGemm {
     int odd[3];
     float scale[3];  // kDact, kDw: of the products
     int segs;       // segments of K (kDx: 2)
+    int width;      // accumulator columns of a tile
     int m_first;    // a problem's tiles run along M first
     int outs;       // kGateUp: 3 with s and a, else 1
     int act;
@@ -391,7 +398,10 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
     constexpr bool PAIR = TT::kTwo;
     constexpr bool A_MN = MODE == kDw;
     constexpr bool B_MN = MODE == kDact || MODE == kDx || MODE == kDw;
-    constexpr int kCols = MODE == kGateUp ? kBN / 2 : kBN;  // output columns of a tile
+    // pairs' tiles may be narrower (a.width) where B is K-major
+    constexpr bool NARROW = PAIR && !B_MN;
+    const int width = NARROW ? a.width : kBN;
+    const int cols = MODE == kGateUp ? width / 2 : width;  // output columns of a tile
     constexpr int BM = TT::kRows;
     constexpr int kStages = TT::kStages;
     constexpr int NACC = TT::kAccBufs;
@@ -413,7 +423,9 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
     const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
     const int64_t tile_step = PAIR ? gridDim.x / 2 : gridDim.x;
     const uint32_t smem0 = (smem_u32(ffn_smem_raw) + 1023u) & ~1023u;  // 1024-byte aligned
-    const int nk = static_cast<int>((a.K + kBK - 1) / kBK);
+    constexpr int kSub = TT::kSub;
+    // stages of a segment (behind K the copies fill zeros)
+    const int nk = static_cast<int>((a.K + kSub * kBK - 1) / (kSub * kBK));
     const int64_t ntiles = a.tile_end[2];
 
     if (threadIdx.x == 0) {
@@ -460,6 +472,8 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 if constexpr (PAIR) pair_load_2d(dst, map, x, y, bar);
                 else tma_load_2d(dst, map, x, y, bar);
             };
+            const uint32_t bytes = NARROW ? kSub * (2u * TT::kA + static_cast<uint32_t>(width) * kBK * 2u)
+                                          : (PAIR ? 2u : 1u) * TT::kStage;
             int s = 0;
             uint32_t ph = 0;
             bool fail = false;
@@ -468,8 +482,8 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 const int p = ffn_problem(a, &tl);
                 // this CTA's rows of A, and its columns of B
                 const int m0 = static_cast<int>(ffn_tile_m(a, p, tl) * BM + rank * kMmaM);
-                const int nt = static_cast<int>(ffn_tile_n(a, p, tl) * kCols);
-                const int n0 = MODE == kGateUp ? nt : nt + static_cast<int>(rank) * (kBN / 2);
+                const int nt = static_cast<int>(ffn_tile_n(a, p, tl) * cols);
+                const int n0 = MODE == kGateUp ? nt : nt + static_cast<int>(rank) * (width / 2);
                 for (int kb = 0; kb < nk * a.segs; ++kb) {
                     if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
                         fail = true;
@@ -478,32 +492,35 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                     // the pair's copies signal its first CTA's barrier, which
                     // expects the bytes of both
                     uint32_t fb = smem_u32(&full_bar[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(fb, (PAIR ? 2u : 1u) * TT::kStage);
+                    if (rank == 0) mbar_arrive_expect_tx(fb, bytes);
                     if constexpr (PAIR) fb = map_to_rank(fb, 0);
-                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage;
                     // the operands' maps: of the problem, or of the segment
                     const int seg = kb >= nk ? 1 : 0;
                     const int i = MODE == kDx ? seg : p;
-                    const int k0 = (kb - seg * nk) * kBK;
-                    if constexpr (A_MN) {
-                        for (uint32_t j = 0; j < TT::kA / kMnBox; ++j)
-                            load(sa + j * kMnBox, &maps.a[i], m0 + 64 * j, k0, fb);
-                    } else {
-                        load(sa, &maps.a[i], k0, m0, fb);
-                    }
-                    const uint32_t sb = sa + TT::kA;
-                    if constexpr (MODE == kGateUp) {
-                        if constexpr (PAIR) {
-                            load(sb, &maps.b[rank], k0, n0, fb);
+#pragma unroll
+                    for (int sub = 0; sub < kSub; ++sub) {
+                        const int k0 = ((kb - seg * nk) * kSub + sub) * kBK;
+                        const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage + sub * TT::kBlock;
+                        if constexpr (A_MN) {
+                            for (uint32_t j = 0; j < TT::kA / kMnBox; ++j)
+                                load(sa + j * kMnBox, &maps.a[i], m0 + 64 * j, k0, fb);
                         } else {
-                            load(sb, &maps.b[0], k0, n0, fb);
-                            load(sb + kBBytes / 2, &maps.b[1], k0, n0, fb);
+                            load(sa, &maps.a[i], k0, m0, fb);
                         }
-                    } else if constexpr (B_MN) {
-                        for (uint32_t j = 0; j < TT::kB / kMnBox; ++j)
-                            load(sb + j * kMnBox, &maps.b[i], n0 + 64 * j, k0, fb);
-                    } else {
-                        load(sb, &maps.b[i], k0, n0, fb);
+                        const uint32_t sb = sa + TT::kA;
+                        if constexpr (MODE == kGateUp) {
+                            if constexpr (PAIR) {
+                                load(sb, &maps.b[rank], k0, n0, fb);
+                            } else {
+                                load(sb, &maps.b[0], k0, n0, fb);
+                                load(sb + kBBytes / 2, &maps.b[1], k0, n0, fb);
+                            }
+                        } else if constexpr (B_MN) {
+                            for (uint32_t j = 0; j < TT::kB / kMnBox; ++j)
+                                load(sb + j * kMnBox, &maps.b[i], n0 + 64 * j, k0, fb);
+                        } else {
+                            load(sb, &maps.b[i], k0, n0, fb);
+                        }
                     }
                     s_issued[s] = 2u + ph;
                     if (++s == kStages) {
@@ -521,9 +538,14 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 if constexpr (PAIR) pair_commit(bar);
                 else tc_commit(bar);
             };
-            constexpr uint32_t idesc =
-                (tc_idesc(AB, A_MN ? 1u : 0u, B_MN ? 1u : 0u) & ~(31u << 24)) |
-                (static_cast<uint32_t>((PAIR ? 256 : 128) >> 4) << 24);
+            const uint32_t idesc =
+                (tc_idesc(AB, A_MN ? 1u : 0u, B_MN ? 1u : 0u) & ~(31u << 24) & ~(63u << 17)) |
+                (static_cast<uint32_t>((PAIR ? 256 : 128) >> 4) << 24) |
+                (static_cast<uint32_t>(width >> 3) << 17);
+            // the operands' descriptors at the ring's start, whose address field
+            // counts 16-byte units
+            const uint64_t a0 = A_MN ? tc_smem_desc_mn(smem0) : tc_smem_desc(smem0);
+            const uint64_t b0 = B_MN ? tc_smem_desc_mn(smem0 + TT::kA) : tc_smem_desc(smem0 + TT::kA);
             int s = 0;
             uint32_t ph = 0;
             int i = 0;  // tiles of this CTA so far
@@ -541,24 +563,23 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 // half h of the tile (rows 128 h ...) in columns (b H + h) 256
                 const uint32_t acc = tmem + static_cast<uint32_t>(b * H * kBN);
                 for (int kb = 0; kb < nk * a.segs; ++kb) {
-                    if (!(PAIR ? pair_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)
-                               : tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns))) {
+                    if (!tc_wait(smem_u32(&full_bar[s]), ph, a.timeout_ns)) {
                         fail = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage;
-                    const uint32_t sb = sa + TT::kA;
+                    const uint32_t at = static_cast<uint32_t>(s) * (TT::kStage >> 4);
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k) {
-                        const uint64_t db = B_MN ? tc_smem_desc_mn(sb + 2048u * k)
-                                                 : tc_smem_desc(sb + 32u * k);
+                    for (int kk = 0; kk < kSub * (kBK / 16); ++kk) {
+                        constexpr uint32_t kPer = kBK / 16;
+                        const uint32_t block = (kk / kPer) * (TT::kBlock >> 4), k = kk % kPer;
+                        // a K step of 16 further in 16-byte units
+                        const uint64_t db = b0 + (at + block + k * (B_MN ? 2048u >> 4 : 32u >> 4));
 #pragma unroll
                         for (int h = 0; h < H; ++h) {
-                            const uint32_t ah = sa + static_cast<uint32_t>(h) * kHalfA;
-                            const uint64_t da = A_MN ? tc_smem_desc_mn(ah + 2048u * k)
-                                                     : tc_smem_desc(ah + 32u * k);
-                            const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+                            const uint64_t da = a0 + (at + block + k * (A_MN ? 2048u >> 4 : 32u >> 4) +
+                                                      static_cast<uint32_t>(h) * (kHalfA >> 4));
+                            const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
                             if constexpr (PAIR) pair_mma(acc, da, db, idesc, add);
                             else tc_mma(acc + static_cast<uint32_t>(h * kBN), da, db, idesc, add);
                         }
@@ -579,7 +600,7 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
     } else {
         // ---- epilogue: warp w reads accumulator lanes 32 (w mod 4) of each
         // 128-row half of the tile; of its columns warps 2-5 take the first
-        // half, warps 6-9 the second
+        // half (rounded up to whole units of 32), warps 6-9 the rest
         const int q = warp & 3, side = (warp - 2) >> 2;
         FfnStore store{smem0 + kRingBytes + static_cast<uint32_t>(warp - 2) * 2u * kFfnBox, 0u, lane};
         PhiloxKey key{};
@@ -590,15 +611,16 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
             int64_t tl = t;
             const int p = ffn_problem(a, &tl);
             const int64_t M = a.M[p], N = a.N[p];
-            const int64_t n0 = ffn_tile_n(a, p, tl) * kCols + side * (kCols / 2);
+            const int first = (cols / 32 + 1) / 2;  // units of the first half
+            const int units = side ? cols / 32 - first : first;
+            const int64_t n0 = ffn_tile_n(a, p, tl) * cols + side * first * 32;
             const int64_t mt = ffn_tile_m(a, p, tl) * BM + rank * kMmaM + q * 32;  // + 128 hh
-            constexpr int kUnits = kCols / 64;  // units of 32 columns of this warp's half
             float4 ps[8], pa[8];  // kDact: pieces of s and a of the next unit
             if constexpr (MODE == kDact) {
                 // while the tile's products run: the others into L2, the first here
                 for (int hh = 0; hh < H; ++hh) {
                     const int64_t row = mt + hh * kMmaM + lane;
-                    for (int c = 0; c < kCols / 2; c += 32) {
+                    for (int c = 0; c < 32 * units; c += 32) {
                         if (row >= M || n0 + c >= N) break;
                         ffn_prefetch(a.s + row * N + n0 + c);
                         ffn_prefetch(a.a + row * N + n0 + c);
@@ -615,15 +637,15 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
             }
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < H * kUnits; ++x) {
-                const int hh = x / kUnits, c = x % kUnits;
+            for (int x = 0; x < H * units; ++x) {
+                const int hh = H == 1 ? 0 : x / units, c = x - hh * units;
                 const int64_t m = mt + hh * kMmaM, n = n0 + c * 32;
                 // the accumulator's column of this unit
                 const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                                     static_cast<uint32_t>((b * H + hh) * kBN + side * (kCols / 2) + c * 32);
+                                     static_cast<uint32_t>((b * H + hh) * kBN + (side * first + c) * 32);
                 // the unit after this one
-                const int y = x + 1 < H * kUnits ? x + 1 : x;
-                const int64_t nm = mt + (y / kUnits) * kMmaM, nn = n0 + (y % kUnits) * 32;
+                const int y = x + 1 < H * units ? x + 1 : x, yh = H == 1 ? 0 : y / units;
+                const int64_t nm = mt + yh * kMmaM, nn = n0 + (y - yh * units) * 32;
                 if (m >= M || n >= N) {  // the same for the whole warp
                     if constexpr (MODE == kDact) {
                         load_pieces(a.s, nn, nm, M, N, lane, ps);
@@ -636,7 +658,7 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 uint4 w[4];
                 if constexpr (MODE == kGateUp) {
                     float u[32];
-                    tc_ld32(acc + kBN / 2, u);
+                    tc_ld32(acc + static_cast<uint32_t>(width / 2), u);
                     if (a.outs == 1) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = ffn_gate<false>(a.act, v[j]).act * u[j];
@@ -838,32 +860,46 @@ struct FfnMatrix {
 // One launch of form `mode`: problems or segments A[i] x B[i].
 ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatrix (&A)[3],
                      const FfnMatrix (&B)[3], const FfnDevice& d, cudaStream_t st) {
-    const int64_t cols = mode == kGateUp ? kBN / 2 : kBN;
     g.timeout_ns = d.timeout_ns;
     g.status = d.status;
     // The tile shape by its rounds of tiles over the SMs (or pairs of SMs)
     // and what a round was measured to take, that of pairs being 100 (per 4096
-    // of K, bf16: 23 us): 256 rows an SM 190 (4096 x 4096 x 24576 468 against
-    // 516 us for pairs), 210 where the epilogue, which it does not overlap,
-    // writes or reads much (512 against 483, 377 against 327 us), 128 rows 107
-    // (1023 x 4096 x 12288 75 against 67 us).
-    const bool heavy = mode == kGateUp || mode == kDact;
-    const int shapes[3] = {kPair, 256, 128};
-    const int64_t round[3] = {100, heavy ? 210 : 190, 107};
+    // of K, bf16: 20.5 us). 256 rows an SM: 195 (4096 x 4096 x 24576 475
+    // against 482 us for pairs, 4096 x 2048 x 16384 156 against 167), 215 where
+    // the epilogue, which it does not overlap, does more than store (4096 x
+    // 12288 x 4096 549 against 472 us, 2048 x 4096 x 12288 136 against 130).
+    // 128 rows: 115 (4096 x 4096 x 12288 300 against 256 us; 300 rows of the
+    // block of 4096 x 12288 117 against 135). Narrower tiles of pairs save little
+    // of a round, but a product of few tiles finds more SMs with them: 224
+    // columns 95, 192 columns 91 (512 rows of 1024 x 4096 40 against 48 us, of
+    // 4096 x 12288 131 against 137).
+    const bool bare = mode == kDx || mode == kDw;
+    const struct {
+        int shape, width;
+        int64_t round;
+    } forms[] = {{kPair, 256, 100}, {256, 256, bare ? 195 : 215}, {128, 256, 115},
+                 {kPair, 192, 91}, {kPair, 224, 95}};
+    // (kGateUp: half the columns are whole units of 32 of the epilogue's)
+    const int count = mode == kDown ? 5 : mode == kGateUp ? 4 : 3;
     int shape = kPair;
     int64_t least = INT64_MAX;
-    for (int i = 0; i < 3; ++i) {
-        const int64_t rows = shapes[i] == 128 ? 128 : 256;
-        const int64_t ctas = shapes[i] == kPair ? std::max(d.sms / 2, 1) : d.sms;
+    g.width = kBN;
+    for (int i = 0; i < count; ++i) {
+        const auto& f = forms[i];
+        const int64_t rows = f.shape == 128 ? 128 : 256;
+        const int64_t across = mode == kGateUp ? f.width / 2 : f.width;
+        const int64_t ctas = f.shape == kPair ? std::max(d.sms / 2, 1) : d.sms;
         int64_t tiles = 0;
         for (int p = 0; p < problems; ++p)
-            tiles += (g.M[p] + rows - 1) / rows * ((g.N[p] + cols - 1) / cols);
-        const int64_t cost = (tiles + ctas - 1) / ctas * round[i];
+            tiles += (g.M[p] + rows - 1) / rows * ((g.N[p] + across - 1) / across);
+        const int64_t cost = (tiles + ctas - 1) / ctas * f.round;
         if (cost < least) {
             least = cost;
-            shape = shapes[i];
+            shape = f.shape;
+            g.width = f.width;
         }
     }
+    const int64_t cols = mode == kGateUp ? g.width / 2 : g.width;
     const int bm = shape == 128 ? 128 : 256;
     int64_t end = 0;
     for (int p = 0; p < 3; ++p) {
@@ -884,7 +920,7 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
                                      a_mn ? 64 : shape == kPair ? 128 : bm);
         if (rc == CE_OK && B[i].p)
             rc = tc_map_16bit(&maps.b[i], B[i].p, dtype, B[i].outer, B[i].inner,
-                              b_mn ? 64 : mode == kGateUp || shape == kPair ? kBN / 2 : kBN);
+                              b_mn ? 64 : mode == kGateUp || shape == kPair ? g.width / 2 : kBN);
         if (rc != CE_OK) return rc;
     }
     const void* fn = ffn_fn(dtype, mode, shape);

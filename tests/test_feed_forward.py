@@ -148,7 +148,7 @@ def test_wrapper_refuses_cpu_tensors():
     (1, 8, 8, 8), (2, 64, 128, 64), (3, 200, 72, 40), (16, 256, 512, 256), (17, 1000, 24, 136),
     (1, 2048, 4096, 2048), (40, 1024, 2048, 1000), (63, 4096, 640, 264),
     (33, 72, 1000, 264), (64, 512, 640, 512), (129, 136, 264, 8), (300, 384, 320, 640),
-    (515, 256, 1032, 256)])
+    (515, 256, 1032, 256), (1000, 64, 72, 4096)])
 def test_forward(dtype, act, rows, H, I, O):
     import softmax_cross_entropy_gb300 as gbce
     x, wg, wu, wd, _, _ = make(rows, H, I, O, dtype)
@@ -206,7 +206,7 @@ def test_gradients_against_differences(act):
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,H,I,O", [(1, 7, 9, 5), (37, 33, 65, 33), (130, 1001, 131, 77),
                                         (300, 65, 131, 77), (513, 128, 203, 300),
-                                        (600, 200, 96, 130)])
+                                        (600, 200, 96, 130), (1000, 64, 70, 4093)])
 @pytest.mark.parametrize("p,residual", [(0.0, False), (0.25, True)])
 def test_odd_sizes(rows, H, I, O, p, residual):
     import softmax_cross_entropy_gb300 as gbce
