@@ -71,10 +71,13 @@ enum FfnMode : int { kGateUp, kDown, kDact, kDx, kDw };
 //    128 rows of the accumulator), 3 stages of 64 KB a CTA, two accumulators.
 //    Each byte staged feeds twice the multiplications of the 128-row tile,
 //    and the epilogue of a tile overlaps the next tile's products. A stage
-//    holds two K blocks: with a wait and a commit for each block of 64 (6
-//    stages) a block took 650 cycles, of which its products are 512, whatever
-//    the tile's width; with one for two 600 (1023 rows of 4096 x 12288 211 ->
-//    196 us). Where B is K-major the tile may be 224 or 192 columns wide.
+//    holds two K blocks, which the products wait for together and give back
+//    one by one: with a wait for each block (6 stages) a block took 620 to 650
+//    cycles, of which its products are 512, whatever the tile's width. The
+//    forward of 1024 rows of 4096 x 12288 205 us then, 194 with a wait and a
+//    return for two, 187 so; 4096 rows 730, 680 and 655; stages of three
+//    blocks 212 and 684. Where B is K-major the tile may be 224 or 192
+//    columns wide.
 constexpr int kPair = 2;
 template <int SHAPE>
 struct FfnTile {
@@ -89,8 +92,9 @@ struct FfnTile {
     static constexpr uint32_t kBlock = kA + kB;
     static constexpr uint32_t kStage = kSub * kBlock;
     static_assert(kStages * kStage == kRingBytes, "one ring for every shape");
+    static_assert(kStages <= 4 && kStages * kSub <= 6, "barriers");
 };
-constexpr int kFfnStages = 4;
+constexpr int kFfnStages = 4, kFfnBlocks = 6;
 
 struct FfnMaps {
     CUtensorMap a[3], b[3];
@@ -407,8 +411,8 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
     constexpr int NACC = TT::kAccBufs;
     constexpr int H = TT::kHalves;
     extern __shared__ unsigned char ffn_smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[kFfnStages];
-    __shared__ __align__(8) uint64_t empty_bar[kFfnStages];
+    __shared__ __align__(8) uint64_t full_bar[kFfnStages];    // of a stage
+    __shared__ __align__(8) uint64_t empty_bar[kFfnBlocks];  // of a K block
     __shared__ __align__(8) uint64_t acc_full[2];
     __shared__ __align__(8) uint64_t acc_empty[2];
     __shared__ __align__(8) uint64_t done_bar;  // every MMA of the CTA completed
@@ -431,9 +435,9 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
-            mbar_init(smem_u32(&empty_bar[s]), 1);
             s_issued[s] = 0;
         }
+        for (int s = 0; s < kStages * TT::kSub; ++s) mbar_init(smem_u32(&empty_bar[s]), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), (PAIR ? 2 : 1) * kFfnEpiWarps);
@@ -485,20 +489,23 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                 const int nt = static_cast<int>(ffn_tile_n(a, p, tl) * cols);
                 const int n0 = MODE == kGateUp ? nt : nt + static_cast<int>(rank) * (width / 2);
                 for (int kb = 0; kb < nk * a.segs; ++kb) {
-                    if (!tc_wait(smem_u32(&empty_bar[s]), ph ^ 1u, a.timeout_ns)) {
-                        fail = true;
-                        break;
-                    }
                     // the pair's copies signal its first CTA's barrier, which
                     // expects the bytes of both
                     uint32_t fb = smem_u32(&full_bar[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(fb, bytes);
                     if constexpr (PAIR) fb = map_to_rank(fb, 0);
                     // the operands' maps: of the problem, or of the segment
                     const int seg = kb >= nk ? 1 : 0;
                     const int i = MODE == kDx ? seg : p;
 #pragma unroll
                     for (int sub = 0; sub < kSub; ++sub) {
+                        if (!tc_wait(smem_u32(&empty_bar[s * kSub + sub]), ph ^ 1u, a.timeout_ns)) {
+                            fail = true;
+                            break;
+                        }
+                        if (sub == 0) {
+                            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), bytes);
+                            s_issued[s] = 2u + ph;
+                        }
                         const int k0 = ((kb - seg * nk) * kSub + sub) * kBK;
                         const uint32_t sa = smem0 + static_cast<uint32_t>(s) * TT::kStage + sub * TT::kBlock;
                         if constexpr (A_MN) {
@@ -522,7 +529,7 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                             load(sb, &maps.b[i], k0, n0, fb);
                         }
                     }
-                    s_issued[s] = 2u + ph;
+                    if (fail) break;
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
@@ -583,8 +590,8 @@ ffn_gemm(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm a
                             if constexpr (PAIR) pair_mma(acc, da, db, idesc, add);
                             else tc_mma(acc + static_cast<uint32_t>(h * kBN), da, db, idesc, add);
                         }
+                        if (k == kPer - 1) commit(smem_u32(&empty_bar[s * kSub + kk / kPer]));
                     }
-                    commit(smem_u32(&empty_bar[s]));
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
