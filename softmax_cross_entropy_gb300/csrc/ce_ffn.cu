@@ -1012,8 +1012,8 @@ struct FfnPacker {
 
 // The most rows that take the form for few rows, whose products have at most
 // 256 columns. Measured, bf16, forward with residual: H 4096, I 12288: 1 row
-// 59 against 124 us for the tiles, 64 rows 65 / 116, 256 rows 91 / 129; H
-// 1024, I 4096: 13 / 36, 16 / 37 and 26 / 38.
+// 59 against 109 us for the tiles, 64 rows 68 / 97, 256 rows 91 / 103; H
+// 1024, I 4096: 13 / 37, 16 / 37 and 26 / 38.
 constexpr int64_t kFewRows = 256;
 
 // Output i of a launch, with rows of `cols` elements.
