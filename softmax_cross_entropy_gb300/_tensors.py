@@ -5,6 +5,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import CEError
@@ -32,6 +33,13 @@ def once(name):
     """Refuses a backward that is itself to be differentiated."""
     if torch.is_grad_enabled():
         raise RuntimeError(f"{name} is differentiable once: its backward has no graph")
+
+
+def forward_mode():
+    """Whether forward-mode derivatives are being taken. A tensor with a tangent
+    need not require a gradient, so calls then go through their autograd
+    Function, which refuses it (none has a forward-mode rule)."""
+    return getattr(forward_ad, "_current_level", 0) >= 0
 
 
 # (a CUDA tensor is at hand, so CUDA is initialised)

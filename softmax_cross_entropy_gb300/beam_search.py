@@ -12,9 +12,10 @@ from __future__ import annotations
 from collections import namedtuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
-from ._tensors import DTYPES, check, on, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, ptr, require_cuda, stream
 
 __all__ = ["beam_search_step", "beam_reorder", "BeamCandidates"]
 
@@ -127,6 +128,8 @@ def beam_reorder(states, beams, inplace=False):
             raise ValueError("a state must be [B, K, ...] or [B * K, ...]")
         if inplace and t.requires_grad:
             raise ValueError("a state that requires a gradient cannot be reordered in place")
+        if inplace and forward_mode() and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("a state with a tangent cannot be reordered in place")
         n = t.numel()
         if t.is_contiguous():
             row = inner = n // (B * K) if n else 0

@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, on, once, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, once, ptr, require_cuda, stream
 from .philox_dropout import check_rng
 
 __all__ = ["gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
@@ -141,9 +141,9 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
         residual = None if residual is None else residual.reshape(-1, O)
     args = (aligned(x), aligned(gate_weight), aligned(up_weight), aligned(down_weight),
             None if residual is None else residual.contiguous(), act, p, seed, offset, state)
-    if torch.is_grad_enabled() and (
+    if forward_mode() or (torch.is_grad_enabled() and (
             x.requires_grad or gate_weight.requires_grad or up_weight.requires_grad or
-            down_weight.requires_grad or (residual is not None and residual.requires_grad)):
+            down_weight.requires_grad or (residual is not None and residual.requires_grad))):
         y = GatedFeedForwardFunction.apply(*args)
     else:
         y = _forward(*args, False)[0]

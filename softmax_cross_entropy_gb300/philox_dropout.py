@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, on, once, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, once, ptr, require_cuda, stream
 
 __all__ = ["dropout", "DropoutFunction"]
 
@@ -90,7 +90,7 @@ def dropout(x, p, seed, offset=0, residual=None):
         residual = residual.contiguous()
     p, seed, offset, state = check_rng(p, seed, offset, x.device)
     x = x.contiguous()
-    if not (torch.is_grad_enabled() and (x.requires_grad or (residual is not None and
-                                                             residual.requires_grad))):
+    if not (forward_mode() or (torch.is_grad_enabled() and (
+            x.requires_grad or (residual is not None and residual.requires_grad)))):
         return _call(x, residual, p, seed, offset, state, None)
     return DropoutFunction.apply(x, residual, p, seed, offset, state)

@@ -125,6 +125,17 @@ def test_wrapper_refuses_cpu_tensors():
         gbce.beam_reorder(torch.zeros(2, 3), torch.zeros(1, 2, dtype=torch.int64))
 
 
+def test_states_with_tangents_are_not_changed_in_place(monkeypatch):
+    import softmax_cross_entropy_gb300 as gbce
+    from softmax_cross_entropy_gb300 import beam_search
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(beam_search, "require_cuda", lambda *a: None)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(torch.randn(2, 3), torch.ones(2, 3))
+        with pytest.raises(ValueError, match="tangent"):
+            gbce.beam_reorder(dual, torch.zeros(1, 2, dtype=torch.int64), inplace=True)
+
+
 # ---------------------------------------------------------------- GPU
 
 def inputs(B, K, V, dtype, seed=0, scale=3.0):

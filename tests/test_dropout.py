@@ -35,6 +35,25 @@ def test_wrapper_refuses_cpu_tensors():
         gbce.dropout(torch.zeros(4), 0.5, 1)
 
 
+def test_tangents_are_refused_not_dropped(monkeypatch):
+    # a dual tensor does not require a gradient (the library's call is a copy here)
+    import softmax_cross_entropy_gb300 as gbce
+    from softmax_cross_entropy_gb300 import philox_dropout
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(philox_dropout, "require_cuda", lambda *a: None)
+    monkeypatch.setattr(philox_dropout, "_call", lambda x, *a: x.detach().clone())
+    x = torch.randn(5)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones(5))
+        for args in ((dual, None), (x, dual)):
+            with pytest.raises(NotImplementedError):
+                gbce.dropout(args[0], 0.0, 1, residual=args[1])
+            with pytest.raises(NotImplementedError), torch.no_grad():
+                gbce.dropout(args[0], 0.0, 1, residual=args[1])
+        assert torch.equal(gbce.dropout(x, 0.0, 1), x)
+    assert torch.equal(gbce.dropout(x, 0.0, 1), x)
+
+
 # ---------------------------------------------------------------- GPU
 
 def expected(x, res, kept, p):

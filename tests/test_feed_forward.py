@@ -139,6 +139,34 @@ def test_wrapper_refuses_cpu_tensors():
         gbce.gated_feed_forward(t, t, t, t)
 
 
+@pytest.fixture
+def stubbed(monkeypatch):
+    """The wrapper on CPU tensors, its library call a plain copy."""
+    from softmax_cross_entropy_gb300 import feed_forward
+
+    def forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad):
+        return x.detach().clone(), x.detach(), torch.zeros(2, *x.shape) if grad else None
+
+    monkeypatch.setattr(feed_forward, "_refuse", lambda *a: None)
+    monkeypatch.setattr(feed_forward, "_forward", forward)
+    return feed_forward
+
+
+def test_tangents_are_refused_not_dropped(stubbed):
+    from torch.autograd import forward_ad
+    t = torch.randn(8, 8).bfloat16()
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(t, torch.ones_like(t))
+        for i in range(5):
+            args = [t] * 5
+            args[i] = dual
+            with pytest.raises(NotImplementedError):
+                stubbed.gated_feed_forward(*args[:4], residual=args[4])
+            with pytest.raises(NotImplementedError), torch.no_grad():
+                stubbed.gated_feed_forward(*args[:4], residual=args[4])
+        assert torch.equal(stubbed.gated_feed_forward(t, t, t, t), t)
+
+
 # ---------------------------------------------------------------- GPU
 
 @pytest.mark.gpu
