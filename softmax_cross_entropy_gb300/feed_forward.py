@@ -52,7 +52,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, residual, act, p, seed, offset, state):
         grad = any(ctx.needs_input_grad[:4])
-        if grad and state is not None and p > 0.0:
+        if grad and state is not None:
             state = state.clone()  # the caller may change it before the backward runs
         y, h, sa = _forward(x, w_gate, w_up, w_down, residual, act, p, seed, offset, state, grad)
         if grad:

@@ -20,14 +20,15 @@ _U64 = (1 << 64) - 1
 
 
 def check_rng(p, seed, offset, device):
-    """(p, seed, offset, state): the arguments of dropout as the library takes them."""
+    """(p, seed, offset, state): the arguments of dropout as the library takes
+    them. A seed tensor is passed on where words are drawn from it (p not 0 or 1)."""
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError("the dropout probability must lie in [0, 1]")
     if isinstance(seed, torch.Tensor):
         if seed.dtype != torch.int64 or seed.numel() != 2 or seed.device != device:
             raise ValueError("a seed tensor holds int64 (seed, offset) on the input's device")
-        return p, 0, int(offset) & _U64, seed.contiguous()
+        return p, 0, int(offset) & _U64, seed.contiguous() if 0.0 < p < 1.0 else None
     if seed is None:
         if p not in (0.0, 1.0):
             raise ValueError("dropout needs a seed")

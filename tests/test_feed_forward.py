@@ -1,5 +1,6 @@
 """The gated feed-forward block: refusals (CPU), and the kernels against the
 formulas in 64 bits (GPU)."""
+import contextlib
 import math
 
 import numpy as np
@@ -165,6 +166,22 @@ def test_tangents_are_refused_not_dropped(stubbed):
             with pytest.raises(NotImplementedError), torch.no_grad():
                 stubbed.gated_feed_forward(*args[:4], residual=args[4])
         assert torch.equal(stubbed.gated_feed_forward(t, t, t, t), t)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.5, 1.0])
+def test_a_seed_tensor_may_change_before_the_backward(stubbed, monkeypatch, p):
+    calls = []
+    monkeypatch.setattr(stubbed._lib, "ce_ffn_bwd_workspace_bytes", lambda *a: 1)
+    monkeypatch.setattr(stubbed._lib, "ce_ffn_bwd", lambda *a: calls.append(a) or 0)
+    monkeypatch.setattr(stubbed, "stream", lambda device: 0)
+    monkeypatch.setattr(stubbed, "on", lambda device: contextlib.nullcontext())
+    t = torch.randn(8, 8).bfloat16()
+    x = t.clone().requires_grad_()
+    seed = torch.tensor([3, 4])
+    y = stubbed.gated_feed_forward(x, t, t, t, dropout_p=p, seed=seed)
+    seed += 1
+    torch.autograd.grad(y.sum(), [x])
+    assert len(calls) == 1
 
 
 # ---------------------------------------------------------------- GPU
@@ -389,6 +406,23 @@ def test_seed_tensor_changed_before_the_backward_and_captured_step():
         torch.cuda.synchronize()
         for a, b in zip(outs, w):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("p", [0.0, 1.0])
+def test_seed_tensor_where_no_words_are_drawn(rows, p):
+    import softmax_cross_entropy_gb300 as gbce
+    x, wg, wu, wd, res, dy = make(rows, 64, 128, 64, "bf16")
+    leaves = [t.requires_grad_() for t in (x, wg, wu, wd)]
+    state = torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+    outs = []
+    for seed in (3, state):
+        y = gbce.gated_feed_forward(x, wg, wu, wd, dropout_p=p, seed=seed, residual=res)
+        state += 1
+        outs.append([y.detach(), *torch.autograd.grad(y, leaves, dy)])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
