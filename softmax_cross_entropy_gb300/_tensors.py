@@ -23,6 +23,12 @@ def ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def plain(t):
+    """t's values in contiguous memory (a negation that a view defers, as that
+    of z.conj().imag does, is carried out)."""
+    return t.contiguous().resolve_neg()
+
+
 def stream(device):
     if _raw_stream is not None and device.index is not None:
         return _raw_stream(device.index)

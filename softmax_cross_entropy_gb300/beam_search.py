@@ -15,7 +15,7 @@ import torch
 from torch.autograd import forward_ad
 
 from . import _lib
-from ._tensors import DTYPES, check, forward_mode, on, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, plain, ptr, require_cuda, stream
 
 __all__ = ["beam_search_step", "beam_reorder", "BeamCandidates"]
 
@@ -54,8 +54,8 @@ def beam_search_step(logits, scores, num_candidates=None, finished=None, pad_tok
         raise ValueError("num_candidates, K and V must be at least 1")
     if not 0 <= int(pad_token) < V:
         raise ValueError("pad_token must lie in [0, V)")
-    logits = logits.contiguous()
-    scores = scores.contiguous()
+    logits = plain(logits)
+    scores = plain(scores)
     finished = None if finished is None else finished.contiguous()
     out = BeamCandidates(torch.empty((B, M), dtype=torch.float32, device=dev),
                          torch.empty((B, M), dtype=torch.int64, device=dev),
@@ -130,6 +130,8 @@ def beam_reorder(states, beams, inplace=False):
             raise ValueError("a state that requires a gradient cannot be reordered in place")
         if inplace and forward_mode() and forward_ad.unpack_dual(t).tangent is not None:
             raise ValueError("a state with a tangent cannot be reordered in place")
+        if not inplace and (t.is_conj() or t.is_neg()):
+            t = t.resolve_conj().resolve_neg()  # (in place the view stays one)
         n = t.numel()
         if t.is_contiguous():
             row = inner = n // (B * K) if n else 0

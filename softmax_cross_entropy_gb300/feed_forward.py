@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, forward_mode, on, once, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, once, plain, ptr, require_cuda, stream
 from .philox_dropout import check_rng
 
 __all__ = ["gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
@@ -91,7 +91,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
 def aligned(t):
     """t as a contiguous tensor whose base the kernels take: 16-byte aligned
     where its rows are whole 16-byte vectors."""
-    t = t.contiguous()
+    t = plain(t)
     return t.clone() if t.data_ptr() % 16 and t.shape[-1] % 8 == 0 else t
 
 
@@ -140,7 +140,7 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
         x = x.reshape(-1, H)
         residual = None if residual is None else residual.reshape(-1, O)
     args = (aligned(x), aligned(gate_weight), aligned(up_weight), aligned(down_weight),
-            None if residual is None else residual.contiguous(), act, p, seed, offset, state)
+            None if residual is None else plain(residual), act, p, seed, offset, state)
     if forward_mode() or (torch.is_grad_enabled() and (
             x.requires_grad or gate_weight.requires_grad or up_weight.requires_grad or
             down_weight.requires_grad or (residual is not None and residual.requires_grad))):

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._tensors import DTYPES, check, forward_mode, on, once, ptr, require_cuda, stream
+from ._tensors import DTYPES, check, forward_mode, on, once, plain, ptr, require_cuda, stream
 
 __all__ = ["dropout", "DropoutFunction"]
 
@@ -67,7 +67,7 @@ class DropoutFunction(torch.autograd.Function):
             used = ctx.saved_tensors[0] if ctx.saved_tensors else None
             if used is not None:
                 offset = 0  # in `used` already
-            dx = _call(dy.contiguous(), None, p, seed, offset, used, None)
+            dx = _call(plain(dy), None, p, seed, offset, used, None)
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None
 
 
@@ -88,9 +88,9 @@ def dropout(x, p, seed, offset=0, residual=None):
         require_cuda(residual, "residual")
         if residual.shape != x.shape or residual.dtype != x.dtype or residual.device != x.device:
             raise ValueError("residual must have the shape, dtype and device of x")
-        residual = residual.contiguous()
+        residual = plain(residual)
     p, seed, offset, state = check_rng(p, seed, offset, x.device)
-    x = x.contiguous()
+    x = plain(x)
     if not (forward_mode() or (torch.is_grad_enabled() and (
             x.requires_grad or (residual is not None and residual.requires_grad)))):
         return _call(x, residual, p, seed, offset, state, None)

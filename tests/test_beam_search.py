@@ -1,5 +1,7 @@
 """The beam search step and the reordering of states: refusals (CPU), and the
 kernels against a stable sort of the definition in 64 bits (GPU)."""
+import contextlib
+import ctypes
 import math
 
 import numpy as np
@@ -123,6 +125,55 @@ def test_wrapper_refuses_cpu_tensors():
         gbce.beam_search_step(torch.zeros(1, 2, 3), torch.zeros(1, 2))
     with pytest.raises(ValueError):
         gbce.beam_reorder(torch.zeros(2, 3), torch.zeros(1, 2, dtype=torch.int64))
+
+
+def host_reorder(states, n, beams, beams_row, B, K, stream):
+    """ce_beam_reorder by its definition on host memory."""
+    if beams_row < K:
+        return 1  # CE_ERR_INVALID_ARG
+    for s in list(states)[:n]:
+        for b in range(B):
+            take = (ctypes.c_int64 * K).from_address(beams + 8 * b * beams_row)
+            rows = [[ctypes.string_at(s.src + (b * K + (f if 0 <= f < K else j)) * s.src_row +
+                                      o * s.src_block, s.block_bytes) for o in range(s.blocks)]
+                    for j, f in enumerate(take)]
+            for j, row in enumerate(rows):
+                for o, block in enumerate(row):
+                    ctypes.memmove(s.dst + (b * K + j) * s.dst_row + o * s.dst_block, block, s.block_bytes)
+    return 0
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """The wrapper on CPU tensors, the library's reordering on host memory."""
+    import softmax_cross_entropy_gb300 as gbce
+    from softmax_cross_entropy_gb300 import beam_search
+    monkeypatch.setattr(beam_search, "require_cuda", lambda *a: None)
+    monkeypatch.setattr(beam_search, "on", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(beam_search, "stream", lambda device: 0)
+    monkeypatch.setattr(beam_search._lib, "ce_beam_reorder", host_reorder)
+    return gbce
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("kind", ["conj", "neg", "conj_strided", "neg_strided"])
+def test_states_that_defer_a_conjugation_or_negation(on_host, inplace, kind):
+    z = torch.randn(6, 5, dtype=torch.complex64)
+    z = z[:, :4] if "strided" in kind else z
+    t = z.conj() if "conj" in kind else z.conj().imag
+    assert t.is_conj() or t.is_neg()
+    beams = torch.tensor([[1, 1, 0], [2, -1, 0]])
+    want = t.clone()[[1, 1, 0, 5, 4, 3]]
+    got = on_host.beam_reorder(t, beams, inplace=inplace)
+    assert (got is t) == inplace and torch.equal(got, want)
+
+
+def test_wrappers_take_the_values_of_negated_views():
+    from softmax_cross_entropy_gb300 import _tensors, feed_forward
+    for t in (torch.tensor([1 + 2j]).conj().imag, torch._neg_view(torch.arange(16.0))):
+        assert t.is_neg() and t.is_contiguous()
+        for f in (_tensors.plain, feed_forward.aligned):
+            assert not f(t).is_neg() and torch.equal(f(t), t)
 
 
 def test_states_with_tangents_are_not_changed_in_place(monkeypatch):
@@ -320,6 +371,19 @@ def test_reorder_in_place_is_seen_by_autograd():
         t = torch.randn(3, 8, device="cuda")
         want = t[[1, 0, 2]]
         assert torch.equal(gbce.beam_reorder(t, beams, inplace=True), want)
+
+
+@pytest.mark.gpu
+def test_values_of_conjugated_and_negated_views():
+    import softmax_cross_entropy_gb300 as gbce
+    z = torch.randn(3, 4, dtype=torch.complex64, device="cuda")
+    beams = torch.tensor([[1, 0, 2]], device="cuda")
+    for t in (z.conj(), z.conj().imag):
+        assert torch.equal(gbce.beam_reorder(t, beams), t.clone()[[1, 0, 2]])
+    x = torch._neg_view(torch.randn(2, 3, 40, device="cuda"))
+    s = torch._neg_view(torch.rand(2, 3, device="cuda"))
+    compare(gbce.beam_search_step(x, s), reference(x.clone(), s.clone(), 3))
+    assert torch.equal(gbce.dropout(x, 0.0, 1, residual=x), 2 * x.clone())
 
 
 @pytest.mark.gpu
