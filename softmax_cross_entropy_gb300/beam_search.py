@@ -117,6 +117,7 @@ def beam_reorder(states, beams, inplace=False):
     dev = beams.device
     if beams.stride(1) != 1 or beams.stride(0) < K:
         beams = beams.contiguous()
+    beams_row = beams.stride(0) if B > 1 else K  # (the stride of a dimension of one says nothing)
     outs, table = [], []
     for t in states:
         require_cuda(t, "a state")
@@ -154,7 +155,7 @@ def beam_reorder(states, beams, inplace=False):
         raise ValueError("a state is given twice")
     table = (_lib.BeamState * n)(*table)
     with on(dev):
-        check(_lib.ce_beam_reorder(table, n, ptr(beams), beams.stride(0), B, K, stream(dev)),
+        check(_lib.ce_beam_reorder(table, n, ptr(beams), beams_row, B, K, stream(dev)),
               "ce_beam_reorder")
     if inplace:  # a backward that saved a state then finds that it was changed
         torch.autograd.graph.increment_version([t for t in outs if not t.is_inference()])

@@ -168,6 +168,14 @@ def test_states_that_defer_a_conjugation_or_negation(on_host, inplace, kind):
     assert (got is t) == inplace and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("beams", [
+    torch.tensor([[1], [0], [1]]).t(), torch.tensor([1, 0, 1]).as_strided((1, 3), (0, 1)),
+    torch.tensor([1, 9, 0, 9, 1]).as_strided((1, 3), (1, 2)), torch.tensor([[1, 0, 1, 7]])[:, :3]])
+def test_beams_of_one_entry_whatever_their_strides(on_host, beams):
+    state = torch.randn(3, 4)
+    assert torch.equal(on_host.beam_reorder(state, beams), state[[1, 0, 1]])
+
+
 def test_wrappers_take_the_values_of_negated_views():
     from softmax_cross_entropy_gb300 import _tensors, feed_forward
     for t in (torch.tensor([1 + 2j]).conj().imag, torch._neg_view(torch.arange(16.0))):
