@@ -176,6 +176,22 @@ def test_beams_of_one_entry_whatever_their_strides(on_host, beams):
     assert torch.equal(on_host.beam_reorder(state, beams), state[[1, 0, 1]])
 
 
+def test_beams_that_are_part_of_a_state(on_host):
+    # the history of the chosen beams [T, B, K] is a state like the others
+    B, K, T = 2, 3, 4
+    parents = torch.randint(0, K, (T, B, K))
+    parents[2] = torch.tensor([[1, 1, 0], [2, 0, 0]])
+    history, cache = parents.permute(1, 2, 0), torch.randn(B * K, 5)
+    rows = [1, 1, 0, 5, 3, 3]
+    want = [history.clone().reshape(B * K, T)[rows].reshape(B, K, T), cache[rows]]
+    on_host.beam_reorder([history, cache], parents[2], inplace=True)
+    assert torch.equal(history, want[0]) and torch.equal(cache, want[1])
+    whole = parents[2].clone()
+    want = whole.reshape(B * K)[rows].reshape(B, K)
+    on_host.beam_reorder([whole, cache], torch.tensor([[1, 1, 0], [2, 0, 0]]), inplace=True)
+    assert torch.equal(whole, want)
+
+
 def test_wrappers_take_the_values_of_negated_views():
     from softmax_cross_entropy_gb300 import _tensors, feed_forward
     for t in (torch.tensor([1 + 2j]).conj().imag, torch._neg_view(torch.arange(16.0))):
@@ -379,6 +395,17 @@ def test_reorder_in_place_is_seen_by_autograd():
         t = torch.randn(3, 8, device="cuda")
         want = t[[1, 0, 2]]
         assert torch.equal(gbce.beam_reorder(t, beams, inplace=True), want)
+
+
+@pytest.mark.gpu
+def test_reorder_of_the_beams_own_history():
+    import softmax_cross_entropy_gb300 as gbce
+    B, K, T = 64, 8, 16
+    parents = torch.randint(0, K, (T, B, K), device="cuda")
+    history, cache = parents.permute(1, 2, 0), torch.randn(B * K, 4096, device="cuda")
+    want = [plain_reorder(t.clone(), parents[5].clone()) for t in (history, cache)]
+    gbce.beam_reorder([history, cache], parents[5], inplace=True)
+    assert torch.equal(history, want[0]) and torch.equal(cache, want[1])
 
 
 @pytest.mark.gpu
