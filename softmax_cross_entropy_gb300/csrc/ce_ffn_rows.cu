@@ -238,7 +238,8 @@ ffn_rows(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUten
             const int b = run & 1;
             const bool ok = tc_wait(smem_u32(&acc_full[b]), static_cast<uint32_t>(run >> 1) & 1u,
                                     a.timeout_ns);
-            if (!ok || *reinterpret_cast<volatile int*>(&s_fail)) {
+            // (the whole warp goes on or none of it: what follows takes all lanes)
+            if (__any_sync(~0u, !ok || *reinterpret_cast<volatile int*>(&s_fail))) {
                 if (lane == 0) s_fail = 1;
                 break;
             }

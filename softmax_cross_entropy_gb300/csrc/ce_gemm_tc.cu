@@ -317,8 +317,9 @@ tc_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtens
             const int b = i % NACC;
             const bool ok = mbar_wait_bounded(smem_u32(&acc_full[b]),
                                               static_cast<uint32_t>(i / NACC) & 1u, a.timeout_ns);
-            if (!ok || *reinterpret_cast<volatile int*>(&s_fail) ||
-                *reinterpret_cast<volatile unsigned*>(a.abort)) {
+            // (the whole warp goes on or none of it: what follows takes all lanes)
+            if (__any_sync(~0u, !ok || *reinterpret_cast<volatile int*>(&s_fail) ||
+                                    *reinterpret_cast<volatile unsigned*>(a.abort))) {
                 if (lane == 0) s_fail = 1;
                 break;
             }
