@@ -53,8 +53,11 @@ constexpr int kScanBuf = 64;        // words of a warp's buffer when merging
 constexpr int kPickThreads = 256;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxCandidates = 64;
-constexpr int kMaxSplits = 128;     // parts a row
-constexpr int64_t kMaxVocab = 1 << 20;  // 94 parts of fp32
+constexpr int64_t kMaxVocab = 1 << 20;
+constexpr int kMergeLists = 128;    // lists of an entry that a warp merges
+// parts that a row needs (94, of 2^20 logits in fp32); with few rows a row
+// has more, but an entry's K rows then no more than about two an SM
+constexpr int kMostParts = (kMaxVocab / 4 + kScanMost - 1) / kScanMost;
 constexpr float kLowest = -3.402823466e38f;
 
 // A candidate inside a row: the logit as an ordered integer above the
@@ -94,9 +97,10 @@ struct BeamArgs {
     int64_t* out_tokens;
 };
 
-// The most shared memory that beam_pick takes: 32 beams of 128 parts and 64
-// candidates squared, or all lists' candidates below that.
-constexpr size_t kPickSmem = 16 * (kMaxBeams * kMaxSplits + kMaxCandidates * kMaxCandidates);
+// The most shared memory that beam_pick takes: the candidates of all lists
+// that are merged, or the first candidates of all lists and M squared.
+constexpr size_t kPickSmem = 16 * kMergeLists * kMaxCandidates;
+static_assert(16 * (kMaxBeams * kMostParts + kMaxCandidates * kMaxCandidates) <= kPickSmem, "beam_pick");
 
 // Whether beam `row` has candidates of its own (a finite score, not finished).
 __device__ __forceinline__ bool beam_lives(const BeamArgs& a, int64_t row) {
@@ -567,7 +571,6 @@ __device__ __forceinline__ void no_pick(const BeamArgs& a, int64_t b, int i) {
 
 // The M best of nl sorted lists of M picks, by one warp: lane i holds the
 // first of lists i, i + 32, ...
-constexpr int kMergeLists = 128;
 __device__ __forceinline__ int merge_lists(const BeamArgs& a, const Pick* all, int nl, int64_t b, int lane) {
     constexpr int R = kMergeLists / 32;
     Pick head[R];
@@ -617,8 +620,7 @@ __device__ __forceinline__ int merge_lists(const BeamArgs& a, const Pick* all, i
     return a.M;
 }
 
-// MERGE: the entry has at most kMergeLists lists, whose candidates fit in
-// shared memory.
+// MERGE: the entry has at most kMergeLists lists.
 template <bool MERGE>
 __global__ void __launch_bounds__(kPickThreads) beam_pick(const __grid_constant__ BeamArgs a) {
     extern __shared__ Pick pick_smem[];
@@ -950,15 +952,19 @@ extern "C" ce_status ce_beam_select(const void* logits, int dtype, int64_t B, in
     a.out_tokens = out_tokens;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* args[] = {&a};
+    const size_t lists_n = static_cast<size_t>(K * a.splits);
+    const bool merge = lists_n <= kMergeLists;
+    const size_t smem = sizeof(Pick) * static_cast<size_t>(merge ? lists_n * M : lists_n + M * M);
+    if (smem > kPickSmem) {
+        record_message("a batch entry's beams have more parts than the selection holds");
+        return CE_ERR_UNSUPPORTED;
+    }
     const void* scan = M <= 32 ? scan_fn<1>(dtype) : scan_fn<2>(dtype);
     rc = tc_smem_limit(scan, 16 * (kScanMost + 1));
     if (rc != CE_OK) return rc;
     cudaError_t e = cudaLaunchKernel(scan, dim3(static_cast<unsigned>(plan.grid)), dim3(kScanThreads), args,
                                      16 * static_cast<size_t>(plan.part_vec + 1), st);
     if (e != cudaSuccess) return record_cuda_failure(e, "beam scan launch");
-    const size_t lists_n = static_cast<size_t>(K * a.splits), all = sizeof(Pick) * lists_n * M;
-    const bool merge = lists_n <= kMergeLists && all <= kPickSmem;
-    const size_t smem = merge ? all : sizeof(Pick) * (lists_n + static_cast<size_t>(M * M));
     const void* pick = merge ? (const void*)&beam_pick<true> : (const void*)&beam_pick<false>;
     if (smem > 48 * 1024) {
         rc = tc_smem_limit(pick, kPickSmem);

@@ -35,8 +35,8 @@ namespace {
 constexpr int kRowsThreads = 192;  // producer, MMA issuer, 4 epilogue warps
 constexpr int kRowsTile = 128;     // weight rows of a tile
 constexpr uint32_t kRowsA = kRowsTile * kBK * 2;  // 16 KB
-constexpr int kRowsStages = 11;
-// The ring: where three units or more fit in the smaller (up to 96 tokens),
+constexpr int kRowsStages = 7;  // units of the ring at most (of 18 KB, up to 16 tokens)
+// The ring: where three units or more fit in the smaller (up to 112 tokens),
 // two CTAs an SM, so that the second product's ring fills while the first
 // product still runs; else one. (Rings of 110 KB each: 60 us for 1 token of
 // 4096 x 12288, 130 and 92 KB 59 us, 148 and 74 KB 60 us.)

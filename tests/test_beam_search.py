@@ -438,6 +438,23 @@ def test_the_largest_vocabulary(V, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,K,M", [(1, 32, 64), (1, 1, 64), (2, 2, 33)])
+def test_the_most_parts(B, K, M):
+    # 32 beams of 94 parts, one row in as many as the GPU is given, and few rows between
+    import softmax_cross_entropy_gb300 as gbce
+    x, s = inputs(B, K, 2 ** 20, "f32", seed=K)
+    got = gbce.beam_search_step(x, s, num_candidates=M)
+    # only a beam's best M can be among them: the rest counts in its log-sum-exp alone
+    val, at = x.topk(M, dim=2)
+    lse = torch.logsumexp(x.double(), 2)
+    tot = (s.double()[..., None] + (val.double() - lse[..., None])).cpu().numpy().reshape(B, -1)
+    at = (torch.arange(K, device="cuda")[:, None] * 2 ** 20 + at).cpu().numpy().reshape(B, -1)
+    order = np.lexsort((at, -tot))[:, :M]
+    tot, at = np.take_along_axis(tot, order, 1), np.take_along_axis(at, order, 1)
+    compare(got, (tot, at // 2 ** 20, at % 2 ** 20))
+
+
+@pytest.mark.gpu
 def test_logits_past_32_bits():
     import softmax_cross_entropy_gb300 as gbce
     B, K, V = 66, 32, 2 ** 20 - 1
