@@ -489,6 +489,19 @@ ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const 
                      size_t workspace_bytes, ce_stream_t stream);
 
 /*
+ * ce_ffn_tiles - the tiles that one of the block's products is dealt out in
+ * on a GPU of `sms` SMs, by its sizes alone (no GPU is asked).
+ * product      0: the projections, 1: the down projection (each for more than
+ *              256 rows; fewer take a form of their own), 2: dh, 3: dx, 4: the
+ *              weight gradients, all three in one launch.
+ * tile         four int64 on the host, written: a tile's rows and columns of
+ *              the output (projections: of each), the SMs that share it (1 or
+ *              2), and the number of tiles.
+ */
+ce_status ce_ffn_tiles(int product, int64_t rows, int64_t H, int64_t I, int64_t O, int sms,
+                       int64_t* tile);
+
+/*
  * ce_ffn_bwd - the gradients of ce_ffn_fwd: with dz = dropout(dy), dh = dz @
  * w_down, dg = dh s and du = dh a:
  *     dx = dg @ w_gate + du @ w_up,  dw_gate = dg^T @ x,  dw_up = du^T @ x,

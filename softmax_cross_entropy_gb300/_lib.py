@@ -49,6 +49,7 @@ SIGNATURES = {
     "ce_ffn_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "ce_ffn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64, _U64, _P, _P,
                         _P, _P, _P, _P, _SZ, _P]),
+    "ce_ffn_tiles": (_I, [_I, _I64, _I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
     "ce_ffn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _D]),
     "ce_ffn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _D, _U64,
                         _U64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -206,6 +207,10 @@ def ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, 
                state, y, h, s, a, workspace, workspace_bytes, stream):
     return load().ce_ffn_fwd(x, w_gate, w_up, w_down, residual, dtype, rows, H, I, O, act, p, seed,
                              offset, state, y, h, s, a, workspace, workspace_bytes, stream)
+
+
+def ce_ffn_tiles(product, rows, H, I, O, sms, tile):
+    return load().ce_ffn_tiles(product, rows, H, I, O, sms, tile)
 
 
 def ce_ffn_bwd_workspace_bytes(rows, H, I, O, p):

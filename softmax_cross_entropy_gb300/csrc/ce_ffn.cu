@@ -865,22 +865,22 @@ struct FfnMatrix {
     int64_t outer, inner;
 };
 
-// One launch of form `mode`: problems or segments A[i] x B[i].
-ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatrix (&A)[3],
-                     const FfnMatrix (&B)[3], const FfnDevice& d, cudaStream_t st) {
-    g.timeout_ns = d.timeout_ns;
-    g.status = d.status;
-    // The tile shape by its rounds of tiles over the SMs (or pairs of SMs)
-    // and what a round was measured to take, that of pairs being 100 (per 4096
-    // of K, bf16: 20.5 us). 256 rows an SM: 195 (4096 x 4096 x 24576 475
-    // against 482 us for pairs, 4096 x 2048 x 16384 156 against 167), 215 where
-    // the epilogue, which it does not overlap, does more than store (4096 x
-    // 12288 x 4096 549 against 472 us, 2048 x 4096 x 12288 136 against 130).
-    // 128 rows: 115 (4096 x 4096 x 12288 300 against 256 us; 300 rows of the
-    // block of 4096 x 12288 117 against 135). Narrower tiles of pairs save little
-    // of a round, but a product of few tiles finds more SMs with them: 224
-    // columns 95, 192 columns 91 (512 rows of 1024 x 4096 40 against 48 us, of
-    // 4096 x 12288 131 against 137).
+// The tile shape of a launch of form `mode` with problems of M x N, by its
+// rounds of tiles over the SMs (or pairs of SMs) and what a round was measured
+// to take, that of pairs being 100 (per 4096 of K, bf16: 20.5 us). 256 rows an
+// SM: 195 (4096 x 4096 x 24576 475 against 482 us for pairs, 4096 x 2048 x
+// 16384 156 against 167), 215 where the epilogue, which it does not overlap,
+// does more than store (4096 x 12288 x 4096 549 against 472 us, 2048 x 4096 x
+// 12288 136 against 130). 128 rows: 115 (4096 x 4096 x 12288 300 against 256
+// us; 300 rows of the block of 4096 x 12288 117 against 135). Narrower tiles
+// of pairs save little of a round, but a product of few tiles finds more SMs
+// with them: 224 columns 95, 192 columns 91 (512 rows of 1024 x 4096 40
+// against 48 us, of 4096 x 12288 131 against 137).
+struct FfnForm {
+    int shape, width;
+    int64_t tiles;
+};
+FfnForm ffn_form(int mode, const int64_t* M, const int64_t* N, int problems, int sms) {
     const bool bare = mode == kDx || mode == kDw;
     const struct {
         int shape, width;
@@ -889,24 +889,33 @@ ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatr
                  {kPair, 192, 91}, {kPair, 224, 95}};
     // (kGateUp: half the columns are whole units of 32 of the epilogue's)
     const int count = mode == kDown ? 5 : mode == kGateUp ? 4 : 3;
-    int shape = kPair;
+    FfnForm best = {kPair, kBN, 0};
     int64_t least = INT64_MAX;
-    g.width = kBN;
     for (int i = 0; i < count; ++i) {
         const auto& f = forms[i];
         const int64_t rows = f.shape == 128 ? 128 : 256;
         const int64_t across = mode == kGateUp ? f.width / 2 : f.width;
-        const int64_t ctas = f.shape == kPair ? std::max(d.sms / 2, 1) : d.sms;
+        const int64_t ctas = f.shape == kPair ? std::max(sms / 2, 1) : sms;
         int64_t tiles = 0;
         for (int p = 0; p < problems; ++p)
-            tiles += (g.M[p] + rows - 1) / rows * ((g.N[p] + across - 1) / across);
+            tiles += (M[p] + rows - 1) / rows * ((N[p] + across - 1) / across);
         const int64_t cost = (tiles + ctas - 1) / ctas * f.round;
         if (cost < least) {
             least = cost;
-            shape = f.shape;
-            g.width = f.width;
+            best = FfnForm{f.shape, f.width, tiles};
         }
     }
+    return best;
+}
+
+// One launch of form `mode`: problems or segments A[i] x B[i].
+ce_status ffn_launch(int mode, int dtype, FfnGemm g, int problems, const FfnMatrix (&A)[3],
+                     const FfnMatrix (&B)[3], const FfnDevice& d, cudaStream_t st) {
+    g.timeout_ns = d.timeout_ns;
+    g.status = d.status;
+    const FfnForm form = ffn_form(mode, g.M, g.N, problems, d.sms);
+    const int shape = form.shape;
+    g.width = form.width;
     const int64_t cols = mode == kGateUp ? g.width / 2 : g.width;
     const int bm = shape == 128 ? 128 : 256;
     int64_t end = 0;
@@ -1102,6 +1111,23 @@ extern "C" ce_status ce_ffn_fwd(const void* x, const void* w_gate, const void* w
     down.res_vec = O % 8 == 0 && aligned(residual) ? 1 : 0;
     ffn_output(&down, 0, y, O);
     return ffn_launch(kDown, dtype, down, 1, {{h, rows, I8}}, {{w_down, O, I8}}, d, st);
+}
+
+extern "C" ce_status ce_ffn_tiles(int product, int64_t rows, int64_t H, int64_t I, int64_t O, int sms,
+                                  int64_t* tile) {
+    if (product < kGateUp || product > kDw || sms < 1 || !tile) return CE_ERR_INVALID_ARG;
+    const ce_status rc = check_ffn(CE_BF16, rows, H, I, O, CE_ACT_SILU);
+    if (rc != CE_OK) return rc;
+    const int64_t I8 = up8(I);
+    const int64_t n[] = {I8, O, I8, H};
+    const bool dw = product == kDw;
+    const int64_t M[3] = {dw ? I : rows, I, O}, N[3] = {dw ? H : n[product], H, I};
+    const FfnForm f = ffn_form(product, M, N, dw ? 3 : 1, sms);
+    tile[0] = f.shape == 128 ? 128 : 256;
+    tile[1] = product == kGateUp ? f.width / 2 : f.width;
+    tile[2] = f.shape == kPair ? 2 : 1;
+    tile[3] = f.tiles;
+    return CE_OK;
 }
 
 extern "C" size_t ce_ffn_bwd_workspace_bytes(int64_t rows, int64_t H, int64_t I, int64_t O, double p) {

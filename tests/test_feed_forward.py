@@ -1,6 +1,7 @@
 """The gated feed-forward block: refusals (CPU), and the kernels against the
 formulas in 64 bits (GPU)."""
 import contextlib
+import ctypes
 import math
 
 import numpy as np
@@ -140,6 +141,52 @@ def test_wrapper_refuses_cpu_tensors():
         gbce.gated_feed_forward(t, t, t, t)
 
 
+UP, DOWN, DH, DX, DW = range(5)  # the block's products
+
+
+def tiles_of(product, rows, H, I, O, sms=152):
+    """((rows, columns, SMs) of a tile, the tiles that the busiest SM or pair works on)."""
+    from softmax_cross_entropy_gb300 import _lib
+    t = (ctypes.c_int64 * 4)()
+    assert _lib.ce_ffn_tiles(product, rows, H, I, O, sms, t) == _lib.CE_OK
+    return tuple(t[:3]), -(-t[3] // (sms // t[2]))
+
+
+# Sizes at which each product takes each of its tile shapes, several tiles an SM (or pair) where
+# the shape is ever taken so: {product: (tile, tiles of the busiest at least)}. Edges are ragged,
+# those with odd sizes store rows that are not whole vectors.
+ONE = {128: (128, 256, 1), 256: (256, 256, 1)}
+PAIR = {w: (256, w, 2) for w in (192, 224, 256)}
+SHAPES = [
+    (300, 72, 38993, 72, {UP: ((128, 128, 1), 6), DH: (ONE[128], 4), DW: (ONE[128], 6)}),
+    (300, 38984, 72, 38984, {DOWN: (ONE[128], 4), DX: (ONE[128], 4), DW: (ONE[128], 5)}),
+    (297, 38993, 71, 38993, {DOWN: (ONE[128], 4), DX: (ONE[128], 4)}),
+    (500, 72, 39000, 72, {UP: ((256, 128, 2), 8), DH: (PAIR[256], 4)}),
+    (497, 72, 7000, 72, {UP: ((256, 96, 2), 2)}),
+    (500, 72, 136, 38000, {DOWN: (PAIR[256], 4)}),
+    (500, 72, 136, 39000, {DOWN: (PAIR[224], 5)}),
+    (499, 72, 136, 13999, {DOWN: (PAIR[192], 2)}),
+    (500, 23000, 504, 72, {DX: (PAIR[256], 3), DW: (PAIR[256], 5)}),
+    (499, 19152, 504, 19152, {DX: (ONE[256], 1), DW: (ONE[256], 3)}),
+    (500, 57496, 72, 72, {DX: (ONE[256], 3)}),
+    (499, 57491, 72, 72, {DX: (ONE[256], 3)})]
+
+
+@pytest.mark.parametrize("rows,H,I,O,forms", SHAPES)
+def test_sizes_take_the_tiles_they_are_meant_for(rows, H, I, O, forms):
+    for product, (tile, least) in forms.items():
+        got, most = tiles_of(product, rows, H, I, O)
+        assert got == tile and most >= least, (product, got, most)
+
+
+def test_tiles_refuses():
+    from softmax_cross_entropy_gb300 import _lib
+    t = (ctypes.c_int64 * 4)()
+    for bad in ((-1, 4, 8, 8, 8, 152, t), (5, 4, 8, 8, 8, 152, t), (0, -1, 8, 8, 8, 152, t),
+                (0, 4, 0, 8, 8, 152, t), (0, 4, 8, 8, 8, 0, t), (0, 4, 8, 8, 8, 152, None)):
+        assert _lib.ce_ffn_tiles(*bad) == _lib.CE_ERR_INVALID_ARG
+
+
 @pytest.fixture
 def stubbed(monkeypatch):
     """The wrapper on CPU tensors, its library call a plain copy."""
@@ -263,6 +310,34 @@ def test_odd_sizes(rows, H, I, O, p, residual):
     for name, got in zip(("dx", "dw_gate", "dw_up", "dw_down"), torch.autograd.grad(y, leaves, dy)):
         assert got.shape == want[name].shape
         check(got, want[name], size[name], torch.bfloat16, 1, H + 2 * I + O + rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,H,I,O,forms", SHAPES)
+def test_every_tile_shape_and_several_tiles_an_sm(dtype, rows, H, I, O, forms):
+    import softmax_cross_entropy_gb300 as gbce
+    dt = DT[dtype]
+    x, wg, wu, wd, res, dy = make(rows, H, I, O, dtype)
+    leaves = [t.requires_grad_() for t in (x, wg, wu, wd)]
+    p = 0.25 if rows * O < 1 << 23 else 0.0  # (the reference's words are formed on the CPU)
+    y = gbce.gated_feed_forward(x, wg, wu, wd, dropout_p=p, seed=21, residual=res)
+    grads = torch.autograd.grad(y, leaves, dy)
+    want, size = reference(x, wg, wu, wd, "silu", mask64(rows, O, p, 21), res, dy)
+    check(y, want["y"], size["y"], dt, 1, H + I)
+    for name, got, n in zip(("dx", "dw_gate", "dw_up", "dw_down"), grads, (O + 2 * I, O + rows, O + rows, rows)):
+        check(got, want[name], size[name], dt, 1, n + H)
+    # the bounds above grow with the terms of a product: a tile or a run of rows that is wrong
+    # shows in its own norm, which holds one rounding of its factors and one of the result
+    eps = torch.finfo(dt).eps
+    for name, got in zip(("y", "dx", "dw_gate", "dw_up", "dw_down"), (y, *grads)):
+        err = (got.detach().double() - want[name]).square()
+        ref = want[name].square()
+        for dim in (0, 1):
+            for e, r in zip(err.split(32, dim), ref.split(32, dim)):
+                if r.numel() >= 4096:
+                    assert float(e.sum()) <= (3 * eps) ** 2 * float(r.sum()), (name, dim)
+    assert gbce.device_status() == 0
 
 
 @pytest.mark.gpu
