@@ -65,7 +65,8 @@ enum FfnMode : int { kGateUp, kDown, kDact, kDx, kDw };
 // Tile shapes, 256 accumulator columns wide:
 //  * 128: 128 rows on one SM, 4 stages of 48 KB, two accumulators;
 //  * 256: 256 rows on one SM, 3 stages of 64 KB, its two halves in all of
-//    the tensor memory: the epilogue does not overlap the next tile;
+//    the tensor memory: the epilogue does not overlap the next tile (dx and
+//    the weight gradients, whose epilogue is short);
 //  * kPair: 256 rows on a pair of SMs (a cluster of two CTAs whose tensor
 //    cores work as one: each holds 128 rows of A, half of B's 256 columns and
 //    128 rows of the accumulator), 3 stages of 64 KB a CTA, two accumulators.
@@ -823,18 +824,19 @@ __global__ void __launch_bounds__(256) ffn_pack(const __grid_constant__ PackArgs
 }
 
 template <uint32_t AB, int MODE>
-const void* ffn_fn(int bm) {
-    return bm == kPair ? (const void*)&ffn_gemm<AB, MODE, kPair>
-           : bm == 256 ? (const void*)&ffn_gemm<AB, MODE, 256> : (const void*)&ffn_gemm<AB, MODE, 128>;
+const void* ffn_fn(int shape) {
+    if constexpr (MODE == kDx || MODE == kDw)
+        if (shape == 256) return (const void*)&ffn_gemm<AB, MODE, 256>;
+    return shape == kPair ? (const void*)&ffn_gemm<AB, MODE, kPair> : (const void*)&ffn_gemm<AB, MODE, 128>;
 }
-const void* ffn_fn(int dtype, int mode, int bm) {
+const void* ffn_fn(int dtype, int mode, int shape) {
     const bool bf = dtype == CE_BF16;
     switch (mode) {
-    case kGateUp: return bf ? ffn_fn<1u, kGateUp>(bm) : ffn_fn<0u, kGateUp>(bm);
-    case kDown: return bf ? ffn_fn<1u, kDown>(bm) : ffn_fn<0u, kDown>(bm);
-    case kDact: return bf ? ffn_fn<1u, kDact>(bm) : ffn_fn<0u, kDact>(bm);
-    case kDx: return bf ? ffn_fn<1u, kDx>(bm) : ffn_fn<0u, kDx>(bm);
-    default: return bf ? ffn_fn<1u, kDw>(bm) : ffn_fn<0u, kDw>(bm);
+    case kGateUp: return bf ? ffn_fn<1u, kGateUp>(shape) : ffn_fn<0u, kGateUp>(shape);
+    case kDown: return bf ? ffn_fn<1u, kDown>(shape) : ffn_fn<0u, kDown>(shape);
+    case kDact: return bf ? ffn_fn<1u, kDact>(shape) : ffn_fn<0u, kDact>(shape);
+    case kDx: return bf ? ffn_fn<1u, kDx>(shape) : ffn_fn<0u, kDx>(shape);
+    default: return bf ? ffn_fn<1u, kDw>(shape) : ffn_fn<0u, kDw>(shape);
     }
 }
 
@@ -869,10 +871,12 @@ struct FfnMatrix {
 // rounds of tiles over the SMs (or pairs of SMs) and what a round was measured
 // to take, that of pairs being 100 (per 4096 of K, bf16: 20.5 us). 256 rows an
 // SM: 195 (4096 x 4096 x 24576 475 against 482 us for pairs, 4096 x 2048 x
-// 16384 156 against 167), 215 where the epilogue, which it does not overlap,
-// does more than store (4096 x 12288 x 4096 549 against 472 us, 2048 x 4096 x
-// 12288 136 against 130). 128 rows: 115 (4096 x 4096 x 12288 300 against 256
-// us; 300 rows of the block of 4096 x 12288 117 against 135). Narrower tiles
+// 16384 156 against 167). Where the epilogue, which that shape does not
+// overlap, does more than store, its round takes 215 (4096 x 12288 x 4096 549
+// against 472 us, 2048 x 4096 x 12288 136 against 130), more than two of pairs:
+// only dx and the weight gradients have it. 128 rows: 115 (4096 x 4096 x 12288
+// 300 against 256 us; 300 rows of the block of 4096 x 12288 117 against 135).
+// Narrower tiles
 // of pairs save little of a round, but a product of few tiles finds more SMs
 // with them: 224 columns 95, 192 columns 91 (512 rows of 1024 x 4096 40
 // against 48 us, of 4096 x 12288 131 against 137).
@@ -885,14 +889,17 @@ FfnForm ffn_form(int mode, const int64_t* M, const int64_t* N, int problems, int
     const struct {
         int shape, width;
         int64_t round;
-    } forms[] = {{kPair, 256, 100}, {256, 256, bare ? 195 : 215}, {128, 256, 115},
-                 {kPair, 192, 91}, {kPair, 224, 95}};
-    // (kGateUp: half the columns are whole units of 32 of the epilogue's)
-    const int count = mode == kDown ? 5 : mode == kGateUp ? 4 : 3;
+        bool taken;
+    } forms[] = {{kPair, 256, 100, true},
+                 {256, 256, 195, bare},
+                 {128, 256, 115, true},
+                 {kPair, 192, 91, mode == kDown || mode == kGateUp},
+                 // (kGateUp: half the columns are whole units of 32 of the epilogue's)
+                 {kPair, 224, 95, mode == kDown}};
     FfnForm best = {kPair, kBN, 0};
     int64_t least = INT64_MAX;
-    for (int i = 0; i < count; ++i) {
-        const auto& f = forms[i];
+    for (const auto& f : forms) {
+        if (!f.taken) continue;
         const int64_t rows = f.shape == 128 ? 128 : 256;
         const int64_t across = mode == kGateUp ? f.width / 2 : f.width;
         const int64_t ctas = f.shape == kPair ? std::max(sms / 2, 1) : sms;

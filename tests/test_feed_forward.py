@@ -179,6 +179,14 @@ def test_sizes_take_the_tiles_they_are_meant_for(rows, H, I, O, forms):
         assert got == tile and most >= least, (product, got, most)
 
 
+@pytest.mark.parametrize("sms", [2, 3, 151, 152])
+def test_long_epilogues_never_take_the_shape_that_does_not_overlap_them(sms):
+    for product in (UP, DOWN, DH):
+        for n in range(1, 400):
+            rows, _, shared = tiles_of(product, 512, 256, 128 * n, 128 * n, sms)[0]
+            assert rows == 128 or shared == 2
+
+
 def test_tiles_refuses():
     from softmax_cross_entropy_gb300 import _lib
     t = (ctypes.c_int64 * 4)()
