@@ -469,7 +469,9 @@ enum {
  *              elements; p = 0 applies none.
  * h            [rows, I8] in dtype, 16-byte aligned, written: act(g) u with
  *              g = x @ w_gate^T and u = x @ w_up^T, rounded once. I8 is I
- *              rounded up to a multiple of 8; the columns behind I get 0.
+ *              rounded up to a multiple of 8; the columns behind I get 0. (In
+ *              fp16 a product above 65504 is infinite there, and so is what y
+ *              gets from it.)
  * s, a         [rows, I8] fp32, 16-byte aligned, written: u act'(g) and
  *              act(g), what ce_ffn_bwd needs besides h; or both NULL.
  * workspace    device memory of at least ce_ffn_fwd_workspace_bytes(rows, H,
@@ -544,12 +546,13 @@ ce_status ce_ffn_bwd(const void* dy, const void* x, const void* w_gate, const vo
  * out_scores, out_beams, out_tokens   [B, M]: candidate (k, v) has the score
  *              scores[k] + logits[k, v] - log sum_j exp(logits[k, j]), formed
  *              in pairs of fp32 (48 bits) and rounded to fp32 for the output;
- *              descending,
- *              equal ones by the lowest k V + v. Within a beam the order is
- *              that of the logits. Tokens with a logit of -inf or NaN are no
- *              candidates (and add nothing to the sum); a beam with no other
- *              token, or with a logit of +inf, has none, nor has a token
- *              whose score is not finite in fp32. Places without a candidate hold the score -inf, beam -1 and pad_token.
+ *              descending, equal ones by the lowest k V + v (a beam's tokens
+ *              whose scores are equal in 48 bits though their logits are not
+ *              come in either order). Tokens with a logit of -inf or NaN are
+ *              no candidates (and add nothing to the sum); a beam with no
+ *              other token, or with a logit of +inf, has none, nor has a token
+ *              whose score is not finite in fp32. Places without a candidate
+ *              hold the score -inf, beam -1 and pad_token.
  * workspace    at least ce_beam_workspace_bytes(...) bytes, 256-byte
  *              aligned, owned by the caller; nothing in it needs to be set.
  * Asynchronous on `stream`; uses no library scratch. Results do not depend on

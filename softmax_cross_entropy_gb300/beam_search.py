@@ -27,7 +27,7 @@ def beam_search_step(logits, scores, num_candidates=None, finished=None, pad_tok
     batch entry: BeamCandidates of scores (float32), beams and tokens (int64),
     each [B, num_candidates], by descending score, equal ones by the lowest
     beam, then token. logits [B, K, V] in float32, bfloat16 or float16, K at
-    most 32, V at most 2^20; scores [B, K] float32, the beams'
+    most 32, B and V at most 2^20; scores [B, K] float32, the beams'
     log-probabilities so far. Gradients are not tracked.
 
     A candidate's score is scores[b, k] + log_softmax(logits[b, k])[v]. Tokens
@@ -97,15 +97,15 @@ def _blocks(t, skip):
 def beam_reorder(states, beams, inplace=False):
     """states[b, j] = states[b, beams[b, j]] for a tensor or a sequence of
     tensors of beams' states, each [B, K, ...] or [B * K, ...], of any dtype.
-    beams [B, K] int64 on their device; a value outside [0, K) (such as the -1
+    beams [B, K] int64 on their device, K at most 32; a value outside [0, K) (such as the -1
     of a place without a candidate) keeps row j as it is.
 
     Returns new tensors, or with inplace=True changes the states and returns
     them (rows that keep their state are not touched). Strided states, such as
     cache[:, :, :length], are taken when their rows are equally spaced blocks
     of contiguous elements (ValueError otherwise). States that are changed in
-    place must not overlap one another. The states' gradients are not
-    tracked."""
+    place must not overlap one another (beams may lie in one of them). The
+    states' gradients are not tracked."""
     one = isinstance(states, torch.Tensor)
     states = [states] if one else list(states)
     require_cuda(beams, "beams")

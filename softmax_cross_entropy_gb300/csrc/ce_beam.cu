@@ -26,10 +26,13 @@
 // Candidates are ordered by (score in 48 bits, then lowest k V + v), so ties
 // and the order in which warps finish do not show in the result.
 //
-// One read of the logits; the scan is bound by the instructions of its two
-// passes (32 logits take a warp 15 of them in 16 bits, 20 in 32; issue slots
-// 55-60% taken): 64 x 8 x 131072 fp32 66 us (4.1 TB/s), bf16 45 us (3 TB/s). The
-// reordering is bound by HBM: 2 x 134 MB of states in 67 us.
+// One read of the logits. The scan fills neither the issue slots (54-60%
+// taken; 32 logits take a warp 15 instructions in 16 bits, 20 in 32) nor HBM
+// (36-49% of ncu's peak): a CTA has one stage, waits for a whole part, crosses
+// about five barriers and asks for the next part after its second pass, which
+// the three other CTAs of the SM hide in part: 64 x 8 x 131072 fp32 66 us (4.1
+// TB/s), bf16 45 us (3 TB/s). The reordering is bound by HBM: 2 x 134 MB of
+// states in 67 us.
 #include <algorithm>
 #include <cstdint>
 #include <string>

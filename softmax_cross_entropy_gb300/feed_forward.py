@@ -111,8 +111,10 @@ def gated_feed_forward(x, gate_weight, up_weight, down_weight, activation="silu"
     x [..., H], gate_weight and up_weight [I, H], down_weight [O, I], residual
     None or [..., O], all bfloat16 or float16 on one CUDA device; activation
     "silu", "gelu" or "gelu_tanh". dropout_p, seed and offset as for dropout()
-    over the [..., O] elements. Differentiable in x, the weights and residual;
-    for that the forward keeps x and 10 bytes for each of the [..., I] elements.
+    over the [..., O] elements. Differentiable (once, in reverse mode) in x, the
+    weights and residual; for that the forward keeps x and 10 bytes for each of
+    the [..., I] elements. act(g) u is rounded to the tensors' type: in float16
+    it is infinite above 65504, and so is what the output gets from it.
 
     H, I and O that are not multiples of 8 cost a packed copy of what they
     concern (x and the projections for H, down_weight for I) on each call."""

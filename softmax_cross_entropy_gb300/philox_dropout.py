@@ -74,7 +74,7 @@ class DropoutFunction(torch.autograd.Function):
 def dropout(x, p, seed, offset=0, residual=None):
     """residual + x with each element dropped with probability p, the others
     scaled by 1 / (1 - p). x (any shape) in float32, bfloat16 or float16 on
-    CUDA; residual None or like x.
+    CUDA; residual None or like x. Differentiable once, in reverse mode.
 
     seed: an int, or an int64 CUDA tensor (seed, offset) that the kernel reads
     when it runs (its offset is added to `offset`): a captured graph then draws
