@@ -26,7 +26,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def plain(t):
     """t's values in contiguous memory (a negation that a view defers, as that
     of z.conj().imag does, is carried out)."""
-    return t.contiguous().resolve_neg()
+    t = t.contiguous()
+    return t.resolve_neg() if t.is_neg() else t
 
 
 def stream(device):
@@ -45,7 +46,7 @@ def forward_mode():
     """Whether forward-mode derivatives are being taken. A tensor with a tangent
     need not require a gradient, so calls then go through their autograd
     Function, which refuses it (none has a forward-mode rule)."""
-    return getattr(forward_ad, "_current_level", 0) >= 0
+    return forward_ad._current_level >= 0
 
 
 # (a CUDA tensor is at hand, so CUDA is initialised)

@@ -118,7 +118,6 @@ def beam_reorder(states, beams, inplace=False):
     if beams.stride(1) != 1 or beams.stride(0) < K:
         beams = beams.contiguous()
     outs, table = [], []
-    beams_at, shared = beams.untyped_storage().data_ptr(), False
     for t in states:
         require_cuda(t, "a state")
         if t.device != dev:
@@ -133,8 +132,6 @@ def beam_reorder(states, beams, inplace=False):
             raise ValueError("a state with a tangent cannot be reordered in place")
         if not inplace and (t.is_conj() or t.is_neg()):
             t = t.resolve_conj().resolve_neg()  # (in place the view stays one)
-        if inplace and t.untyped_storage().data_ptr() == beams_at:
-            shared = True
         n = t.numel()
         if t.is_contiguous():
             row = inner = n // (B * K) if n else 0
@@ -152,12 +149,16 @@ def beam_reorder(states, beams, inplace=False):
             to = (row * b, block_stride * b) if inplace else (blocks * inner * b, inner * b)
             table.append((t.data_ptr(), out.data_ptr(), row * b, block_stride * b, *to, blocks,
                           inner * b))
-    if shared:
-        beams = beams.clone(memory_format=torch.contiguous_format)  # read while the states change
     beams_row = beams.stride(0) if B > 1 else K  # (the stride of a dimension of one says nothing)
     n = len(table)
     if len({at[1] for at in table}) < n:
         raise ValueError("a state is given twice")
+    if inplace and n:  # beams that lie among a state's rows are read while these change
+        first = beams.data_ptr()
+        last = first + 8 * ((B - 1) * beams_row + K)
+        if any(at[1] < last and first < at[1] + (B * K - 1) * at[4] + (at[6] - 1) * at[5] + at[7]
+               for at in table):
+            beams, beams_row = beams.clone(memory_format=torch.contiguous_format), K
     table = (_lib.BeamState * n)(*table)
     with on(dev):
         check(_lib.ce_beam_reorder(table, n, ptr(beams), beams_row, B, K, stream(dev)),

@@ -91,7 +91,9 @@ class GatedFeedForwardFunction(torch.autograd.Function):
 def aligned(t):
     """t as a contiguous tensor whose base the kernels take: 16-byte aligned
     where its rows are whole 16-byte vectors."""
-    t = plain(t)
+    t = t.contiguous()
+    if t.is_neg():
+        t = t.resolve_neg()
     return t.clone() if t.data_ptr() % 16 and t.shape[-1] % 8 == 0 else t
 
 
