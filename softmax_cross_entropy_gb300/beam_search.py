@@ -117,6 +117,10 @@ def beam_reorder(states, beams, inplace=False):
     dev = beams.device
     if beams.stride(1) != 1 or beams.stride(0) < K:
         beams = beams.contiguous()
+    beams_row = beams.stride(0) if B > 1 else K  # (the stride of a dimension of one says nothing)
+    beams_at = beams.data_ptr()
+    beams_end = beams_at + 8 * ((B - 1) * beams_row + K)
+    dual, shared = inplace and forward_mode(), False
     outs, table = [], []
     for t in states:
         require_cuda(t, "a state")
@@ -128,7 +132,7 @@ def beam_reorder(states, beams, inplace=False):
             raise ValueError("a state must be [B, K, ...] or [B * K, ...]")
         if inplace and t.requires_grad:
             raise ValueError("a state that requires a gradient cannot be reordered in place")
-        if inplace and forward_mode() and forward_ad.unpack_dual(t).tangent is not None:
+        if dual and forward_ad.unpack_dual(t).tangent is not None:
             raise ValueError("a state with a tangent cannot be reordered in place")
         if not inplace and (t.is_conj() or t.is_neg()):
             t = t.resolve_conj().resolve_neg()  # (in place the view stays one)
@@ -147,18 +151,16 @@ def beam_reorder(states, beams, inplace=False):
         if n:
             b = t.element_size()
             to = (row * b, block_stride * b) if inplace else (blocks * inner * b, inner * b)
-            table.append((t.data_ptr(), out.data_ptr(), row * b, block_stride * b, *to, blocks,
-                          inner * b))
-    beams_row = beams.stride(0) if B > 1 else K  # (the stride of a dimension of one says nothing)
+            src = t.data_ptr()
+            table.append((src, out.data_ptr(), row * b, block_stride * b, *to, blocks, inner * b))
+            if inplace and src < beams_end and beams_at < src + b * (
+                    (B * K - 1) * row + (blocks - 1) * block_stride + inner):
+                shared = True
     n = len(table)
     if len({at[1] for at in table}) < n:
         raise ValueError("a state is given twice")
-    if inplace and n:  # beams that lie among a state's rows are read while these change
-        first = beams.data_ptr()
-        last = first + 8 * ((B - 1) * beams_row + K)
-        if any(at[1] < last and first < at[1] + (B * K - 1) * at[4] + (at[6] - 1) * at[5] + at[7]
-               for at in table):
-            beams, beams_row = beams.clone(memory_format=torch.contiguous_format), K
+    if shared:  # beams that lie among a state's rows would be read while these change
+        beams, beams_row = beams.clone(memory_format=torch.contiguous_format), K
     table = (_lib.BeamState * n)(*table)
     with on(dev):
         check(_lib.ce_beam_reorder(table, n, ptr(beams), beams_row, B, K, stream(dev)),
