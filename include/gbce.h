@@ -586,8 +586,9 @@ typedef struct {
  * all states are reordered in place or none, and no dst is given twice
  * (CE_ERR_INVALID_ARG); states that overlap one another otherwise, or a dst
  * that overlaps a src or `beams` (which is read while rows are written), are
- * the caller's error. Bytes between blocks and rows are left as they were. K at most 32 (CE_ERR_UNSUPPORTED above). Asynchronous on
- * `stream`; uses no library scratch.
+ * the caller's error. Bytes between blocks and rows are left as they were. K
+ * at most 32 (CE_ERR_UNSUPPORTED above). Asynchronous on `stream`; uses no
+ * library scratch.
  */
 ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* beams,
                           int64_t beams_row, int64_t B, int64_t K, ce_stream_t stream);

@@ -18,16 +18,16 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# The current stream as an integer; the plain call builds a Stream object
-# first (some microseconds, as much as the rest of a short call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def plain(t):
     """t's values in contiguous memory (a negation that a view defers, as that
     of z.conj().imag does, is carried out)."""
     t = t.contiguous()
     return t.resolve_neg() if t.is_neg() else t
+
+
+# The current stream as an integer; the plain call builds a Stream object
+# first (some microseconds, as much as the rest of a short call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def stream(device):
@@ -36,9 +36,10 @@ def stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def once(name):
-    """Refuses a backward that is itself to be differentiated."""
-    if torch.is_grad_enabled():
+def once(name, dy):
+    """Refuses a backward that is itself to be differentiated, in either mode."""
+    if torch.is_grad_enabled() or (
+            forward_mode() and forward_ad.unpack_dual(dy).tangent is not None):
         raise RuntimeError(f"{name} is differentiable once: its backward has no graph")
 
 

@@ -62,7 +62,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        once("gated_feed_forward")
+        once("gated_feed_forward", dy)
         need = ctx.needs_input_grad
         dx = dwg = dwu = dwd = None
         if any(need[:4]):

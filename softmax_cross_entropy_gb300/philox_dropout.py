@@ -60,7 +60,7 @@ class DropoutFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        once("dropout")
+        once("dropout", dy)
         dx = None
         if ctx.needs_input_grad[0]:
             p, seed, offset = ctx.rng

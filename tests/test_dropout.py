@@ -54,6 +54,20 @@ def test_tangents_are_refused_not_dropped(monkeypatch):
     assert torch.equal(gbce.dropout(x, 0.0, 1), x)
 
 
+def test_a_gradient_with_a_tangent_is_refused(monkeypatch):
+    import softmax_cross_entropy_gb300 as gbce
+    from softmax_cross_entropy_gb300 import philox_dropout
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(philox_dropout, "require_cuda", lambda *a: None)
+    monkeypatch.setattr(philox_dropout, "_call", lambda x, *a: x.detach().clone())
+    x, dy = torch.randn(5, requires_grad=True), torch.randn(5)
+    with forward_ad.dual_level():
+        y = gbce.dropout(x, 0.0, 1)
+        with pytest.raises(RuntimeError, match="once"):
+            torch.autograd.grad(y, [x], forward_ad.make_dual(dy, torch.ones(5)), retain_graph=True)
+        assert torch.equal(torch.autograd.grad(y, [x], dy)[0], dy)
+
+
 # ---------------------------------------------------------------- GPU
 
 def expected(x, res, kept, p):

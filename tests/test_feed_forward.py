@@ -223,6 +223,16 @@ def test_tangents_are_refused_not_dropped(stubbed):
         assert torch.equal(stubbed.gated_feed_forward(t, t, t, t), t)
 
 
+def test_a_gradient_with_a_tangent_is_refused(stubbed):
+    from torch.autograd import forward_ad
+    t = torch.randn(8, 8).bfloat16()
+    with forward_ad.dual_level():
+        x = t.clone().requires_grad_()
+        y = stubbed.gated_feed_forward(x, t, t, t)
+        with pytest.raises(RuntimeError, match="once"):
+            torch.autograd.grad(y, [x], forward_ad.make_dual(t, torch.ones_like(t)))
+
+
 @pytest.mark.parametrize("p", [0.0, 0.5, 1.0])
 def test_a_seed_tensor_may_change_before_the_backward(stubbed, monkeypatch, p):
     calls = []
