@@ -244,7 +244,8 @@ def _own_pref(s, case):
     out = gbce.preference_loss(s["logits"], s["tokens"],
                                offsets=s["offsets"] if case["packed"] else None,
                                ref_log_probs=s["ref"], beta=0.1, loss_type=case["loss"],
-                               label_smoothing=case["smoothing"],
+                               # (the plain form of "ipo" has no smoothing)
+                               label_smoothing=case["smoothing"] * (case["loss"] == "sigmoid"),
                                length_average=case["average"], scale=_scale(case),
                                return_scores=True)
     dlogits, = torch.autograd.grad(out.loss, s["logits"])
