@@ -594,6 +594,176 @@ ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* bea
                           int64_t beams_row, int64_t B, int64_t K, ce_stream_t stream);
 
 /*
+ * Token losses: the losses of post-training over rows of logits. The method
+ * has no counterpart: they continue _log_softmax over the same logits. Per
+ * row, with z = x / T (T the temperature), lse = log sum_j exp(z_j), p =
+ * exp(z - lse) and the token t:
+ *
+ *   lp = z_t - lse          H = -sum_j p_j log p_j  (p log p = 0 where p = 0)
+ *
+ * Logits of -inf have p = 0 and a gradient of 0. A counted row without a
+ * finite logit, or with a NaN or +inf among them, gives NaN. Arithmetic is in
+ * fp32 (the sums over rows, sequences and teachers' lists in fp64); gradients
+ * are rounded once into the logits' type.
+ */
+typedef struct {
+    const void* data;     /* logits, elements of dtype (CE_F32, CE_BF16, CE_F16) */
+    void* grad;           /* their gradient, or NULL: the same strides, and the same
+                             address modulo 16 bytes; may be data itself */
+    int dtype;
+    float temperature;    /* T, in [1e-6, 1e6] */
+    int64_t rows, V;      /* V at most 2^19 (CE_ERR_UNSUPPORTED above) */
+    int64_t inner, outer_stride, row_stride; /* row r starts at element
+                             (r / inner) outer_stride + (r % inner) row_stride;
+                             rows must not overlap */
+} ce_rows;
+
+/* Bytes of the workspace that the losses below take (16-byte aligned, owned
+ * by the caller; nothing in it needs to be set). Calls that may overlap in
+ * time, graphs replayed at once among them, need workspaces of their own. */
+size_t ce_rows_workspace_bytes(void);
+
+/*
+ * ce_token_logp - lp and, where entropy is not NULL, H of each row.
+ *
+ * x            x->grad is not used.
+ * tokens       [rows] int32 (int64 with CE_FLAG_TARGET_I64, the only flag).
+ *              A row whose token is ignore_index is not read and gets 0; so
+ *              does one whose token lies outside [0, V), and
+ *              CE_ERR_TARGET_RANGE is recorded for ce_device_status.
+ * logp, entropy   [rows] fp32.
+ * kept         [rows, 4] fp32, 16-byte aligned, or NULL: what
+ *              ce_token_logp_bwd needs of the counted rows (the entropy too
+ *              if it was asked for).
+ */
+ce_status ce_token_logp(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                        uint32_t flags, float* logp, float* entropy, float* kept,
+                        ce_stream_t stream);
+
+/*
+ * ce_token_logp_bwd - x->grad = sum over rows of grad_logp d lp / dx +
+ * grad_entropy d H / dx: per row ([j = t] - p_j) grad_logp / T -
+ * p_j (log p_j + H) grad_entropy / T; exact +0 for rows that do not count.
+ * grad_logp, grad_entropy   [rows] fp32 or NULL (0). The other arguments as
+ *              they were given to ce_token_logp (with entropy not NULL where
+ *              grad_entropy is given).
+ */
+ce_status ce_token_logp_bwd(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                            uint32_t flags, const float* kept, const float* grad_logp,
+                            const float* grad_entropy, ce_stream_t stream);
+
+/*
+ * ce_policy_loss - the clipped policy loss of sampled tokens:
+ *
+ *   r = exp(lp - old)                           (old NULL: r = 1, with lp's slope)
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *     + kl_coef (exp(ref - lp) - (ref - lp) - 1)             (ref NULL: 0)
+ *     - entropy_coef H
+ *   loss = scale sum_i w_i l_i / D   D = sum of w over counted rows ("mean"),
+ *                                    1 ("sum"); "none": scale w_i l_i a row
+ *
+ * and, where x->grad is not NULL, the gradient of the loss ("none": of the
+ * sum of the rows'), in the same pass over the logits. The slope of min at
+ * equal sides is that of r A.
+ *
+ * tokens, ignore_index, flags   as for ce_token_logp; rows that do not count
+ *              have l = 0 and a gradient of exact +0. With no counted row the
+ *              mean is NaN.
+ * advantages   fp32, one for every advantage_rows consecutive rows.
+ * old_logp, ref_logp   [rows] fp32 or NULL.
+ * weight       [rows] fp32 or NULL (1).
+ * clip_low     in [0, 1]; clip_high at least 0 (infinity: no border).
+ * loss         fp32, [rows] for CE_RED_NONE else [1].
+ * logp, entropy, kl   [rows] fp32 or NULL: lp, H, and exp(ref - lp) -
+ *              (ref - lp) - 1; clipped [rows] bytes or NULL: 1 where the clip's
+ *              side was taken. 0 for rows that do not count.
+ */
+ce_status ce_policy_loss(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                         uint32_t flags, const float* advantages, int64_t advantage_rows,
+                         const float* old_logp, const float* ref_logp, const float* weight,
+                         double clip_low, double clip_high, float kl_coef, float entropy_coef,
+                         float scale, int reduction, float* loss, float* logp, float* entropy,
+                         float* kl, uint8_t* clipped, void* workspace, size_t workspace_bytes,
+                         ce_stream_t stream);
+
+/*
+ * ce_distill_loss - distillation from the K largest logits of a teacher:
+ * with its values v_k of the classes j_k,
+ *
+ *   teacher_lse NULL:  q = softmax(v / T)
+ *     l = sum_k q_k (log q_k - log p_{j_k})
+ *   else:              q_k = exp(v_k / T - teacher_lse), q' = max(0, 1 - sum_k q_k)
+ *     l = sum_k q_k (log q_k - log p_{j_k}) + q' (log q' - log p')
+ *     with p' = the sum of p over the classes that no entry names; where
+ *     every such p is 0 the last term is left out
+ *
+ * (terms with q = 0 are 0), reduced as ce_policy_loss reduces, and the
+ * gradient where x->grad is not NULL. teacher_lse is log sum_j exp(v_j / T)
+ * over the teacher's whole vocabulary.
+ *
+ * teacher      [rows, K] of teacher_dtype; index [rows, K] int32 (int64 with
+ *              CE_FLAG_TARGET_I64). An entry with a negative index is
+ *              padding. A row whose first index is negative does not count:
+ *              it is not read and has a gradient of exact +0. An index of V
+ *              or above is treated as a negative one and recorded
+ *              (CE_ERR_TARGET_RANGE). A class named twice has two terms.
+ * K            1..256 (CE_ERR_UNSUPPORTED above).
+ */
+ce_status ce_distill_loss(const ce_rows* x, const void* teacher, int teacher_dtype,
+                          const void* index, int64_t K, const float* teacher_lse, uint32_t flags,
+                          const float* weight, float scale, int reduction, float* loss,
+                          void* workspace, size_t workspace_bytes, ce_stream_t stream);
+
+enum { CE_PAIR_SIGMOID = 0, CE_PAIR_HINGE = 1, CE_PAIR_IPO = 2 };
+
+/*
+ * ce_preference_loss - the loss of pairs of sequences: sequence i is
+ * preferred to sequence pairs + i. With s the sum of lp over the counted rows
+ * of a sequence (average: divided by their number; 0 with none) and
+ * d_i = (s_i - s_{pairs+i}) - (ref_i - ref_{pairs+i}), h = beta d - margin:
+ *
+ *   CE_PAIR_SIGMOID  -(1 - label_smoothing) log sigma(h) - label_smoothing log sigma(-h)
+ *   CE_PAIR_HINGE    max(0, 1 - h)
+ *   CE_PAIR_IPO      (d - 1 / (2 beta))^2          (margin must be 0)
+ *
+ * loss = scale times the mean or sum over pairs, or a value a pair.
+ *
+ * offsets      [2 pairs + 1] int64 on the device: sequence s has the rows
+ *              offsets[s] <= r < offsets[s + 1] (values are cut to [0, rows];
+ *              rows of no sequence take no part); NULL: every sequence has
+ *              rows / (2 pairs) rows.
+ * ref_scores   [2 pairs] fp32, the reference model's s, or NULL (0).
+ * label_smoothing   in [0, 1]; 0 unless CE_PAIR_SIGMOID.
+ * loss         fp32, [pairs] for CE_RED_NONE else [1].
+ * scores       [2 pairs] fp32 or NULL: s.
+ * dscore       [2 pairs] fp32 or NULL: d loss / d lp of a sequence's rows.
+ * kept         [rows, 4] fp32, 16-byte aligned.
+ *
+ * ce_preference_loss_bwd: x->grad = the gradient of grad_output times the
+ * loss, from kept and dscore; grad_output is one fp32, or with
+ * grad_per_pair one a pair.
+ */
+ce_status ce_preference_loss(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                             uint32_t flags, int64_t pairs, const int64_t* offsets,
+                             const float* ref_scores, int kind, double beta, double margin,
+                             double label_smoothing, int average, float scale, int reduction,
+                             float* loss, float* scores, float* dscore, float* kept,
+                             void* workspace, size_t workspace_bytes, ce_stream_t stream);
+
+ce_status ce_preference_loss_bwd(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                                 uint32_t flags, int64_t pairs, const int64_t* offsets,
+                                 const float* kept, const float* dscore, const float* grad_output,
+                                 int grad_per_pair, ce_stream_t stream);
+
+/*
+ * ce_rows_scale - x->grad *= grad_output (one fp32, or with grad_per_row one
+ * a row): the backward of ce_policy_loss and ce_distill_loss. x->data is not
+ * read. Rows whose factor is exactly 1 are left untouched.
+ */
+ce_status ce_rows_scale(const ce_rows* x, const float* grad_output, int grad_per_row,
+                        ce_stream_t stream);
+
+/*
  * ce_bwd - backward (§Backward Pass: the stored gradient times
  * grad_output): dlogits *= grad_output, in place.
  *

@@ -20,7 +20,8 @@ buffer by grad_output. Every step runs in the CUDA kernels of libgbce.so
 
 Around the loss: fused_linear_cross_entropy, gated_feed_forward (the block
 whose output it takes), dropout, and for generating beam_search_step and
-beam_reorder.
+beam_reorder. For post-training over the same logits: token_log_probs,
+policy_loss, preference_loss and distillation_loss.
 """
 from __future__ import annotations
 
@@ -37,6 +38,10 @@ from ._lib import (CEError, ce_bwd, ce_bwd_nd, ce_count, ce_device_status, ce_fl
 from .beam_search import BeamCandidates, beam_reorder, beam_search_step
 from .feed_forward import GatedFeedForward, GatedFeedForwardFunction, gated_feed_forward
 from .philox_dropout import DropoutFunction, dropout
+from .token_losses import (DistillationLossFunction, PolicyLossFunction, PolicyLossOutput,
+                           PreferenceLossFunction, PreferenceLossOutput, TokenLogProbs,
+                           TokenLogProbsFunction, distillation_loss, policy_loss,
+                           preference_loss, token_log_probs)
 
 __all__ = ["cross_entropy", "CrossEntropyLoss", "CrossEntropyFunction", "CrossEntropyOutput",
            "CEError", "device_status", "shard_counts", "ce_fwd", "ce_fwd_shard", "ce_count",
@@ -44,7 +49,10 @@ __all__ = ["cross_entropy", "CrossEntropyLoss", "CrossEntropyFunction", "CrossEn
            "ce_scale_round", "ce_device_status", "ce_status_string", "ce_last_error",
            "fused_linear_cross_entropy", "FusedLinearCrossEntropyFunction", "dropout",
            "DropoutFunction", "beam_search_step", "beam_reorder", "BeamCandidates",
-           "gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction"]
+           "gated_feed_forward", "GatedFeedForward", "GatedFeedForwardFunction",
+           "token_log_probs", "policy_loss", "preference_loss", "distillation_loss",
+           "TokenLogProbs", "PolicyLossOutput", "PreferenceLossOutput", "TokenLogProbsFunction",
+           "PolicyLossFunction", "PreferenceLossFunction", "DistillationLossFunction"]
 
 CrossEntropyOutput = namedtuple("CrossEntropyOutput",
                                 ["loss", "z_loss", "token_accuracy", "predicted_tokens"])

@@ -29,6 +29,14 @@ class BeamState(ctypes.Structure):
                 ("dst_row", _I64), ("dst_block", _I64), ("blocks", _I64), ("block_bytes", _I64)]
 
 
+class Rows(ctypes.Structure):
+    """ce_rows."""
+    _fields_ = [("data", _P), ("grad", _P), ("dtype", _I), ("temperature", _F), ("rows", _I64),
+                ("V", _I64), ("inner", _I64), ("outer_stride", _I64), ("row_stride", _I64)]
+
+
+_ROWS = ctypes.POINTER(Rows)
+
 SIGNATURES = {
     "ce_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P, _P, _P, _P]),
     "ce_fwd_noalloc": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _F, _F, _F, _I, _U32, _P, _P, _P, _P,
@@ -57,6 +65,16 @@ SIGNATURES = {
     "ce_beam_select": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ,
                             _P]),
     "ce_beam_reorder": (_I, [ctypes.POINTER(BeamState), _I, _P, _I64, _I64, _I64, _P]),
+    "ce_rows_workspace_bytes": (_SZ, []),
+    "ce_token_logp": (_I, [_ROWS, _P, _I64, _U32, _P, _P, _P, _P]),
+    "ce_token_logp_bwd": (_I, [_ROWS, _P, _I64, _U32, _P, _P, _P, _P]),
+    "ce_policy_loss": (_I, [_ROWS, _P, _I64, _U32, _P, _I64, _P, _P, _P, _D, _D, _F, _F, _F, _I, _P,
+                            _P, _P, _P, _P, _P, _SZ, _P]),
+    "ce_distill_loss": (_I, [_ROWS, _P, _I, _P, _I64, _P, _U32, _P, _F, _I, _P, _P, _SZ, _P]),
+    "ce_preference_loss": (_I, [_ROWS, _P, _I64, _U32, _I64, _P, _P, _I, _D, _D, _D, _I, _F, _I, _P,
+                                _P, _P, _P, _P, _SZ, _P]),
+    "ce_preference_loss_bwd": (_I, [_ROWS, _P, _I64, _U32, _I64, _P, _P, _P, _P, _I, _P]),
+    "ce_rows_scale": (_I, [_ROWS, _P, _I, _P]),
     "ce_bwd": (_I, [_P, _I, _P, _I, _I64, _I64, _P]),
     "ce_log_softmax": (_I, [_P, _P, _I, _I64, _I64, _P]),
     "ce_nll_loss_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I64, _I, _U32, _P, _P, _P]),
@@ -237,6 +255,55 @@ def ce_beam_select(logits, dtype, B, K, V, scores, finished, pad_token, M, out_s
 
 def ce_beam_reorder(states, n, beams, beams_row, B, K, stream):
     return load().ce_beam_reorder(states, n, beams, beams_row, B, K, stream)
+
+
+CE_PAIR_SIGMOID, CE_PAIR_HINGE, CE_PAIR_IPO = 0, 1, 2
+
+
+def ce_rows_workspace_bytes():
+    return load().ce_rows_workspace_bytes()
+
+
+def ce_token_logp(x, tokens, ignore_index, flags, logp, entropy, kept, stream):
+    return load().ce_token_logp(x, tokens, ignore_index, flags, logp, entropy, kept, stream)
+
+
+def ce_token_logp_bwd(x, tokens, ignore_index, flags, kept, grad_logp, grad_entropy, stream):
+    return load().ce_token_logp_bwd(x, tokens, ignore_index, flags, kept, grad_logp, grad_entropy,
+                                    stream)
+
+
+def ce_policy_loss(x, tokens, ignore_index, flags, advantages, advantage_rows, old_logp, ref_logp,
+                   weight, clip_low, clip_high, kl_coef, entropy_coef, scale, reduction, loss, logp,
+                   entropy, kl, clipped, workspace, workspace_bytes, stream):
+    return load().ce_policy_loss(x, tokens, ignore_index, flags, advantages, advantage_rows,
+                                 old_logp, ref_logp, weight, clip_low, clip_high, kl_coef,
+                                 entropy_coef, scale, reduction, loss, logp, entropy, kl, clipped,
+                                 workspace, workspace_bytes, stream)
+
+
+def ce_distill_loss(x, teacher, teacher_dtype, index, K, teacher_lse, flags, weight, scale,
+                    reduction, loss, workspace, workspace_bytes, stream):
+    return load().ce_distill_loss(x, teacher, teacher_dtype, index, K, teacher_lse, flags, weight,
+                                  scale, reduction, loss, workspace, workspace_bytes, stream)
+
+
+def ce_preference_loss(x, tokens, ignore_index, flags, pairs, offsets, ref_scores, kind, beta,
+                       margin, label_smoothing, average, scale, reduction, loss, scores, dscore,
+                       kept, workspace, workspace_bytes, stream):
+    return load().ce_preference_loss(x, tokens, ignore_index, flags, pairs, offsets, ref_scores,
+                                     kind, beta, margin, label_smoothing, average, scale, reduction,
+                                     loss, scores, dscore, kept, workspace, workspace_bytes, stream)
+
+
+def ce_preference_loss_bwd(x, tokens, ignore_index, flags, pairs, offsets, kept, dscore,
+                           grad_output, grad_per_pair, stream):
+    return load().ce_preference_loss_bwd(x, tokens, ignore_index, flags, pairs, offsets, kept,
+                                         dscore, grad_output, grad_per_pair, stream)
+
+
+def ce_rows_scale(x, grad_output, grad_per_row, stream):
+    return load().ce_rows_scale(x, grad_output, grad_per_row, stream)
 
 
 def ce_device_status(stream):

@@ -1,0 +1,203 @@
+// What the kernels of the token losses share (ce_rows.cu, ce_rows_grad.cu): the
+// log-probabilities of given tokens, the clipped policy loss, the preference
+// loss and distillation from a teacher's top logits, all over rows of logits.
+#pragma once
+
+#include <cstdint>
+
+#include "ce_kernels.cuh"
+
+namespace gbce {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTopMax = 256;  // entries of a teacher's list
+constexpr int kRowsMaxCtas = 4096;  // CTAs whose sums a workspace holds
+
+enum RowOp : int { kRowLogp = 0, kRowPolicy = 1, kRowDistill = 2 };
+
+// Row r of the logits starts at element (r / inner) outer + (r % inner) step;
+// its gradient sits at the same place behind dx.
+struct RowPlace {
+    const void* x;
+    void* dx;
+    int64_t rows, V, inner, outer, step;
+    __device__ __forceinline__ int64_t at(int64_t r) const {
+        if (inner >= rows) return r * step;
+        const int64_t o = r / inner;
+        return o * outer + (r - o * inner) * step;
+    }
+};
+
+// What a counted row keeps for the backward: the largest logit m, the sum S of
+// exp((x - m) / T), the entropy and the token's log-probability.
+struct __align__(16) RowKept {
+    float m, S, H, logp;
+};
+
+struct RowArgs {
+    RowPlace p;
+    // log2(e) / T in two parts (its error alone, times the arguments' size, would
+    // move every row's sum the same way): exp((x - m) / T) = 2^((x - m) (c + c_low));
+    // c_low > 0
+    float c, c_low;
+    double invT;
+    const void* tokens;  // [rows], int32 or int64
+    int tok64;
+    int64_t ignore_index;
+    int reduction;
+    float scale;
+    const float* weight;  // [rows] or nullptr
+    float* loss;
+    double* D;         // sum of the counted rows' weights (rows_count writes it)
+    double* partial;   // a sum a CTA
+    unsigned* ticket;  // of the sum over CTAs: zeroed by rows_count; of the pairs': by the row kernel
+    unsigned* status;
+    uint64_t timeout_ns;
+    // log-probabilities and policy loss
+    float *logp, *entropy;  // [rows] or nullptr
+    RowKept* kept;          // [rows] or nullptr
+    // policy loss
+    const float *adv, *old, *ref;
+    int64_t adv_rows;  // consecutive rows that share an advantage
+    float low, high;   // the ratio's borders
+    float kl, ent;     // coefficients
+    float* kl_out;
+    uint8_t* clipped;
+    // distillation
+    const void* teacher;  // [rows, K]
+    int teacher_dtype;
+    const void* index;  // [rows, K], int32 or int64
+    int idx64;
+    int K;
+    const float* teacher_lse;  // [rows] or nullptr
+};
+
+__device__ __forceinline__ int64_t load_index(const void* p, int is64, int64_t i) {
+    return is64 ? reinterpret_cast<const int64_t*>(p)[i]
+                : static_cast<int64_t>(reinterpret_cast<const int32_t*>(p)[i]);
+}
+
+// A row as single elements in front of the first 16-byte boundary, whole
+// vectors, and single elements behind them.
+struct RowSpan {
+    int head, nvec, tail;
+};
+
+template <typename T>
+__device__ __forceinline__ RowSpan row_span(const void* p, int64_t V) {
+    constexpr int VE = Vec<T>::N;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / static_cast<int>(sizeof(T));
+    RowSpan s;
+    s.head = static_cast<int>(min(V, static_cast<int64_t>(off ? VE - off : 0)));
+    s.nvec = static_cast<int>((V - s.head) / VE);
+    s.tail = static_cast<int>(V - s.head) - s.nvec * VE;
+    return s;
+}
+
+// log p of a logit in a row with largest logit m and log S = logS.
+__device__ __forceinline__ float log_prob(float x, float m, double invT, float logS) {
+    return static_cast<float>(static_cast<double>(x - m) * invT - static_cast<double>(logS));
+}
+
+// The softmax statistics of part of a row: its largest logit m, S = sum
+// 2^a and Q = sum 2^a a with a = (x - m) c. No element: m = -inf, S = Q = 0.
+struct RowPart {
+    float m, S, Q;
+};
+
+// Adds b to a; the same bits whichever of the two comes first.
+template <bool ENT>
+__device__ __forceinline__ void part_merge(RowPart& a, const RowPart& b, float c) {
+    const float M = fmaxf(a.m, b.m);
+    // (an empty side has S = Q = 0, and a factor of 1)
+    const float da = a.m == M ? 0.f : fmaxf(__fmul_rn(__fsub_rn(a.m, M), c), -256.f);
+    const float db = b.m == M ? 0.f : fmaxf(__fmul_rn(__fsub_rn(b.m, M), c), -256.f);
+    const float fa = ex2(da), fb = ex2(db);
+    if (ENT)
+        a.Q = __fadd_rn(__fmul_rn(fa, __fmaf_rn(da, a.S, a.Q)), __fmul_rn(fb, __fmaf_rn(db, b.S, b.Q)));
+    a.S = __fadd_rn(__fmul_rn(fa, a.S), __fmul_rn(fb, b.S));
+    a.m = M;
+}
+
+template <bool ENT>
+__device__ __forceinline__ void part_warp_merge(RowPart& v, float c) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        RowPart b;
+        b.m = __shfl_xor_sync(0xffffffffu, v.m, o);
+        b.S = __shfl_xor_sync(0xffffffffu, v.S, o);
+        b.Q = ENT ? __shfl_xor_sync(0xffffffffu, v.Q, o) : 0.f;
+        part_merge<ENT>(v, b, c);
+    }
+}
+
+// The policy loss of one token from its log-probability: the loss without the
+// entropy term, its derivative by the log-probability, the KL estimate.
+struct PolicyRow {
+    float loss, slope, kl;
+    bool clipped;
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const RowArgs& a, float lp, float adv, float old,
+                                                float ref) {
+    PolicyRow o;
+    const float ratio = a.old ? expf(lp - old) : 1.f;
+    // min(r A, clip(r) A): the clip acts above the border for A >= 0, below for A < 0
+    o.clipped = adv >= 0.f ? ratio > a.high : ratio < a.low;
+    const float used = o.clipped ? (adv >= 0.f ? a.high : a.low) : ratio;
+    o.loss = -used * adv;
+    o.slope = o.clipped ? 0.f : -ratio * adv;
+    o.kl = 0.f;
+    if (a.ref) {
+        // exp(g) - g - 1 loses its digits near g = 0 where exp(g) - 1 does not
+        const float g = ref - lp, e1 = expm1f(g);
+        o.kl = e1 - g;
+        o.loss = fmaf(a.kl, o.kl, o.loss);
+        o.slope = fmaf(-a.kl, e1, o.slope);
+    }
+    return o;
+}
+
+// exp of a 64-bit argument, to fp32's precision whatever its size.
+__device__ __forceinline__ float exp_wide(double a) {
+    const float hi = static_cast<float>(a);
+    if (!(fabsf(hi) < 1e30f)) return expf(hi);  // (and -inf, NaN)
+    const float lo = static_cast<float>(a - static_cast<double>(hi));
+    const float e = expf(hi);
+    return fmaf(e, lo, e);
+}
+
+// The mean's denominator, or the sum's 1; a row's gradient is multiplied by it.
+__device__ __forceinline__ float row_scale(const RowArgs& a, double weight) {
+    const double d = a.reduction == kRedMean ? __ldcg(a.D) : 1.0;
+    return static_cast<float>(static_cast<double>(a.scale) * weight / d);
+}
+
+// The reduced loss: thread 0 of each CTA holds its rows' sum; the last CTA to
+// arrive adds the CTAs' in a fixed order. Called by every thread.
+__device__ __forceinline__ void rows_finish(const RowArgs& a, double sum, int ncta, int cta,
+                                            double* red, int* flag) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        a.partial[cta] = sum;
+        unsigned t;
+        asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(t) : "l"(a.ticket) : "memory");
+        *flag = t == static_cast<unsigned>(ncta - 1);
+    }
+    __syncthreads();
+    if (!*flag) return;
+    double s = 0.0;
+    for (int i = tid; i < ncta; i += blockDim.x) s += __ldcg(a.partial + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    if (tid != 0) return;
+    s = 0.0;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
+    s *= static_cast<double>(a.scale);
+    if (a.reduction == kRedMean) s /= __ldcg(a.D);  // (no counted row: 0 / 0 = NaN)
+    a.loss[0] = static_cast<float>(s);
+}
+
+}  // namespace gbce

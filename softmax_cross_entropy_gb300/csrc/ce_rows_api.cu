@@ -1,0 +1,353 @@
+// C ABI of the token losses (stated in include/gbce.h): argument checks, the
+// workspace's layout, and the order of the launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+#include <string>
+
+#include "ce_rows.cuh"
+#include "ce_rows_grad.cuh"
+#include "gbce.h"
+
+namespace gbce {
+ce_status record_cuda_failure(cudaError_t e, const char* what);
+void record_message(const std::string& msg);
+ce_status library_status_word(cudaStream_t st, unsigned** out);
+
+namespace {
+
+constexpr int64_t kMaxVocabulary = int64_t{1} << 19;
+constexpr size_t kWorkHeader = 64;  // D, the ticket
+constexpr size_t kWorkBytes = kWorkHeader + sizeof(double) * kRowsMaxCtas;
+
+struct Device {
+    int sms = 0;
+    unsigned* status = nullptr;
+    uint64_t timeout_ns = 0;
+};
+
+ce_status device_of(cudaStream_t st, Device* d) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return record_cuda_failure(e, "token loss device");
+    const char* env = std::getenv("GBCE_WAIT_TIMEOUT_MS");
+    d->timeout_ns = ((env && *env) ? static_cast<uint64_t>(std::atoll(env)) : 2000ull) * 1000000ull;
+    return library_status_word(st, &d->status);
+}
+
+bool bad_reduction(int r) { return r != CE_RED_NONE && r != CE_RED_SUM && r != CE_RED_MEAN; }
+
+ce_status check_rows(const ce_rows* x, bool need_grad) {
+    if (!x) return CE_ERR_INVALID_ARG;
+    if (x->dtype != CE_F32 && x->dtype != CE_BF16 && x->dtype != CE_F16) return CE_ERR_INVALID_ARG;
+    if (x->rows < 0 || x->V < 1 || x->inner < 1) return CE_ERR_INVALID_ARG;
+    if (!(x->temperature >= 1e-6f && x->temperature <= 1e6f)) return CE_ERR_INVALID_ARG;
+    if (x->V > kMaxVocabulary || x->rows > (int64_t{1} << 40)) {
+        record_message("the token losses take up to 2^19 classes and 2^40 rows");
+        return CE_ERR_UNSUPPORTED;
+    }
+    // rows that do not overlap
+    if (x->rows > 1 && x->inner > 1 && x->row_stride < x->V) return CE_ERR_INVALID_ARG;
+    if (x->rows > x->inner) {
+        const int64_t reach = x->inner > 1 ? x->row_stride : 0;
+        if (x->outer_stride < x->V || reach > (INT64_MAX - x->V) / x->inner ||
+            x->outer_stride < (x->inner - 1) * reach + x->V)
+            return CE_ERR_INVALID_ARG;
+    }
+    if (x->rows == 0) return CE_OK;
+    const uintptr_t b = x->dtype == CE_F32 ? 4 : 2;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x->data), g = reinterpret_cast<uintptr_t>(x->grad);
+    if (!p || p % b) return CE_ERR_INVALID_ARG;
+    if (need_grad && !g) return CE_ERR_INVALID_ARG;
+    if (g && ((p ^ g) & 15u)) {
+        record_message("the gradient's address must equal the logits' modulo 16 bytes");
+        return CE_ERR_INVALID_ARG;
+    }
+    return CE_OK;
+}
+
+RowPlace place_of(const ce_rows* x) {
+    return RowPlace{x->data, x->grad, x->rows, x->V, x->inner, x->outer_stride, x->row_stride};
+}
+
+void fill_rows(RowArgs* a, const ce_rows* x, const Device& d) {
+    a->p = place_of(x);
+    a->invT = 1.0 / static_cast<double>(x->temperature);
+    const double c = 1.4426950408889634 * a->invT;
+    a->c = static_cast<float>(c);
+    // (c_low > 0, so that both products of -inf are -inf)
+    if (static_cast<double>(a->c) >= c) a->c = std::nextafterf(a->c, 0.f);
+    a->c_low = static_cast<float>(c - static_cast<double>(a->c));
+    a->status = d.status;
+    a->timeout_ns = d.timeout_ns;
+}
+
+void fill_work(RowArgs* a, void* workspace) {
+    a->D = static_cast<double*>(workspace);
+    a->ticket = reinterpret_cast<unsigned*>(a->D + 1);
+    a->partial = reinterpret_cast<double*>(static_cast<char*>(workspace) + kWorkHeader);
+}
+
+bool bad_work(const void* workspace, size_t bytes) {
+    return !workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || bytes < kWorkBytes;
+}
+
+}  // namespace
+}  // namespace gbce
+
+using namespace gbce;
+
+extern "C" size_t ce_rows_workspace_bytes(void) { return kWorkBytes; }
+
+extern "C" ce_status ce_token_logp(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                                   uint32_t flags, float* logp, float* entropy, float* kept,
+                                   ce_stream_t stream) {
+    ce_status rc = check_rows(x, false);
+    if (rc != CE_OK) return rc;
+    if (flags & ~static_cast<uint32_t>(CE_FLAG_TARGET_I64)) return CE_ERR_INVALID_ARG;
+    if (x->rows == 0) return CE_OK;
+    if (!tokens || !logp || reinterpret_cast<uintptr_t>(kept) % 16) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    RowArgs a = {};
+    fill_rows(&a, x, d);
+    a.p.dx = nullptr;
+    a.tokens = tokens;
+    a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.ignore_index = ignore_index;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.kept = reinterpret_cast<RowKept*>(kept);
+    return rows_launch(kRowLogp, entropy != nullptr, x->dtype, a, d.sms, st);
+}
+
+extern "C" ce_status ce_token_logp_bwd(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                                       uint32_t flags, const float* kept, const float* grad_logp,
+                                       const float* grad_entropy, ce_stream_t stream) {
+    ce_status rc = check_rows(x, true);
+    if (rc != CE_OK) return rc;
+    if (flags & ~static_cast<uint32_t>(CE_FLAG_TARGET_I64)) return CE_ERR_INVALID_ARG;
+    if (x->rows == 0) return CE_OK;
+    if (!tokens || !kept || reinterpret_cast<uintptr_t>(kept) % 16) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    GradArgs a = {};
+    a.p = place_of(x);
+    a.invT = static_cast<float>(1.0 / static_cast<double>(x->temperature));
+    a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(x->temperature));
+    a.tokens = tokens;
+    a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.ignore_index = ignore_index;
+    a.kept = reinterpret_cast<const RowKept*>(kept);
+    a.g_logp = grad_logp;
+    a.g_entropy = grad_entropy;
+    return rows_grad_launch(a, x->dtype, d.sms, st);
+}
+
+extern "C" ce_status ce_policy_loss(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                                    uint32_t flags, const float* advantages, int64_t advantage_rows,
+                                    const float* old_logp, const float* ref_logp,
+                                    const float* weight, double clip_low, double clip_high,
+                                    float kl_coef, float entropy_coef, float scale, int reduction,
+                                    float* loss, float* logp, float* entropy, float* kl,
+                                    uint8_t* clipped, void* workspace, size_t workspace_bytes,
+                                    ce_stream_t stream) {
+    ce_status rc = check_rows(x, false);
+    if (rc != CE_OK) return rc;
+    if (flags & ~static_cast<uint32_t>(CE_FLAG_TARGET_I64)) return CE_ERR_INVALID_ARG;
+    if (bad_reduction(reduction) || advantage_rows < 1) return CE_ERR_INVALID_ARG;
+    if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0)) return CE_ERR_INVALID_ARG;
+    if (!std::isfinite(kl_coef) || !std::isfinite(entropy_coef) || !std::isfinite(scale))
+        return CE_ERR_INVALID_ARG;
+    if (x->rows == 0 && reduction == CE_RED_NONE) return CE_OK;
+    if (!loss || (x->rows > 0 && (!tokens || !advantages))) return CE_ERR_INVALID_ARG;
+    if (bad_work(workspace, workspace_bytes)) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    RowArgs a = {};
+    fill_rows(&a, x, d);
+    fill_work(&a, workspace);
+    a.tokens = tokens;
+    a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.ignore_index = ignore_index;
+    a.reduction = reduction;
+    a.scale = scale;
+    a.weight = weight;
+    a.loss = loss;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.adv = advantages;
+    a.adv_rows = advantage_rows;
+    a.old = old_logp;
+    a.ref = ref_logp;
+    a.low = static_cast<float>(1.0 - clip_low);
+    a.high = static_cast<float>(1.0 + clip_high);
+    a.kl = kl_coef;
+    a.ent = entropy_coef;
+    a.kl_out = kl;
+    a.clipped = clipped;
+    if (reduction != CE_RED_NONE && (rc = rows_count_launch(a, st)) != CE_OK) return rc;
+    return rows_launch(kRowPolicy, entropy != nullptr || entropy_coef != 0.f, x->dtype, a, d.sms, st);
+}
+
+extern "C" ce_status ce_distill_loss(const ce_rows* x, const void* teacher, int teacher_dtype,
+                                     const void* index, int64_t K, const float* teacher_lse,
+                                     uint32_t flags, const float* weight, float scale,
+                                     int reduction, float* loss, void* workspace,
+                                     size_t workspace_bytes, ce_stream_t stream) {
+    ce_status rc = check_rows(x, false);
+    if (rc != CE_OK) return rc;
+    if (flags & ~static_cast<uint32_t>(CE_FLAG_TARGET_I64)) return CE_ERR_INVALID_ARG;
+    if (teacher_dtype != CE_F32 && teacher_dtype != CE_BF16 && teacher_dtype != CE_F16)
+        return CE_ERR_INVALID_ARG;
+    if (bad_reduction(reduction) || K < 1 || !std::isfinite(scale)) return CE_ERR_INVALID_ARG;
+    if (K > kTopMax) {
+        record_message("distillation takes at most 256 entries a row");
+        return CE_ERR_UNSUPPORTED;
+    }
+    if (x->rows == 0 && reduction == CE_RED_NONE) return CE_OK;
+    if (!loss || (x->rows > 0 && (!teacher || !index))) return CE_ERR_INVALID_ARG;
+    if (bad_work(workspace, workspace_bytes)) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    RowArgs a = {};
+    fill_rows(&a, x, d);
+    fill_work(&a, workspace);
+    a.reduction = reduction;
+    a.scale = scale;
+    a.weight = weight;
+    a.loss = loss;
+    a.teacher = teacher;
+    a.teacher_dtype = teacher_dtype;
+    a.index = index;
+    a.idx64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.K = static_cast<int>(K);
+    a.teacher_lse = teacher_lse;
+    if (reduction != CE_RED_NONE && (rc = rows_count_launch(a, st)) != CE_OK) return rc;
+    return rows_launch(kRowDistill, false, x->dtype, a, d.sms, st);
+}
+
+namespace {
+
+// The pairs' arguments that both directions take.
+ce_status check_pairs(const ce_rows* x, const void* tokens, uint32_t flags, int64_t pairs,
+                      const int64_t* offsets) {
+    if (flags & ~static_cast<uint32_t>(CE_FLAG_TARGET_I64)) return CE_ERR_INVALID_ARG;
+    if (pairs < 0 || pairs > (int64_t{1} << 30) || (x->rows > 0 && !tokens)) return CE_ERR_INVALID_ARG;
+    if (!offsets && (pairs == 0 ? x->rows != 0 : x->rows % (2 * pairs) != 0)) return CE_ERR_INVALID_ARG;
+    return CE_OK;
+}
+
+}  // namespace
+
+extern "C" ce_status ce_preference_loss(const ce_rows* x, const void* tokens, int64_t ignore_index,
+                                        uint32_t flags, int64_t pairs, const int64_t* offsets,
+                                        const float* ref_scores, int kind, double beta,
+                                        double margin, double label_smoothing, int average,
+                                        float scale, int reduction, float* loss, float* scores,
+                                        float* dscore, float* kept, void* workspace,
+                                        size_t workspace_bytes, ce_stream_t stream) {
+    ce_status rc = check_rows(x, false);
+    if (rc != CE_OK) return rc;
+    if ((rc = check_pairs(x, tokens, flags, pairs, offsets)) != CE_OK) return rc;
+    if (kind != CE_PAIR_SIGMOID && kind != CE_PAIR_HINGE && kind != CE_PAIR_IPO) return CE_ERR_INVALID_ARG;
+    if (!std::isfinite(beta) || beta <= 0.0 || !std::isfinite(margin) ||
+        !(label_smoothing >= 0.0 && label_smoothing <= 1.0) || !std::isfinite(scale))
+        return CE_ERR_INVALID_ARG;
+    if (kind != CE_PAIR_SIGMOID && label_smoothing != 0.0) return CE_ERR_INVALID_ARG;
+    if (kind == CE_PAIR_IPO && margin != 0.0) return CE_ERR_INVALID_ARG;
+    if (bad_reduction(reduction)) return CE_ERR_INVALID_ARG;
+    if (pairs == 0 && reduction == CE_RED_NONE) return CE_OK;
+    if (!loss || (x->rows > 0 && (!kept || reinterpret_cast<uintptr_t>(kept) % 16)))
+        return CE_ERR_INVALID_ARG;
+    if (bad_work(workspace, workspace_bytes)) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    RowArgs a = {};
+    fill_rows(&a, x, d);
+    fill_work(&a, workspace);
+    a.p.dx = nullptr;
+    a.tokens = tokens;
+    a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.ignore_index = ignore_index;
+    a.kept = reinterpret_cast<RowKept*>(kept);
+    // (also without rows: it clears the ticket)
+    if ((rc = rows_launch(kRowLogp, false, x->dtype, a, d.sms, st)) != CE_OK) return rc;
+    PairArgs p = {};
+    p.pairs = pairs;
+    p.rows = x->rows;
+    p.V = x->V;
+    p.offsets = offsets;
+    p.seq_rows = pairs ? x->rows / (2 * pairs) : 0;
+    p.tokens = tokens;
+    p.tok64 = a.tok64;
+    p.ignore_index = ignore_index;
+    p.kept = a.kept;
+    p.ref = ref_scores;
+    p.kind = kind;
+    p.average = average;
+    p.reduction = reduction;
+    p.beta = beta;
+    p.margin = margin;
+    p.smoothing = label_smoothing;
+    p.scale = scale;
+    p.loss = loss;
+    p.scores = scores;
+    p.dscore = dscore;
+    p.partial = a.partial;
+    p.ticket = a.ticket;
+    return pair_launch(p, st);
+}
+
+extern "C" ce_status ce_preference_loss_bwd(const ce_rows* x, const void* tokens,
+                                            int64_t ignore_index, uint32_t flags, int64_t pairs,
+                                            const int64_t* offsets, const float* kept,
+                                            const float* dscore, const float* grad_output,
+                                            int grad_per_pair, ce_stream_t stream) {
+    ce_status rc = check_rows(x, true);
+    if (rc != CE_OK) return rc;
+    if ((rc = check_pairs(x, tokens, flags, pairs, offsets)) != CE_OK) return rc;
+    if (x->rows == 0) return CE_OK;
+    if (!kept || reinterpret_cast<uintptr_t>(kept) % 16 || !dscore || !grad_output)
+        return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    GradArgs a = {};
+    a.p = place_of(x);
+    a.invT = static_cast<float>(1.0 / static_cast<double>(x->temperature));
+    a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(x->temperature));
+    a.tokens = tokens;
+    a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
+    a.ignore_index = ignore_index;
+    a.kept = reinterpret_cast<const RowKept*>(kept);
+    a.dscore = dscore;
+    a.offsets = offsets;
+    a.pairs = pairs;
+    a.seq_rows = pairs ? x->rows / (2 * pairs) : 0;
+    a.grad_output = grad_output;
+    a.per_pair = grad_per_pair != 0 ? 1 : 0;
+    return rows_grad_launch(a, x->dtype, d.sms, st);
+}
+
+extern "C" ce_status ce_rows_scale(const ce_rows* x, const float* grad_output, int grad_per_row,
+                                   ce_stream_t stream) {
+    ce_status rc = check_rows(x, true);
+    if (rc != CE_OK) return rc;
+    if (x->rows == 0) return CE_OK;
+    if (!grad_output) return CE_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if ((rc = device_of(st, &d)) != CE_OK) return rc;
+    GradArgs a = {};
+    a.p = place_of(x);
+    a.grad_output = grad_output;
+    a.per_pair = grad_per_row != 0 ? 1 : 0;
+    return rows_scale_launch(a, x->dtype, d.sms, st);
+}

@@ -1,0 +1,353 @@
+// The rest of the token losses: the batch's count, the preference loss of
+// pairs of sequences from their tokens' log-probabilities, the gradient of
+// log-probabilities from a row's kept statistics, and the scaling of a
+// gradient that the forward has written.
+#include <algorithm>
+
+#include "ce_rows.cuh"
+#include "ce_rows_grad.cuh"
+#include "gbce.h"
+
+namespace gbce {
+ce_status record_cuda_failure(cudaError_t e, const char* what);
+
+namespace {
+
+constexpr int kCountThreadsRows = 1024;
+
+// D = the sum of the counted rows' weights; clears the ticket of the sum that
+// follows. One CTA; each thread adds its rows in 64 bits, then a fixed
+// butterfly and warp order.
+__global__ void __launch_bounds__(kCountThreadsRows) rows_count(const __grid_constant__ RowArgs a) {
+    __shared__ double red[kCountThreadsRows / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    const bool top = a.index != nullptr;
+    const int64_t step = top ? a.K : 1;
+    double d = 0.0;
+#pragma unroll 8
+    for (int64_t r = tid; r < a.p.rows; r += kCountThreadsRows) {
+        const int64_t t = load_index(top ? a.index : a.tokens, top ? a.idx64 : a.tok64, r * step);
+        const bool counts = t >= 0 && t < a.p.V && (top || t != a.ignore_index);
+        const float w = a.weight ? __ldg(a.weight + r) : 1.f;
+        d += counts ? static_cast<double>(w) : 0.0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) red[warp] = d;
+    __syncthreads();
+    if (tid == 0) {
+        d = 0.0;
+        for (int w = 0; w < kCountThreadsRows / 32; ++w) d += red[w];
+        *a.D = d;
+        *a.ticket = 0u;
+    }
+}
+
+// ---------------------------------------------------------------- pairs of sequences
+
+constexpr int kPairThreads = 256;
+
+__device__ __forceinline__ int64_t seq_begin(const PairArgs& a, int64_t s) {
+    if (!a.offsets) return s * a.seq_rows;
+    return min(max(a.offsets[s], int64_t{0}), a.rows);
+}
+
+// One CTA a pair: the two sequences' sums of log-probabilities in 64 bits, the
+// pair's loss and its derivative by each sequence's summed log-probability.
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
+    __shared__ double red[2][kPairThreads / 32];
+    __shared__ int64_t red_n[2][kPairThreads / 32];
+    __shared__ int s_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    double sum = 0.0;
+    for (int64_t p = blockIdx.x; p < a.pairs; p += gridDim.x) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t s = p + h * a.pairs;
+            const int64_t lo = seq_begin(a, s), hi = seq_begin(a, s + 1);
+            double d = 0.0;
+            int64_t n = 0;
+#pragma unroll 4
+            for (int64_t r = lo + tid; r < hi; r += kPairThreads) {
+                const int64_t t = load_index(a.tokens, a.tok64, r);
+                if (t != a.ignore_index && t >= 0 && t < a.V) {
+                    d += a.kept[r].logp;
+                    ++n;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+            }
+            if (lane == 0) {
+                red[h][warp] = d;
+                red_n[h][warp] = n;
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {
+            double v[2], per[2];
+            for (int h = 0; h < 2; ++h) {
+                double d = 0.0;
+                int64_t n = 0;
+                for (int w = 0; w < kPairThreads / 32; ++w) {
+                    d += red[h][w];
+                    n += red_n[h][w];
+                }
+                per[h] = a.average ? 1.0 / static_cast<double>(n > 0 ? n : 1) : 1.0;
+                v[h] = d * per[h];
+                if (a.scores) a.scores[p + h * a.pairs] = static_cast<float>(v[h]);
+            }
+            double delta = v[0] - v[1];
+            if (a.ref) delta -= static_cast<double>(a.ref[p]) - static_cast<double>(a.ref[p + a.pairs]);
+            double loss, slope;  // slope: by delta
+            if (a.kind == kPairIpo) {
+                const double gap = delta - 0.5 / a.beta;
+                loss = gap * gap;
+                slope = 2.0 * gap;
+            } else {
+                const double x = a.beta * delta - a.margin;
+                if (a.kind == kPairHinge) {
+                    loss = x < 1.0 ? 1.0 - x : x >= 1.0 ? 0.0 : x;  // (NaN stays)
+                    slope = x < 1.0 ? -a.beta : 0.0;
+                } else {
+                    // softplus(-x) and the logistic function without overflow
+                    const double e = exp(-fabs(x)), l = log1p(e);
+                    const double neg = (x < 0.0 ? -x : 0.0) + l, pos = (x > 0.0 ? x : 0.0) + l;
+                    const double q = x >= 0.0 ? 1.0 / (1.0 + e) : e / (1.0 + e);
+                    loss = x == x ? (1.0 - a.smoothing) * neg + a.smoothing * pos : x;
+                    slope = a.beta * (q - (1.0 - a.smoothing));
+                }
+            }
+            const double scale = static_cast<double>(a.scale) /
+                                 (a.reduction == kRedMean ? static_cast<double>(a.pairs) : 1.0);
+            if (a.dscore) {
+                a.dscore[p] = static_cast<float>(slope * scale * per[0]);
+                a.dscore[p + a.pairs] = static_cast<float>(-slope * scale * per[1]);
+            }
+            if (a.reduction == kRedNone)
+                a.loss[p] = static_cast<float>(loss * scale);
+            else
+                sum += loss * scale;
+        }
+        __syncthreads();
+    }
+    if (a.reduction == kRedNone) return;
+    // the last CTA to arrive adds the CTAs' sums in order
+    if (tid == 0) {
+        a.partial[blockIdx.x] = sum;
+        unsigned t;
+        asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(t) : "l"(a.ticket) : "memory");
+        s_flag = t == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_flag) return;
+    double s = 0.0;
+    for (unsigned i = tid; i < gridDim.x; i += kPairThreads) s += __ldcg(a.partial + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[0][warp] = s;
+    __syncthreads();
+    if (tid != 0) return;
+    s = 0.0;
+    for (int w = 0; w < kPairThreads / 32; ++w) s += red[0][w];
+    a.loss[0] = a.pairs > 0 ? static_cast<float>(s)
+                            : a.reduction == kRedMean ? nanf("") : 0.f;
+}
+
+// ---------------------------------------------------------------- gradients
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVec = 4;  // vectors a thread has in flight
+
+// What the gradient of one row needs: g_j = 2^((x_j - m) c) (u0 + u1 a_j),
+// plus `at` at the token.
+struct GradRow {
+    float m, u0, u1, at;
+    int64_t t;  // -1: the row does not count
+};
+
+__device__ __forceinline__ GradRow grad_row(const GradArgs& a, int64_t r) {
+    GradRow g = {0.f, 0.f, 0.f, 0.f, -1};
+    const int64_t t = load_index(a.tokens, a.tok64, r);
+    if (t == a.ignore_index || t < 0 || t >= a.p.V) return g;
+    float gl = 0.f, ge = 0.f;
+    if (a.dscore) {  // of the sequence that the row is in
+        int64_t s = -1;
+        if (a.offsets) {
+            int64_t lo = 0, hi = 2 * a.pairs;  // the last offset that is at most r
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) >> 1;
+                if (__ldg(a.offsets + mid) <= r) lo = mid; else hi = mid - 1;
+            }
+            if (lo < 2 * a.pairs && __ldg(a.offsets + lo) <= r) s = lo;
+        } else {
+            s = r / a.seq_rows;
+        }
+        if (s < 0) return g;  // a row of no sequence
+        const int64_t p = s < a.pairs ? s : s - a.pairs;
+        gl = __ldg(a.dscore + s) * __ldg(a.grad_output + (a.per_pair ? p : 0));
+    } else {
+        gl = a.g_logp ? __ldg(a.g_logp + r) : 0.f;
+        ge = a.g_entropy ? __ldg(a.g_entropy + r) : 0.f;
+    }
+    const RowKept k = a.kept[r];
+    gl *= a.invT;
+    ge *= a.invT;
+    g.t = t;
+    g.m = k.m;
+    g.at = gl;
+    // d lp = [j = t] - p_j; d H = -p_j (log p_j + H), log p_j = a_j ln 2 - log S
+    g.u0 = a.g_entropy ? (-gl - ge * (k.H - logf(k.S))) / k.S : -gl / k.S;
+    g.u1 = -ge * kLn2 / k.S;
+    return g;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kGradThreads) rows_grad(const __grid_constant__ GradArgs a) {
+    using VT = Vec<T>;
+    constexpr int VE = VT::N;
+    const int tid = threadIdx.x;
+    const int64_t units = a.p.rows * a.parts;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        // from the last row on: the forward read it last
+        const int64_t i = units - 1 - u, r = i / a.parts;
+        const int part = static_cast<int>(i - r * a.parts);
+        const int64_t at = a.p.at(r);
+        const T* x = reinterpret_cast<const T*>(a.p.x) + at;
+        T* dx = reinterpret_cast<T*>(a.p.dx) + at;
+        const RowSpan sp = row_span<T>(x, a.p.V);
+        const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+        uint4* dv = reinterpret_cast<uint4*>(dx + sp.head);
+        const GradRow g = grad_row(a, r);
+        const int v0 = part * a.part_vec, v1 = min(sp.nvec, v0 + a.part_vec);
+        const int edges = part == 0 ? sp.head + sp.tail : 0;
+        const int64_t edge = tid < sp.head ? tid : a.p.V - sp.tail + (tid - sp.head);
+        if (g.t < 0) {
+            for (int v = v0 + tid; v < v1; v += kGradThreads) dv[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (tid < edges) VT::store1(dx, edge, 0.f);
+            continue;
+        }
+        auto grad = [&](float f) {
+            const float arg = (f - g.m) * a.c;
+            const float e = ex2(arg);
+            return e * (ENT ? fmaf(g.u1, fmaxf(arg, -256.f), g.u0) : g.u0);
+        };
+        const int64_t tv = g.t - sp.head;  // the token's place among the vectors
+        for (int base = v0; base < v1; base += kGradThreads * kGradVec) {
+            uint4 q[kGradVec];
+#pragma unroll
+            for (int k = 0; k < kGradVec; ++k) {
+                const int v = base + k * kGradThreads + tid;
+                if (v < v1) q[k] = xv[v];
+            }
+#pragma unroll
+            for (int k = 0; k < kGradVec; ++k) {
+                const int v = base + k * kGradThreads + tid;
+                if (v >= v1) break;
+                float f[VE];
+                VT::unpack(q[k], f);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) f[e] = grad(f[e]);
+                if (tv >= 0 && tv / VE == v) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        if (tv % VE == e) f[e] += g.at;
+                }
+                dv[v] = VT::pack(f);
+            }
+        }
+        if (tid < edges) VT::store1(dx, edge, grad(VT::load1(x, edge)) + (edge == g.t ? g.at : 0.f));
+    }
+}
+
+// dx *= factor (one, or one a row); rows whose factor is 1 are left as they are.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) rows_scale(const __grid_constant__ GradArgs a) {
+    using VT = Vec<T>;
+    constexpr int VE = VT::N;
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const bool per_row = a.per_pair != 0;
+    if (!per_row && __ldg(a.grad_output) == 1.f) return;
+    for (int64_t r = blockIdx.x; r < a.p.rows; r += gridDim.x) {
+        const float g = __ldg(a.grad_output + (per_row ? r : 0));
+        if (g == 1.f) continue;
+        T* dx = reinterpret_cast<T*>(a.p.dx) + a.p.at(r);
+        const RowSpan sp = row_span<T>(dx, a.p.V);
+        uint4* dv = reinterpret_cast<uint4*>(dx + sp.head);
+#pragma unroll 4
+        for (int v = tid; v < sp.nvec; v += kGradThreads) {
+            float f[VE];
+            VT::unpack(dv[v], f);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) f[e] *= g;
+            dv[v] = VT::pack(f);
+        }
+        if (tid < sp.head + sp.tail) {
+            const int64_t edge = tid < sp.head ? tid : a.p.V - sp.tail + (tid - sp.head);
+            VT::store1(dx, edge, VT::load1(dx, edge) * g);
+        }
+    }
+}
+
+template <bool ENT>
+const void* grad_fn(int dtype) {
+    return dtype == CE_F32    ? (const void*)&rows_grad<float, ENT>
+           : dtype == CE_BF16 ? (const void*)&rows_grad<__nv_bfloat16, ENT>
+                              : (const void*)&rows_grad<__half, ENT>;
+}
+
+ce_status launch(const void* fn, int64_t grid, int threads, void* arg, cudaStream_t st, bool early,
+                 const char* what) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(grid));
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = &attr;
+    lc.numAttrs = early ? 1 : 0;
+    void* args[] = {arg};
+    const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+    return e == cudaSuccess ? CE_OK : record_cuda_failure(e, what);
+}
+
+}  // namespace
+
+ce_status rows_count_launch(const RowArgs& args, cudaStream_t st) {
+    RowArgs a = args;
+    return launch((const void*)&rows_count, 1, kCountThreadsRows, &a, st, false, "token count launch");
+}
+
+ce_status pair_launch(const PairArgs& args, cudaStream_t st) {
+    PairArgs a = args;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(a.pairs, kPairMaxCtas));
+    return launch((const void*)&pair_kernel, grid, kPairThreads, &a, st, true, "preference launch");
+}
+
+ce_status rows_grad_launch(const GradArgs& args, int dtype, int sms, cudaStream_t st) {
+    GradArgs a = args;
+    const int64_t vecs = a.p.V * (dtype == CE_F32 ? 4 : 2) / 16 + 1;
+    constexpr int64_t kPart = int64_t{kGradThreads} * kGradVec * 2;
+    a.parts = static_cast<int>((vecs + kPart - 1) / kPart);
+    a.part_vec = static_cast<int>((vecs + a.parts - 1) / a.parts);
+    const int64_t grid = std::min<int64_t>(a.p.rows * a.parts, 8L * sms);
+    return launch(a.g_entropy ? grad_fn<true>(dtype) : grad_fn<false>(dtype), grid, kGradThreads, &a, st,
+                  false, "log-probability gradient launch");
+}
+
+ce_status rows_scale_launch(const GradArgs& args, int dtype, int sms, cudaStream_t st) {
+    GradArgs a = args;
+    const void* fn = dtype == CE_F32    ? (const void*)&rows_scale<float>
+                     : dtype == CE_BF16 ? (const void*)&rows_scale<__nv_bfloat16>
+                                        : (const void*)&rows_scale<__half>;
+    return launch(fn, std::min<int64_t>(a.p.rows, 8L * sms), kGradThreads, &a, st, true,
+                  "gradient scaling launch");
+}
+
+}  // namespace gbce

@@ -1,0 +1,54 @@
+// Arguments of the token losses' smaller kernels (ce_rows_grad.cu).
+#pragma once
+
+#include "ce_rows.cuh"
+#include "gbce.h"
+
+namespace gbce {
+
+enum PairKind : int { kPairSigmoid = 0, kPairHinge = 1, kPairIpo = 2 };
+constexpr int kPairMaxCtas = 1024;
+
+struct PairArgs {
+    int64_t pairs, rows, V;
+    const int64_t* offsets;  // [2 pairs + 1] or nullptr: seq_rows rows each
+    int64_t seq_rows;
+    const void* tokens;
+    int tok64;
+    int64_t ignore_index;
+    const RowKept* kept;  // [rows]
+    const float* ref;     // [2 pairs] or nullptr
+    int kind, average, reduction;
+    double beta, margin, smoothing;
+    float scale;
+    float* loss;
+    float* scores;  // [2 pairs] or nullptr
+    float* dscore;  // [2 pairs] or nullptr: d loss / d (a token's log-probability)
+    double* partial;
+    unsigned* ticket;
+};
+
+struct GradArgs {
+    RowPlace p;
+    float c, invT;
+    const void* tokens;
+    int tok64;
+    int64_t ignore_index;
+    const RowKept* kept;
+    const float *g_logp, *g_entropy;  // [rows] or nullptr
+    // preference loss: the sequences' derivatives instead of g_logp
+    const float* dscore;
+    const int64_t* offsets;
+    int64_t pairs, seq_rows;
+    const float* grad_output;  // one value, or with per_pair one a pair (scaling: a row)
+    int per_pair;
+    int parts, part_vec;
+};
+
+ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& a, int sms, cudaStream_t st);
+ce_status rows_count_launch(const RowArgs& a, cudaStream_t st);
+ce_status pair_launch(const PairArgs& a, cudaStream_t st);
+ce_status rows_grad_launch(const GradArgs& a, int dtype, int sms, cudaStream_t st);
+ce_status rows_scale_launch(const GradArgs& a, int dtype, int sms, cudaStream_t st);
+
+}  // namespace gbce

@@ -1,0 +1,558 @@
+"""The losses of post-training over logits: log-probabilities of given tokens,
+the clipped policy loss, the preference loss of pairs of sequences, and
+distillation from a teacher's top logits.
+
+    old = token_log_probs(logits, tokens)                        # no gradient: one read
+    loss = policy_loss(logits, tokens, advantages, old, ref_log_probs=ref, kl_coef=0.04)
+    loss = preference_loss(logits, tokens, ref_log_probs=ref)    # [2 pairs, T, V]
+    loss = distillation_loss(logits, teacher_logits, teacher_indices, temperature=2.0)
+
+The definitions are those of ce_token_logp, ce_policy_loss, ce_preference_loss
+and ce_distill_loss (include/gbce.h). logits are [..., V] CUDA tensors in
+float32, bfloat16 or float16, V at most 2^19; a view whose rows are evenly
+spaced, such as logits[:, :-1], is taken as it is. The policy and distillation
+losses form the gradient of the logits along with the loss, in the same pass;
+the other two form it in the backward. With inplace=True it is written over the
+logits themselves, whose values are then gone (policy_loss, distillation_loss:
+after the call; token_log_probs, preference_loss: after the backward). All are
+differentiable once, in reverse mode, with respect to the logits alone. Runs in
+libgbce.so; there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from collections import namedtuple
+
+import torch
+
+from . import _lib
+from ._tensors import DTYPES, check, forward_mode, on, once, plain, ptr, require_cuda, stream
+
+__all__ = ["token_log_probs", "policy_loss", "preference_loss", "distillation_loss",
+           "TokenLogProbs", "PolicyLossOutput", "PreferenceLossOutput",
+           "TokenLogProbsFunction", "PolicyLossFunction", "PreferenceLossFunction",
+           "DistillationLossFunction"]
+
+TokenLogProbs = namedtuple("TokenLogProbs", ["log_probs", "entropy"])
+PolicyLossOutput = namedtuple("PolicyLossOutput",
+                              ["loss", "log_probs", "entropy", "kl", "clipped"])
+PreferenceLossOutput = namedtuple("PreferenceLossOutput", ["loss", "scores"])
+
+_REDUCTIONS = {"none": _lib.CE_RED_NONE, "sum": _lib.CE_RED_SUM, "mean": _lib.CE_RED_MEAN}
+_KINDS = {"sigmoid": _lib.CE_PAIR_SIGMOID, "hinge": _lib.CE_PAIR_HINGE, "ipo": _lib.CE_PAIR_IPO}
+
+
+# ---------------------------------------------------------------- arguments
+
+def _rows_of(t):
+    """(rows, inner, outer stride, row stride) of t [..., V], or None where its
+    rows are not two evenly spaced, nested levels of contiguous elements."""
+    V = t.shape[-1]
+    if t.is_contiguous():
+        rows = t.numel() // V
+        return rows, max(rows, 1), 0, V
+    if t.is_neg() or (V > 1 and t.stride(-1) != 1):
+        return None
+    levels = []  # (count, stride) from the innermost on
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if levels and s == levels[-1][0] * levels[-1][1]:
+            levels[-1][0] *= n
+        else:
+            levels.append([n, s])
+    if len(levels) > 2:
+        return None
+    inner, step = levels[0] if levels else (1, V)
+    outer_n, outer = levels[1] if len(levels) == 2 else (1, 0)
+    if (inner > 1 and step < V) or (outer_n > 1 and outer < (inner - 1) * step + V):
+        return None  # rows that overlap, or whose order is not that of the addresses
+    return inner * outer_n, inner, outer, step
+
+
+def _logits(logits, inplace):
+    """logits with rows that the kernels take (a copy where they have others)."""
+    require_cuda(logits, "logits")
+    if logits.dim() < 2 or logits.shape[-1] < 1:
+        raise ValueError("logits must be [..., V] with at least two dimensions and V >= 1")
+    if logits.dtype not in DTYPES:
+        raise TypeError(f"logits dtype {logits.dtype} is not supported "
+                        "(float32, bfloat16, float16)")
+    if _rows_of(logits) is None:
+        if inplace:
+            raise ValueError("logits whose rows are not evenly spaced, apart and contiguous "
+                             "cannot take their gradient in place")
+        return plain(logits)
+    if logits.is_neg():  # (contiguous)
+        if inplace:
+            raise ValueError("logits that defer a negation cannot take their gradient in place")
+        return plain(logits)
+    return logits
+
+
+def _tokens(tokens, shape, device, name="tokens"):
+    if not isinstance(tokens, torch.Tensor) or tokens.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64")
+    if tokens.device != device:
+        raise ValueError(f"{name} must be on the logits' device")
+    return tokens.contiguous()
+
+
+def _floats(t, shape, device, name):
+    """t as contiguous float32 of this shape, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the logits' device")
+    if not t.is_floating_point():
+        raise TypeError(f"{name} must be floating-point")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} takes no gradient: detach it")
+    return plain(t if t.dtype is torch.float32 else t.float())
+
+
+def _number(v, name, low=-math.inf):
+    v = float(v)
+    if not math.isfinite(v) or v < low:
+        raise ValueError(f"{name} must be finite" + (f" and at least {low:g}" if low > -math.inf
+                                                      else ""))
+    return v
+
+
+def _temperature(t):
+    t = float(t)
+    if not 1e-6 <= t <= 1e6:
+        raise ValueError("temperature must lie in [1e-6, 1e6]")
+    return t
+
+
+def _reduction(name):
+    if name not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
+    return _REDUCTIONS[name]
+
+
+def _differentiates(*tensors):
+    """Whether a call goes through its autograd Function (which also refuses tangents)."""
+    return forward_mode() or (torch.is_grad_enabled() and tensors[0].requires_grad)
+
+
+def _flags(tokens):
+    return _lib.CE_FLAG_TARGET_I64 if tokens.dtype == torch.int64 else 0
+
+
+def _table(logits, grad, temperature=1.0):
+    """ce_rows of logits and their gradient."""
+    rows, inner, outer, step = _rows_of(logits)
+    return ctypes.byref(_lib.Rows(ptr(logits), ptr(grad), DTYPES[logits.dtype], temperature, rows,
+                                  logits.shape[-1], inner, outer, step))
+
+
+def _gradient_like(logits):
+    """An empty gradient: logits' strides, and their place within 16 bytes, so
+    that both are read and written in whole vectors."""
+    off = logits.data_ptr() % 16
+    if off == 0 and logits.is_contiguous():
+        return torch.empty_like(logits, memory_format=torch.contiguous_format)
+    rows, inner, outer, step = _rows_of(logits)
+    span = (rows // max(inner, 1) - 1) * outer + (inner - 1) * step + logits.shape[-1] if rows else 0
+    off //= logits.element_size()
+    flat = torch.empty(span + off, dtype=logits.dtype, device=logits.device)
+    return flat.as_strided(logits.shape, logits.stride(), off)
+
+
+def _workspace(device):
+    n = _lib.ce_rows_workspace_bytes()
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def _overwritten(logits):
+    """A gradient now stands in logits: a backward that saved their values finds it out."""
+    if not logits.is_inference():
+        torch.autograd.graph.increment_version(logits)
+
+
+# ---------------------------------------------------------------- log-probabilities
+
+def _log_probs(logits, tokens, temperature, ignore_index, want_entropy, keep):
+    dev = logits.device
+    logp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    entropy = torch.empty(tokens.shape, dtype=torch.float32, device=dev) if want_entropy else None
+    kept = torch.empty((tokens.numel(), 4), dtype=torch.float32, device=dev) if keep else None
+    with on(dev):
+        check(_lib.ce_token_logp(_table(logits, None, temperature), ptr(tokens), ignore_index,
+                                 _flags(tokens), ptr(logp), ptr(entropy), ptr(kept), stream(dev)),
+              "ce_token_logp")
+    return logp, entropy, kept
+
+
+class TokenLogProbsFunction(torch.autograd.Function):
+    """Autograd wrapper of ce_token_logp and ce_token_logp_bwd. The forward
+    keeps the logits and 16 bytes a row."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, ignore_index, want_entropy, inplace):
+        ctx.set_materialize_grads(False)
+        grad = ctx.needs_input_grad[0]
+        logp, entropy, kept = _log_probs(logits, tokens, temperature, ignore_index, want_entropy,
+                                         grad)
+        if grad:
+            ctx.save_for_backward(logits, tokens, kept)
+            ctx.args = temperature, ignore_index, inplace
+        return logp, entropy
+
+    @staticmethod
+    def backward(ctx, d_logp, d_entropy=None):
+        given = [d for d in (d_logp, d_entropy) if d is not None]
+        for d in given:
+            once("token_log_probs", d)
+        none = (None,) * 5
+        if not given or not ctx.needs_input_grad[0]:
+            return None, *none
+        logits, tokens, kept = ctx.saved_tensors
+        temperature, ignore_index, inplace = ctx.args
+        d_logp, d_entropy = (None if d is None else plain(d.float()) for d in (d_logp, d_entropy))
+        dx = logits.detach() if inplace else _gradient_like(logits)
+        dev = logits.device
+        with on(dev):
+            check(_lib.ce_token_logp_bwd(_table(logits, dx, temperature), ptr(tokens), ignore_index,
+                                         _flags(tokens), ptr(kept), ptr(d_logp), ptr(d_entropy),
+                                         stream(dev)), "ce_token_logp_bwd")
+        if inplace:
+            _overwritten(logits)
+        return dx, *none
+
+
+def token_log_probs(logits, tokens, temperature=1.0, ignore_index=-100, return_entropy=False,
+                    inplace=False):
+    """log_softmax(logits / temperature) at the given tokens, in float32:
+    tokens int32 or int64 of the shape logits.shape[:-1]. Rows whose token is
+    ignore_index are not read, give 0 and have a gradient of zero (so do rows
+    whose token lies outside [0, V), which device_status reports).
+
+    return_entropy: returns TokenLogProbs(log_probs, entropy), entropy that of
+    softmax(logits / temperature); both are differentiable."""
+    logits = _logits(logits, inplace)
+    tokens = _tokens(tokens, logits.shape[:-1], logits.device)
+    temperature, ignore_index = _temperature(temperature), int(ignore_index)
+    want_entropy = bool(return_entropy)
+    if _differentiates(logits):
+        logp, entropy = TokenLogProbsFunction.apply(logits, tokens, temperature, ignore_index,
+                                                    want_entropy, bool(inplace))
+    else:
+        logp, entropy, _ = _log_probs(logits, tokens, temperature, ignore_index, want_entropy,
+                                      False)
+    return TokenLogProbs(logp, entropy) if want_entropy else logp
+
+
+# ---------------------------------------------------------------- gradients of the forward
+
+def _forward_gradient(ctx, logits, call, inplace):
+    """Runs call(dx) with the place of the gradient, which it keeps for the backward."""
+    if not ctx.needs_input_grad[0]:
+        return call(None)
+    dx = logits.detach() if inplace else _gradient_like(logits)
+    out = call(dx)
+    if inplace:
+        _overwritten(logits)
+    ctx.save_for_backward(dx)
+    ctx.spent = False
+    return out
+
+
+def _scaled_gradient(ctx, d_loss, name, per_row):
+    """The gradient that the forward left, times d_loss."""
+    once(name, d_loss)
+    (dx,) = ctx.saved_tensors
+    if ctx.spent:
+        raise RuntimeError(f"{name}'s gradient was given to an earlier backward")
+    ctx.spent = True
+    g, dev = plain(d_loss.float()), dx.device
+    with on(dev):
+        check(_lib.ce_rows_scale(_table(dx, dx), ptr(g), per_row, stream(dev)), "ce_rows_scale")
+    return dx
+
+
+# ---------------------------------------------------------------- policy loss
+
+def _policy(logits, dx, tokens, advantages, advantage_rows, old, ref, weight, temperature,
+            ignore_index, clip_low, clip_high, kl_coef, entropy_coef, scale, red, stats):
+    dev, shape = logits.device, tokens.shape
+    f32 = dict(dtype=torch.float32, device=dev)
+    loss = torch.empty(shape if red == _lib.CE_RED_NONE else (), **f32)
+    logp = entropy = kl = clipped = None
+    if stats:
+        logp, entropy, kl = (torch.empty(shape, **f32) for _ in range(3))
+        clipped = torch.empty(shape, dtype=torch.bool, device=dev)
+    with on(dev):
+        ws, nbytes = _workspace(dev)
+        check(_lib.ce_policy_loss(_table(logits, dx, temperature), ptr(tokens), ignore_index,
+                                  _flags(tokens), ptr(advantages), advantage_rows, ptr(old),
+                                  ptr(ref), ptr(weight), clip_low, clip_high, kl_coef, entropy_coef,
+                                  scale, red, ptr(loss), ptr(logp), ptr(entropy), ptr(kl),
+                                  ptr(clipped), ptr(ws), nbytes, stream(dev)), "ce_policy_loss")
+    return loss, logp, entropy, kl, clipped
+
+
+class PolicyLossFunction(torch.autograd.Function):
+    """Autograd wrapper of ce_policy_loss: the forward leaves the gradient in a
+    buffer (with inplace, in the logits), which the backward scales."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, advantages, old, ref, weight, inplace, args):
+        out = _forward_gradient(
+            ctx, logits,
+            lambda dx: _policy(logits, dx, tokens, advantages, args[0], old, ref, weight,
+                               *args[1:]), inplace)
+        ctx.mark_non_differentiable(*(t for t in out[1:] if t is not None))
+        ctx.per_row = out[0].dim() > 0
+        return out
+
+    @staticmethod
+    def backward(ctx, d_loss, *unused):
+        dx = _scaled_gradient(ctx, d_loss, "policy_loss", 1 if ctx.per_row else 0)
+        return (dx,) + (None,) * 7
+
+
+def policy_loss(logits, tokens, advantages, old_log_probs=None, ref_log_probs=None, weight=None,
+                clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0,
+                ignore_index=-100, scale=1.0, reduction="mean", inplace=False, return_stats=False):
+    """The clipped policy loss of sampled tokens, with a KL term towards a
+    reference policy and an entropy bonus:
+
+        r = exp(log_probs - old_log_probs)
+        -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+            + kl_coef (exp(g) - g - 1) - entropy_coef entropy,  g = ref_log_probs - log_probs
+
+    tokens as for token_log_probs (mark prompts and padding with ignore_index).
+    advantages: one a token (tokens.shape), or one for each entry of tokens'
+    first dimensions ([B] or [B, 1] for tokens [B, T]). old_log_probs (None:
+    the present ones, r = 1), ref_log_probs (None: no KL term) and weight (None:
+    1) have tokens' shape.
+
+    "mean": scale sum(weight loss) / sum(weight) over the tokens that count
+    (NaN with none); "sum"; "none": scale weight loss, a value a token. scale
+    multiplies loss and gradient without another pass over the gradient, as
+    a factor on the returned loss would need.
+
+    return_stats: PolicyLossOutput(loss, log_probs, entropy, kl, clipped), the
+    last four a value a token, without gradients."""
+    logits = _logits(logits, inplace)
+    dev, shape = logits.device, logits.shape[:-1]
+    tokens = _tokens(tokens, shape, dev)
+    if not isinstance(advantages, torch.Tensor):
+        raise ValueError("advantages must be a tensor")
+    lead = list(advantages.shape)
+    while lead and lead[-1] == 1 and lead != list(shape[:len(lead)]):
+        lead.pop()
+    if lead != list(shape[:len(lead)]) or (not lead and shape.numel() != 1) or \
+            advantages.dim() > len(shape):
+        raise ValueError("advantages must have tokens' shape, or that of its first dimensions")
+    advantages = _floats(advantages, advantages.shape, dev, "advantages")
+    advantage_rows = max(1, math.prod(shape[len(lead):]))
+    old = _floats(old_log_probs, shape, dev, "old_log_probs")
+    ref = _floats(ref_log_probs, shape, dev, "ref_log_probs")
+    weight = _floats(weight, shape, dev, "weight")
+    clip_low, clip_high = float(clip_low), float(clip_high)
+    if not 0.0 <= clip_low <= 1.0 or not clip_high >= 0.0:
+        raise ValueError("clip_low must lie in [0, 1] and clip_high be at least 0")
+    args = (advantage_rows, _temperature(temperature), int(ignore_index), clip_low, clip_high,
+            _number(kl_coef, "kl_coef"), _number(entropy_coef, "entropy_coef"),
+            _number(scale, "scale"), _reduction(reduction), bool(return_stats))
+    if _differentiates(logits):
+        out = PolicyLossFunction.apply(logits, tokens, advantages, old, ref, weight, bool(inplace),
+                                       args)
+    else:
+        out = _policy(logits, None, tokens, advantages, args[0], old, ref, weight, *args[1:])
+    return PolicyLossOutput(*out) if return_stats else out[0]
+
+
+# ---------------------------------------------------------------- distillation
+
+def _distill(logits, dx, teacher, index, teacher_lse, weight, temperature, scale, red):
+    dev = logits.device
+    loss = torch.empty(logits.shape[:-1] if red == _lib.CE_RED_NONE else (), dtype=torch.float32,
+                       device=dev)
+    with on(dev):
+        ws, nbytes = _workspace(dev)
+        check(_lib.ce_distill_loss(_table(logits, dx, temperature), ptr(teacher),
+                                   DTYPES[teacher.dtype], ptr(index), index.shape[-1],
+                                   ptr(teacher_lse), _flags(index), ptr(weight), scale, red,
+                                   ptr(loss), ptr(ws), nbytes, stream(dev)), "ce_distill_loss")
+    return loss
+
+
+class DistillationLossFunction(torch.autograd.Function):
+    """Autograd wrapper of ce_distill_loss, as PolicyLossFunction."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher, index, teacher_lse, weight, inplace, args):
+        loss = _forward_gradient(
+            ctx, logits,
+            lambda dx: _distill(logits, dx, teacher, index, teacher_lse, weight, *args), inplace)
+        ctx.per_row = loss.dim() > 0
+        return loss
+
+    @staticmethod
+    def backward(ctx, d_loss):
+        dx = _scaled_gradient(ctx, d_loss, "distillation_loss", 1 if ctx.per_row else 0)
+        return (dx,) + (None,) * 6
+
+
+def distillation_loss(logits, teacher_logits, teacher_indices, teacher_lse=None, temperature=1.0,
+                      weight=None, scale=1.0, reduction="mean", inplace=False):
+    """KL divergence of the softmax of logits / temperature from a teacher
+    known by its K largest logits (K at most 256): teacher_logits and
+    teacher_indices [..., K] (float32, bfloat16 or float16; int32 or int64).
+
+    Without teacher_lse the teacher's probabilities are the softmax of its K
+    values over the temperature. With teacher_lse [...], the log-sum-exp of
+    all its logits over the temperature, they are exp(value / temperature -
+    teacher_lse), and what remains of the teacher's mass is compared, as one
+    more outcome, with the mass that the student gives to all other classes.
+
+    An entry with a negative index is padding. A row whose first index is
+    negative does not count: it is not read, and its gradient is zero.
+    weight, scale and reduction as for policy_loss (scale=temperature ** 2
+    keeps the gradients' size)."""
+    logits = _logits(logits, inplace)
+    dev, shape = logits.device, logits.shape[:-1]
+    if not isinstance(teacher_indices, torch.Tensor) or teacher_indices.dim() != len(shape) + 1 or \
+            teacher_indices.shape[-1] < 1:
+        raise ValueError("teacher_indices must be [..., K] with K >= 1")
+    wide = shape + teacher_indices.shape[-1:]
+    index = _tokens(teacher_indices, wide, dev, "teacher_indices")
+    if not isinstance(teacher_logits, torch.Tensor) or teacher_logits.shape != wide or \
+            teacher_logits.device != dev:
+        raise ValueError("teacher_logits must have the shape and device of teacher_indices")
+    if teacher_logits.dtype not in DTYPES:
+        raise TypeError("teacher_logits must be float32, bfloat16 or float16")
+    if teacher_logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError("teacher_logits takes no gradient: detach it")
+    teacher = plain(teacher_logits)
+    teacher_lse = _floats(teacher_lse, shape, dev, "teacher_lse")
+    weight = _floats(weight, shape, dev, "weight")
+    args = (_temperature(temperature), _number(scale, "scale"), _reduction(reduction))
+    if _differentiates(logits):
+        return DistillationLossFunction.apply(logits, teacher, index, teacher_lse, weight,
+                                              bool(inplace), args)
+    return _distill(logits, None, teacher, index, teacher_lse, weight, *args)
+
+
+# ---------------------------------------------------------------- preference loss
+
+def _preference(logits, tokens, offsets, ref, ignore_index, pairs, kind, beta, margin, smoothing,
+                average, scale, red, grad):
+    dev = logits.device
+    f32 = dict(dtype=torch.float32, device=dev)
+    loss = torch.empty((pairs,) if red == _lib.CE_RED_NONE else (), **f32)
+    scores = torch.empty(2 * pairs, **f32)
+    dscore = torch.empty(2 * pairs, **f32) if grad else None
+    kept = torch.empty((tokens.numel(), 4), **f32)
+    with on(dev):
+        ws, nbytes = _workspace(dev)
+        check(_lib.ce_preference_loss(_table(logits, None), ptr(tokens), ignore_index,
+                                      _flags(tokens), pairs, ptr(offsets), ptr(ref), kind, beta,
+                                      margin, smoothing, average, scale, red, ptr(loss),
+                                      ptr(scores), ptr(dscore), ptr(kept), ptr(ws), nbytes,
+                                      stream(dev)), "ce_preference_loss")
+    return loss, scores, dscore, kept
+
+
+class PreferenceLossFunction(torch.autograd.Function):
+    """Autograd wrapper of ce_preference_loss and its backward. The forward
+    keeps the logits and 16 bytes a row."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, offsets, ref, inplace, args):
+        grad = ctx.needs_input_grad[0]
+        loss, scores, dscore, kept = _preference(logits, tokens, offsets, ref, *args, grad)
+        if grad:
+            ctx.save_for_backward(logits, tokens, offsets, kept, dscore)
+            ctx.args = args[0], args[1], inplace
+        ctx.mark_non_differentiable(scores)
+        return loss, scores
+
+    @staticmethod
+    def backward(ctx, d_loss, *unused):
+        once("preference_loss", d_loss)
+        logits, tokens, offsets, kept, dscore = ctx.saved_tensors
+        ignore_index, pairs, inplace = ctx.args
+        g, dev = plain(d_loss.float()), logits.device
+        dx = logits.detach() if inplace else _gradient_like(logits)
+        with on(dev):
+            check(_lib.ce_preference_loss_bwd(_table(logits, dx), ptr(tokens), ignore_index,
+                                              _flags(tokens), pairs, ptr(offsets), ptr(kept),
+                                              ptr(dscore), ptr(g), 1 if g.dim() else 0,
+                                              stream(dev)), "ce_preference_loss_bwd")
+        if inplace:
+            _overwritten(logits)
+        return (dx,) + (None,) * 5
+
+
+def preference_loss(logits, tokens, offsets=None, ref_log_probs=None, beta=0.1,
+                    loss_type="sigmoid", label_smoothing=0.0, margin=0.0, length_average=False,
+                    ignore_index=-100, scale=1.0, reduction="mean", inplace=False,
+                    return_scores=False):
+    """The loss of pairs of sequences, the first half of which is preferred
+    each to its partner in the second half. A sequence's score is the sum (with
+    length_average, the mean) of its tokens' log-probabilities; with d the
+    difference of a pair's scores less that of their ref_log_probs and
+    h = beta d - margin:
+
+        "sigmoid"  -(1 - label_smoothing) log sigma(h) - label_smoothing log sigma(-h)
+        "hinge"    max(0, 1 - h)
+        "ipo"      (d - 1 / (2 beta))^2
+
+    logits [2 pairs, T, V] and tokens [2 pairs, T], padded with ignore_index;
+    or, with offsets (integers [2 pairs + 1] on the device), the sequences'
+    rows one behind another: logits [rows, V], tokens [rows], sequence s in the
+    rows from offsets[s] up to offsets[s + 1] (rows of none take no part).
+    ref_log_probs [2 pairs]: the reference model's scores (None: 0). reduction
+    over the pairs; scale as for policy_loss.
+
+    return_scores: PreferenceLossOutput(loss, scores [2 pairs], without
+    gradient)."""
+    logits = _logits(logits, inplace)
+    dev = logits.device
+    if offsets is None:
+        if logits.dim() != 3 or logits.shape[0] % 2:
+            raise ValueError("logits must be [2 pairs, T, V] (or [rows, V] with offsets)")
+        pairs = logits.shape[0] // 2
+    else:
+        if logits.dim() != 2:
+            raise ValueError("logits must be [rows, V] with offsets")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or \
+                offsets.shape[0] % 2 != 1 or offsets.dtype not in (torch.int32, torch.int64):
+            raise ValueError("offsets must hold 2 pairs + 1 integers")
+        if offsets.device != dev:
+            raise ValueError("offsets must be on the logits' device")
+        pairs = offsets.shape[0] // 2
+        offsets = offsets.to(torch.int64).contiguous()
+    tokens = _tokens(tokens, logits.shape[:-1], dev)
+    ref = _floats(ref_log_probs, torch.Size((2 * pairs,)), dev, "ref_log_probs")
+    if loss_type not in _KINDS:
+        raise ValueError(f"loss_type must be one of {sorted(_KINDS)}")
+    beta, margin = _number(beta, "beta"), _number(margin, "margin")
+    if beta <= 0.0:
+        raise ValueError("beta must be positive")
+    smoothing = float(label_smoothing)
+    if not 0.0 <= smoothing <= 1.0:
+        raise ValueError("label_smoothing must lie in [0, 1]")
+    if loss_type != "sigmoid" and smoothing != 0.0:
+        raise ValueError('label_smoothing belongs to the "sigmoid" loss')
+    if loss_type == "ipo" and margin != 0.0:
+        raise ValueError('the "ipo" loss has no margin')
+    args = (int(ignore_index), pairs, _KINDS[loss_type], beta, margin, smoothing,
+            1 if length_average else 0, _number(scale, "scale"), _reduction(reduction))
+    if _differentiates(logits):
+        loss, scores = PreferenceLossFunction.apply(logits, tokens, offsets, ref, bool(inplace),
+                                                    args)
+    else:
+        loss, scores, _, _ = _preference(logits, tokens, offsets, ref, *args, False)
+    return PreferenceLossOutput(loss, scores) if return_scores else loss
