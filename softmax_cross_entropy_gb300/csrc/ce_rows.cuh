@@ -34,13 +34,25 @@ struct __align__(16) RowKept {
     float m, S, H, logp;
 };
 
+constexpr int kMaxRowCluster = 16;  // CTAs that share a row
+
+// An entry of a teacher's list.
+struct __align__(16) Entry {
+    float x;   // the student's logit of its class
+    float q;   // the teacher's probability (0: padding)
+    float lq;  // its logarithm
+    float qs;  // the sum of q over the entries of this class, in the first of them
+    int j;     // the class; -1: padding, or not the first of its class
+    int pad[3];
+};
+
 struct RowArgs {
     RowPlace p;
     // log2(e) / T in two parts (its error alone, times the arguments' size, would
     // move every row's sum the same way): exp((x - m) / T) = 2^((x - m) (c + c_low));
     // c_low > 0
     float c, c_low;
-    double invT;
+    float invT, invT_low;  // 1 / T in two parts
     const void* tokens;  // [rows], int32 or int64
     int tok64;
     int64_t ignore_index;
@@ -70,6 +82,9 @@ struct RowArgs {
     int idx64;
     int K;
     const float* teacher_lse;  // [rows] or nullptr
+    // layout: CTAs a row, 16-byte vectors of a CTA's slice, its buffers and their bytes
+    int cluster, slice_vec, nbuf;
+    uint32_t buf_bytes;
 };
 
 __device__ __forceinline__ int64_t load_index(const void* p, int is64, int64_t i) {
@@ -95,40 +110,36 @@ __device__ __forceinline__ RowSpan row_span(const void* p, int64_t V) {
 }
 
 // log p of a logit in a row with largest logit m and log S = logS.
-__device__ __forceinline__ float log_prob(float x, float m, double invT, float logS) {
-    return static_cast<float>(static_cast<double>(x - m) * invT - static_cast<double>(logS));
+__device__ __forceinline__ float log_prob(const RowArgs& a, float x, float m, float logS) {
+    const float d = x - m;
+    // (an infinite d: the second product of a zero and -inf would be NaN)
+    return fmaf(d, a.invT, fmaf(fmaxf(d, -3.0e38f), a.invT_low, -logS));
 }
 
 // The softmax statistics of part of a row: its largest logit m, S = sum
-// 2^a and Q = sum 2^a a with a = (x - m) c. No element: m = -inf, S = Q = 0.
-struct RowPart {
-    float m, S, Q;
+// 2^a and Q = sum 2^a a with a = (x - m) c; x: the token's logit where the
+// part holds it, else -inf. No element: m = -inf, S = Q = 0.
+struct __align__(16) RowPart {
+    float m, S, Q, x;
 };
 
-// Adds b to a; the same bits whichever of the two comes first.
-template <bool ENT>
-__device__ __forceinline__ void part_merge(RowPart& a, const RowPart& b, float c) {
-    const float M = fmaxf(a.m, b.m);
-    // (an empty side has S = Q = 0, and a factor of 1)
-    const float da = a.m == M ? 0.f : fmaxf(__fmul_rn(__fsub_rn(a.m, M), c), -256.f);
-    const float db = b.m == M ? 0.f : fmaxf(__fmul_rn(__fsub_rn(b.m, M), c), -256.f);
-    const float fa = ex2(da), fb = ex2(db);
-    if (ENT)
-        a.Q = __fadd_rn(__fmul_rn(fa, __fmaf_rn(da, a.S, a.Q)), __fmul_rn(fb, __fmaf_rn(db, b.S, b.Q)));
-    a.S = __fadd_rn(__fmul_rn(fa, a.S), __fmul_rn(fb, b.S));
-    a.m = M;
+// The factor and shift that bring statistics with maximum m to the maximum M
+// (m <= M; an empty part has S = Q = 0 and any factor).
+__device__ __forceinline__ void part_raise(RowPart& v, float M, float c, bool ent) {
+    const float base = M == -INFINITY ? 0.f : M;
+    const float d = fmaxf((v.m - base) * c, -256.f), f = ex2(d);
+    if (ent) v.Q = f * fmaf(d, v.S, v.Q);
+    v.S *= f;
+    v.m = M;
 }
 
-template <bool ENT>
-__device__ __forceinline__ void part_warp_merge(RowPart& v, float c) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        RowPart b;
-        b.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-        b.S = __shfl_xor_sync(0xffffffffu, v.S, o);
-        b.Q = ENT ? __shfl_xor_sync(0xffffffffu, v.Q, o) : 0.f;
-        part_merge<ENT>(v, b, c);
-    }
+// The statistics of a warp's parts together, the same bits in every lane.
+template <bool ENT, bool TOKEN>
+__device__ __forceinline__ void part_warp(RowPart& v, float c) {
+    part_raise(v, warp_max_f32(v.m), c, ENT);
+    v.S = warp_sum(v.S);
+    if (ENT) v.Q = warp_sum(v.Q);
+    if (TOKEN) v.x = warp_max_f32(v.x);
 }
 
 // The policy loss of one token from its log-probability: the loss without the
@@ -158,19 +169,15 @@ __device__ __forceinline__ PolicyRow policy_row(const RowArgs& a, float lp, floa
     return o;
 }
 
-// exp of a 64-bit argument, to fp32's precision whatever its size.
-__device__ __forceinline__ float exp_wide(double a) {
-    const float hi = static_cast<float>(a);
-    if (!(fabsf(hi) < 1e30f)) return expf(hi);  // (and -inf, NaN)
-    const float lo = static_cast<float>(a - static_cast<double>(hi));
-    const float e = expf(hi);
-    return fmaf(e, lo, e);
-}
-
-// The mean's denominator, or the sum's 1; a row's gradient is multiplied by it.
-__device__ __forceinline__ float row_scale(const RowArgs& a, double weight) {
-    const double d = a.reduction == kRedMean ? __ldcg(a.D) : 1.0;
-    return static_cast<float>(static_cast<double>(a.scale) * weight / d);
+// v / T - shift in two parts: the rounded value, and what it lacks. (A
+// teacher's log-probabilities: exp would carry their rounding, 2^-24 of up to
+// some tens, into the remaining mass.)
+__device__ __forceinline__ float2 scaled_minus(const RowArgs& a, float v, float shift) {
+    const float p = v * a.invT;
+    const float hi = p - shift, b = hi - p;
+    float lo = (p - (hi - b)) + (-shift - b);
+    lo += fmaf(v, a.invT, -p) + v * a.invT_low;
+    return make_float2(hi, fabsf(lo) < 1.f ? lo : 0.f);  // (infinities have no second part)
 }
 
 // The reduced loss: thread 0 of each CTA holds its rows' sum; the last CTA to

@@ -73,8 +73,10 @@ RowPlace place_of(const ce_rows* x) {
 
 void fill_rows(RowArgs* a, const ce_rows* x, const Device& d) {
     a->p = place_of(x);
-    a->invT = 1.0 / static_cast<double>(x->temperature);
-    const double c = 1.4426950408889634 * a->invT;
+    const double inv = 1.0 / static_cast<double>(x->temperature);
+    a->invT = static_cast<float>(inv);
+    a->invT_low = static_cast<float>(inv - static_cast<double>(a->invT));
+    const double c = 1.4426950408889634 * inv;
     a->c = static_cast<float>(c);
     // (c_low > 0, so that both products of -inf are -inf)
     if (static_cast<double>(a->c) >= c) a->c = std::nextafterf(a->c, 0.f);
@@ -120,7 +122,7 @@ extern "C" ce_status ce_token_logp(const ce_rows* x, const void* tokens, int64_t
     a.logp = logp;
     a.entropy = entropy;
     a.kept = reinterpret_cast<RowKept*>(kept);
-    return rows_launch(kRowLogp, entropy != nullptr, x->dtype, a, d.sms, st);
+    return rows_launch(kRowLogp, entropy != nullptr, x->dtype, a, d.sms, false, st);
 }
 
 extern "C" ce_status ce_token_logp_bwd(const ce_rows* x, const void* tokens, int64_t ignore_index,
@@ -191,7 +193,8 @@ extern "C" ce_status ce_policy_loss(const ce_rows* x, const void* tokens, int64_
     a.kl_out = kl;
     a.clipped = clipped;
     if (reduction != CE_RED_NONE && (rc = rows_count_launch(a, st)) != CE_OK) return rc;
-    return rows_launch(kRowPolicy, entropy != nullptr || entropy_coef != 0.f, x->dtype, a, d.sms, st);
+    return rows_launch(kRowPolicy, entropy != nullptr || entropy_coef != 0.f, x->dtype, a, d.sms,
+                       reduction != CE_RED_NONE, st);
 }
 
 extern "C" ce_status ce_distill_loss(const ce_rows* x, const void* teacher, int teacher_dtype,
@@ -229,7 +232,7 @@ extern "C" ce_status ce_distill_loss(const ce_rows* x, const void* teacher, int 
     a.K = static_cast<int>(K);
     a.teacher_lse = teacher_lse;
     if (reduction != CE_RED_NONE && (rc = rows_count_launch(a, st)) != CE_OK) return rc;
-    return rows_launch(kRowDistill, false, x->dtype, a, d.sms, st);
+    return rows_launch(kRowDistill, false, x->dtype, a, d.sms, reduction != CE_RED_NONE, st);
 }
 
 namespace {
@@ -278,7 +281,7 @@ extern "C" ce_status ce_preference_loss(const ce_rows* x, const void* tokens, in
     a.ignore_index = ignore_index;
     a.kept = reinterpret_cast<RowKept*>(kept);
     // (also without rows: it clears the ticket)
-    if ((rc = rows_launch(kRowLogp, false, x->dtype, a, d.sms, st)) != CE_OK) return rc;
+    if ((rc = rows_launch(kRowLogp, false, x->dtype, a, d.sms, false, st)) != CE_OK) return rc;
     PairArgs p = {};
     p.pairs = pairs;
     p.rows = x->rows;

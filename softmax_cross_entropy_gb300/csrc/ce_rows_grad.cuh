@@ -45,7 +45,8 @@ struct GradArgs {
     int parts, part_vec;
 };
 
-ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& a, int sms, cudaStream_t st);
+ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& a, int sms, bool after_count,
+                      cudaStream_t st);
 ce_status rows_count_launch(const RowArgs& a, cudaStream_t st);
 ce_status pair_launch(const PairArgs& a, cudaStream_t st);
 ce_status rows_grad_launch(const GradArgs& a, int dtype, int sms, cudaStream_t st);

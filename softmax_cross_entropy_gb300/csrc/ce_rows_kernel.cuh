@@ -1,0 +1,632 @@
+// The token losses' forward over rows of logits: one kernel in three forms
+// (log-probabilities of given tokens; the clipped policy loss; distillation
+// from a teacher's top logits), each with its gradient in the same pass.
+//
+// Mathematics. One pass forms a row's running maximum m and S = sum
+// 2^((x - m) log2(e) / T) (and Q = sum 2^a a for the entropy, H = log S - ln 2
+// Q / S); every loss's gradient is then an element's 2^a times a constant of
+// the row (for the entropy, times a constant plus a multiple of a), with
+// other values at the token or the teacher's classes alone. So a row is read
+// from memory once, kept on chip, and its gradient is written once.
+//
+// Layout. A cluster of 1 to 16 CTAs owns a row at a time; a CTA holds its
+// slice of the row in shared memory. A producer warp copies the slices of the
+// next rows (1-D bulk copies into a ring of buffers, counted on mbarriers)
+// and looks up what the rows need besides (token, advantage, the teacher's
+// list with its softmax and its classes' logits), while the other warps pass
+// over the present slice twice: statistics, then gradient. Their partial
+// statistics meet in shared memory, a row's over its cluster by remote stores
+// that complete on an mbarrier of each receiver. Rows start at any element:
+// a slice is copied in whole 16-byte vectors, and the vectors that a row
+// shares with its neighbours are filled element by element.
+#pragma once
+
+#include "ce_rows.cuh"
+
+namespace gbce {
+
+constexpr int kMaxBuf = 4;
+constexpr uint32_t kBulk = 32768;
+
+// What the producer leaves of a row beside its logits.
+struct __align__(16) RowInfo {
+    int64_t at;  // the row's first element
+    int t;       // the token (distillation: any value >= 0); -1: the row does not count
+    int bad;     // the token was out of range
+    int n;       // vectors of this CTA's slice; those from w0 up to w1 are the row's alone
+    int w0, w1;
+    int first;   // the class of the slice's first element (below 0 where it is in front of the row)
+    float adv, old, ref, weight;
+    float mass, rest, top;  // the list: sum of q, what remains, the largest of its logits
+    int pad;
+};
+
+// What every warp needs for the gradient: 2^((x - m) c) (u0 + u1 a), and x at
+// the token; distillation: u0 outside the list, in it u1 and less x times q.
+struct __align__(16) RowConst {
+    float m, u0, u1, x;
+};
+
+// CTAs of an SM that a kernel's registers are to leave room for.
+constexpr int rows_ctas(int nt) { return nt == 32 ? 16 : nt == 64 ? 10 : nt == 128 ? 5 : 3; }
+
+// Of lanes 0-7 the vector that the row's start shares with what is before it,
+// of lanes 8-15 the one that its end shares; -1: there is none.
+__device__ __forceinline__ int edge_vector(const RowInfo& in, int lane) {
+    if (lane < 8) return in.w0 > 0 ? 0 : -1;
+    return lane < 16 && in.w1 < in.n ? in.w1 : -1;
+}
+
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Four words into the shared memory of a CTA of the cluster, counted on its
+// mbarrier.
+__device__ __forceinline__ void st_async_v4(uint32_t dst, const RowPart& v, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+        "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.S)), "r"(__float_as_uint(v.Q)),
+        "r"(__float_as_uint(v.x)), "r"(bar)
+        : "memory");
+}
+
+// mbar_wait_bounded for a barrier that other CTAs of the cluster complete.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > timeout_ns) return false;
+    }
+}
+
+template <typename T>
+struct Lowest;  // a vector of -inf
+template <>
+struct Lowest<float> {
+    static constexpr uint32_t w = 0xFF800000u;
+};
+template <>
+struct Lowest<__nv_bfloat16> {
+    static constexpr uint32_t w = 0xFF80FF80u;
+};
+template <>
+struct Lowest<__half> {
+    static constexpr uint32_t w = 0xFC00FC00u;
+};
+template <typename T>
+__device__ __forceinline__ uint4 lowest4() {
+    return make_uint4(Lowest<T>::w, Lowest<T>::w, Lowest<T>::w, Lowest<T>::w);
+}
+
+
+// A warp forms row r's list: the teacher's softmax, its classes' logits, and
+// which entry stands for a class that is named more than once.
+template <typename T>
+__device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* row, Entry* ent, RowInfo& in,
+                                         int lane) {
+    float top_v = -INFINITY, top_x = -INFINITY;
+    for (int e = lane; e < a.K; e += 32) {
+        const int64_t w = r * a.K + e;
+        const int64_t j = load_index(a.index, a.idx64, w);
+        const float v = a.teacher_dtype == 0   ? Vec<float>::load1(a.teacher, w)
+                        : a.teacher_dtype == 1 ? Vec<__nv_bfloat16>::load1(a.teacher, w)
+                                               : Vec<__half>::load1(a.teacher, w);
+        const bool ok = j >= 0 && j < a.p.V;
+        if (j >= a.p.V) atomicOr(a.status, kDevErrTarget);
+        const float x = ok ? Vec<T>::load1(row, j) : -INFINITY;
+        ent[e].j = ok ? static_cast<int>(j) : -1;
+        ent[e].lq = ok ? v : -INFINITY;
+        ent[e].x = x;
+        if (ok) top_v = fmaxf(top_v, v);
+        top_x = fmaxf(top_x, x);
+    }
+    __syncwarp();
+    const bool tail = a.teacher_lse != nullptr;
+    const float shift = tail ? __ldg(a.teacher_lse + r) : warp_max_f32(top_v) * a.invT;
+    in.top = warp_max_f32(top_x);
+    double mass = 0.0;
+    for (int e = lane; e < a.K; e += 32) {
+        const float2 l = scaled_minus(a, ent[e].lq, shift);
+        const float q = ent[e].j < 0 ? 0.f : expf(l.x);
+        ent[e].lq = l.x;
+        ent[e].q = fmaf(q, l.y, q);
+        mass += ent[e].q;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    in.mass = static_cast<float>(mass);
+    if (tail) {
+        in.rest = static_cast<float>(fmax(0.0, 1.0 - mass));
+    } else {
+        const float lm = logf(in.mass), im = 1.f / in.mass;
+        for (int e = lane; e < a.K; e += 32) {
+            ent[e].q *= im;
+            ent[e].lq -= lm;
+        }
+        in.mass = 1.f;
+    }
+    __syncwarp();
+    for (int e = lane; e < a.K; e += 32) {
+        const int j = ent[e].j;
+        float qs = 0.f;
+        bool is_first = true;
+        for (int o = 0; o < a.K; ++o) {
+            if (ent[o].j == j) {
+                qs += ent[o].q;
+                is_first = is_first && o >= e;
+            }
+        }
+        ent[e].qs = is_first ? qs : -1.f;
+    }
+    __syncwarp();
+    for (int e = lane; e < a.K; e += 32)
+        if (ent[e].qs < 0.f) ent[e].j = -1;
+}
+
+template <typename T, int OP, bool ENT, int NT>
+__global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __grid_constant__ RowArgs a) {
+    using VT = Vec<T>;
+    constexpr int VE = VT::N;
+    constexpr int NW = NT / 32;
+    constexpr int U = 4;  // vectors a thread takes at once
+    extern __shared__ __align__(128) unsigned char smem[];  // buffers, then the lists
+    __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], met[2], meeting,
+        ready;
+    __shared__ RowPart parts[2][kMaxRowCluster];  // of the cluster's CTAs, two rows in turn
+    __shared__ RowPart red[kMaxBuf][NW];          // of the warps
+    __shared__ RowInfo info[kMaxBuf];
+    __shared__ RowConst consts[kMaxBuf];
+    __shared__ double red_d[NW + 1];
+    __shared__ int s_flag;
+
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = a.cluster;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int64_t first = C > 1 ? cluster_id_x() : blockIdx.x;
+    const int64_t step = gridDim.x / static_cast<unsigned>(C);
+    const int NB = a.nbuf;
+    Entry* lists = reinterpret_cast<Entry*>(smem + static_cast<size_t>(NB) * a.buf_bytes);
+    const bool tail = OP == kRowDistill && a.teacher_lse != nullptr;
+    if (OP == kRowLogp && a.ticket && blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
+    if (tid == 0) {
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(smem_u32(&full[i]), 2);
+            mbar_init(smem_u32(&empty[i]), NW);
+            mbar_init(smem_u32(&together[i]), NW);
+        }
+        mbar_init(smem_u32(&met[0]), 1);
+        mbar_init(smem_u32(&met[1]), 1);
+        mbar_init(smem_u32(&meeting), NW);
+        mbar_init(smem_u32(&ready), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (C > 1) cluster_sync();
+
+    // A wait that runs out ends its warp's rows (the lanes agree on it), and so
+    // in time those of every warp that waits for it; all meet at the end.
+    auto timed_out = [&](bool ok) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) atomicOr(a.status, kDevErrTimeout);
+        return !ok;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return !timed_out(mbar_wait_bounded(smem_u32(bar), parity, a.timeout_ns));
+    };
+    double sum = 0.0;
+    const T* X = reinterpret_cast<const T*>(a.p.x);
+
+    if (warp == NW) {
+        // ---------------------------------------------------------- producer
+        const uint64_t pol = l2_evict_first_policy();
+        auto token = [&](int64_t r) {
+            return OP == kRowDistill ? load_index(a.index, a.idx64, r * a.K)
+                                     : load_index(a.tokens, a.tok64, r);
+        };
+        int k = 0;
+        uint32_t phase = 1;   // of `empty`: the buffers are free at first
+        uint32_t filled = 0;  // bit i: buffer i has been filled
+        int64_t t_next = first < a.p.rows ? token(first) : 0;
+        for (int64_t r = first; r < a.p.rows; r += step) {
+            const int64_t t = t_next;
+            if (r + step < a.p.rows) t_next = token(r + step);
+            RowInfo in = {};
+            in.at = a.p.at(r);
+            const bool in_range = t >= 0 && t < a.p.V;
+            const bool counts = in_range && (OP == kRowDistill || t != a.ignore_index);
+            in.t = counts ? static_cast<int>(t) : -1;
+            in.bad = !in_range && (OP == kRowDistill ? t >= 0 : t != a.ignore_index);
+            in.weight = 1.f;
+            if (counts && OP != kRowLogp) {
+                if (a.weight) in.weight = __ldg(a.weight + r);
+                if (OP == kRowPolicy) {
+                    in.adv = __ldg(a.adv + (a.adv_rows == 1 ? r : r / a.adv_rows));
+                    if (a.old) in.old = __ldg(a.old + r);
+                    if (a.ref) in.ref = __ldg(a.ref + r);
+                }
+            }
+            const T* row = X + in.at;
+            {
+                // vector 0 of a row is the one that its first element lies in
+                const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) /
+                                static_cast<int>(sizeof(T));
+                const int end = off + static_cast<int>(a.p.V);
+                const int lo = min(rank * a.slice_vec, (end + VE - 1) / VE);
+                in.n = min(a.slice_vec, (end + VE - 1) / VE - lo);
+                in.w0 = min(max((off ? 1 : 0) - lo, 0), in.n);
+                in.w1 = max(min(end / VE - lo, in.n), in.w0);
+                in.first = lo * VE - off;
+            }
+            if (!wait(&empty[k], phase)) break;
+            const uint32_t bar = smem_u32(&full[k]);
+            unsigned char* buf = smem + static_cast<size_t>(k) * a.buf_bytes;
+            if (counts) {
+                fence_proxy_async();  // edges of earlier rows lay where this copy may land
+                __syncwarp();
+                if (lane == 0) {
+                    if (in.w1 > in.w0) {
+                        const uint32_t bytes = static_cast<uint32_t>(in.w1 - in.w0) * 16u;
+                        const uint32_t dst = smem_u32(buf) + static_cast<uint32_t>(in.w0) * 16u;
+                        const char* src = reinterpret_cast<const char*>(row + in.first + in.w0 * VE);
+                        mbar_arrive_expect_tx(bar, bytes);
+                        for (uint32_t o = 0; o < bytes; o += kBulk)
+                            bulk_g2s(dst + o, src + o, min(kBulk, bytes - o), bar, pol);
+                    } else {
+                        mbar_arrive(bar);
+                    }
+                }
+                // vectors that the row shares with others: lanes 0-7 the first, 8-15 the last
+                const int v = edge_vector(in, lane), i = lane & 7;
+                if (v >= 0 && i < VE) {
+                    const int j = in.first + v * VE + i;
+                    T* to = reinterpret_cast<T*>(buf) + v * VE + i;
+                    if (j >= 0 && j < a.p.V)
+                        *to = row[j];
+                    else
+                        VT::store1(to, 0, -INFINITY);
+                }
+                if (OP == kRowDistill) top_list<T>(a, r, row, lists + static_cast<size_t>(k) * a.K, in, lane);
+            } else if (lane == 0) {
+                mbar_arrive(bar);
+            }
+            if (lane == 0) info[k] = in;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            filled |= 1u << k;
+            if (++k == NB) {
+                k = 0;
+                phase ^= 1u;
+            }
+        }
+        // the last copy into each buffer has landed (where every row was taken, it has)
+        for (int i = 0; i < NB; ++i)
+            if ((filled >> i) & 1u)
+                (void)mbar_wait_bounded(smem_u32(&full[i]), (i < k ? phase : phase ^ 1u) ^ 1u, a.timeout_ns);
+    } else {
+        // ---------------------------------------------------------- consumers
+        float scale = a.scale;
+        bool have_scale = OP == kRowLogp || a.reduction != kRedMean;
+        int k = 0, turn = 0;                // buffer; which of the two exchange slots
+        uint32_t phase = 0, met_phase = 0;  // bit i of met_phase: parity of met[i]'s next completion
+        uint32_t together_phase = 0;        // bit i: parity of together[i]'s next completion
+        uint32_t meeting_phase = 0, ready_phase = 0;
+        const float2 c2 = make_float2(a.c, a.c);
+        for (int64_t r = first; r < a.p.rows; r += step) {
+            if (!wait(&full[k], phase)) break;
+            const int kb = k;
+            if (++k == NB) {
+                k = 0;
+                phase ^= 1u;
+            }
+            const RowInfo& in = info[kb];
+            const int n = in.n, w0 = in.w0, w1 = in.w1, slice0 = in.first, t = in.t;
+            T* drow = a.p.dx ? reinterpret_cast<T*>(a.p.dx) + in.at : nullptr;
+            uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
+            auto release = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&empty[kb]));
+            };
+            if (t < 0) {  // exact +0, and the row is not read
+                if (drow) {
+                    for (int v = w0 + tid; v < w1; v += NT) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
+                    const int v = edge_vector(in, lane), j = slice0 + v * VE + (lane & 7);
+                    if (warp == NW - 1 && v >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V)
+                        VT::store1(drow, j, 0.f);
+                }
+                if (rank == 0 && tid == 0) {
+                    if (in.bad) atomicOr(a.status, kDevErrTarget);
+                    if (OP != kRowLogp && a.reduction == kRedNone) a.loss[r] = 0.f;
+                    if (OP != kRowDistill) {
+                        if (a.logp) a.logp[r] = 0.f;
+                        if (a.entropy) a.entropy[r] = 0.f;
+                        if (a.kl_out) a.kl_out[r] = 0.f;
+                        if (a.clipped) a.clipped[r] = 0;
+                    }
+                }
+                release();
+                continue;
+            }
+            unsigned char* buf = smem + static_cast<size_t>(kb) * a.buf_bytes;
+            const uint4* vec = reinterpret_cast<const uint4*>(buf);
+            const Entry* ent = lists + static_cast<size_t>(kb) * a.K;
+            auto meet = [&]() {  // all consumer warps
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&meeting));
+                const uint32_t p = meeting_phase;
+                meeting_phase ^= 1u;
+                return wait(&meeting, p);
+            };
+            if (tail) {
+                // the classes of the list leave the row: the sum is that of the others
+                for (int e = tid; e < a.K; e += NT) {
+                    const int j = ent[e].j - slice0;
+                    if (ent[e].j >= 0 && j >= 0 && j < n * VE) VT::store1(buf, j, -INFINITY);
+                }
+                fence_proxy_async();  // (a copy will land there)
+                if (!meet()) break;
+            }
+            // ---- statistics of the slice
+            RowPart st = {-INFINITY, 0.f, 0.f, -INFINITY};
+            {
+                float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
+                const float2 cl2 = make_float2(a.c_low, a.c_low);
+                auto add = [&](const uint4(&q)[U]) {
+                    typename VT::MaxAcc acc = VT::max_init();
+#pragma unroll
+                    for (int u = 0; u < U; ++u) acc = VT::max_fold(acc, q[u]);
+                    const float top = VT::max_value(acc);
+                    if (top > st.m) {
+                        const float d = fmaxf((st.m - top) * a.c, -256.f), f = ex2(d);
+                        if (ENT) q2 = fmul2(ffma2(make_float2(d, d), s2, q2), make_float2(f, f));
+                        s2 = fmul2(s2, make_float2(f, f));
+                        st.m = top;
+                    }
+                    const float base = st.m == -INFINITY ? 0.f : st.m;
+                    const float2 b2 = make_float2(-base, -base);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float f[VE];
+                        VT::unpack(q[u], f);
+#pragma unroll
+                        for (int i = 0; i < VE; i += 2) {
+                            const float2 d = fadd2(make_float2(f[i], f[i + 1]), b2);
+                            const float2 g = ffma2(d, c2, fmul2(d, cl2));
+                            const float2 e = make_float2(ex2(g.x), ex2(g.y));
+                            s2 = fadd2(s2, e);
+                            if (ENT)
+                                q2 = ffma2(e, make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), q2);
+                        }
+                    }
+                };
+                int v = tid;
+                uint4 q[U];
+                for (; v + (U - 1) * NT < n; v += NT * U) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
+                    add(q);
+                }
+                if (v < n) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) q[u] = v + u * NT < n ? vec[v + u * NT] : lowest4<T>();
+                    add(q);
+                }
+                st.S = s2.x + s2.y;
+                st.Q = q2.x + q2.y;
+            }
+            __syncwarp();
+            part_warp<ENT, false>(st, a.c);
+            if (NW > 1) {
+                if (lane == 0) red[kb][warp] = st;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&together[kb]));
+            }
+            // ---- warp 0: the row's statistics, its outputs, and its gradient's constants
+            RowConst k_;
+            if (warp == 0) {
+                if (NW > 1) {
+                    if (!wait(&together[kb], (together_phase >> kb) & 1u)) break;
+                    st = lane < NW ? red[kb][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+                    part_warp<ENT, false>(st, a.c);
+                }
+                const int tj = t - slice0;  // the token's place in the slice
+                if (OP != kRowDistill && tj >= 0 && tj < n * VE) st.x = VT::load1(buf, tj);
+                if (C > 1) {
+                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[turn]), 16u * C);
+                    __syncwarp();
+                    if (lane < C)
+                        st_async_v4(map_to_rank(smem_u32(&parts[turn][rank]), lane), st,
+                                    map_to_rank(smem_u32(&met[turn]), lane));
+                    if (timed_out(mbar_wait_cluster(smem_u32(&met[turn]), (met_phase >> turn) & 1u,
+                                                    a.timeout_ns)))
+                        break;
+                    met_phase ^= 1u << turn;
+                    st = lane < C ? parts[turn][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+                    part_warp<ENT, OP != kRowDistill>(st, a.c);
+                    turn ^= 1;
+                }
+                if (!have_scale && a.p.dx) {
+                    pdl_wait();
+                    scale = static_cast<float>(static_cast<double>(a.scale) / __ldcg(a.D));
+                    have_scale = true;
+                }
+                const float weight = in.weight;
+                float loss = 0.f;
+                k_.m = st.m;
+                if (OP == kRowDistill) {
+                    float S = st.S, left = st.S;
+                    if (tail) {
+                        // both sums by the row's maximum, that of the list included
+                        k_.m = fmaxf(st.m, in.top);
+                        part_raise(st, k_.m, a.c, false);
+                        left = st.S;
+                        float listed = 0.f;
+                        for (int e = lane; e < a.K; e += 32)
+                            if (ent[e].j >= 0) listed += ex2((ent[e].x - k_.m) * a.c);
+                        S = left + warp_sum(listed);
+                    }
+                    const float logS = logf(S), rest = in.rest;
+                    if (rank == 0) {
+                        for (int e = lane; e < a.K; e += 32)
+                            if (ent[e].q != 0.f)
+                                loss += ent[e].q * (ent[e].lq - log_prob(a, ent[e].x, k_.m, logS));
+                        loss = warp_sum(loss);
+                        if (tail && rest > 0.f && left > 0.f) loss += rest * (logf(rest) - (logf(left) - logS));
+                    }
+                    const float f = scale * weight * a.invT, mass = in.mass + rest;
+                    const float cut = tail && left > 0.f ? rest * (S / left) : 0.f;
+                    k_.u0 = f * (mass - cut) / S;
+                    k_.u1 = f * mass / S;  // (of a listed class, less f q)
+                    k_.x = f;
+                } else {
+                    const float logS = logf(st.S);
+                    const float lp = log_prob(a, st.x, st.m, logS);
+                    const float H = ENT ? fmaf(-kLn2, st.Q / st.S, logS) : 0.f;
+                    if (rank == 0 && lane == 0) {
+                        if (a.logp) a.logp[r] = lp;
+                        if (a.entropy) a.entropy[r] = H;
+                        if (a.kept) a.kept[r] = RowKept{st.m, st.S, H, lp};
+                    }
+                    if (OP == kRowPolicy) {
+                        const PolicyRow pr = policy_row(a, lp, in.adv, in.old, in.ref);
+                        loss = ENT ? fmaf(-a.ent, H, pr.loss) : pr.loss;
+                        if (rank == 0 && lane == 0) {
+                            if (a.kl_out) a.kl_out[r] = pr.kl;
+                            if (a.clipped) a.clipped[r] = pr.clipped ? 1 : 0;
+                        }
+                        // g_j = 2^a_j (u0 + u1 a_j), plus the slope at the token
+                        const float f = scale * weight * a.invT, slope = pr.slope * f, k1 = a.ent * f;
+                        k_.u0 = (ENT ? fmaf(k1, H - logS, -slope) : -slope) / st.S;
+                        k_.u1 = ENT ? k1 * kLn2 / st.S : 0.f;
+                        k_.x = slope;
+                    }
+                }
+                if (OP != kRowLogp && rank == 0 && lane == 0) {
+                    if (a.reduction == kRedNone)
+                        a.loss[r] = a.scale * weight * loss;
+                    else
+                        sum += static_cast<double>(weight) * static_cast<double>(loss);
+                }
+                if (OP != kRowLogp && NW > 1) {
+                    if (lane == 0) {
+                        consts[kb] = k_;
+                        mbar_arrive(smem_u32(&ready));
+                    }
+                }
+            }
+            together_phase ^= 1u << kb;
+            if (OP == kRowLogp) {
+                release();
+                continue;
+            }
+            if (NW > 1) {
+                if (warp != 0) {
+                    if (!wait(&ready, ready_phase)) break;
+                    k_ = consts[kb];
+                }
+                ready_phase ^= 1u;
+            }
+            // ---- the slice's gradient
+            if (drow) {
+                const float m = k_.m, u0 = k_.u0, u1 = k_.u1;
+                const float2 b2 = make_float2(-m, -m), uu0 = make_float2(u0, u0), uu1 = make_float2(u1, u1);
+                auto grad = [&](const uint4& q) {
+                    float f[VE];
+                    VT::unpack(q, f);
+#pragma unroll
+                    for (int i = 0; i < VE; i += 2) {
+                        const float2 g = fmul2(fadd2(make_float2(f[i], f[i + 1]), b2), c2);
+                        const float2 e = make_float2(ex2(g.x), ex2(g.y));
+                        const float2 w =
+                            ENT ? ffma2(uu1, make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), uu0) : uu0;
+                        const float2 o = fmul2(e, w);
+                        f[i] = o.x;
+                        f[i + 1] = o.y;
+                    }
+                    return VT::pack(f);
+                };
+                int v = w0 + tid;
+                for (; v + (U - 1) * NT < w1; v += NT * U) {
+                    uint4 q[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) dvec[v + u * NT] = grad(q[u]);
+                }
+                for (; v < w1; v += NT) dvec[v] = grad(vec[v]);
+                auto element = [&](float x) {
+                    const float g = (x - m) * a.c;
+                    return ex2(g) * (ENT ? fmaf(u1, fmaxf(g, -256.f), u0) : u0);
+                };
+                if (warp == NW - 1) {  // the vectors that the row shares with others
+                    const int ev = edge_vector(in, lane), i = ev * VE + (lane & 7), j = slice0 + i;
+                    if (ev >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V) {
+                        const float g = element(VT::load1(buf, i));
+                        VT::store1(drow, j, OP == kRowPolicy && j == t ? g + k_.x : g);
+                    }
+                }
+                if (OP == kRowPolicy) {
+                    // the token's element again, by the thread that stored its vector
+                    const int i = t - slice0, tv = i >= 0 ? i / VE : -1;
+                    if (tv >= w0 && tv < w1 && (tv - w0) % NT == tid)
+                        VT::store1(drow, t, element(VT::load1(buf, i)) + k_.x);
+                }
+                if (OP == kRowDistill) {
+                    if (NW > 1) {
+                        if (!meet()) break;  // the listed classes', after every thread's stores
+                    } else {
+                        __syncwarp();
+                    }
+                    for (int e = tid; e < a.K; e += NT) {
+                        const int j = ent[e].j;
+                        if (j >= 0 && j >= slice0 && j - slice0 < n * VE)
+                            VT::store1(drow, j,
+                                       fmaf(u1, ex2((ent[e].x - m) * a.c), -k_.x * ent[e].qs));
+                    }
+                }
+            }
+            release();
+        }
+    }
+    if (OP != kRowLogp && a.reduction != kRedNone) {
+        pdl_wait();
+        __syncthreads();
+        if (rank == 0) rows_finish(a, sum, static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
+    }
+    // no CTA leaves while another may still send to it
+    __syncthreads();
+    if (C > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
+}
+
+template <typename T, int OP, bool ENT>
+const void* rows_threads(int nt) {
+    return nt == 32    ? (const void*)&rows_kernel<T, OP, ENT, 32>
+           : nt == 64  ? (const void*)&rows_kernel<T, OP, ENT, 64>
+           : nt == 128 ? (const void*)&rows_kernel<T, OP, ENT, 128>
+                       : (const void*)&rows_kernel<T, OP, ENT, 256>;
+}
+
+template <typename T>
+const void* rows_kernel_of(int op, bool ent, int nt) {
+    if (op == kRowLogp) return ent ? rows_threads<T, kRowLogp, true>(nt) : rows_threads<T, kRowLogp, false>(nt);
+    if (op == kRowPolicy)
+        return ent ? rows_threads<T, kRowPolicy, true>(nt) : rows_threads<T, kRowPolicy, false>(nt);
+    return rows_threads<T, kRowDistill, false>(nt);
+}
+
+}  // namespace gbce

@@ -265,8 +265,10 @@ def _forward_gradient(ctx, logits, call, inplace):
     return out
 
 
-def _scaled_gradient(ctx, d_loss, name, per_row):
-    """The gradient that the forward left, times d_loss."""
+def _scaled_gradient(ctx, d_loss, name):
+    """The gradient that the forward left, times d_loss (one value, or one a row)."""
+    if d_loss is None:
+        return None
     once(name, d_loss)
     (dx,) = ctx.saved_tensors
     if ctx.spent:
@@ -274,7 +276,7 @@ def _scaled_gradient(ctx, d_loss, name, per_row):
     ctx.spent = True
     g, dev = plain(d_loss.float()), dx.device
     with on(dev):
-        check(_lib.ce_rows_scale(_table(dx, dx), ptr(g), per_row, stream(dev)), "ce_rows_scale")
+        check(_lib.ce_rows_scale(_table(dx, dx), ptr(g), 1 if g.dim() else 0, stream(dev)), "ce_rows_scale")
     return dx
 
 
@@ -305,18 +307,17 @@ class PolicyLossFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, tokens, advantages, old, ref, weight, inplace, args):
+        ctx.set_materialize_grads(False)
         out = _forward_gradient(
             ctx, logits,
             lambda dx: _policy(logits, dx, tokens, advantages, args[0], old, ref, weight,
                                *args[1:]), inplace)
         ctx.mark_non_differentiable(*(t for t in out[1:] if t is not None))
-        ctx.per_row = out[0].dim() > 0
         return out
 
     @staticmethod
     def backward(ctx, d_loss, *unused):
-        dx = _scaled_gradient(ctx, d_loss, "policy_loss", 1 if ctx.per_row else 0)
-        return (dx,) + (None,) * 7
+        return (_scaled_gradient(ctx, d_loss, "policy_loss"),) + (None,) * 7
 
 
 def policy_loss(logits, tokens, advantages, old_log_probs=None, ref_log_probs=None, weight=None,
@@ -392,16 +393,15 @@ class DistillationLossFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, teacher, index, teacher_lse, weight, inplace, args):
+        ctx.set_materialize_grads(False)
         loss = _forward_gradient(
             ctx, logits,
             lambda dx: _distill(logits, dx, teacher, index, teacher_lse, weight, *args), inplace)
-        ctx.per_row = loss.dim() > 0
         return loss
 
     @staticmethod
     def backward(ctx, d_loss):
-        dx = _scaled_gradient(ctx, d_loss, "distillation_loss", 1 if ctx.per_row else 0)
-        return (dx,) + (None,) * 6
+        return (_scaled_gradient(ctx, d_loss, "distillation_loss"),) + (None,) * 6
 
 
 def distillation_loss(logits, teacher_logits, teacher_indices, teacher_lse=None, temperature=1.0,
@@ -470,6 +470,7 @@ class PreferenceLossFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, tokens, offsets, ref, inplace, args):
+        ctx.set_materialize_grads(False)
         grad = ctx.needs_input_grad[0]
         loss, scores, dscore, kept = _preference(logits, tokens, offsets, ref, *args, grad)
         if grad:
@@ -480,6 +481,8 @@ class PreferenceLossFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, d_loss, *unused):
+        if d_loss is None:
+            return (None,) * 6
         once("preference_loss", d_loss)
         logits, tokens, offsets, kept, dscore = ctx.saved_tensors
         ignore_index, pairs, inplace = ctx.args
