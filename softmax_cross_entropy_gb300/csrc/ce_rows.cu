@@ -101,14 +101,15 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
     const void* fn = dtype == CE_F32    ? rows_kernel_f32(op, ent, nt)
                      : dtype == CE_BF16 ? rows_kernel_bf16(op, ent, nt)
                                         : rows_kernel_f16(op, ent, nt);
+    const int threads = nt + (op == kRowDistill ? 64 : 32);
     int fit = 0;
-    ce_status rc = clusters_that_fit(fn, C, nt + 32, smem, sms, &fit);
+    ce_status rc = clusters_that_fit(fn, C, threads, smem, sms, &fit);
     if (rc != CE_OK) return rc;
     const int64_t clusters =
         std::max<int64_t>(1, std::min<int64_t>({a.p.rows, int64_t{fit}, int64_t{kRowsMaxCtas}}));
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(clusters * C));
-    lc.blockDim = dim3(static_cast<unsigned>(nt + 32));
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
     lc.dynamicSmemBytes = smem;
     lc.stream = st;
     cudaLaunchAttribute attr[2];

@@ -21,6 +21,8 @@
 // shares with its neighbours are filled element by element.
 #pragma once
 
+#include <type_traits>
+
 #include "ce_rows.cuh"
 
 namespace gbce {
@@ -37,8 +39,12 @@ struct __align__(16) RowInfo {
     int w0, w1;
     int first;   // the class of the slice's first element (below 0 where it is in front of the row)
     float adv, old, ref, weight;
-    float mass, rest, top;  // the list: sum of q, what remains, the largest of its logits
-    int pad;
+};
+
+// What the list's warp leaves: the sum of q, what remains of the teacher's
+// mass, the largest of the list's logits.
+struct __align__(16) ListInfo {
+    float mass, rest, top, pad;
 };
 
 // What every warp needs for the gradient: 2^((x - m) c) (u0 + u1 a), and x at
@@ -49,6 +55,9 @@ struct __align__(16) RowConst {
 
 // CTAs of an SM that a kernel's registers are to leave room for.
 constexpr int rows_ctas(int nt) { return nt == 32 ? 16 : nt == 64 ? 10 : nt == 128 ? 5 : 3; }
+
+// A CTA's threads: the consumers, the producer warp, distillation's list warp.
+constexpr int rows_threads_of(int op, int nt) { return nt + (op == kRowDistill ? 64 : 32); }
 
 // Of lanes 0-7 the vector that the row's start shares with what is before it,
 // of lanes 8-15 the one that its end shares; -1: there is none.
@@ -91,6 +100,10 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 template <typename T>
 struct Lowest;  // a vector of -inf
 template <>
@@ -111,11 +124,193 @@ __device__ __forceinline__ uint4 lowest4() {
 }
 
 
-// A warp forms row r's list: the teacher's softmax, its classes' logits, and
-// which entry stands for a class that is named more than once.
+// Logits beyond this (masks of a type's lowest value, mostly) take the
+// careful forms below: times log2(e) / T they could overflow.
+constexpr float kFarLogit = 1e18f;
+
+// Products with an element's argument where 2^argument is 0: the logits are
+// cut at -1e30 (bf16 pairs in one instruction), or, where -inf is not far from
+// the type's other values, the arguments at -256.
 template <typename T>
-__device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* row, Entry* ent, RowInfo& in,
-                                         int lane) {
+constexpr bool kCutLogits = !std::is_same<T, __half>::value;
+
+template <typename T>
+__device__ __forceinline__ uint4 at_least(const uint4& q) {
+    uint4 o;
+    const uint32_t* w = &q.x;
+    uint32_t* z = &o.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            float m;  // (a NaN stays)
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(w[i])), "f"(-1e30f));
+            z[i] = __float_as_uint(m);
+        } else {
+            const __nv_bfloat16 low = __ushort_as_bfloat16(0xF149u);
+            const __nv_bfloat162 v =
+                __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), __halves2bfloat162(low, low));
+            z[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    return o;
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void unpack_cut(const uint4& q, float (&f)[Vec<T>::N]) {
+    if constexpr (ENT && kCutLogits<T>)
+        Vec<T>::unpack(at_least<T>(q), f);
+    else
+        Vec<T>::unpack(q, f);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 cut_argument(float2 g) {
+    return kCutLogits<T> ? g : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f));
+}
+
+// The careful form of a thread's statistics: a running maximum, differences
+// before products.
+template <typename T, bool ENT, int NT>
+__device__ __noinline__ RowPart slice_stats_careful(const uint4* vec, int n, int tid, float c, float c_low) {
+    using VT = Vec<T>;
+    RowPart st = {-INFINITY, 0.f, 0.f, -INFINITY};
+    for (int v = tid; v < n; v += NT) {
+        const uint4 q = vec[v];
+        const float top = VT::max_value(VT::max_fold(VT::max_init(), q));
+        if (top > st.m) part_raise(st, top, c, ENT);
+        const float base = st.m == -INFINITY ? 0.f : st.m;
+        float f[VT::N];
+        VT::unpack(q, f);
+#pragma unroll
+        for (int i = 0; i < VT::N; ++i) {
+            const float d = f[i] - base, g = fmaf(d, c, d * c_low), e = ex2(g);
+            st.S += e;
+            if (ENT) st.Q = fmaf(e, fmaxf(g, -256.f), st.Q);
+        }
+    }
+    return st;
+}
+
+// A thread's statistics of a slice. The reference need not be the maximum,
+// only near it, so the largest of the thread's first vectors serves for all:
+// one that lies far above it shows in a sum of 2^100 or more, and the careful
+// form follows. 2^(x c - B), B = m c rounded, is one product and sum an element
+// (the product is exact before the sum is rounded); what B's rounding and c's
+// take from the result is put right once: B's by the factor 2^-(m c - B), c's
+// (c_low d = (c_low / c) a, a the argument) by an element's second product or,
+// where Q = sum 2^a a is formed anyway, by S + ln 2 (c_low / c) Q.
+template <typename T, bool ENT, int NT, int U>
+__device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid, float c, float c_low) {
+    using VT = Vec<T>;
+    constexpr int VE = VT::N;
+    RowPart st = {-INFINITY, 0.f, 0.f, -INFINITY};
+    if (tid >= n) return st;
+    uint4 q[U];
+    auto load = [&](int v) {
+        if (v + (U - 1) * NT < n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = v + u * NT < n ? vec[v + u * NT] : lowest4<T>();
+        }
+    };
+    load(tid);
+    typename VT::MaxAcc acc = VT::max_init();
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = VT::max_fold(acc, q[u]);
+    st.m = VT::max_value(acc);
+    if (fabsf(st.m) < kFarLogit) {
+        const float B = st.m * c;
+        const float rho = c_low / c;
+        const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), rho2 = make_float2(rho, rho);
+        float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
+        for (int v = tid;;) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[VE];
+                unpack_cut<T, ENT>(q[u], f);
+#pragma unroll
+                for (int i = 0; i < VE; i += 2) {
+                    float2 g = ffma2(make_float2(f[i], f[i + 1]), c2, nb2);
+                    if (!ENT) g = ffma2(g, rho2, g);
+                    const float2 e = make_float2(ex2(g.x), ex2(g.y));
+                    s2 = fadd2(s2, e);
+                    if (ENT) q2 = ffma2(e, cut_argument<T>(g), q2);
+                }
+            }
+            v += NT * U;
+            if (v >= n) break;
+            load(v);
+        }
+        st.S = s2.x + s2.y;
+        st.Q = q2.x + q2.y;
+        const float delta = fmaf(st.m, c, -B);
+        if (ENT) {
+            st.S = fmaf(kLn2 * rho, st.Q, st.S);
+            st.Q = fmaf(-delta, st.S, st.Q);
+            st.Q = fmaf(-kLn2 * delta, st.Q, st.Q);
+        }
+        st.S = fmaf(-kLn2 * delta, st.S, st.S);
+        if (st.S < 1.2676506e30f) return st;  // (2^100; not NaN)
+    }
+    return slice_stats_careful<T, ENT, NT>(vec, n, tid, c, c_low);
+}
+
+// A thread's part of a slice's gradient, 2^a (u0 + u1 a) with a = (x - m) c;
+// NEAR: a as x c - B, B = m c rounded, whose error goes into u0 and u1.
+template <typename T, bool ENT, int NT, int U, bool NEAR>
+__device__ __forceinline__ void slice_gradient(const uint4* vec, uint4* dvec, int w0, int w1, int tid, float c,
+                                               float m, float u0, float u1) {
+    using VT = Vec<T>;
+    constexpr int VE = VT::N;
+    const float B = m * c;
+    if (NEAR) {
+        const float delta = fmaf(m, c, -B);
+        u0 = fmaf(-delta, u1, u0);
+        u0 = fmaf(-kLn2 * delta, u0, u0);
+        u1 = fmaf(-kLn2 * delta, u1, u1);
+    }
+    const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), nm2 = make_float2(-m, -m);
+    const float2 uu0 = make_float2(u0, u0), uu1 = make_float2(u1, u1);
+    auto grad = [&](const uint4& q) {
+        float f[VE];
+        unpack_cut<T, ENT && NEAR>(q, f);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+            const float2 x = make_float2(f[i], f[i + 1]);
+            const float2 g = NEAR ? ffma2(x, c2, nb2) : fmul2(fadd2(x, nm2), c2);
+            const float2 e = make_float2(ex2(g.x), ex2(g.y));
+            float2 w = uu0;
+            if (ENT) w = ffma2(uu1, NEAR ? cut_argument<T>(g) : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), uu0);
+            const float2 o = fmul2(e, w);
+            f[i] = o.x;
+            f[i + 1] = o.y;
+        }
+        return VT::pack(f);
+    };
+    int v = w0 + tid;
+    if (NEAR) {
+        for (; v + (U - 1) * NT < w1; v += NT * U) {
+            uint4 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) dvec[v + u * NT] = grad(q[u]);
+        }
+    }
+#pragma unroll 1
+    for (; v < w1; v += NT) dvec[v] = grad(vec[v]);
+}
+
+constexpr int kSeenWords = 256;  // of a table of the classes seen: a bit a hash value
+
+// A warp forms row r's list: the teacher's softmax, its classes' logits, and
+// which entry stands for a class that is named more than once. seen: two
+// tables of kSeenWords words, zero between calls.
+template <typename T>
+__device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* row, Entry* ent,
+                                         uint32_t* seen, ListInfo& out, int lane) {
     float top_v = -INFINITY, top_x = -INFINITY;
     for (int e = lane; e < a.K; e += 32) {
         const int64_t w = r * a.K + e;
@@ -135,29 +330,47 @@ __device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* r
     __syncwarp();
     const bool tail = a.teacher_lse != nullptr;
     const float shift = tail ? __ldg(a.teacher_lse + r) : warp_max_f32(top_v) * a.invT;
-    in.top = warp_max_f32(top_x);
+    out.top = warp_max_f32(top_x);
     double mass = 0.0;
+    bool twice = false;
     for (int e = lane; e < a.K; e += 32) {
         const float2 l = scaled_minus(a, ent[e].lq, shift);
-        const float q = ent[e].j < 0 ? 0.f : expf(l.x);
+        const int j = ent[e].j;
+        const float q = j < 0 ? 0.f : expf(l.x);
         ent[e].lq = l.x;
-        ent[e].q = fmaf(q, l.y, q);
-        mass += ent[e].q;
+        const float q1 = fmaf(q, l.y, q);
+        ent[e].q = q1;
+        mass += q1;
+        if (j >= 0) {
+            // seen before by two hashes: most likely the same class
+            const uint32_t h = static_cast<uint32_t>(j), g = h * 2654435761u >> 19;
+            const uint32_t b0 = 1u << (h & 31u), b1 = 1u << (g & 31u);
+            const uint32_t o0 = atomicOr(&seen[(h >> 5) & (kSeenWords - 1)], b0);
+            const uint32_t o1 = atomicOr(&seen[kSeenWords + (g >> 5)], b1);
+            twice = twice || ((o0 & b0) && (o1 & b1));
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    in.mass = static_cast<float>(mass);
-    if (tail) {
-        in.rest = static_cast<float>(fmax(0.0, 1.0 - mass));
-    } else {
-        const float lm = logf(in.mass), im = 1.f / in.mass;
-        for (int e = lane; e < a.K; e += 32) {
-            ent[e].q *= im;
-            ent[e].lq -= lm;
+    out.mass = static_cast<float>(mass);
+    out.rest = tail ? static_cast<float>(fmax(0.0, 1.0 - mass)) : 0.f;
+    const float lm = tail ? 0.f : logf(out.mass), im = tail ? 1.f : 1.f / out.mass;
+    if (!tail) out.mass = 1.f;
+    twice = __any_sync(0xffffffffu, twice);
+    for (int e = lane; e < a.K; e += 32) {
+        const float q = ent[e].q * im;
+        ent[e].q = q;
+        ent[e].qs = q;
+        ent[e].lq -= lm;
+        const int j = ent[e].j;
+        if (j >= 0) {
+            const uint32_t h = static_cast<uint32_t>(j), g = h * 2654435761u >> 19;
+            seen[(h >> 5) & (kSeenWords - 1)] = 0u;
+            seen[kSeenWords + (g >> 5)] = 0u;
         }
-        in.mass = 1.f;
     }
     __syncwarp();
+    if (!twice) return;
     for (int e = lane; e < a.K; e += 32) {
         const int j = ent[e].j;
         float qs = 0.f;
@@ -173,10 +386,12 @@ __device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* r
     __syncwarp();
     for (int e = lane; e < a.K; e += 32)
         if (ent[e].qs < 0.f) ent[e].j = -1;
+    __syncwarp();
 }
 
 template <typename T, int OP, bool ENT, int NT>
-__global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(rows_threads_of(OP, NT), rows_ctas(NT))
+rows_kernel(const __grid_constant__ RowArgs a) {
     using VT = Vec<T>;
     constexpr int VE = VT::N;
     constexpr int NW = NT / 32;
@@ -188,7 +403,9 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
     __shared__ RowPart red[kMaxBuf][NW];          // of the warps
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
-    __shared__ double red_d[NW + 1];
+    __shared__ ListInfo linfo[OP == kRowDistill ? kMaxBuf : 1];
+    __shared__ uint32_t seen[OP == kRowDistill ? 2 * kSeenWords : 1];
+    __shared__ double red_d[NW + 2];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -203,7 +420,7 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
     if (OP == kRowLogp && a.ticket && blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
     if (tid == 0) {
         for (int i = 0; i < NB; ++i) {
-            mbar_init(smem_u32(&full[i]), 2);
+            mbar_init(smem_u32(&full[i]), OP == kRowDistill ? 3 : 2);
             mbar_init(smem_u32(&empty[i]), NW);
             mbar_init(smem_u32(&together[i]), NW);
         }
@@ -213,6 +430,8 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
         mbar_init(smem_u32(&ready), 1);
         fence_mbar_init();
     }
+    if (OP == kRowDistill)
+        for (int i = tid; i < 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
     __syncthreads();
     if (C > 1) cluster_sync();
 
@@ -298,7 +517,6 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
                     else
                         VT::store1(to, 0, -INFINITY);
                 }
-                if (OP == kRowDistill) top_list<T>(a, r, row, lists + static_cast<size_t>(k) * a.K, in, lane);
             } else if (lane == 0) {
                 mbar_arrive(bar);
             }
@@ -315,6 +533,35 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
         for (int i = 0; i < NB; ++i)
             if ((filled >> i) & 1u)
                 (void)mbar_wait_bounded(smem_u32(&full[i]), (i < k ? phase : phase ^ 1u) ^ 1u, a.timeout_ns);
+    } else if (warp > NW) {
+        // ---------------------------------------------------------- distillation: the lists
+        int k = 0;
+        uint32_t phase = 1;
+        int64_t t_next = first < a.p.rows ? load_index(a.index, a.idx64, first * a.K) : 0;
+        for (int64_t r = first; r < a.p.rows; r += step) {
+            const int64_t t = t_next;
+            if (r + step < a.p.rows) {
+                t_next = load_index(a.index, a.idx64, (r + step) * a.K);
+                // the next row's list on its way to L2
+                for (int e = lane; e < a.K; e += 32) {
+                    const int64_t w = (r + step) * a.K + e;
+                    prefetch_l2(static_cast<const char*>(a.index) + w * (a.idx64 ? 8 : 4));
+                    prefetch_l2(static_cast<const char*>(a.teacher) + w * (a.teacher_dtype == 0 ? 4 : 2));
+                }
+            }
+            if (!wait(&empty[k], phase)) break;
+            if (t >= 0 && t < a.p.V) {
+                ListInfo li = {};
+                top_list<T>(a, r, X + a.p.at(r), lists + static_cast<size_t>(k) * a.K, seen, li, lane);
+                if (lane == 0) linfo[k] = li;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[k]));
+            if (++k == NB) {
+                k = 0;
+                phase ^= 1u;
+            }
+        }
     } else {
         // ---------------------------------------------------------- consumers
         float scale = a.scale;
@@ -323,7 +570,6 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
         uint32_t phase = 0, met_phase = 0;  // bit i of met_phase: parity of met[i]'s next completion
         uint32_t together_phase = 0;        // bit i: parity of together[i]'s next completion
         uint32_t meeting_phase = 0, ready_phase = 0;
-        const float2 c2 = make_float2(a.c, a.c);
         for (int64_t r = first; r < a.p.rows; r += step) {
             if (!wait(&full[k], phase)) break;
             const int kb = k;
@@ -379,53 +625,7 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
                 if (!meet()) break;
             }
             // ---- statistics of the slice
-            RowPart st = {-INFINITY, 0.f, 0.f, -INFINITY};
-            {
-                float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
-                const float2 cl2 = make_float2(a.c_low, a.c_low);
-                auto add = [&](const uint4(&q)[U]) {
-                    typename VT::MaxAcc acc = VT::max_init();
-#pragma unroll
-                    for (int u = 0; u < U; ++u) acc = VT::max_fold(acc, q[u]);
-                    const float top = VT::max_value(acc);
-                    if (top > st.m) {
-                        const float d = fmaxf((st.m - top) * a.c, -256.f), f = ex2(d);
-                        if (ENT) q2 = fmul2(ffma2(make_float2(d, d), s2, q2), make_float2(f, f));
-                        s2 = fmul2(s2, make_float2(f, f));
-                        st.m = top;
-                    }
-                    const float base = st.m == -INFINITY ? 0.f : st.m;
-                    const float2 b2 = make_float2(-base, -base);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float f[VE];
-                        VT::unpack(q[u], f);
-#pragma unroll
-                        for (int i = 0; i < VE; i += 2) {
-                            const float2 d = fadd2(make_float2(f[i], f[i + 1]), b2);
-                            const float2 g = ffma2(d, c2, fmul2(d, cl2));
-                            const float2 e = make_float2(ex2(g.x), ex2(g.y));
-                            s2 = fadd2(s2, e);
-                            if (ENT)
-                                q2 = ffma2(e, make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), q2);
-                        }
-                    }
-                };
-                int v = tid;
-                uint4 q[U];
-                for (; v + (U - 1) * NT < n; v += NT * U) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
-                    add(q);
-                }
-                if (v < n) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) q[u] = v + u * NT < n ? vec[v + u * NT] : lowest4<T>();
-                    add(q);
-                }
-                st.S = s2.x + s2.y;
-                st.Q = q2.x + q2.y;
-            }
+            RowPart st = slice_stats<T, ENT, NT, U>(vec, n, tid, a.c, a.c_low);
             __syncwarp();
             part_warp<ENT, false>(st, a.c);
             if (NW > 1) {
@@ -469,7 +669,7 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
                     float S = st.S, left = st.S;
                     if (tail) {
                         // both sums by the row's maximum, that of the list included
-                        k_.m = fmaxf(st.m, in.top);
+                        k_.m = fmaxf(st.m, linfo[kb].top);
                         part_raise(st, k_.m, a.c, false);
                         left = st.S;
                         float listed = 0.f;
@@ -477,7 +677,7 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
                             if (ent[e].j >= 0) listed += ex2((ent[e].x - k_.m) * a.c);
                         S = left + warp_sum(listed);
                     }
-                    const float logS = logf(S), rest = in.rest;
+                    const float logS = logf(S), rest = linfo[kb].rest;
                     if (rank == 0) {
                         for (int e = lane; e < a.K; e += 32)
                             if (ent[e].q != 0.f)
@@ -485,7 +685,7 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
                         loss = warp_sum(loss);
                         if (tail && rest > 0.f && left > 0.f) loss += rest * (logf(rest) - (logf(left) - logS));
                     }
-                    const float f = scale * weight * a.invT, mass = in.mass + rest;
+                    const float f = scale * weight * a.invT, mass = linfo[kb].mass + rest;
                     const float cut = tail && left > 0.f ? rest * (S / left) : 0.f;
                     k_.u0 = f * (mass - cut) / S;
                     k_.u1 = f * mass / S;  // (of a listed class, less f q)
@@ -541,31 +741,10 @@ __global__ void __launch_bounds__(NT + 32, rows_ctas(NT)) rows_kernel(const __gr
             // ---- the slice's gradient
             if (drow) {
                 const float m = k_.m, u0 = k_.u0, u1 = k_.u1;
-                const float2 b2 = make_float2(-m, -m), uu0 = make_float2(u0, u0), uu1 = make_float2(u1, u1);
-                auto grad = [&](const uint4& q) {
-                    float f[VE];
-                    VT::unpack(q, f);
-#pragma unroll
-                    for (int i = 0; i < VE; i += 2) {
-                        const float2 g = fmul2(fadd2(make_float2(f[i], f[i + 1]), b2), c2);
-                        const float2 e = make_float2(ex2(g.x), ex2(g.y));
-                        const float2 w =
-                            ENT ? ffma2(uu1, make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), uu0) : uu0;
-                        const float2 o = fmul2(e, w);
-                        f[i] = o.x;
-                        f[i + 1] = o.y;
-                    }
-                    return VT::pack(f);
-                };
-                int v = w0 + tid;
-                for (; v + (U - 1) * NT < w1; v += NT * U) {
-                    uint4 q[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) dvec[v + u * NT] = grad(q[u]);
-                }
-                for (; v < w1; v += NT) dvec[v] = grad(vec[v]);
+                if (fabsf(m) < kFarLogit)
+                    slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, m, u0, u1);
+                else
+                    slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, m, u0, u1);
                 auto element = [&](float x) {
                     const float g = (x - m) * a.c;
                     return ex2(g) * (ENT ? fmaf(u1, fmaxf(g, -256.f), u0) : u0);
