@@ -54,10 +54,11 @@ struct __align__(16) RowConst {
 };
 
 // CTAs of an SM that a kernel's registers are to leave room for.
-constexpr int rows_ctas(int nt) { return nt == 32 ? 16 : nt == 64 ? 10 : nt == 128 ? 5 : 3; }
+constexpr int rows_ctas(int nt) { return nt == 32 ? 10 : nt == 64 ? 7 : nt == 128 ? 4 : 2; }
 
-// A CTA's threads: the consumers, the producer warp, distillation's list warp.
-constexpr int rows_threads_of(int op, int nt) { return nt + (op == kRowDistill ? 64 : 32); }
+// A CTA's threads: the consumers, the producer warp, the warp that brings a
+// row's statistics together, distillation's list warp.
+constexpr int rows_threads_of(int op, int nt) { return nt + (op == kRowDistill ? 96 : 64); }
 
 // Of lanes 0-7 the vector that the row's start shares with what is before it,
 // of lanes 8-15 the one that its end shares; -1: there is none.
@@ -397,15 +398,17 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     constexpr int NW = NT / 32;
     constexpr int U = 4;  // vectors a thread takes at once
     extern __shared__ __align__(128) unsigned char smem[];  // buffers, then the lists
-    __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], met[2], meeting,
-        ready;
+    // a buffer's mbarriers: filled; given back; its row's statistics are all
+    // there; its row's constants are there
+    __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], ready[kMaxBuf];
+    __shared__ __align__(8) uint64_t met[2], meeting;
     __shared__ RowPart parts[2][kMaxRowCluster];  // of the cluster's CTAs, two rows in turn
     __shared__ RowPart red[kMaxBuf][NW];          // of the warps
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
     __shared__ ListInfo linfo[OP == kRowDistill ? kMaxBuf : 1];
     __shared__ uint32_t seen[OP == kRowDistill ? 2 * kSeenWords : 1];
-    __shared__ double red_d[NW + 2];
+    __shared__ double s_sum, red_d[NW + 3];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -417,18 +420,20 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     const int NB = a.nbuf;
     Entry* lists = reinterpret_cast<Entry*>(smem + static_cast<size_t>(NB) * a.buf_bytes);
     const bool tail = OP == kRowDistill && a.teacher_lse != nullptr;
+    const bool two = OP != kRowLogp && a.p.dx != nullptr;  // a second pass forms the gradient
     if (OP == kRowLogp && a.ticket && blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
     if (tid == 0) {
         for (int i = 0; i < NB; ++i) {
             mbar_init(smem_u32(&full[i]), OP == kRowDistill ? 3 : 2);
-            mbar_init(smem_u32(&empty[i]), NW);
+            mbar_init(smem_u32(&empty[i]), two ? NW : NW + 1);
             mbar_init(smem_u32(&together[i]), NW);
+            mbar_init(smem_u32(&ready[i]), 1);
         }
         mbar_init(smem_u32(&met[0]), 1);
         mbar_init(smem_u32(&met[1]), 1);
         mbar_init(smem_u32(&meeting), NW);
-        mbar_init(smem_u32(&ready), 1);
         fence_mbar_init();
+        s_sum = 0.0;
     }
     if (OP == kRowDistill)
         for (int i = tid; i < 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
@@ -445,8 +450,19 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return !timed_out(mbar_wait_bounded(smem_u32(bar), parity, a.timeout_ns));
     };
-    double sum = 0.0;
+    auto arrive = [&](uint64_t* bar) {  // once a warp, after all that its lanes did
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(bar));
+    };
     const T* X = reinterpret_cast<const T*>(a.p.x);
+    int k = 0;           // the next row's buffer
+    uint32_t phase = 0;  // how often the ring came round, modulo 2
+    auto next = [&]() {
+        if (++k == NB) {
+            k = 0;
+            phase ^= 1u;
+        }
+    };
 
     if (warp == NW) {
         // ---------------------------------------------------------- producer
@@ -455,8 +471,6 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             return OP == kRowDistill ? load_index(a.index, a.idx64, r * a.K)
                                      : load_index(a.tokens, a.tok64, r);
         };
-        int k = 0;
-        uint32_t phase = 1;   // of `empty`: the buffers are free at first
         uint32_t filled = 0;  // bit i: buffer i has been filled
         int64_t t_next = first < a.p.rows ? token(first) : 0;
         for (int64_t r = first; r < a.p.rows; r += step) {
@@ -489,7 +503,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 in.w1 = max(min(end / VE - lo, in.n), in.w0);
                 in.first = lo * VE - off;
             }
-            if (!wait(&empty[k], phase)) break;
+            if (!wait(&empty[k], phase ^ 1u)) break;
             const uint32_t bar = smem_u32(&full[k]);
             unsigned char* buf = smem + static_cast<size_t>(k) * a.buf_bytes;
             if (counts) {
@@ -521,22 +535,16 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 mbar_arrive(bar);
             }
             if (lane == 0) info[k] = in;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
+            arrive(&full[k]);
             filled |= 1u << k;
-            if (++k == NB) {
-                k = 0;
-                phase ^= 1u;
-            }
+            next();
         }
         // the last copy into each buffer has landed (where every row was taken, it has)
         for (int i = 0; i < NB; ++i)
             if ((filled >> i) & 1u)
-                (void)mbar_wait_bounded(smem_u32(&full[i]), (i < k ? phase : phase ^ 1u) ^ 1u, a.timeout_ns);
-    } else if (warp > NW) {
+                (void)mbar_wait_bounded(smem_u32(&full[i]), i < k ? phase : phase ^ 1u, a.timeout_ns);
+    } else if (warp > NW + 1) {
         // ---------------------------------------------------------- distillation: the lists
-        int k = 0;
-        uint32_t phase = 1;
         int64_t t_next = first < a.p.rows ? load_index(a.index, a.idx64, first * a.K) : 0;
         for (int64_t r = first; r < a.p.rows; r += step) {
             const int64_t t = t_next;
@@ -549,50 +557,30 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                     prefetch_l2(static_cast<const char*>(a.teacher) + w * (a.teacher_dtype == 0 ? 4 : 2));
                 }
             }
-            if (!wait(&empty[k], phase)) break;
+            if (!wait(&empty[k], phase ^ 1u)) break;
             if (t >= 0 && t < a.p.V) {
                 ListInfo li = {};
                 top_list<T>(a, r, X + a.p.at(r), lists + static_cast<size_t>(k) * a.K, seen, li, lane);
                 if (lane == 0) linfo[k] = li;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[k]));
-            if (++k == NB) {
-                k = 0;
-                phase ^= 1u;
-            }
+            arrive(&full[k]);
+            next();
         }
-    } else {
-        // ---------------------------------------------------------- consumers
+    } else if (warp == NW + 1) {
+        // ---------------------------------------------------------- a row's statistics together, its
+        // outputs, and its gradient's constants
         float scale = a.scale;
-        bool have_scale = OP == kRowLogp || a.reduction != kRedMean;
-        int k = 0, turn = 0;                // buffer; which of the two exchange slots
-        uint32_t phase = 0, met_phase = 0;  // bit i of met_phase: parity of met[i]'s next completion
-        uint32_t together_phase = 0;        // bit i: parity of together[i]'s next completion
-        uint32_t meeting_phase = 0, ready_phase = 0;
-        for (int64_t r = first; r < a.p.rows; r += step) {
+        bool have_scale = !two || a.reduction != kRedMean;
+        int turn = 0;             // which of the two exchange slots
+        uint32_t met_phase = 0;   // bit i: parity of met[i]'s next completion
+        uint32_t used = 0;        // bit i: parity of together[i]'s next completion
+        const bool out = rank == 0 && lane == 0;
+        double sum = 0.0;
+        for (int64_t r = first; r < a.p.rows; r += step, next()) {
             if (!wait(&full[k], phase)) break;
-            const int kb = k;
-            if (++k == NB) {
-                k = 0;
-                phase ^= 1u;
-            }
-            const RowInfo& in = info[kb];
-            const int n = in.n, w0 = in.w0, w1 = in.w1, slice0 = in.first, t = in.t;
-            T* drow = a.p.dx ? reinterpret_cast<T*>(a.p.dx) + in.at : nullptr;
-            uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
-            auto release = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&empty[kb]));
-            };
-            if (t < 0) {  // exact +0, and the row is not read
-                if (drow) {
-                    for (int v = w0 + tid; v < w1; v += NT) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
-                    const int v = edge_vector(in, lane), j = slice0 + v * VE + (lane & 7);
-                    if (warp == NW - 1 && v >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V)
-                        VT::store1(drow, j, 0.f);
-                }
-                if (rank == 0 && tid == 0) {
+            const RowInfo in = info[k];
+            if (in.t < 0) {
+                if (out) {
                     if (in.bad) atomicOr(a.status, kDevErrTarget);
                     if (OP != kRowLogp && a.reduction == kRedNone) a.loss[r] = 0.f;
                     if (OP != kRowDistill) {
@@ -602,187 +590,225 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                         if (a.clipped) a.clipped[r] = 0;
                     }
                 }
-                release();
+                if (!two) arrive(&empty[k]);
                 continue;
             }
+            const Entry* ent = lists + static_cast<size_t>(k) * a.K;
+            if (!wait(&together[k], (used >> k) & 1u)) break;
+            used ^= 1u << k;
+            RowPart st = lane < NW ? red[k][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+            if (OP == kRowLogp) arrive(&empty[k]);
+            if (NW > 1) part_warp<ENT, OP != kRowDistill>(st, a.c);
+            else st = RowPart{__shfl_sync(~0u, st.m, 0), __shfl_sync(~0u, st.S, 0), __shfl_sync(~0u, st.Q, 0),
+                              __shfl_sync(~0u, st.x, 0)};
+            if (C > 1) {
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[turn]), 16u * C);
+                __syncwarp();
+                if (lane < C)
+                    st_async_v4(map_to_rank(smem_u32(&parts[turn][rank]), lane), st,
+                                map_to_rank(smem_u32(&met[turn]), lane));
+                if (timed_out(mbar_wait_cluster(smem_u32(&met[turn]), (met_phase >> turn) & 1u, a.timeout_ns)))
+                    break;
+                met_phase ^= 1u << turn;
+                st = lane < C ? parts[turn][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+                part_warp<ENT, OP != kRowDistill>(st, a.c);
+                turn ^= 1;
+            }
+            if (!have_scale) {
+                pdl_wait();
+                scale = static_cast<float>(static_cast<double>(a.scale) / __ldcg(a.D));
+                have_scale = true;
+            }
+            float loss = 0.f;
+            RowConst kc = {st.m, 0.f, 0.f, 0.f};
+            if (OP == kRowDistill) {
+                const ListInfo li = linfo[k];
+                float S = st.S, left = st.S;
+                if (tail) {
+                    // both sums by the row's maximum, that of the list included
+                    kc.m = fmaxf(st.m, li.top);
+                    part_raise(st, kc.m, a.c, false);
+                    left = st.S;
+                    float listed = 0.f;
+                    for (int e = lane; e < a.K; e += 32)
+                        if (ent[e].j >= 0) listed += ex2((ent[e].x - kc.m) * a.c);
+                    S = left + warp_sum(listed);
+                }
+                const float f = scale * in.weight * a.invT, mass = li.mass + li.rest;
+                const float cut = tail && left > 0.f ? li.rest * (S / left) : 0.f;
+                kc.u0 = f * (mass - cut) / S;
+                kc.u1 = f * mass / S;  // (of a listed class, less f q)
+                kc.x = f;
+                if (rank == 0) {
+                    const float logS = logf(S);
+                    for (int e = lane; e < a.K; e += 32)
+                        if (ent[e].q != 0.f)
+                            loss += ent[e].q * (ent[e].lq - log_prob(a, ent[e].x, kc.m, logS));
+                    loss = warp_sum(loss);
+                    if (tail && li.rest > 0.f && left > 0.f)
+                        loss += li.rest * (logf(li.rest) - (logf(left) - logS));
+                }
+            } else {
+                const float logS = logf(st.S);
+                const float lp = log_prob(a, st.x, st.m, logS);
+                const float H = ENT ? fmaf(-kLn2, st.Q / st.S, logS) : 0.f;
+                if (OP == kRowPolicy) {
+                    const PolicyRow pr = policy_row(a, lp, in.adv, in.old, in.ref);
+                    loss = ENT ? fmaf(-a.ent, H, pr.loss) : pr.loss;
+                    // g_j = 2^a_j (u0 + u1 a_j), plus the slope at the token
+                    const float f = scale * in.weight * a.invT, slope = pr.slope * f, k1 = a.ent * f;
+                    const float iS = 1.f / st.S;
+                    kc.u0 = (ENT ? fmaf(k1, H - logS, -slope) : -slope) * iS;
+                    kc.u1 = ENT ? k1 * kLn2 * iS : 0.f;
+                    kc.x = slope;
+                    if (out) {
+                        if (a.kl_out) a.kl_out[r] = pr.kl;
+                        if (a.clipped) a.clipped[r] = pr.clipped ? 1 : 0;
+                    }
+                }
+                if (out) {
+                    if (a.logp) a.logp[r] = lp;
+                    if (a.entropy) a.entropy[r] = H;
+                    if (a.kept) a.kept[r] = RowKept{st.m, st.S, H, lp};
+                }
+            }
+            if (two) {
+                if (lane == 0) consts[k] = kc;
+                arrive(&ready[k]);
+            } else if (OP != kRowLogp) {
+                arrive(&empty[k]);
+            }
+            if (OP != kRowLogp && out) {
+                if (a.reduction == kRedNone)
+                    a.loss[r] = a.scale * in.weight * loss;
+                else
+                    sum += static_cast<double>(in.weight) * static_cast<double>(loss);
+            }
+        }
+        if (out) s_sum = sum;
+    } else {
+        // ---------------------------------------------------------- consumers
+        uint32_t given = 0;  // bit i: parity of ready[i]'s next completion
+        uint32_t meeting_phase = 0;
+        auto meet = [&]() {  // all consumer warps
+            arrive(&meeting);
+            const uint32_t p = meeting_phase;
+            meeting_phase ^= 1u;
+            return wait(&meeting, p);
+        };
+        // the gradient of the row in buffer kb, which is then given back
+        auto second_pass = [&](int kb) {
+            if (!wait(&ready[kb], (given >> kb) & 1u)) return false;
+            given ^= 1u << kb;
+            const RowInfo& in = info[kb];
+            const RowConst kc = consts[kb];
             unsigned char* buf = smem + static_cast<size_t>(kb) * a.buf_bytes;
             const uint4* vec = reinterpret_cast<const uint4*>(buf);
-            const Entry* ent = lists + static_cast<size_t>(kb) * a.K;
-            auto meet = [&]() {  // all consumer warps
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&meeting));
-                const uint32_t p = meeting_phase;
-                meeting_phase ^= 1u;
-                return wait(&meeting, p);
+            const int w0 = in.w0, w1 = in.w1, slice0 = in.first, t = in.t;
+            T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
+            uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
+            if (fabsf(kc.m) < kFarLogit)
+                slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, kc.m, kc.u0, kc.u1);
+            else
+                slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, kc.m, kc.u0, kc.u1);
+            auto element = [&](float x) {
+                const float g = (x - kc.m) * a.c;
+                return ex2(g) * (ENT ? fmaf(kc.u1, fmaxf(g, -256.f), kc.u0) : kc.u0);
             };
-            if (tail) {
-                // the classes of the list leave the row: the sum is that of the others
-                for (int e = tid; e < a.K; e += NT) {
-                    const int j = ent[e].j - slice0;
-                    if (ent[e].j >= 0 && j >= 0 && j < n * VE) VT::store1(buf, j, -INFINITY);
+            if (warp == NW - 1) {  // the vectors that the row shares with others
+                const int ev = edge_vector(in, lane), i = ev * VE + (lane & 7), j = slice0 + i;
+                if (ev >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V) {
+                    const float g = element(VT::load1(buf, i));
+                    VT::store1(drow, j, OP == kRowPolicy && j == t ? g + kc.x : g);
                 }
-                fence_proxy_async();  // (a copy will land there)
-                if (!meet()) break;
             }
-            // ---- statistics of the slice
-            RowPart st = slice_stats<T, ENT, NT, U>(vec, n, tid, a.c, a.c_low);
-            __syncwarp();
-            part_warp<ENT, false>(st, a.c);
-            if (NW > 1) {
-                if (lane == 0) red[kb][warp] = st;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&together[kb]));
+            if (OP == kRowPolicy) {
+                // the token's element again, by the thread that stored its vector
+                const int i = t - slice0, tv = i >= 0 ? i / VE : -1;
+                if (tv >= w0 && tv < w1 && (tv - w0) % NT == tid)
+                    VT::store1(drow, t, element(VT::load1(buf, i)) + kc.x);
             }
-            // ---- warp 0: the row's statistics, its outputs, and its gradient's constants
-            RowConst k_;
-            if (warp == 0) {
+            if (OP == kRowDistill) {
+                // the listed classes', after every thread's stores
                 if (NW > 1) {
-                    if (!wait(&together[kb], (together_phase >> kb) & 1u)) break;
-                    st = lane < NW ? red[kb][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-                    part_warp<ENT, false>(st, a.c);
-                }
-                const int tj = t - slice0;  // the token's place in the slice
-                if (OP != kRowDistill && tj >= 0 && tj < n * VE) st.x = VT::load1(buf, tj);
-                if (C > 1) {
-                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[turn]), 16u * C);
-                    __syncwarp();
-                    if (lane < C)
-                        st_async_v4(map_to_rank(smem_u32(&parts[turn][rank]), lane), st,
-                                    map_to_rank(smem_u32(&met[turn]), lane));
-                    if (timed_out(mbar_wait_cluster(smem_u32(&met[turn]), (met_phase >> turn) & 1u,
-                                                    a.timeout_ns)))
-                        break;
-                    met_phase ^= 1u << turn;
-                    st = lane < C ? parts[turn][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-                    part_warp<ENT, OP != kRowDistill>(st, a.c);
-                    turn ^= 1;
-                }
-                if (!have_scale && a.p.dx) {
-                    pdl_wait();
-                    scale = static_cast<float>(static_cast<double>(a.scale) / __ldcg(a.D));
-                    have_scale = true;
-                }
-                const float weight = in.weight;
-                float loss = 0.f;
-                k_.m = st.m;
-                if (OP == kRowDistill) {
-                    float S = st.S, left = st.S;
-                    if (tail) {
-                        // both sums by the row's maximum, that of the list included
-                        k_.m = fmaxf(st.m, linfo[kb].top);
-                        part_raise(st, k_.m, a.c, false);
-                        left = st.S;
-                        float listed = 0.f;
-                        for (int e = lane; e < a.K; e += 32)
-                            if (ent[e].j >= 0) listed += ex2((ent[e].x - k_.m) * a.c);
-                        S = left + warp_sum(listed);
-                    }
-                    const float logS = logf(S), rest = linfo[kb].rest;
-                    if (rank == 0) {
-                        for (int e = lane; e < a.K; e += 32)
-                            if (ent[e].q != 0.f)
-                                loss += ent[e].q * (ent[e].lq - log_prob(a, ent[e].x, k_.m, logS));
-                        loss = warp_sum(loss);
-                        if (tail && rest > 0.f && left > 0.f) loss += rest * (logf(rest) - (logf(left) - logS));
-                    }
-                    const float f = scale * weight * a.invT, mass = linfo[kb].mass + rest;
-                    const float cut = tail && left > 0.f ? rest * (S / left) : 0.f;
-                    k_.u0 = f * (mass - cut) / S;
-                    k_.u1 = f * mass / S;  // (of a listed class, less f q)
-                    k_.x = f;
+                    if (!meet()) return false;
                 } else {
-                    const float logS = logf(st.S);
-                    const float lp = log_prob(a, st.x, st.m, logS);
-                    const float H = ENT ? fmaf(-kLn2, st.Q / st.S, logS) : 0.f;
-                    if (rank == 0 && lane == 0) {
-                        if (a.logp) a.logp[r] = lp;
-                        if (a.entropy) a.entropy[r] = H;
-                        if (a.kept) a.kept[r] = RowKept{st.m, st.S, H, lp};
-                    }
-                    if (OP == kRowPolicy) {
-                        const PolicyRow pr = policy_row(a, lp, in.adv, in.old, in.ref);
-                        loss = ENT ? fmaf(-a.ent, H, pr.loss) : pr.loss;
-                        if (rank == 0 && lane == 0) {
-                            if (a.kl_out) a.kl_out[r] = pr.kl;
-                            if (a.clipped) a.clipped[r] = pr.clipped ? 1 : 0;
-                        }
-                        // g_j = 2^a_j (u0 + u1 a_j), plus the slope at the token
-                        const float f = scale * weight * a.invT, slope = pr.slope * f, k1 = a.ent * f;
-                        k_.u0 = (ENT ? fmaf(k1, H - logS, -slope) : -slope) / st.S;
-                        k_.u1 = ENT ? k1 * kLn2 / st.S : 0.f;
-                        k_.x = slope;
-                    }
+                    __syncwarp();
                 }
-                if (OP != kRowLogp && rank == 0 && lane == 0) {
-                    if (a.reduction == kRedNone)
-                        a.loss[r] = a.scale * weight * loss;
-                    else
-                        sum += static_cast<double>(weight) * static_cast<double>(loss);
-                }
-                if (OP != kRowLogp && NW > 1) {
-                    if (lane == 0) {
-                        consts[kb] = k_;
-                        mbar_arrive(smem_u32(&ready));
-                    }
+                const Entry* ent = lists + static_cast<size_t>(kb) * a.K;
+                for (int e = tid; e < a.K; e += NT) {
+                    const int j = ent[e].j;
+                    if (j >= 0 && j >= slice0 && j - slice0 < in.n * VE)
+                        VT::store1(drow, j, fmaf(kc.u1, ex2((ent[e].x - kc.m) * a.c), -kc.x * ent[e].qs));
                 }
             }
-            together_phase ^= 1u << kb;
-            if (OP == kRowLogp) {
-                release();
-                continue;
-            }
-            if (NW > 1) {
-                if (warp != 0) {
-                    if (!wait(&ready, ready_phase)) break;
-                    k_ = consts[kb];
-                }
-                ready_phase ^= 1u;
-            }
-            // ---- the slice's gradient
-            if (drow) {
-                const float m = k_.m, u0 = k_.u0, u1 = k_.u1;
-                if (fabsf(m) < kFarLogit)
-                    slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, m, u0, u1);
-                else
-                    slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, m, u0, u1);
-                auto element = [&](float x) {
-                    const float g = (x - m) * a.c;
-                    return ex2(g) * (ENT ? fmaf(u1, fmaxf(g, -256.f), u0) : u0);
-                };
-                if (warp == NW - 1) {  // the vectors that the row shares with others
-                    const int ev = edge_vector(in, lane), i = ev * VE + (lane & 7), j = slice0 + i;
-                    if (ev >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V) {
-                        const float g = element(VT::load1(buf, i));
-                        VT::store1(drow, j, OP == kRowPolicy && j == t ? g + k_.x : g);
-                    }
-                }
-                if (OP == kRowPolicy) {
-                    // the token's element again, by the thread that stored its vector
-                    const int i = t - slice0, tv = i >= 0 ? i / VE : -1;
-                    if (tv >= w0 && tv < w1 && (tv - w0) % NT == tid)
-                        VT::store1(drow, t, element(VT::load1(buf, i)) + k_.x);
-                }
-                if (OP == kRowDistill) {
-                    if (NW > 1) {
-                        if (!meet()) break;  // the listed classes', after every thread's stores
-                    } else {
-                        __syncwarp();
-                    }
+            arrive(&empty[kb]);
+            return true;
+        };
+        // the second pass over a row follows the first over the next one, so
+        // that the row's statistics meet meanwhile
+        int waiting = -1;
+        bool ok = true;
+        for (int64_t r = first; r < a.p.rows; r += step, next()) {
+            ok = wait(&full[k], phase);
+            if (!ok) break;
+            const RowInfo& in = info[k];
+            const int n = in.n, slice0 = in.first, t = in.t;
+            unsigned char* buf = smem + static_cast<size_t>(k) * a.buf_bytes;
+            if (t >= 0) {
+                if (tail) {
+                    // the classes of the list leave the row: the sum is that of the others
+                    const Entry* ent = lists + static_cast<size_t>(k) * a.K;
                     for (int e = tid; e < a.K; e += NT) {
-                        const int j = ent[e].j;
-                        if (j >= 0 && j >= slice0 && j - slice0 < n * VE)
-                            VT::store1(drow, j,
-                                       fmaf(u1, ex2((ent[e].x - m) * a.c), -k_.x * ent[e].qs));
+                        const int j = ent[e].j - slice0;
+                        if (ent[e].j >= 0 && j >= 0 && j < n * VE) VT::store1(buf, j, -INFINITY);
                     }
+                    fence_proxy_async();  // (a copy will land there)
+                    ok = meet();
+                    if (!ok) break;
+                }
+                RowPart st =
+                    slice_stats<T, ENT, NT, U>(reinterpret_cast<const uint4*>(buf), n, tid, a.c, a.c_low);
+                __syncwarp();
+                part_warp<ENT, false>(st, a.c);
+                if (OP != kRowDistill && warp == 0) {
+                    const int tj = t - slice0;  // the token's place in the slice
+                    if (tj >= 0 && tj < n * VE) st.x = VT::load1(buf, tj);
+                }
+                if (lane == 0) red[k][warp] = st;
+                arrive(&together[k]);
+                if (!two) arrive(&empty[k]);
+            }
+            if (two) {
+                if (waiting >= 0) {
+                    ok = second_pass(waiting);
+                    if (!ok) break;
+                }
+                waiting = t >= 0 ? k : -1;
+                if (NB == 1 && waiting >= 0) {  // (the next row needs this buffer)
+                    ok = second_pass(waiting);
+                    if (!ok) break;
+                    waiting = -1;
                 }
             }
-            release();
+            if (t < 0) {  // exact +0, and the row was not read
+                if (a.p.dx && OP != kRowLogp) {
+                    T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
+                    uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
+                    for (int v = in.w0 + tid; v < in.w1; v += NT) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
+                    const int v = edge_vector(in, lane), j = slice0 + v * VE + (lane & 7);
+                    if (warp == NW - 1 && v >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V)
+                        VT::store1(drow, j, 0.f);
+                }
+                arrive(&empty[k]);
+            }
         }
+        if (ok && waiting >= 0) (void)second_pass(waiting);
     }
     if (OP != kRowLogp && a.reduction != kRedNone) {
         pdl_wait();
         __syncthreads();
-        if (rank == 0) rows_finish(a, sum, static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
+        if (rank == 0) rows_finish(a, s_sum, static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
     }
     // no CTA leaves while another may still send to it
     __syncthreads();
