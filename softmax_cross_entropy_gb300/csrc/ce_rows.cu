@@ -94,14 +94,14 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
                                                 : a.slice_vec <= 512 ? 64
                                                 : a.slice_vec <= 1024 ? 128
                                                                       : 256);
-    const size_t list = op == kRowDistill ? sizeof(Entry) * static_cast<size_t>(a.K) : 0;
+    const size_t lists = op == kRowDistill ? 4 * kListWords * kLists * static_cast<size_t>(a.K) : 0;
     a.nbuf = env_int("GBCE_ROWS_BUFFERS", 3);
-    while (a.nbuf > 1 && a.nbuf * (a.buf_bytes + list) > 200 * 1024) --a.nbuf;
-    const size_t smem = a.nbuf * (a.buf_bytes + list);
+    while (a.nbuf > 1 && a.nbuf * a.buf_bytes + lists > 200 * 1024) --a.nbuf;
+    const size_t smem = a.nbuf * a.buf_bytes + lists;
     const void* fn = dtype == CE_F32    ? rows_kernel_f32(op, ent, nt)
                      : dtype == CE_BF16 ? rows_kernel_bf16(op, ent, nt)
                                         : rows_kernel_f16(op, ent, nt);
-    const int threads = nt + (op == kRowDistill ? 96 : 64);
+    const int threads = nt + 96 + (op == kRowDistill ? 32 * kLists : 0);
     int fit = 0;
     ce_status rc = clusters_that_fit(fn, C, threads, smem, sms, &fit);
     if (rc != CE_OK) return rc;

@@ -36,15 +36,18 @@ struct __align__(16) RowKept {
 
 constexpr int kMaxRowCluster = 16;  // CTAs that share a row
 
-// An entry of a teacher's list.
-struct __align__(16) Entry {
-    float x;   // the student's logit of its class
-    float q;   // the teacher's probability (0: padding)
-    float lq;  // its logarithm
-    float qs;  // the sum of q over the entries of this class, in the first of them
-    int j;     // the class; -1: padding, or not the first of its class
-    int pad[3];
+constexpr int kMaxBuf = 4;          // buffers of a CTA
+
+// A teacher's list in shared memory, an array a part.
+struct TopList {
+    float* x;   // the student's logit of the class
+    float* q;   // the teacher's probability (0: padding)
+    float* lq;  // its logarithm
+    float* qs;  // the sum of q over the entries of this class, in the first of them
+    int* j;     // the class; -1: padding, or not the first of its class
 };
+constexpr int kListWords = 5;
+constexpr int kLists = 4;  // of a CTA, each with a warp of its own
 
 struct RowArgs {
     RowPlace p;

@@ -27,7 +27,6 @@
 
 namespace gbce {
 
-constexpr int kMaxBuf = 4;
 constexpr uint32_t kBulk = 32768;
 
 // What the producer leaves of a row beside its logits.
@@ -42,9 +41,14 @@ struct __align__(16) RowInfo {
 };
 
 // What the list's warp leaves: the sum of q, what remains of the teacher's
-// mass, the largest of the list's logits.
+// mass, the largest of the list's logits. And what it needs in the end, when
+// it stores the listed classes' elements of the gradient: the row, the CTA's
+// classes, and the gradient's constants (RowConst; lo = hi: nothing to store).
 struct __align__(16) ListInfo {
-    float mass, rest, top, pad;
+    float mass, rest, top;
+    int lo, hi;
+    float m, u1, x;
+    int64_t at;
 };
 
 // What every warp needs for the gradient: 2^((x - m) c) (u0 + u1 a), and x at
@@ -54,11 +58,14 @@ struct __align__(16) RowConst {
 };
 
 // CTAs of an SM that a kernel's registers are to leave room for.
-constexpr int rows_ctas(int nt) { return nt == 32 ? 10 : nt == 64 ? 7 : nt == 128 ? 4 : 2; }
+constexpr int rows_ctas(int op, int nt) {
+    if (op == kRowDistill) return nt <= 64 ? 3 : 2;
+    return nt == 32 ? 7 : nt == 64 ? 6 : nt == 128 ? 4 : 2;
+}
 
-// A CTA's threads: the consumers, the producer warp, the warp that brings a
-// row's statistics together, distillation's list warp.
-constexpr int rows_threads_of(int op, int nt) { return nt + (op == kRowDistill ? 96 : 64); }
+// A CTA's threads: the consumers, the producer warp, the two warps that bring
+// a row's statistics together, distillation's list warps.
+constexpr int rows_threads_of(int op, int nt) { return nt + 96 + (op == kRowDistill ? 32 * kLists : 0); }
 
 // Of lanes 0-7 the vector that the row's start shares with what is before it,
 // of lanes 8-15 the one that its end shares; -1: there is none.
@@ -304,15 +311,16 @@ __device__ __forceinline__ void slice_gradient(const uint4* vec, uint4* dvec, in
     for (; v < w1; v += NT) dvec[v] = grad(vec[v]);
 }
 
-constexpr int kSeenWords = 256;  // of a table of the classes seen: a bit a hash value
+constexpr int kSeenWords = 128;  // of a table of the classes seen: a bit a hash value
 
 // A warp forms row r's list: the teacher's softmax, its classes' logits, and
 // which entry stands for a class that is named more than once. seen: two
 // tables of kSeenWords words, zero between calls.
 template <typename T>
-__device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* row, Entry* ent,
+__device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* row, const TopList& L,
                                          uint32_t* seen, ListInfo& out, int lane) {
     float top_v = -INFINITY, top_x = -INFINITY;
+#pragma unroll 1
     for (int e = lane; e < a.K; e += 32) {
         const int64_t w = r * a.K + e;
         const int64_t j = load_index(a.index, a.idx64, w);
@@ -322,9 +330,9 @@ __device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* r
         const bool ok = j >= 0 && j < a.p.V;
         if (j >= a.p.V) atomicOr(a.status, kDevErrTarget);
         const float x = ok ? Vec<T>::load1(row, j) : -INFINITY;
-        ent[e].j = ok ? static_cast<int>(j) : -1;
-        ent[e].lq = ok ? v : -INFINITY;
-        ent[e].x = x;
+        L.j[e] = ok ? static_cast<int>(j) : -1;
+        L.lq[e] = ok ? v : -INFINITY;
+        L.x[e] = x;
         if (ok) top_v = fmaxf(top_v, v);
         top_x = fmaxf(top_x, x);
     }
@@ -334,20 +342,27 @@ __device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* r
     out.top = warp_max_f32(top_x);
     double mass = 0.0;
     bool twice = false;
+    auto hash = [&](int j, uint32_t& w0, uint32_t& b0, uint32_t& w1, uint32_t& b1) {
+        const uint32_t h = static_cast<uint32_t>(j), g = h * 2654435761u >> 20;
+        w0 = (h >> 5) % kSeenWords;
+        b0 = 1u << (h & 31u);
+        w1 = kSeenWords + (g >> 5);
+        b1 = 1u << (g & 31u);
+    };
+#pragma unroll 1
     for (int e = lane; e < a.K; e += 32) {
-        const float2 l = scaled_minus(a, ent[e].lq, shift);
-        const int j = ent[e].j;
+        const float2 l = scaled_minus(a, L.lq[e], shift);
+        const int j = L.j[e];
         const float q = j < 0 ? 0.f : expf(l.x);
-        ent[e].lq = l.x;
+        L.lq[e] = l.x;
         const float q1 = fmaf(q, l.y, q);
-        ent[e].q = q1;
+        L.q[e] = q1;
         mass += q1;
         if (j >= 0) {
             // seen before by two hashes: most likely the same class
-            const uint32_t h = static_cast<uint32_t>(j), g = h * 2654435761u >> 19;
-            const uint32_t b0 = 1u << (h & 31u), b1 = 1u << (g & 31u);
-            const uint32_t o0 = atomicOr(&seen[(h >> 5) & (kSeenWords - 1)], b0);
-            const uint32_t o1 = atomicOr(&seen[kSeenWords + (g >> 5)], b1);
+            uint32_t w0, b0, w1, b1;
+            hash(j, w0, b0, w1, b1);
+            const uint32_t o0 = atomicOr(&seen[w0], b0), o1 = atomicOr(&seen[w1], b1);
             twice = twice || ((o0 & b0) && (o1 & b1));
         }
     }
@@ -358,40 +373,41 @@ __device__ __forceinline__ void top_list(const RowArgs& a, int64_t r, const T* r
     const float lm = tail ? 0.f : logf(out.mass), im = tail ? 1.f : 1.f / out.mass;
     if (!tail) out.mass = 1.f;
     twice = __any_sync(0xffffffffu, twice);
+#pragma unroll 1
     for (int e = lane; e < a.K; e += 32) {
-        const float q = ent[e].q * im;
-        ent[e].q = q;
-        ent[e].qs = q;
-        ent[e].lq -= lm;
-        const int j = ent[e].j;
-        if (j >= 0) {
-            const uint32_t h = static_cast<uint32_t>(j), g = h * 2654435761u >> 19;
-            seen[(h >> 5) & (kSeenWords - 1)] = 0u;
-            seen[kSeenWords + (g >> 5)] = 0u;
+        const float q = L.q[e] * im;
+        L.q[e] = q;
+        L.qs[e] = q;
+        L.lq[e] -= lm;
+        if (L.j[e] >= 0) {
+            uint32_t w0, b0, w1, b1;
+            hash(L.j[e], w0, b0, w1, b1);
+            seen[w0] = 0u;
+            seen[w1] = 0u;
         }
     }
     __syncwarp();
     if (!twice) return;
     for (int e = lane; e < a.K; e += 32) {
-        const int j = ent[e].j;
+        const int j = L.j[e];
         float qs = 0.f;
         bool is_first = true;
         for (int o = 0; o < a.K; ++o) {
-            if (ent[o].j == j) {
-                qs += ent[o].q;
+            if (L.j[o] == j) {
+                qs += L.q[o];
                 is_first = is_first && o >= e;
             }
         }
-        ent[e].qs = is_first ? qs : -1.f;
+        L.qs[e] = is_first ? qs : -1.f;
     }
     __syncwarp();
     for (int e = lane; e < a.K; e += 32)
-        if (ent[e].qs < 0.f) ent[e].j = -1;
+        if (L.qs[e] < 0.f) L.j[e] = -1;
     __syncwarp();
 }
 
 template <typename T, int OP, bool ENT, int NT>
-__global__ void __launch_bounds__(rows_threads_of(OP, NT), rows_ctas(NT))
+__global__ void __launch_bounds__(rows_threads_of(OP, NT), rows_ctas(OP, NT))
 rows_kernel(const __grid_constant__ RowArgs a) {
     using VT = Vec<T>;
     constexpr int VE = VT::N;
@@ -401,14 +417,16 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     // a buffer's mbarriers: filled; given back; its row's statistics are all
     // there; its row's constants are there
     __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], ready[kMaxBuf];
-    __shared__ __align__(8) uint64_t met[2], meeting;
-    __shared__ RowPart parts[2][kMaxRowCluster];  // of the cluster's CTAs, two rows in turn
+    __shared__ __align__(8) uint64_t met[4], meeting;
+    // the lists' own ring, a slot a list warp: a list takes longer than a row
+    __shared__ __align__(8) uint64_t listed[kLists], unlisted[kLists];
+    __shared__ RowPart parts[4][kMaxRowCluster];  // of the cluster's CTAs, for two rows of each statistics warp
     __shared__ RowPart red[kMaxBuf][NW];          // of the warps
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
-    __shared__ ListInfo linfo[OP == kRowDistill ? kMaxBuf : 1];
-    __shared__ uint32_t seen[OP == kRowDistill ? 2 * kSeenWords : 1];
-    __shared__ double s_sum, red_d[NW + 3];
+    __shared__ ListInfo linfo[OP == kRowDistill ? kLists : 1];
+    __shared__ uint32_t seen[OP == kRowDistill ? kLists * 2 * kSeenWords : 1];
+    __shared__ double s_sum[2], red_d[NW + 3 + kLists];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -418,25 +436,32 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     const int64_t first = C > 1 ? cluster_id_x() : blockIdx.x;
     const int64_t step = gridDim.x / static_cast<unsigned>(C);
     const int NB = a.nbuf;
-    Entry* lists = reinterpret_cast<Entry*>(smem + static_cast<size_t>(NB) * a.buf_bytes);
+    auto list_of = [&](int kb) {
+        float* w = reinterpret_cast<float*>(smem + static_cast<size_t>(NB) * a.buf_bytes) +
+                   static_cast<size_t>(kb) * kListWords * a.K;
+        return TopList{w, w + a.K, w + 2 * a.K, w + 3 * a.K, reinterpret_cast<int*>(w + 4 * a.K)};
+    };
     const bool tail = OP == kRowDistill && a.teacher_lse != nullptr;
     const bool two = OP != kRowLogp && a.p.dx != nullptr;  // a second pass forms the gradient
     if (OP == kRowLogp && a.ticket && blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
     if (tid == 0) {
         for (int i = 0; i < NB; ++i) {
-            mbar_init(smem_u32(&full[i]), OP == kRowDistill ? 3 : 2);
+            mbar_init(smem_u32(&full[i]), 2);
             mbar_init(smem_u32(&empty[i]), two ? NW : NW + 1);
             mbar_init(smem_u32(&together[i]), NW);
             mbar_init(smem_u32(&ready[i]), 1);
         }
-        mbar_init(smem_u32(&met[0]), 1);
-        mbar_init(smem_u32(&met[1]), 1);
+        for (int i = 0; i < kLists; ++i) {
+            mbar_init(smem_u32(&listed[i]), 1);
+            mbar_init(smem_u32(&unlisted[i]), two ? NW + 1 : 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&met[i]), 1);
         mbar_init(smem_u32(&meeting), NW);
         fence_mbar_init();
-        s_sum = 0.0;
+        s_sum[0] = s_sum[1] = 0.0;
     }
     if (OP == kRowDistill)
-        for (int i = tid; i < 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
+        for (int i = tid; i < kLists * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
     __syncthreads();
     if (C > 1) cluster_sync();
 
@@ -457,7 +482,13 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     const T* X = reinterpret_cast<const T*>(a.p.x);
     int k = 0;           // the next row's buffer
     uint32_t phase = 0;  // how often the ring came round, modulo 2
+    int l = 0;                // the next row's list
+    uint32_t list_phase = 0;  // how often the lists' ring came round, modulo 2
     auto next = [&]() {
+        if (++l == kLists) {
+            l = 0;
+            list_phase ^= 1u;
+        }
         if (++k == NB) {
             k = 0;
             phase ^= 1u;
@@ -543,40 +574,68 @@ rows_kernel(const __grid_constant__ RowArgs a) {
         for (int i = 0; i < NB; ++i)
             if ((filled >> i) & 1u)
                 (void)mbar_wait_bounded(smem_u32(&full[i]), i < k ? phase : phase ^ 1u, a.timeout_ns);
-    } else if (warp > NW + 1) {
+    } else if (warp > NW + 2) {
         // ---------------------------------------------------------- distillation: the lists
-        int64_t t_next = first < a.p.rows ? load_index(a.index, a.idx64, first * a.K) : 0;
-        for (int64_t r = first; r < a.p.rows; r += step) {
-            const int64_t t = t_next;
-            if (r + step < a.p.rows) {
-                t_next = load_index(a.index, a.idx64, (r + step) * a.K);
-                // the next row's list on its way to L2
-                for (int e = lane; e < a.K; e += 32) {
-                    const int64_t w = (r + step) * a.K + e;
-                    prefetch_l2(static_cast<const char*>(a.index) + w * (a.idx64 ? 8 : 4));
-                    prefetch_l2(static_cast<const char*>(a.teacher) + w * (a.teacher_dtype == 0 ? 4 : 2));
-                }
+        const int slot = warp - NW - 3;
+        const TopList L = list_of(slot);
+        ListInfo& li = linfo[slot];
+        int64_t r = first + slot * step;
+        auto ahead = [&]() {  // row r's list, and the logits that it names, on their way to L2
+            if (r >= a.p.rows) return;
+            const T* row = X + a.p.at(r);
+            for (int e = lane; e < a.K; e += 32) {
+                const int64_t w = r * a.K + e;
+                prefetch_l2(static_cast<const char*>(a.teacher) + w * (a.teacher_dtype == 0 ? 4 : 2));
+                const int64_t j = load_index(a.index, a.idx64, w);
+                if (j >= 0 && j < a.p.V) prefetch_l2(row + j);
             }
-            if (!wait(&empty[k], phase ^ 1u)) break;
-            if (t >= 0 && t < a.p.V) {
-                ListInfo li = {};
-                top_list<T>(a, r, X + a.p.at(r), lists + static_cast<size_t>(k) * a.K, seen, li, lane);
-                if (lane == 0) linfo[k] = li;
+        };
+        // the listed classes' elements, after every thread's stores
+        auto store_listed = [&]() {
+            if (!wait(&unlisted[slot], list_phase)) return false;
+            const ListInfo in = li;
+            T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
+#pragma unroll 1
+            for (int e = lane; e < a.K; e += 32) {
+                const int j = L.j[e];
+                if (j >= in.lo && j < in.hi)
+                    VT::store1(drow, j, fmaf(in.u1, ex2((L.x[e] - in.m) * a.c), -in.x * L.qs[e]));
             }
-            arrive(&full[k]);
-            next();
+            list_phase ^= 1u;
+            __syncwarp();
+            return true;
+        };
+        bool ok = true, any = false;
+        for (; r < a.p.rows; any = true) {
+            const int64_t t = load_index(a.index, a.idx64, r * a.K);
+            if (any && !(ok = store_listed())) break;
+            ListInfo in = {};
+            if (t >= 0 && t < a.p.V)
+                top_list<T>(a, r, X + a.p.at(r), L, seen + slot * 2 * kSeenWords, in, lane);
+            if (lane == 0) li = in;
+            arrive(&listed[slot]);
+            r += kLists * step;
+            ahead();
         }
-    } else if (warp == NW + 1) {
+        if (ok && any) (void)store_listed();
+    } else if (warp > NW) {
         // ---------------------------------------------------------- a row's statistics together, its
-        // outputs, and its gradient's constants
+        // outputs, and its gradient's constants: every second row each of two warps (the
+        // exchange between CTAs takes longer than a row; two slots of each warp's make it
+        // safe, for none sends for a row before it has all of the one before)
+        const int half = warp - NW - 1;
         float scale = a.scale;
         bool have_scale = !two || a.reduction != kRedMean;
-        int turn = 0;             // which of the two exchange slots
-        uint32_t met_phase = 0;   // bit i: parity of met[i]'s next completion
-        uint32_t used = 0;        // bit i: parity of together[i]'s next completion
+        int slot = half;
+        uint32_t met_phase = 0;  // bit i: parity of met[i]'s next completion
         const bool out = rank == 0 && lane == 0;
-        double sum = 0.0;
-        for (int64_t r = first; r < a.p.rows; r += step, next()) {
+        float sum = 0.f, sum_low = 0.f;  // (two parts: 48 bits)
+        int64_t r = first;
+        if (half) {
+            r += step;
+            next();
+        }
+        for (; r < a.p.rows; r += 2 * step, next(), next()) {
             if (!wait(&full[k], phase)) break;
             const RowInfo in = info[k];
             if (in.t < 0) {
@@ -591,28 +650,26 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                     }
                 }
                 if (!two) arrive(&empty[k]);
+                if (OP == kRowDistill) arrive(&unlisted[l]);
                 continue;
             }
-            const Entry* ent = lists + static_cast<size_t>(k) * a.K;
-            if (!wait(&together[k], (used >> k) & 1u)) break;
-            used ^= 1u << k;
+            if (!wait(&together[k], phase)) break;
             RowPart st = lane < NW ? red[k][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-            if (OP == kRowLogp) arrive(&empty[k]);
-            if (NW > 1) part_warp<ENT, OP != kRowDistill>(st, a.c);
-            else st = RowPart{__shfl_sync(~0u, st.m, 0), __shfl_sync(~0u, st.S, 0), __shfl_sync(~0u, st.Q, 0),
-                              __shfl_sync(~0u, st.x, 0)};
+            if (!two) arrive(&empty[k]);
+            if (OP == kRowDistill && !wait(&listed[l], list_phase)) break;
+            part_warp<ENT, OP != kRowDistill>(st, a.c);
             if (C > 1) {
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[turn]), 16u * C);
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[slot]), 16u * C);
                 __syncwarp();
                 if (lane < C)
-                    st_async_v4(map_to_rank(smem_u32(&parts[turn][rank]), lane), st,
-                                map_to_rank(smem_u32(&met[turn]), lane));
-                if (timed_out(mbar_wait_cluster(smem_u32(&met[turn]), (met_phase >> turn) & 1u, a.timeout_ns)))
+                    st_async_v4(map_to_rank(smem_u32(&parts[slot][rank]), lane), st,
+                                map_to_rank(smem_u32(&met[slot]), lane));
+                if (timed_out(mbar_wait_cluster(smem_u32(&met[slot]), (met_phase >> slot) & 1u, a.timeout_ns)))
                     break;
-                met_phase ^= 1u << turn;
-                st = lane < C ? parts[turn][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+                met_phase ^= 1u << slot;
+                st = lane < C ? parts[slot][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
                 part_warp<ENT, OP != kRowDistill>(st, a.c);
-                turn ^= 1;
+                slot ^= 2;
             }
             if (!have_scale) {
                 pdl_wait();
@@ -622,32 +679,48 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             float loss = 0.f;
             RowConst kc = {st.m, 0.f, 0.f, 0.f};
             if (OP == kRowDistill) {
-                const ListInfo li = linfo[k];
+                const TopList L = list_of(l);
+                ListInfo& li = linfo[l];
                 float S = st.S, left = st.S;
                 if (tail) {
                     // both sums by the row's maximum, that of the list included
                     kc.m = fmaxf(st.m, li.top);
                     part_raise(st, kc.m, a.c, false);
                     left = st.S;
-                    float listed = 0.f;
+                    float inside = 0.f;
+#pragma unroll 1
                     for (int e = lane; e < a.K; e += 32)
-                        if (ent[e].j >= 0) listed += ex2((ent[e].x - kc.m) * a.c);
-                    S = left + warp_sum(listed);
+                        if (L.j[e] >= 0) inside += ex2((L.x[e] - kc.m) * a.c);
+                    S = left + warp_sum(inside);
                 }
-                const float f = scale * in.weight * a.invT, mass = li.mass + li.rest;
-                const float cut = tail && left > 0.f ? li.rest * (S / left) : 0.f;
-                kc.u0 = f * (mass - cut) / S;
-                kc.u1 = f * mass / S;  // (of a listed class, less f q)
-                kc.x = f;
+                if (two) {
+                    const float f = scale * in.weight * a.invT, mass = li.mass + li.rest, iS = 1.f / S;
+                    kc.u1 = f * mass * iS;  // (of a listed class, less f q)
+                    kc.u0 = tail && left > 0.f ? fmaf(-f, li.rest / left, kc.u1) : kc.u1;
+                    kc.x = f;
+                    if (lane == 0) {
+                        li.at = in.at;
+                        li.lo = max(in.first, 0);
+                        li.hi = min(in.first + in.n * VE, static_cast<int>(a.p.V));
+                        li.m = kc.m;
+                        li.u1 = kc.u1;
+                        li.x = f;
+                        consts[k] = kc;
+                    }
+                    arrive(&ready[k]);
+                }
                 if (rank == 0) {
                     const float logS = logf(S);
-                    for (int e = lane; e < a.K; e += 32)
-                        if (ent[e].q != 0.f)
-                            loss += ent[e].q * (ent[e].lq - log_prob(a, ent[e].x, kc.m, logS));
+#pragma unroll 1
+                    for (int e = lane; e < a.K; e += 32) {
+                        const float q = L.q[e];
+                        if (q != 0.f) loss += q * (L.lq[e] - log_prob(a, L.x[e], kc.m, logS));
+                    }
                     loss = warp_sum(loss);
                     if (tail && li.rest > 0.f && left > 0.f)
                         loss += li.rest * (logf(li.rest) - (logf(left) - logS));
                 }
+                arrive(&unlisted[l]);
             } else {
                 const float logS = logf(st.S);
                 const float lp = log_prob(a, st.x, st.m, logS);
@@ -655,12 +728,16 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 if (OP == kRowPolicy) {
                     const PolicyRow pr = policy_row(a, lp, in.adv, in.old, in.ref);
                     loss = ENT ? fmaf(-a.ent, H, pr.loss) : pr.loss;
-                    // g_j = 2^a_j (u0 + u1 a_j), plus the slope at the token
-                    const float f = scale * in.weight * a.invT, slope = pr.slope * f, k1 = a.ent * f;
-                    const float iS = 1.f / st.S;
-                    kc.u0 = (ENT ? fmaf(k1, H - logS, -slope) : -slope) * iS;
-                    kc.u1 = ENT ? k1 * kLn2 * iS : 0.f;
-                    kc.x = slope;
+                    if (two) {
+                        // g_j = 2^a_j (u0 + u1 a_j), plus the slope at the token
+                        const float f = scale * in.weight * a.invT, slope = pr.slope * f, k1 = a.ent * f;
+                        const float iS = 1.f / st.S;
+                        kc.u0 = (ENT ? fmaf(k1, H - logS, -slope) : -slope) * iS;
+                        kc.u1 = ENT ? k1 * kLn2 * iS : 0.f;
+                        kc.x = slope;
+                        if (lane == 0) consts[k] = kc;
+                        arrive(&ready[k]);
+                    }
                     if (out) {
                         if (a.kl_out) a.kl_out[r] = pr.kl;
                         if (a.clipped) a.clipped[r] = pr.clipped ? 1 : 0;
@@ -672,20 +749,17 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                     if (a.kept) a.kept[r] = RowKept{st.m, st.S, H, lp};
                 }
             }
-            if (two) {
-                if (lane == 0) consts[k] = kc;
-                arrive(&ready[k]);
-            } else if (OP != kRowLogp) {
-                arrive(&empty[k]);
-            }
             if (OP != kRowLogp && out) {
-                if (a.reduction == kRedNone)
+                if (a.reduction == kRedNone) {
                     a.loss[r] = a.scale * in.weight * loss;
-                else
-                    sum += static_cast<double>(in.weight) * static_cast<double>(loss);
+                } else {
+                    const float v = in.weight * loss, s = sum + v, b = s - sum;
+                    sum_low += fmaf(in.weight, loss, -v) + ((sum - (s - b)) + (v - b));
+                    sum = s;
+                }
             }
         }
-        if (out) s_sum = sum;
+        if (out) s_sum[half] = static_cast<double>(sum) + static_cast<double>(fabsf(sum) < INFINITY ? sum_low : 0.f);
     } else {
         // ---------------------------------------------------------- consumers
         uint32_t given = 0;  // bit i: parity of ready[i]'s next completion
@@ -696,8 +770,8 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             meeting_phase ^= 1u;
             return wait(&meeting, p);
         };
-        // the gradient of the row in buffer kb, which is then given back
-        auto second_pass = [&](int kb) {
+        // the gradient of the row in buffer kb, which is then given back (and its list)
+        auto second_pass = [&](int kb, int lb) {
             if (!wait(&ready[kb], (given >> kb) & 1u)) return false;
             given ^= 1u << kb;
             const RowInfo& in = info[kb];
@@ -728,26 +802,13 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 if (tv >= w0 && tv < w1 && (tv - w0) % NT == tid)
                     VT::store1(drow, t, element(VT::load1(buf, i)) + kc.x);
             }
-            if (OP == kRowDistill) {
-                // the listed classes', after every thread's stores
-                if (NW > 1) {
-                    if (!meet()) return false;
-                } else {
-                    __syncwarp();
-                }
-                const Entry* ent = lists + static_cast<size_t>(kb) * a.K;
-                for (int e = tid; e < a.K; e += NT) {
-                    const int j = ent[e].j;
-                    if (j >= 0 && j >= slice0 && j - slice0 < in.n * VE)
-                        VT::store1(drow, j, fmaf(kc.u1, ex2((ent[e].x - kc.m) * a.c), -kc.x * ent[e].qs));
-                }
-            }
+            if (OP == kRowDistill) arrive(&unlisted[lb]);
             arrive(&empty[kb]);
             return true;
         };
         // the second pass over a row follows the first over the next one, so
         // that the row's statistics meet meanwhile
-        int waiting = -1;
+        int waiting = -1, waiting_list = 0;
         bool ok = true;
         for (int64_t r = first; r < a.p.rows; r += step, next()) {
             ok = wait(&full[k], phase);
@@ -758,10 +819,13 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             if (t >= 0) {
                 if (tail) {
                     // the classes of the list leave the row: the sum is that of the others
-                    const Entry* ent = lists + static_cast<size_t>(k) * a.K;
+                    ok = wait(&listed[l], list_phase);
+                    if (!ok) break;
+                    const int* classes = list_of(l).j;
                     for (int e = tid; e < a.K; e += NT) {
-                        const int j = ent[e].j - slice0;
-                        if (ent[e].j >= 0 && j >= 0 && j < n * VE) VT::store1(buf, j, -INFINITY);
+                        const int j = classes[e];
+                        if (j >= 0 && j >= slice0 && j - slice0 < n * VE)
+                            VT::store1(buf, j - slice0, -INFINITY);
                     }
                     fence_proxy_async();  // (a copy will land there)
                     ok = meet();
@@ -781,12 +845,13 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             }
             if (two) {
                 if (waiting >= 0) {
-                    ok = second_pass(waiting);
+                    ok = second_pass(waiting, waiting_list);
                     if (!ok) break;
                 }
                 waiting = t >= 0 ? k : -1;
+                waiting_list = l;
                 if (NB == 1 && waiting >= 0) {  // (the next row needs this buffer)
-                    ok = second_pass(waiting);
+                    ok = second_pass(waiting, waiting_list);
                     if (!ok) break;
                     waiting = -1;
                 }
@@ -800,15 +865,17 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                     if (warp == NW - 1 && v >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V)
                         VT::store1(drow, j, 0.f);
                 }
+                if (OP == kRowDistill && two) arrive(&unlisted[l]);
+                arrive(&together[k]);  // (its phases go with the ring)
                 arrive(&empty[k]);
             }
         }
-        if (ok && waiting >= 0) (void)second_pass(waiting);
+        if (ok && waiting >= 0) (void)second_pass(waiting, waiting_list);
     }
     if (OP != kRowLogp && a.reduction != kRedNone) {
         pdl_wait();
         __syncthreads();
-        if (rank == 0) rows_finish(a, s_sum, static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
+        if (rank == 0) rows_finish(a, s_sum[0] + s_sum[1], static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
     }
     // no CTA leaves while another may still send to it
     __syncthreads();
