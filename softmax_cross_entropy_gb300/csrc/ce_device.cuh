@@ -98,6 +98,13 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
     return pol;
 }
 
+// L2 policy of an ordinary access.
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
 // L2 policy for data read twice in a row: keep it over other lines.
 __device__ __forceinline__ uint64_t l2_evict_last_policy() {
     uint64_t pol;

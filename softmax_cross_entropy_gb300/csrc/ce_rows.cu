@@ -18,6 +18,8 @@ const void* rows_kernel_f16(int op, bool ent, int nt);
 
 namespace {
 
+constexpr int64_t kKeepBytes = int64_t{96} << 20;  // of the 129 MB L2
+
 // How many clusters of C CTAs fit the device at once.
 std::mutex g_fit_mu;
 std::map<std::tuple<int, const void*, int, size_t>, int> g_fit;
@@ -94,6 +96,8 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
                                                 : a.slice_vec <= 512 ? 64
                                                 : a.slice_vec <= 1024 ? 128
                                                                       : 256);
+    // what the backward finds in L2 when it begins: the last rows, where there is one
+    a.keep_from = a.kept ? std::max<int64_t>(0, a.p.rows - kKeepBytes / (a.p.V * esz)) : a.p.rows;
     const size_t lists = op == kRowDistill ? 4 * kListWords * kLists * static_cast<size_t>(a.K) : 0;
     a.nbuf = env_int("GBCE_ROWS_BUFFERS", 3);
     while (a.nbuf > 1 && a.nbuf * a.buf_bytes + lists > 200 * 1024) --a.nbuf;

@@ -85,6 +85,7 @@ struct RowArgs {
     int idx64;
     int K;
     const float* teacher_lse;  // [rows] or nullptr
+    int64_t keep_from;  // rows from here on stay in L2 for the backward, which begins with the last
     // layout: CTAs a row, 16-byte vectors of a CTA's slice, its buffers and their bytes
     int cluster, slice_vec, nbuf;
     uint32_t buf_bytes;

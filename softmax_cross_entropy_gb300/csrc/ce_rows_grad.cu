@@ -4,7 +4,7 @@
 // gradient that the forward has written.
 #include <algorithm>
 
-#include "ce_rows.cuh"
+#include "ce_rows_math.cuh"
 #include "ce_rows_grad.cuh"
 #include "gbce.h"
 
@@ -13,35 +13,78 @@ ce_status record_cuda_failure(cudaError_t e, const char* what);
 
 namespace {
 
-constexpr int kCountThreadsRows = 1024;
+constexpr int kCountThreadsRows = 512;
+constexpr int kCountCtas = 8;  // one cluster
 
 // D = the sum of the counted rows' weights; clears the ticket of the sum that
-// follows. One CTA; each thread adds its rows in 64 bits, then a fixed
-// butterfly and warp order.
-__global__ void __launch_bounds__(kCountThreadsRows) rows_count(const __grid_constant__ RowArgs a) {
+// follows. One cluster; a thread adds its rows' weights in two fp32 parts
+// (the fp64 pipe is narrow: a sum in fp64 from the start took 16 us for 16384
+// rows, this takes 4), a fixed butterfly and order in fp64 the rest.
+__global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThreadsRows)
+rows_count(const __grid_constant__ RowArgs a) {
     __shared__ double red[kCountThreadsRows / 32];
+    __shared__ __align__(8) double mine;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cluster_ctarank());
     pdl_launch_dependents();
-    const bool top = a.index != nullptr;
-    const int64_t step = top ? a.K : 1;
-    double d = 0.0;
-#pragma unroll 8
-    for (int64_t r = tid; r < a.p.rows; r += kCountThreadsRows) {
-        const int64_t t = load_index(top ? a.index : a.tokens, top ? a.idx64 : a.tok64, r * step);
-        const bool counts = t >= 0 && t < a.p.V && (top || t != a.ignore_index);
-        const float w = a.weight ? __ldg(a.weight + r) : 1.f;
-        d += counts ? static_cast<double>(w) : 0.0;
-    }
+    if (a.reduction == kRedMean) {
+        const bool top = a.index != nullptr;
+        const void* marks = top ? a.index : a.tokens;
+        const int is64 = top ? a.idx64 : a.tok64;
+        const int64_t step = top ? a.K : 1;
+        constexpr int B = 8;  // rows a thread loads at once
+        float hi = 0.f, lo = 0.f;
+        int64_t n = 0;
+        for (int64_t r0 = rank * kCountThreadsRows + tid; r0 < a.p.rows;
+             r0 += int64_t{kCountCtas} * kCountThreadsRows * B) {
+            int64_t t[B];
+            float w[B];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) red[warp] = d;
+            for (int b = 0; b < B; ++b) {
+                const int64_t r = r0 + int64_t{b} * kCountCtas * kCountThreadsRows;
+                t[b] = r < a.p.rows ? load_index(marks, is64, r * step) : -1;
+                w[b] = r < a.p.rows && a.weight ? __ldg(a.weight + r) : 1.f;
+                if (r >= a.p.rows || (!top && t[b] == a.ignore_index)) t[b] = -1;
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (t[b] < 0 || t[b] >= a.p.V) continue;
+                ++n;
+                if (a.weight) {
+                    const float s = hi + w[b], z = s - hi;
+                    lo += (hi - (s - z)) + (w[b] - z);
+                    hi = s;
+                }
+            }
+        }
+        double d = !a.weight ? static_cast<double>(n)
+                             : static_cast<double>(hi) + static_cast<double>(fabsf(hi) < INFINITY ? lo : 0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) red[warp] = d;
+        __syncthreads();
+        if (tid == 0) {
+            d = 0.0;
+            for (int w = 0; w < kCountThreadsRows / 32; ++w) d += red[w];
+            mine = d;
+        }
+    }
     __syncthreads();
-    if (tid == 0) {
-        d = 0.0;
-        for (int w = 0; w < kCountThreadsRows / 32; ++w) d += red[w];
-        *a.D = d;
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+        if (a.reduction == kRedMean) {
+            double d = 0.0;
+            for (int c = 0; c < kCountCtas; ++c) {
+                double v;
+                asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(smem_u32(&mine), c)) : "memory");
+                d += v;
+            }
+            *a.D = d;
+        }
         *a.ticket = 0u;
     }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves before its sum is read
 }
 
 // ---------------------------------------------------------------- pairs of sequences
@@ -231,36 +274,40 @@ __global__ void __launch_bounds__(kGradThreads) rows_grad(const __grid_constant_
             if (tid < edges) VT::store1(dx, edge, 0.f);
             continue;
         }
-        auto grad = [&](float f) {
+        auto element = [&](float f) {
             const float arg = (f - g.m) * a.c;
-            const float e = ex2(arg);
-            return e * (ENT ? fmaf(g.u1, fmaxf(arg, -256.f), g.u0) : g.u0);
+            return ex2(arg) * (ENT ? fmaf(g.u1, fmaxf(arg, -256.f), g.u0) : g.u0);
         };
-        const int64_t tv = g.t - sp.head;  // the token's place among the vectors
-        for (int base = v0; base < v1; base += kGradThreads * kGradVec) {
-            uint4 q[kGradVec];
-#pragma unroll
-            for (int k = 0; k < kGradVec; ++k) {
-                const int v = base + k * kGradThreads + tid;
-                if (v < v1) q[k] = xv[v];
-            }
-#pragma unroll
-            for (int k = 0; k < kGradVec; ++k) {
-                const int v = base + k * kGradThreads + tid;
-                if (v >= v1) break;
+        auto vectors = [&](auto near) {
+            const GradTerms<decltype(near)::value> t(a.c, g.m, g.u0, g.u1);
+            auto grad = [&](const uint4& q) {
                 float f[VE];
-                VT::unpack(q[k], f);
+                grad_vector<T, ENT, decltype(near)::value>(t, q, f);
+                return VT::pack(f);
+            };
+            int v = v0 + tid;
+            for (; v + (kGradVec - 1) * kGradThreads < v1; v += kGradThreads * kGradVec) {
+                uint4 q[kGradVec];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] = grad(f[e]);
-                if (tv >= 0 && tv / VE == v) {
+                for (int k = 0; k < kGradVec; ++k) q[k] = xv[v + k * kGradThreads];
 #pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        if (tv % VE == e) f[e] += g.at;
-                }
-                dv[v] = VT::pack(f);
+                for (int k = 0; k < kGradVec; ++k) dv[v + k * kGradThreads] = grad(q[k]);
             }
-        }
-        if (tid < edges) VT::store1(dx, edge, grad(VT::load1(x, edge)) + (edge == g.t ? g.at : 0.f));
+#pragma unroll 1
+            for (; v < v1; v += kGradThreads) dv[v] = grad(xv[v]);
+        };
+        // the token's vector is stored again, element by element, by the thread that stored it
+        // (its logit is read first: dx may be x)
+        const int64_t ti = g.t - sp.head;
+        const bool owner = ti >= 0 && ti / VE >= v0 && ti / VE < v1 &&
+                           (static_cast<int>(ti / VE) - v0) % kGradThreads == tid;
+        const float xt = owner ? VT::load1(x, g.t) : 0.f;
+        if (fabsf(g.m) < kFarLogit)
+            vectors(std::true_type{});
+        else
+            vectors(std::false_type{});
+        if (owner) VT::store1(dx, g.t, element(xt) + g.at);
+        if (tid < edges) VT::store1(dx, edge, element(VT::load1(x, edge)) + (edge == g.t ? g.at : 0.f));
     }
 }
 
@@ -321,7 +368,7 @@ ce_status launch(const void* fn, int64_t grid, int threads, void* arg, cudaStrea
 
 ce_status rows_count_launch(const RowArgs& args, cudaStream_t st) {
     RowArgs a = args;
-    return launch((const void*)&rows_count, 1, kCountThreadsRows, &a, st, false, "token count launch");
+    return launch((const void*)&rows_count, kCountCtas, kCountThreadsRows, &a, st, false, "token count launch");
 }
 
 ce_status pair_launch(const PairArgs& args, cudaStream_t st) {
@@ -332,9 +379,11 @@ ce_status pair_launch(const PairArgs& args, cudaStream_t st) {
 
 ce_status rows_grad_launch(const GradArgs& args, int dtype, int sms, cudaStream_t st) {
     GradArgs a = args;
+    // a row a CTA; rows are split while there are few of them
     const int64_t vecs = a.p.V * (dtype == CE_F32 ? 4 : 2) / 16 + 1;
-    constexpr int64_t kPart = int64_t{kGradThreads} * kGradVec * 2;
-    a.parts = static_cast<int>((vecs + kPart - 1) / kPart);
+    constexpr int64_t kPart = int64_t{kGradThreads} * kGradVec;
+    a.parts = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((vecs + kPart - 1) / kPart, (16L * sms + a.p.rows - 1) / a.p.rows)));
     a.part_vec = static_cast<int>((vecs + a.parts - 1) / a.parts);
     const int64_t grid = std::min<int64_t>(a.p.rows * a.parts, 8L * sms);
     return launch(a.g_entropy ? grad_fn<true>(dtype) : grad_fn<false>(dtype), grid, kGradThreads, &a, st,

@@ -21,9 +21,7 @@
 // shares with its neighbours are filled element by element.
 #pragma once
 
-#include <type_traits>
-
-#include "ce_rows.cuh"
+#include "ce_rows_math.cuh"
 
 namespace gbce {
 
@@ -77,6 +75,11 @@ __device__ __forceinline__ int edge_vector(const RowInfo& in, int lane) {
 __device__ __forceinline__ void fence_proxy_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+
+// Rows whose statistics may be on their way between the CTAs at once: with at
+// most kMaxBuf buffers a CTA's are less than 2 kMaxBuf + 1 apart.
+constexpr int kMeetings = 16;
+static_assert(kMeetings > 2 * kMaxBuf, "rows on their way");
 
 // Four words into the shared memory of a CTA of the cluster, counted on its
 // mbarrier.
@@ -132,50 +135,6 @@ __device__ __forceinline__ uint4 lowest4() {
 }
 
 
-// Logits beyond this (masks of a type's lowest value, mostly) take the
-// careful forms below: times log2(e) / T they could overflow.
-constexpr float kFarLogit = 1e18f;
-
-// Products with an element's argument where 2^argument is 0: the logits are
-// cut at -1e30 (bf16 pairs in one instruction), or, where -inf is not far from
-// the type's other values, the arguments at -256.
-template <typename T>
-constexpr bool kCutLogits = !std::is_same<T, __half>::value;
-
-template <typename T>
-__device__ __forceinline__ uint4 at_least(const uint4& q) {
-    uint4 o;
-    const uint32_t* w = &q.x;
-    uint32_t* z = &o.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            float m;  // (a NaN stays)
-            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(w[i])), "f"(-1e30f));
-            z[i] = __float_as_uint(m);
-        } else {
-            const __nv_bfloat16 low = __ushort_as_bfloat16(0xF149u);
-            const __nv_bfloat162 v =
-                __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), __halves2bfloat162(low, low));
-            z[i] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-    }
-    return o;
-}
-
-template <typename T, bool ENT>
-__device__ __forceinline__ void unpack_cut(const uint4& q, float (&f)[Vec<T>::N]) {
-    if constexpr (ENT && kCutLogits<T>)
-        Vec<T>::unpack(at_least<T>(q), f);
-    else
-        Vec<T>::unpack(q, f);
-}
-
-template <typename T>
-__device__ __forceinline__ float2 cut_argument(float2 g) {
-    return kCutLogits<T> ? g : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f));
-}
-
 // The careful form of a thread's statistics: a running maximum, differences
 // before products.
 template <typename T, bool ENT, int NT>
@@ -203,10 +162,9 @@ __device__ __noinline__ RowPart slice_stats_careful(const uint4* vec, int n, int
 // only near it, so the largest of the thread's first vectors serves for all:
 // one that lies far above it shows in a sum of 2^100 or more, and the careful
 // form follows. 2^(x c - B), B = m c rounded, is one product and sum an element
-// (the product is exact before the sum is rounded); what B's rounding and c's
-// take from the result is put right once: B's by the factor 2^-(m c - B), c's
-// (c_low d = (c_low / c) a, a the argument) by an element's second product or,
-// where Q = sum 2^a a is formed anyway, by S + ln 2 (c_low / c) Q.
+// (the product is exact before the sum is rounded); what c's rounding takes from
+// the argument a, c_low d = (c_low / c) a, is added by a second one, and B's
+// is put right once, by the factor 2^-(m c - B).
 template <typename T, bool ENT, int NT, int U>
 __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid, float c, float c_low) {
     using VT = Vec<T>;
@@ -241,7 +199,7 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
 #pragma unroll
                 for (int i = 0; i < VE; i += 2) {
                     float2 g = ffma2(make_float2(f[i], f[i + 1]), c2, nb2);
-                    if (!ENT) g = ffma2(g, rho2, g);
+                    g = ffma2(g, rho2, g);
                     const float2 e = make_float2(ex2(g.x), ex2(g.y));
                     s2 = fadd2(s2, e);
                     if (ENT) q2 = ffma2(e, cut_argument<T>(g), q2);
@@ -255,7 +213,6 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
         st.Q = q2.x + q2.y;
         const float delta = fmaf(st.m, c, -B);
         if (ENT) {
-            st.S = fmaf(kLn2 * rho, st.Q, st.S);
             st.Q = fmaf(-delta, st.S, st.Q);
             st.Q = fmaf(-kLn2 * delta, st.Q, st.Q);
         }
@@ -265,37 +222,15 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
     return slice_stats_careful<T, ENT, NT>(vec, n, tid, c, c_low);
 }
 
-// A thread's part of a slice's gradient, 2^a (u0 + u1 a) with a = (x - m) c;
-// NEAR: a as x c - B, B = m c rounded, whose error goes into u0 and u1.
+// A thread's part of a slice's gradient.
 template <typename T, bool ENT, int NT, int U, bool NEAR>
 __device__ __forceinline__ void slice_gradient(const uint4* vec, uint4* dvec, int w0, int w1, int tid, float c,
-                                               float m, float u0, float u1) {
-    using VT = Vec<T>;
-    constexpr int VE = VT::N;
-    const float B = m * c;
-    if (NEAR) {
-        const float delta = fmaf(m, c, -B);
-        u0 = fmaf(-delta, u1, u0);
-        u0 = fmaf(-kLn2 * delta, u0, u0);
-        u1 = fmaf(-kLn2 * delta, u1, u1);
-    }
-    const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), nm2 = make_float2(-m, -m);
-    const float2 uu0 = make_float2(u0, u0), uu1 = make_float2(u1, u1);
+                                               const RowConst& k) {
+    const GradTerms<NEAR> t(c, k.m, k.u0, k.u1);
     auto grad = [&](const uint4& q) {
-        float f[VE];
-        unpack_cut<T, ENT && NEAR>(q, f);
-#pragma unroll
-        for (int i = 0; i < VE; i += 2) {
-            const float2 x = make_float2(f[i], f[i + 1]);
-            const float2 g = NEAR ? ffma2(x, c2, nb2) : fmul2(fadd2(x, nm2), c2);
-            const float2 e = make_float2(ex2(g.x), ex2(g.y));
-            float2 w = uu0;
-            if (ENT) w = ffma2(uu1, NEAR ? cut_argument<T>(g) : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)), uu0);
-            const float2 o = fmul2(e, w);
-            f[i] = o.x;
-            f[i + 1] = o.y;
-        }
-        return VT::pack(f);
+        float f[Vec<T>::N];
+        grad_vector<T, ENT, NEAR>(t, q, f);
+        return Vec<T>::pack(f);
     };
     int v = w0 + tid;
     if (NEAR) {
@@ -417,16 +352,16 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     // a buffer's mbarriers: filled; given back; its row's statistics are all
     // there; its row's constants are there
     __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], ready[kMaxBuf];
-    __shared__ __align__(8) uint64_t met[4], meeting;
+    __shared__ __align__(8) uint64_t met[kMeetings], meeting;
     // the lists' own ring, a slot a list warp: a list takes longer than a row
     __shared__ __align__(8) uint64_t listed[kLists], unlisted[kLists];
-    __shared__ RowPart parts[4][kMaxRowCluster];  // of the cluster's CTAs, for two rows of each statistics warp
+    __shared__ RowPart parts[kMeetings][kMaxRowCluster];  // of the cluster's CTAs
     __shared__ RowPart red[kMaxBuf][NW];          // of the warps
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
     __shared__ ListInfo linfo[OP == kRowDistill ? kLists : 1];
     __shared__ uint32_t seen[OP == kRowDistill ? kLists * 2 * kSeenWords : 1];
-    __shared__ double s_sum[2], red_d[NW + 3 + kLists];
+    __shared__ double s_sum, red_d[NW + 3 + kLists];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -447,18 +382,18 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     if (tid == 0) {
         for (int i = 0; i < NB; ++i) {
             mbar_init(smem_u32(&full[i]), 2);
-            mbar_init(smem_u32(&empty[i]), two ? NW : NW + 1);
+            mbar_init(smem_u32(&empty[i]), NW + 2);
             mbar_init(smem_u32(&together[i]), NW);
             mbar_init(smem_u32(&ready[i]), 1);
         }
         for (int i = 0; i < kLists; ++i) {
             mbar_init(smem_u32(&listed[i]), 1);
-            mbar_init(smem_u32(&unlisted[i]), two ? NW + 1 : 1);
+            mbar_init(smem_u32(&unlisted[i]), NW + 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&met[i]), 1);
+        for (int i = 0; i < kMeetings; ++i) mbar_init(smem_u32(&met[i]), 1);
         mbar_init(smem_u32(&meeting), NW);
         fence_mbar_init();
-        s_sum[0] = s_sum[1] = 0.0;
+        s_sum = 0.0;
     }
     if (OP == kRowDistill)
         for (int i = tid; i < kLists * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
@@ -497,7 +432,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
 
     if (warp == NW) {
         // ---------------------------------------------------------- producer
-        const uint64_t pol = l2_evict_first_policy();
+        const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
         auto token = [&](int64_t r) {
             return OP == kRowDistill ? load_index(a.index, a.idx64, r * a.K)
                                      : load_index(a.tokens, a.tok64, r);
@@ -547,7 +482,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                         const char* src = reinterpret_cast<const char*>(row + in.first + in.w0 * VE);
                         mbar_arrive_expect_tx(bar, bytes);
                         for (uint32_t o = 0; o < bytes; o += kBulk)
-                            bulk_g2s(dst + o, src + o, min(kBulk, bytes - o), bar, pol);
+                            bulk_g2s(dst + o, src + o, min(kBulk, bytes - o), bar, r < a.keep_from ? once : again);
                     } else {
                         mbar_arrive(bar);
                     }
@@ -618,26 +553,47 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             ahead();
         }
         if (ok && any) (void)store_listed();
-    } else if (warp > NW) {
+    } else if (warp == NW + 1) {
+        // ---------------------------------------------------------- a row's statistics from the CTA's
+        // warps, and on to every CTA of the cluster
+        int slot = 0;
+        for (int64_t r = first; r < a.p.rows; r += step, next()) {
+            if (!wait(&full[k], phase)) break;
+            if (info[k].t < 0) {
+                arrive(&empty[k]);
+                continue;
+            }
+            if (!wait(&together[k], phase)) break;
+            RowPart st = lane < NW ? red[k][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
+            arrive(&empty[k]);
+            part_warp<ENT, OP != kRowDistill>(st, a.c);
+            if (C > 1) {
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[slot]), 16u * C);
+                __syncwarp();
+                if (lane < C)
+                    st_async_v4(map_to_rank(smem_u32(&parts[slot][rank]), lane), st,
+                                map_to_rank(smem_u32(&met[slot]), lane));
+            } else {
+                if (lane == 0) parts[slot][0] = st;
+                arrive(&met[slot]);
+            }
+            slot = (slot + 1) % kMeetings;
+        }
+    } else if (warp == NW + 2) {
         // ---------------------------------------------------------- a row's statistics together, its
-        // outputs, and its gradient's constants: every second row each of two warps (the
-        // exchange between CTAs takes longer than a row; two slots of each warp's make it
-        // safe, for none sends for a row before it has all of the one before)
-        const int half = warp - NW - 1;
+        // outputs, and its gradient's constants (rows are on their way between the CTAs
+        // meanwhile: that takes about as long as a row)
         float scale = a.scale;
         bool have_scale = !two || a.reduction != kRedMean;
-        int slot = half;
-        uint32_t met_phase = 0;  // bit i: parity of met[i]'s next completion
+        int slot = 0;
+        uint32_t met_phase = 0;  // how often the slots came round, modulo 2
         const bool out = rank == 0 && lane == 0;
         float sum = 0.f, sum_low = 0.f;  // (two parts: 48 bits)
-        int64_t r = first;
-        if (half) {
-            r += step;
-            next();
-        }
-        for (; r < a.p.rows; r += 2 * step, next(), next()) {
+        for (int64_t r = first; r < a.p.rows; r += step, next()) {
             if (!wait(&full[k], phase)) break;
             const RowInfo in = info[k];
+            arrive(&empty[k]);
+            if (OP == kRowDistill && !wait(&listed[l], list_phase)) break;
             if (in.t < 0) {
                 if (out) {
                     if (in.bad) atomicOr(a.status, kDevErrTarget);
@@ -649,27 +605,15 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                         if (a.clipped) a.clipped[r] = 0;
                     }
                 }
-                if (!two) arrive(&empty[k]);
                 if (OP == kRowDistill) arrive(&unlisted[l]);
                 continue;
             }
-            if (!wait(&together[k], phase)) break;
-            RowPart st = lane < NW ? red[k][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-            if (!two) arrive(&empty[k]);
-            if (OP == kRowDistill && !wait(&listed[l], list_phase)) break;
+            if (timed_out(mbar_wait_cluster(smem_u32(&met[slot]), met_phase, a.timeout_ns))) break;
+            RowPart st = lane < C ? parts[slot][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
             part_warp<ENT, OP != kRowDistill>(st, a.c);
-            if (C > 1) {
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[slot]), 16u * C);
-                __syncwarp();
-                if (lane < C)
-                    st_async_v4(map_to_rank(smem_u32(&parts[slot][rank]), lane), st,
-                                map_to_rank(smem_u32(&met[slot]), lane));
-                if (timed_out(mbar_wait_cluster(smem_u32(&met[slot]), (met_phase >> slot) & 1u, a.timeout_ns)))
-                    break;
-                met_phase ^= 1u << slot;
-                st = lane < C ? parts[slot][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-                part_warp<ENT, OP != kRowDistill>(st, a.c);
-                slot ^= 2;
+            if (++slot == kMeetings) {
+                slot = 0;
+                met_phase ^= 1u;
             }
             if (!have_scale) {
                 pdl_wait();
@@ -759,7 +703,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 }
             }
         }
-        if (out) s_sum[half] = static_cast<double>(sum) + static_cast<double>(fabsf(sum) < INFINITY ? sum_low : 0.f);
+        if (out) s_sum = static_cast<double>(sum) + static_cast<double>(fabsf(sum) < INFINITY ? sum_low : 0.f);
     } else {
         // ---------------------------------------------------------- consumers
         uint32_t given = 0;  // bit i: parity of ready[i]'s next completion
@@ -782,9 +726,9 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
             uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
             if (fabsf(kc.m) < kFarLogit)
-                slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, kc.m, kc.u0, kc.u1);
+                slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, kc);
             else
-                slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, kc.m, kc.u0, kc.u1);
+                slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, kc);
             auto element = [&](float x) {
                 const float g = (x - kc.m) * a.c;
                 return ex2(g) * (ENT ? fmaf(kc.u1, fmaxf(g, -256.f), kc.u0) : kc.u0);
@@ -816,11 +760,13 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             const RowInfo& in = info[k];
             const int n = in.n, slice0 = in.first, t = in.t;
             unsigned char* buf = smem + static_cast<size_t>(k) * a.buf_bytes;
+            if (OP == kRowDistill) {  // (each list, so that its parity says which one it is)
+                ok = wait(&listed[l], list_phase);
+                if (!ok) break;
+            }
             if (t >= 0) {
                 if (tail) {
                     // the classes of the list leave the row: the sum is that of the others
-                    ok = wait(&listed[l], list_phase);
-                    if (!ok) break;
                     const int* classes = list_of(l).j;
                     for (int e = tid; e < a.K; e += NT) {
                         const int j = classes[e];
@@ -841,7 +787,10 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 }
                 if (lane == 0) red[k][warp] = st;
                 arrive(&together[k]);
-                if (!two) arrive(&empty[k]);
+                if (!two) {
+                    if (OP == kRowDistill) arrive(&unlisted[l]);
+                    arrive(&empty[k]);
+                }
             }
             if (two) {
                 if (waiting >= 0) {
@@ -865,7 +814,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                     if (warp == NW - 1 && v >= 0 && (lane & 7) < VE && j >= 0 && j < a.p.V)
                         VT::store1(drow, j, 0.f);
                 }
-                if (OP == kRowDistill && two) arrive(&unlisted[l]);
+                if (OP == kRowDistill) arrive(&unlisted[l]);
                 arrive(&together[k]);  // (its phases go with the ring)
                 arrive(&empty[k]);
             }
@@ -875,7 +824,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     if (OP != kRowLogp && a.reduction != kRedNone) {
         pdl_wait();
         __syncthreads();
-        if (rank == 0) rows_finish(a, s_sum[0] + s_sum[1], static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
+        if (rank == 0) rows_finish(a, s_sum, static_cast<int>(step), static_cast<int>(first), red_d, &s_flag);
     }
     // no CTA leaves while another may still send to it
     __syncthreads();

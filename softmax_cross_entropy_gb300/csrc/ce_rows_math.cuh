@@ -1,0 +1,93 @@
+// Element arithmetic that the token losses' kernels share.
+#pragma once
+
+#include <type_traits>
+
+#include "ce_rows.cuh"
+
+namespace gbce {
+
+// Logits beyond this (masks of a type's lowest value, mostly) take the
+// careful forms below: times log2(e) / T they could overflow.
+constexpr float kFarLogit = 1e18f;
+
+// Products with an element's argument where 2^argument is 0: the logits are
+// cut at -1e30 (bf16 pairs in one instruction), or, where -inf is not far from
+// the type's other values, the arguments at -256.
+template <typename T>
+constexpr bool kCutLogits = !std::is_same<T, __half>::value;
+
+template <typename T>
+__device__ __forceinline__ uint4 at_least(const uint4& q) {
+    uint4 o;
+    const uint32_t* w = &q.x;
+    uint32_t* z = &o.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            float m;  // (a NaN stays)
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(w[i])), "f"(-1e30f));
+            z[i] = __float_as_uint(m);
+        } else {
+            const __nv_bfloat16 low = __ushort_as_bfloat16(0xF149u);
+            const __nv_bfloat162 v =
+                __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), __halves2bfloat162(low, low));
+            z[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    return o;
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void unpack_cut(const uint4& q, float (&f)[Vec<T>::N]) {
+    if constexpr (ENT && kCutLogits<T>)
+        Vec<T>::unpack(at_least<T>(q), f);
+    else
+        Vec<T>::unpack(q, f);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 cut_argument(float2 g) {
+    return kCutLogits<T> ? g : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f));
+}
+
+// The constants of a vector's gradient 2^a (u0 + u1 a), a = (x - m) c; NEAR (m
+// below kFarLogit): a as x c - B, B = m c rounded, whose error goes into u0
+// and u1.
+template <bool NEAR>
+struct GradTerms {
+    float2 c2, b2, uu0, uu1;
+    __device__ __forceinline__ GradTerms(float c, float m, float u0, float u1) {
+        const float B = m * c;
+        if (NEAR) {
+            const float delta = fmaf(m, c, -B);
+            u0 = fmaf(-delta, u1, u0);
+            u0 = fmaf(-kLn2 * delta, u0, u0);
+            u1 = fmaf(-kLn2 * delta, u1, u1);
+        }
+        c2 = make_float2(c, c);
+        b2 = NEAR ? make_float2(-B, -B) : make_float2(-m, -m);
+        uu0 = make_float2(u0, u0);
+        uu1 = make_float2(u1, u1);
+    }
+};
+
+template <typename T, bool ENT, bool NEAR>
+__device__ __forceinline__ void grad_vector(const GradTerms<NEAR>& t, const uint4& q, float (&f)[Vec<T>::N]) {
+    unpack_cut<T, ENT && NEAR>(q, f);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; i += 2) {
+        const float2 x = make_float2(f[i], f[i + 1]);
+        const float2 g = NEAR ? ffma2(x, t.c2, t.b2) : fmul2(fadd2(x, t.b2), t.c2);
+        const float2 e = make_float2(ex2(g.x), ex2(g.y));
+        float2 w = t.uu0;
+        if (ENT)
+            w = ffma2(t.uu1, NEAR ? cut_argument<T>(g) : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f)),
+                      t.uu0);
+        const float2 o = fmul2(e, w);
+        f[i] = o.x;
+        f[i + 1] = o.y;
+    }
+}
+
+}  // namespace gbce

@@ -303,6 +303,16 @@ def test_tangents_and_second_derivatives_are_refused(monkeypatch):
 
 # ---------------------------------------------------------------- GPU
 
+@pytest.fixture(autouse=True)
+def no_device_errors(request):
+    """Nothing was recorded on the device: no wait ran out, no token out of range."""
+    yield
+    if request.node.get_closest_marker("gpu"):
+        import softmax_cross_entropy_gb300 as gbce
+        from softmax_cross_entropy_gb300 import _lib
+        assert gbce.device_status() == _lib.CE_OK
+
+
 def put(x64, dtype, how="plain"):
     """(logits on the GPU, the values they hold in 64 bits [rows, V])."""
     t = torch.from_numpy(x64).to(DT[dtype])
@@ -854,6 +864,105 @@ def test_factors_on_the_loss(name, dtype):
     with torch.enable_grad():
         (f(x) * 0.5 + f(x) * 0.5).backward()
     assert torch.allclose(x.grad.float(), one.float(), rtol=2.0 ** -7, atol=0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("B,T,V,dtype", [(8, 700, 1000, "bf16"), (6, 601, 4099, "f16"),
+                                         (4, 600, 9000, "f32"), (2, 700, 40000, "bf16"),
+                                         (2, 300, 70001, "f32"), (2, 250, 131072, "bf16")])
+def test_runs_of_rows_that_do_not_count(B, T, V, dtype, entropy):
+    """Many rows a CTA, prompts and padding among them in runs: every loss against 64 bits."""
+    import softmax_cross_entropy_gb300 as gbce
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = (torch.randn(B, T, V, generator=g, device="cuda") * 2).to(DT[dtype]).requires_grad_()
+    tok = torch.randint(V, (B, T), generator=g, device="cuda")
+    start = torch.randint(T // 3, (B, 1), generator=g, device="cuda")
+    at = torch.arange(T, device="cuda")[None]
+    tok[(at < start) | (at > start + T // 2)] = IGN
+    tok[:, T // 2] = IGN
+    keep = tok != IGN
+    K = 20
+    idx = torch.randint(V, (B, T, K), generator=g, device="cuda")
+    idx[~keep] = -1
+    val = torch.randn(B, T, K, generator=g, device="cuda")
+    adv = torch.randn(B, T, generator=g, device="cuda")
+    lsm = torch.log_softmax(x.detach().double(), -1)
+    p = lsm.exp()
+    onto = torch.zeros_like(p).scatter_(-1, tok.clamp(min=0)[..., None], 1.0)
+    lp = torch.where(keep, lsm.gather(-1, tok.clamp(min=0)[..., None])[..., 0], 0.0)
+    h = torch.where(keep, -(p * lsm).sum(-1), 0.0)
+    n = int(keep.sum())
+    near = dict(rtol=2.0 ** -19, atol=2.0 ** -18)
+
+    def same(dx, c, hc=None):
+        want = c[..., None] * (onto - p)
+        size = c.abs()
+        if hc is not None:
+            want = want - hc[..., None] * p * (lsm + h[..., None])
+            size = size + hc.abs() * 30
+        eps = torch.finfo(DT[dtype]).eps / 2
+        tiny = torch.finfo(DT[dtype]).smallest_normal * eps
+        tol = want.abs() * eps + size[..., None] * (p + onto * 2.0 ** -5) * 2.0 ** -14 + tiny
+        assert bool(((dx.double() - want).abs() <= tol).all())
+        assert plus_zero(dx[~keep])
+
+    got = gbce.token_log_probs(x, tok, return_entropy=entropy)
+    glp, gh = got if entropy else (got, None)
+    assert torch.allclose(glp.double(), lp, **near)
+    assert gh is None or torch.allclose(gh.double(), h, **near)
+    up = torch.randn(B, T, generator=g, device="cuda")
+    ups = [up, up * 0.1] if entropy else [up]
+    dx, = torch.autograd.grad([glp, gh] if entropy else [glp], x, ups)
+    c = torch.where(keep, up.double(), 0.0)
+    same(dx, c, c * 0.1 if entropy else None)
+    coef = 0.02 if entropy else 0.0
+    for scale in (64.0,):
+        loss = gbce.policy_loss(x, tok, adv, entropy_coef=coef, scale=scale)
+        want = torch.where(keep, -adv.double() - coef * h, 0.0).sum() * scale / n
+        assert torch.allclose(loss.double(), want, rtol=2.0 ** -18, atol=scale * 2.0 ** -18)
+        dx, = torch.autograd.grad(loss, x)
+        f = keep * scale / n
+        same(dx, -adv.double() * f, -coef * f.double() if entropy else None)
+    with torch.no_grad():
+        assert torch.equal(gbce.policy_loss(x, tok, adv, entropy_coef=coef, scale=64.0), loss)
+    # distillation: the list's mass, and with the remaining mass as one outcome more
+    lse = torch.logsumexp(val.double(), -1).float() + 0.5 if entropy else None
+    lq = val.double() - (torch.logsumexp(val.double(), -1) if lse is None else lse.double())[..., None]
+    q = lq.exp()
+    j = idx.clamp(min=0)
+    rows = (q * (lq - lsm.gather(-1, j))).sum(-1)
+    want = p * q.sum(-1, keepdim=True)
+    want = want.scatter_add(-1, j, -q)
+    if lse is not None:
+        rest = 1 - q.sum(-1)
+        others = p.scatter(-1, j, 0.0)
+        left = others.sum(-1)
+        rows = rows + rest * (rest.log() - left.log())
+        want = want + rest[..., None] * p - others * (rest / left)[..., None]
+    loss = gbce.distillation_loss(x, val, idx, teacher_lse=lse, scale=64.0)
+    total = torch.where(keep, rows, 0.0).sum() * 64 / n
+    assert torch.allclose(loss.double(), total, rtol=2.0 ** -18)
+    dx, = torch.autograd.grad(loss, x)
+    want = torch.where(keep[..., None], want, 0.0) * 64 / n
+    eps = torch.finfo(DT[dtype]).eps / 2
+    tiny = torch.finfo(DT[dtype]).smallest_normal * eps
+    named = torch.zeros_like(p).scatter_(-1, j, 1.0)
+    tol = want.abs() * eps + 64 / n * (2 * p + named * 2.0 ** -5) * 2.0 ** -14 + tiny
+    assert bool(((dx.double() - want).abs() <= tol).all())
+    assert plus_zero(dx[~keep])
+    with torch.no_grad():
+        assert torch.equal(gbce.distillation_loss(x, val, idx, teacher_lse=lse, scale=64.0), loss)
+    # pairs
+    out = gbce.preference_loss(x, tok, beta=0.1, scale=64.0, return_scores=True)
+    s = lp.sum(1)
+    assert torch.allclose(out.scores.double(), s, rtol=2.0 ** -20, atol=n * 2.0 ** -20)
+    d = s[:B // 2] - s[B // 2:]
+    dx, = torch.autograd.grad(out.loss, x)
+    sl = 0.1 * (torch.sigmoid(0.1 * d) - 1) * 64 / (B // 2)
+    c = torch.where(keep, torch.cat([sl, -sl])[:, None].double(), 0.0)
+    same(dx, c)
 
 
 @pytest.mark.gpu
