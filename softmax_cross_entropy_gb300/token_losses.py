@@ -20,11 +20,11 @@ libgbce.so; there is no CPU fallback.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 from collections import namedtuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._tensors import DTYPES, check, forward_mode, on, once, plain, ptr, require_cuda, stream
@@ -52,7 +52,7 @@ def _rows_of(t):
     if t.is_contiguous():
         rows = t.numel() // V
         return rows, max(rows, 1), 0, V
-    if t.is_neg() or (V > 1 and t.stride(-1) != 1):
+    if V > 1 and t.stride(-1) != 1:
         return None
     levels = []  # (count, stride) from the innermost on
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
@@ -72,23 +72,22 @@ def _rows_of(t):
 
 
 def _logits(logits, inplace):
-    """logits with rows that the kernels take (a copy where they have others)."""
+    """logits with rows that the kernels take (a copy where they have others),
+    and their layout."""
     require_cuda(logits, "logits")
     if logits.dim() < 2 or logits.shape[-1] < 1:
         raise ValueError("logits must be [..., V] with at least two dimensions and V >= 1")
     if logits.dtype not in DTYPES:
         raise TypeError(f"logits dtype {logits.dtype} is not supported "
                         "(float32, bfloat16, float16)")
-    if _rows_of(logits) is None:
+    layout = None if logits.is_neg() else _rows_of(logits)
+    if layout is None:
         if inplace:
-            raise ValueError("logits whose rows are not evenly spaced, apart and contiguous "
-                             "cannot take their gradient in place")
-        return plain(logits)
-    if logits.is_neg():  # (contiguous)
-        if inplace:
-            raise ValueError("logits that defer a negation cannot take their gradient in place")
-        return plain(logits)
-    return logits
+            raise ValueError("logits whose rows are not evenly spaced, apart and contiguous (or "
+                             "that defer a negation) cannot take their gradient in place")
+        logits = plain(logits)
+        layout = _rows_of(logits)
+    return logits, layout
 
 
 def _tokens(tokens, shape, device, name="tokens"):
@@ -109,11 +108,13 @@ def _floats(t, shape, device, name):
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on the logits' device")
-    if not t.is_floating_point():
-        raise TypeError(f"{name} must be floating-point")
+    if t.dtype is not torch.float32:
+        if not t.is_floating_point():
+            raise TypeError(f"{name} must be floating-point")
+        t = t.float()
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} takes no gradient: detach it")
-    return plain(t if t.dtype is torch.float32 else t.float())
+    return plain(t)
 
 
 def _number(v, name, low=-math.inf):
@@ -137,38 +138,47 @@ def _reduction(name):
     return _REDUCTIONS[name]
 
 
-def _differentiates(*tensors):
-    """Whether a call goes through its autograd Function (which also refuses tangents)."""
-    return forward_mode() or (torch.is_grad_enabled() and tensors[0].requires_grad)
+def _differentiates(logits, *others):
+    """Whether a call goes through its autograd Function (which refuses logits
+    with a tangent; the other tensors, which it does not see, are looked at here)."""
+    if forward_mode():
+        for t in others:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("the token losses have no forward-mode derivative")
+        return True
+    return torch.is_grad_enabled() and logits.requires_grad
 
 
 def _flags(tokens):
     return _lib.CE_FLAG_TARGET_I64 if tokens.dtype == torch.int64 else 0
 
 
-def _table(logits, grad, temperature=1.0):
+def _table(logits, grad, layout, temperature=1.0):
     """ce_rows of logits and their gradient."""
-    rows, inner, outer, step = _rows_of(logits)
-    return ctypes.byref(_lib.Rows(ptr(logits), ptr(grad), DTYPES[logits.dtype], temperature, rows,
-                                  logits.shape[-1], inner, outer, step))
+    return _lib.Rows(logits.data_ptr(), None if grad is None else grad.data_ptr(),
+                     DTYPES[logits.dtype], temperature, layout[0], logits.shape[-1], *layout[1:])
 
 
-def _gradient_like(logits):
+def _gradient_like(logits, layout):
     """An empty gradient: logits' strides, and their place within 16 bytes, so
     that both are read and written in whole vectors."""
     off = logits.data_ptr() % 16
     if off == 0 and logits.is_contiguous():
         return torch.empty_like(logits, memory_format=torch.contiguous_format)
-    rows, inner, outer, step = _rows_of(logits)
+    rows, inner, outer, step = layout
     span = (rows // max(inner, 1) - 1) * outer + (inner - 1) * step + logits.shape[-1] if rows else 0
     off //= logits.element_size()
     flat = torch.empty(span + off, dtype=logits.dtype, device=logits.device)
     return flat.as_strided(logits.shape, logits.stride(), off)
 
 
+_work_bytes = 0
+
+
 def _workspace(device):
-    n = _lib.ce_rows_workspace_bytes()
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    global _work_bytes
+    _work_bytes = _work_bytes or _lib.ce_rows_workspace_bytes()
+    return torch.empty(_work_bytes, dtype=torch.uint8, device=device), _work_bytes
 
 
 def _overwritten(logits):
@@ -179,13 +189,13 @@ def _overwritten(logits):
 
 # ---------------------------------------------------------------- log-probabilities
 
-def _log_probs(logits, tokens, temperature, ignore_index, want_entropy, keep):
+def _log_probs(logits, layout, tokens, temperature, ignore_index, want_entropy, keep):
     dev = logits.device
     logp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
     entropy = torch.empty(tokens.shape, dtype=torch.float32, device=dev) if want_entropy else None
     kept = torch.empty((tokens.numel(), 4), dtype=torch.float32, device=dev) if keep else None
     with on(dev):
-        check(_lib.ce_token_logp(_table(logits, None, temperature), ptr(tokens), ignore_index,
+        check(_lib.ce_token_logp(_table(logits, None, layout, temperature), ptr(tokens), ignore_index,
                                  _flags(tokens), ptr(logp), ptr(entropy), ptr(kept), stream(dev)),
               "ce_token_logp")
     return logp, entropy, kept
@@ -196,14 +206,14 @@ class TokenLogProbsFunction(torch.autograd.Function):
     keeps the logits and 16 bytes a row."""
 
     @staticmethod
-    def forward(ctx, logits, tokens, temperature, ignore_index, want_entropy, inplace):
+    def forward(ctx, logits, tokens, layout, temperature, ignore_index, want_entropy, inplace):
         ctx.set_materialize_grads(False)
         grad = ctx.needs_input_grad[0]
-        logp, entropy, kept = _log_probs(logits, tokens, temperature, ignore_index, want_entropy,
-                                         grad)
+        logp, entropy, kept = _log_probs(logits, layout, tokens, temperature, ignore_index,
+                                         want_entropy, grad)
         if grad:
             ctx.save_for_backward(logits, tokens, kept)
-            ctx.args = temperature, ignore_index, inplace
+            ctx.args = layout, temperature, ignore_index, inplace
         return logp, entropy
 
     @staticmethod
@@ -211,18 +221,18 @@ class TokenLogProbsFunction(torch.autograd.Function):
         given = [d for d in (d_logp, d_entropy) if d is not None]
         for d in given:
             once("token_log_probs", d)
-        none = (None,) * 5
+        none = (None,) * 6
         if not given or not ctx.needs_input_grad[0]:
             return None, *none
         logits, tokens, kept = ctx.saved_tensors
-        temperature, ignore_index, inplace = ctx.args
+        layout, temperature, ignore_index, inplace = ctx.args
         d_logp, d_entropy = (None if d is None else plain(d.float()) for d in (d_logp, d_entropy))
-        dx = logits.detach() if inplace else _gradient_like(logits)
+        dx = logits.detach() if inplace else _gradient_like(logits, layout)
         dev = logits.device
         with on(dev):
-            check(_lib.ce_token_logp_bwd(_table(logits, dx, temperature), ptr(tokens), ignore_index,
-                                         _flags(tokens), ptr(kept), ptr(d_logp), ptr(d_entropy),
-                                         stream(dev)), "ce_token_logp_bwd")
+            check(_lib.ce_token_logp_bwd(_table(logits, dx, layout, temperature), ptr(tokens),
+                                         ignore_index, _flags(tokens), ptr(kept), ptr(d_logp),
+                                         ptr(d_entropy), stream(dev)), "ce_token_logp_bwd")
         if inplace:
             _overwritten(logits)
         return dx, *none
@@ -237,31 +247,33 @@ def token_log_probs(logits, tokens, temperature=1.0, ignore_index=-100, return_e
 
     return_entropy: returns TokenLogProbs(log_probs, entropy), entropy that of
     softmax(logits / temperature); both are differentiable."""
-    logits = _logits(logits, inplace)
+    logits, layout = _logits(logits, inplace)
     tokens = _tokens(tokens, logits.shape[:-1], logits.device)
     temperature, ignore_index = _temperature(temperature), int(ignore_index)
     want_entropy = bool(return_entropy)
     if _differentiates(logits):
-        logp, entropy = TokenLogProbsFunction.apply(logits, tokens, temperature, ignore_index,
-                                                    want_entropy, bool(inplace))
+        logp, entropy = TokenLogProbsFunction.apply(logits, tokens, layout, temperature,
+                                                    ignore_index, want_entropy, bool(inplace))
     else:
-        logp, entropy, _ = _log_probs(logits, tokens, temperature, ignore_index, want_entropy,
-                                      False)
+        logp, entropy, _ = _log_probs(logits, layout, tokens, temperature, ignore_index,
+                                      want_entropy, False)
     return TokenLogProbs(logp, entropy) if want_entropy else logp
 
 
 # ---------------------------------------------------------------- gradients of the forward
 
-def _forward_gradient(ctx, logits, call, inplace):
-    """Runs call(dx) with the place of the gradient, which it keeps for the backward."""
+def _forward_gradient(ctx, logits, layout, call, args, inplace):
+    """Runs call(logits, dx, layout, *args) with the place dx of the gradient,
+    which it keeps for the backward."""
+    ctx.set_materialize_grads(False)
     if not ctx.needs_input_grad[0]:
-        return call(None)
-    dx = logits.detach() if inplace else _gradient_like(logits)
-    out = call(dx)
+        return call(logits, None, layout, *args)
+    dx = logits.detach() if inplace else _gradient_like(logits, layout)
+    out = call(logits, dx, layout, *args)
     if inplace:
         _overwritten(logits)
     ctx.save_for_backward(dx)
-    ctx.spent = False
+    ctx.layout = layout
     return out
 
 
@@ -271,18 +283,19 @@ def _scaled_gradient(ctx, d_loss, name):
         return None
     once(name, d_loss)
     (dx,) = ctx.saved_tensors
-    if ctx.spent:
+    layout, ctx.layout = ctx.layout, None
+    if layout is None:
         raise RuntimeError(f"{name}'s gradient was given to an earlier backward")
-    ctx.spent = True
-    g, dev = plain(d_loss.float()), dx.device
+    g, dev = plain(d_loss), dx.device
     with on(dev):
-        check(_lib.ce_rows_scale(_table(dx, dx), ptr(g), 1 if g.dim() else 0, stream(dev)), "ce_rows_scale")
+        check(_lib.ce_rows_scale(_table(dx, dx, layout), g.data_ptr(), 1 if g.dim() else 0,
+                                 stream(dev)), "ce_rows_scale")
     return dx
 
 
 # ---------------------------------------------------------------- policy loss
 
-def _policy(logits, dx, tokens, advantages, advantage_rows, old, ref, weight, temperature,
+def _policy(logits, dx, layout, tokens, advantages, advantage_rows, old, ref, weight, temperature,
             ignore_index, clip_low, clip_high, kl_coef, entropy_coef, scale, red, stats):
     dev, shape = logits.device, tokens.shape
     f32 = dict(dtype=torch.float32, device=dev)
@@ -293,8 +306,9 @@ def _policy(logits, dx, tokens, advantages, advantage_rows, old, ref, weight, te
         clipped = torch.empty(shape, dtype=torch.bool, device=dev)
     with on(dev):
         ws, nbytes = _workspace(dev)
-        check(_lib.ce_policy_loss(_table(logits, dx, temperature), ptr(tokens), ignore_index,
-                                  _flags(tokens), ptr(advantages), advantage_rows, ptr(old),
+        check(_lib.ce_policy_loss(_table(logits, dx, layout, temperature), ptr(tokens),
+                                  ignore_index, _flags(tokens), ptr(advantages),
+                                  advantage_rows, ptr(old),
                                   ptr(ref), ptr(weight), clip_low, clip_high, kl_coef, entropy_coef,
                                   scale, red, ptr(loss), ptr(logp), ptr(entropy), ptr(kl),
                                   ptr(clipped), ptr(ws), nbytes, stream(dev)), "ce_policy_loss")
@@ -306,18 +320,15 @@ class PolicyLossFunction(torch.autograd.Function):
     buffer (with inplace, in the logits), which the backward scales."""
 
     @staticmethod
-    def forward(ctx, logits, tokens, advantages, old, ref, weight, inplace, args):
-        ctx.set_materialize_grads(False)
-        out = _forward_gradient(
-            ctx, logits,
-            lambda dx: _policy(logits, dx, tokens, advantages, args[0], old, ref, weight,
-                               *args[1:]), inplace)
-        ctx.mark_non_differentiable(*(t for t in out[1:] if t is not None))
+    def forward(ctx, logits, layout, inplace, args):
+        out = _forward_gradient(ctx, logits, layout, _policy, args, inplace)
+        if out[1] is not None:
+            ctx.mark_non_differentiable(*out[1:])
         return out
 
     @staticmethod
     def backward(ctx, d_loss, *unused):
-        return (_scaled_gradient(ctx, d_loss, "policy_loss"),) + (None,) * 7
+        return _scaled_gradient(ctx, d_loss, "policy_loss"), None, None, None
 
 
 def policy_loss(logits, tokens, advantages, old_log_probs=None, ref_log_probs=None, weight=None,
@@ -343,45 +354,48 @@ def policy_loss(logits, tokens, advantages, old_log_probs=None, ref_log_probs=No
 
     return_stats: PolicyLossOutput(loss, log_probs, entropy, kl, clipped), the
     last four a value a token, without gradients."""
-    logits = _logits(logits, inplace)
+    logits, layout = _logits(logits, inplace)
     dev, shape = logits.device, logits.shape[:-1]
     tokens = _tokens(tokens, shape, dev)
     if not isinstance(advantages, torch.Tensor):
         raise ValueError("advantages must be a tensor")
-    lead = list(advantages.shape)
-    while lead and lead[-1] == 1 and lead != list(shape[:len(lead)]):
-        lead.pop()
-    if lead != list(shape[:len(lead)]) or (not lead and shape.numel() != 1) or \
-            advantages.dim() > len(shape):
-        raise ValueError("advantages must have tokens' shape, or that of its first dimensions")
+    if advantages.shape == shape:
+        advantage_rows = 1
+    else:
+        lead = list(advantages.shape)
+        while lead and lead[-1] == 1 and lead != list(shape[:len(lead)]):
+            lead.pop()
+        if lead != list(shape[:len(lead)]) or (not lead and shape.numel() != 1) or \
+                advantages.dim() > len(shape):
+            raise ValueError("advantages must have tokens' shape, or that of its first dimensions")
+        advantage_rows = max(1, math.prod(shape[len(lead):]))
     advantages = _floats(advantages, advantages.shape, dev, "advantages")
-    advantage_rows = max(1, math.prod(shape[len(lead):]))
     old = _floats(old_log_probs, shape, dev, "old_log_probs")
     ref = _floats(ref_log_probs, shape, dev, "ref_log_probs")
     weight = _floats(weight, shape, dev, "weight")
     clip_low, clip_high = float(clip_low), float(clip_high)
     if not 0.0 <= clip_low <= 1.0 or not clip_high >= 0.0:
         raise ValueError("clip_low must lie in [0, 1] and clip_high be at least 0")
-    args = (advantage_rows, _temperature(temperature), int(ignore_index), clip_low, clip_high,
-            _number(kl_coef, "kl_coef"), _number(entropy_coef, "entropy_coef"),
-            _number(scale, "scale"), _reduction(reduction), bool(return_stats))
-    if _differentiates(logits):
-        out = PolicyLossFunction.apply(logits, tokens, advantages, old, ref, weight, bool(inplace),
-                                       args)
+    args = (tokens, advantages, advantage_rows, old, ref, weight, _temperature(temperature),
+            int(ignore_index), clip_low, clip_high, _number(kl_coef, "kl_coef"),
+            _number(entropy_coef, "entropy_coef"), _number(scale, "scale"), _reduction(reduction),
+            bool(return_stats))
+    if _differentiates(logits, advantages, old, ref, weight):
+        out = PolicyLossFunction.apply(logits, layout, bool(inplace), args)
     else:
-        out = _policy(logits, None, tokens, advantages, args[0], old, ref, weight, *args[1:])
+        out = _policy(logits, None, layout, *args)
     return PolicyLossOutput(*out) if return_stats else out[0]
 
 
 # ---------------------------------------------------------------- distillation
 
-def _distill(logits, dx, teacher, index, teacher_lse, weight, temperature, scale, red):
+def _distill(logits, dx, layout, teacher, index, teacher_lse, weight, temperature, scale, red):
     dev = logits.device
     loss = torch.empty(logits.shape[:-1] if red == _lib.CE_RED_NONE else (), dtype=torch.float32,
                        device=dev)
     with on(dev):
         ws, nbytes = _workspace(dev)
-        check(_lib.ce_distill_loss(_table(logits, dx, temperature), ptr(teacher),
+        check(_lib.ce_distill_loss(_table(logits, dx, layout, temperature), ptr(teacher),
                                    DTYPES[teacher.dtype], ptr(index), index.shape[-1],
                                    ptr(teacher_lse), _flags(index), ptr(weight), scale, red,
                                    ptr(loss), ptr(ws), nbytes, stream(dev)), "ce_distill_loss")
@@ -392,16 +406,12 @@ class DistillationLossFunction(torch.autograd.Function):
     """Autograd wrapper of ce_distill_loss, as PolicyLossFunction."""
 
     @staticmethod
-    def forward(ctx, logits, teacher, index, teacher_lse, weight, inplace, args):
-        ctx.set_materialize_grads(False)
-        loss = _forward_gradient(
-            ctx, logits,
-            lambda dx: _distill(logits, dx, teacher, index, teacher_lse, weight, *args), inplace)
-        return loss
+    def forward(ctx, logits, layout, inplace, args):
+        return _forward_gradient(ctx, logits, layout, _distill, args, inplace)
 
     @staticmethod
     def backward(ctx, d_loss):
-        return (_scaled_gradient(ctx, d_loss, "distillation_loss"),) + (None,) * 6
+        return _scaled_gradient(ctx, d_loss, "distillation_loss"), None, None, None
 
 
 def distillation_loss(logits, teacher_logits, teacher_indices, teacher_lse=None, temperature=1.0,
@@ -420,7 +430,7 @@ def distillation_loss(logits, teacher_logits, teacher_indices, teacher_lse=None,
     negative does not count: it is not read, and its gradient is zero.
     weight, scale and reduction as for policy_loss (scale=temperature ** 2
     keeps the gradients' size)."""
-    logits = _logits(logits, inplace)
+    logits, layout = _logits(logits, inplace)
     dev, shape = logits.device, logits.shape[:-1]
     if not isinstance(teacher_indices, torch.Tensor) or teacher_indices.dim() != len(shape) + 1 or \
             teacher_indices.shape[-1] < 1:
@@ -437,16 +447,16 @@ def distillation_loss(logits, teacher_logits, teacher_indices, teacher_lse=None,
     teacher = plain(teacher_logits)
     teacher_lse = _floats(teacher_lse, shape, dev, "teacher_lse")
     weight = _floats(weight, shape, dev, "weight")
-    args = (_temperature(temperature), _number(scale, "scale"), _reduction(reduction))
-    if _differentiates(logits):
-        return DistillationLossFunction.apply(logits, teacher, index, teacher_lse, weight,
-                                              bool(inplace), args)
-    return _distill(logits, None, teacher, index, teacher_lse, weight, *args)
+    args = (teacher, index, teacher_lse, weight, _temperature(temperature),
+            _number(scale, "scale"), _reduction(reduction))
+    if _differentiates(logits, teacher, teacher_lse, weight):
+        return DistillationLossFunction.apply(logits, layout, bool(inplace), args)
+    return _distill(logits, None, layout, *args)
 
 
 # ---------------------------------------------------------------- preference loss
 
-def _preference(logits, tokens, offsets, ref, ignore_index, pairs, kind, beta, margin, smoothing,
+def _preference(logits, layout, tokens, offsets, ref, ignore_index, pairs, kind, beta, margin, smoothing,
                 average, scale, red, grad):
     dev = logits.device
     f32 = dict(dtype=torch.float32, device=dev)
@@ -456,7 +466,7 @@ def _preference(logits, tokens, offsets, ref, ignore_index, pairs, kind, beta, m
     kept = torch.empty((tokens.numel(), 4), **f32)
     with on(dev):
         ws, nbytes = _workspace(dev)
-        check(_lib.ce_preference_loss(_table(logits, None), ptr(tokens), ignore_index,
+        check(_lib.ce_preference_loss(_table(logits, None, layout), ptr(tokens), ignore_index,
                                       _flags(tokens), pairs, ptr(offsets), ptr(ref), kind, beta,
                                       margin, smoothing, average, scale, red, ptr(loss),
                                       ptr(scores), ptr(dscore), ptr(kept), ptr(ws), nbytes,
@@ -469,33 +479,34 @@ class PreferenceLossFunction(torch.autograd.Function):
     keeps the logits and 16 bytes a row."""
 
     @staticmethod
-    def forward(ctx, logits, tokens, offsets, ref, inplace, args):
+    def forward(ctx, logits, tokens, offsets, layout, ref, inplace, args):
         ctx.set_materialize_grads(False)
         grad = ctx.needs_input_grad[0]
-        loss, scores, dscore, kept = _preference(logits, tokens, offsets, ref, *args, grad)
+        loss, scores, dscore, kept = _preference(logits, layout, tokens, offsets, ref[0], *args,
+                                                 grad)
         if grad:
             ctx.save_for_backward(logits, tokens, offsets, kept, dscore)
-            ctx.args = args[0], args[1], inplace
+            ctx.args = layout, args[0], args[1], inplace
         ctx.mark_non_differentiable(scores)
         return loss, scores
 
     @staticmethod
     def backward(ctx, d_loss, *unused):
         if d_loss is None:
-            return (None,) * 6
+            return (None,) * 7
         once("preference_loss", d_loss)
         logits, tokens, offsets, kept, dscore = ctx.saved_tensors
-        ignore_index, pairs, inplace = ctx.args
-        g, dev = plain(d_loss.float()), logits.device
-        dx = logits.detach() if inplace else _gradient_like(logits)
+        layout, ignore_index, pairs, inplace = ctx.args
+        g, dev = plain(d_loss), logits.device
+        dx = logits.detach() if inplace else _gradient_like(logits, layout)
         with on(dev):
-            check(_lib.ce_preference_loss_bwd(_table(logits, dx), ptr(tokens), ignore_index,
-                                              _flags(tokens), pairs, ptr(offsets), ptr(kept),
-                                              ptr(dscore), ptr(g), 1 if g.dim() else 0,
+            check(_lib.ce_preference_loss_bwd(_table(logits, dx, layout), ptr(tokens),
+                                              ignore_index, _flags(tokens), pairs, ptr(offsets),
+                                              ptr(kept), ptr(dscore), ptr(g), 1 if g.dim() else 0,
                                               stream(dev)), "ce_preference_loss_bwd")
         if inplace:
             _overwritten(logits)
-        return (dx,) + (None,) * 5
+        return (dx,) + (None,) * 6
 
 
 def preference_loss(logits, tokens, offsets=None, ref_log_probs=None, beta=0.1,
@@ -521,7 +532,7 @@ def preference_loss(logits, tokens, offsets=None, ref_log_probs=None, beta=0.1,
 
     return_scores: PreferenceLossOutput(loss, scores [2 pairs], without
     gradient)."""
-    logits = _logits(logits, inplace)
+    logits, layout = _logits(logits, inplace)
     dev = logits.device
     if offsets is None:
         if logits.dim() != 3 or logits.shape[0] % 2:
@@ -553,9 +564,9 @@ def preference_loss(logits, tokens, offsets=None, ref_log_probs=None, beta=0.1,
         raise ValueError('the "ipo" loss has no margin')
     args = (int(ignore_index), pairs, _KINDS[loss_type], beta, margin, smoothing,
             1 if length_average else 0, _number(scale, "scale"), _reduction(reduction))
-    if _differentiates(logits):
-        loss, scores = PreferenceLossFunction.apply(logits, tokens, offsets, ref, bool(inplace),
-                                                    args)
+    if _differentiates(logits, ref):
+        loss, scores = PreferenceLossFunction.apply(logits, tokens, offsets, layout, (ref,),
+                                                    bool(inplace), args)
     else:
-        loss, scores, _, _ = _preference(logits, tokens, offsets, ref, *args, False)
+        loss, scores, _, _ = _preference(logits, layout, tokens, offsets, ref, *args, False)
     return PreferenceLossOutput(loss, scores) if return_scores else loss

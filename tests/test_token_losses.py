@@ -193,9 +193,9 @@ def test_layout_of_views(make, want):
 @pytest.mark.parametrize("make", [lambda x: x, lambda x: x[:, :-1], lambda x: x[:, 1:],
                                   lambda x: x.reshape(-1)[3:3 + 6 * 9].reshape(6, 9)])
 def test_gradient_has_the_layout_of_the_logits(make):
-    from softmax_cross_entropy_gb300.token_losses import _gradient_like
+    from softmax_cross_entropy_gb300.token_losses import _gradient_like, _rows_of
     x = make(torch.zeros(4, 7, 9, dtype=torch.bfloat16))
-    g = _gradient_like(x)
+    g = _gradient_like(x, _rows_of(x))
     assert g.shape == x.shape and g.stride() == x.stride() and g.dtype == x.dtype
     assert (g.data_ptr() - x.data_ptr()) % 16 == 0
 
