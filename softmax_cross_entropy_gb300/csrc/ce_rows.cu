@@ -18,6 +18,8 @@ const void* rows_kernel_f16(int op, bool ent, int nt);
 
 namespace {
 
+// dynamic shared memory that leaves room for a second CTA on the SM
+constexpr size_t kHalfSm = 109 * 1000;
 constexpr int64_t kKeepBytes = int64_t{96} << 20;  // of the 129 MB L2
 
 // How many clusters of C CTAs fit the device at once.
@@ -92,20 +94,19 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
     a.cluster = C;
     a.slice_vec = static_cast<int>(slice());
     a.buf_bytes = static_cast<uint32_t>((a.slice_vec * 16 + 127) / 128 * 128);
-    const int nt = env_int("GBCE_ROWS_THREADS", a.slice_vec <= 256   ? 32
-                                                : a.slice_vec <= 512 ? 64
-                                                : a.slice_vec <= 1024 ? 128
-                                                                      : 256);
-    // what the backward finds in L2 when it begins: the last rows, where there is one
-    a.keep_from = a.kept ? std::max<int64_t>(0, a.p.rows - kKeepBytes / (a.p.V * esz)) : a.p.rows;
-    const size_t lists = op == kRowDistill ? 4 * kListWords * kLists * static_cast<size_t>(a.K) : 0;
-    a.nbuf = env_int("GBCE_ROWS_BUFFERS", 3);
-    while (a.nbuf > 1 && a.nbuf * a.buf_bytes + lists > 200 * 1024) --a.nbuf;
-    const size_t smem = a.nbuf * a.buf_bytes + lists;
+    const int nt = env_int("GBCE_ROWS_THREADS", a.slice_vec > 1152 ? 256
+                                                : a.slice_vec > 576 || op == kRowDistill ? 64
+                                                                                         : 32);
+    a.nbuf = env_int("GBCE_ROWS_BUFFERS", kMaxBuf);
+    while (a.nbuf > 1 && a.nbuf * a.buf_bytes > 200 * 1024) --a.nbuf;
+    const size_t list = op == kRowDistill ? 4 * kListWords * static_cast<size_t>(a.K) : 0;
+    a.nlist = kMaxLists;
+    while (a.nlist > kListWarps && a.nbuf * a.buf_bytes + a.nlist * list > kHalfSm) --a.nlist;
+    const size_t smem = a.nbuf * a.buf_bytes + (op == kRowDistill ? a.nlist : 0) * list;
     const void* fn = dtype == CE_F32    ? rows_kernel_f32(op, ent, nt)
                      : dtype == CE_BF16 ? rows_kernel_bf16(op, ent, nt)
                                         : rows_kernel_f16(op, ent, nt);
-    const int threads = nt + 96 + (op == kRowDistill ? 32 * kLists : 0);
+    const int threads = nt + 96 + (op == kRowDistill ? 32 * kListWarps : 0);
     int fit = 0;
     ce_status rc = clusters_that_fit(fn, C, threads, smem, sms, &fit);
     if (rc != CE_OK) return rc;

@@ -36,7 +36,7 @@ struct __align__(16) RowKept {
 
 constexpr int kMaxRowCluster = 16;  // CTAs that share a row
 
-constexpr int kMaxBuf = 4;          // buffers of a CTA
+constexpr int kMaxBuf = 3;          // buffers of a CTA
 
 // A teacher's list in shared memory, an array a part.
 struct TopList {
@@ -47,7 +47,8 @@ struct TopList {
     int* j;     // the class; -1: padding, or not the first of its class
 };
 constexpr int kListWords = 5;
-constexpr int kLists = 4;  // of a CTA, each with a warp of its own
+constexpr int kMaxLists = 6;   // of a CTA at once
+constexpr int kListWarps = 3;  // that build them, each every third row's
 
 struct RowArgs {
     RowPlace p;
@@ -86,8 +87,8 @@ struct RowArgs {
     int K;
     const float* teacher_lse;  // [rows] or nullptr
     int64_t keep_from;  // rows from here on stay in L2 for the backward, which begins with the last
-    // layout: CTAs a row, 16-byte vectors of a CTA's slice, its buffers and their bytes
-    int cluster, slice_vec, nbuf;
+    // layout: CTAs a row, 16-byte vectors of a CTA's slice, its buffers, its lists, a buffer's bytes
+    int cluster, slice_vec, nbuf, nlist;
     uint32_t buf_bytes;
 };
 

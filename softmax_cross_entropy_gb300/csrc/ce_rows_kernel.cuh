@@ -57,13 +57,13 @@ struct __align__(16) RowConst {
 
 // CTAs of an SM that a kernel's registers are to leave room for.
 constexpr int rows_ctas(int op, int nt) {
-    if (op == kRowDistill) return nt <= 64 ? 3 : 2;
-    return nt == 32 ? 7 : nt == 64 ? 6 : nt == 128 ? 4 : 2;
+    if (op == kRowDistill) return nt <= 64 ? 4 : 2;
+    return nt == 32 ? 7 : nt == 64 ? 6 : 2;
 }
 
 // A CTA's threads: the consumers, the producer warp, the two warps that bring
 // a row's statistics together, distillation's list warps.
-constexpr int rows_threads_of(int op, int nt) { return nt + 96 + (op == kRowDistill ? 32 * kLists : 0); }
+constexpr int rows_threads_of(int op, int nt) { return nt + 96 + (op == kRowDistill ? 32 * kListWarps : 0); }
 
 // Of lanes 0-7 the vector that the row's start shares with what is before it,
 // of lanes 8-15 the one that its end shares; -1: there is none.
@@ -78,7 +78,7 @@ __device__ __forceinline__ void fence_proxy_async() {
 
 // Rows whose statistics may be on their way between the CTAs at once: with at
 // most kMaxBuf buffers a CTA's are less than 2 kMaxBuf + 1 apart.
-constexpr int kMeetings = 16;
+constexpr int kMeetings = 8;
 static_assert(kMeetings > 2 * kMaxBuf, "rows on their way");
 
 // Four words into the shared memory of a CTA of the cluster, counted on its
@@ -353,15 +353,15 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     // there; its row's constants are there
     __shared__ __align__(8) uint64_t full[kMaxBuf], empty[kMaxBuf], together[kMaxBuf], ready[kMaxBuf];
     __shared__ __align__(8) uint64_t met[kMeetings], meeting;
-    // the lists' own ring, a slot a list warp: a list takes longer than a row
-    __shared__ __align__(8) uint64_t listed[kLists], unlisted[kLists];
+    // the lists' own, longer ring: a list takes longer than a row
+    __shared__ __align__(8) uint64_t listed[kMaxLists], unlisted[kMaxLists];
     __shared__ RowPart parts[kMeetings][kMaxRowCluster];  // of the cluster's CTAs
     __shared__ RowPart red[kMaxBuf][NW];          // of the warps
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
-    __shared__ ListInfo linfo[OP == kRowDistill ? kLists : 1];
-    __shared__ uint32_t seen[OP == kRowDistill ? kLists * 2 * kSeenWords : 1];
-    __shared__ double s_sum, red_d[NW + 3 + kLists];
+    __shared__ ListInfo linfo[OP == kRowDistill ? kMaxLists : 1];
+    __shared__ uint32_t seen[OP == kRowDistill ? kListWarps * 2 * kSeenWords : 1];
+    __shared__ double s_sum, red_d[NW + 3 + kListWarps];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -370,7 +370,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t first = C > 1 ? cluster_id_x() : blockIdx.x;
     const int64_t step = gridDim.x / static_cast<unsigned>(C);
-    const int NB = a.nbuf;
+    const int NB = a.nbuf, NL = a.nlist;
     auto list_of = [&](int kb) {
         float* w = reinterpret_cast<float*>(smem + static_cast<size_t>(NB) * a.buf_bytes) +
                    static_cast<size_t>(kb) * kListWords * a.K;
@@ -386,7 +386,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             mbar_init(smem_u32(&together[i]), NW);
             mbar_init(smem_u32(&ready[i]), 1);
         }
-        for (int i = 0; i < kLists; ++i) {
+        for (int i = 0; i < NL; ++i) {
             mbar_init(smem_u32(&listed[i]), 1);
             mbar_init(smem_u32(&unlisted[i]), NW + 1);
         }
@@ -396,7 +396,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
         s_sum = 0.0;
     }
     if (OP == kRowDistill)
-        for (int i = tid; i < kLists * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
+        for (int i = tid; i < kListWarps * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
     __syncthreads();
     if (C > 1) cluster_sync();
 
@@ -420,7 +420,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     int l = 0;                // the next row's list
     uint32_t list_phase = 0;  // how often the lists' ring came round, modulo 2
     auto next = [&]() {
-        if (++l == kLists) {
+        if (++l == NL) {
             l = 0;
             list_phase ^= 1u;
         }
@@ -511,48 +511,53 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 (void)mbar_wait_bounded(smem_u32(&full[i]), i < k ? phase : phase ^ 1u, a.timeout_ns);
     } else if (warp > NW + 2) {
         // ---------------------------------------------------------- distillation: the lists
-        const int slot = warp - NW - 3;
-        const TopList L = list_of(slot);
-        ListInfo& li = linfo[slot];
-        int64_t r = first + slot * step;
-        auto ahead = [&]() {  // row r's list, and the logits that it names, on their way to L2
+        const int w = warp - NW - 3;
+        uint32_t* mine = seen + w * 2 * kSeenWords;
+        auto ahead = [&](int64_t r) {  // row r's list on its way to L2
             if (r >= a.p.rows) return;
-            const T* row = X + a.p.at(r);
-            for (int e = lane; e < a.K; e += 32) {
-                const int64_t w = r * a.K + e;
-                prefetch_l2(static_cast<const char*>(a.teacher) + w * (a.teacher_dtype == 0 ? 4 : 2));
-                const int64_t j = load_index(a.index, a.idx64, w);
-                if (j >= 0 && j < a.p.V) prefetch_l2(row + j);
-            }
-        };
-        // the listed classes' elements, after every thread's stores
-        auto store_listed = [&]() {
-            if (!wait(&unlisted[slot], list_phase)) return false;
-            const ListInfo in = li;
-            T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
 #pragma unroll 1
             for (int e = lane; e < a.K; e += 32) {
-                const int j = L.j[e];
-                if (j >= in.lo && j < in.hi)
-                    VT::store1(drow, j, fmaf(in.u1, ex2((L.x[e] - in.m) * a.c), -in.x * L.qs[e]));
+                const int64_t at = r * a.K + e;
+                prefetch_l2(static_cast<const char*>(a.teacher) + at * (a.teacher_dtype == 0 ? 4 : 2));
+                prefetch_l2(static_cast<const char*>(a.index) + at * (a.idx64 ? 8 : 4));
             }
-            list_phase ^= 1u;
-            __syncwarp();
-            return true;
         };
-        bool ok = true, any = false;
-        for (; r < a.p.rows; any = true) {
-            const int64_t t = load_index(a.index, a.idx64, r * a.K);
-            if (any && !(ok = store_listed())) break;
-            ListInfo in = {};
-            if (t >= 0 && t < a.p.V)
-                top_list<T>(a, r, X + a.p.at(r), L, seen + slot * 2 * kSeenWords, in, lane);
-            if (lane == 0) li = in;
-            arrive(&listed[slot]);
-            r += kLists * step;
-            ahead();
+        // The warp's rows in turn. A list's slot is held until its row is done, about three times
+        // as long as building it takes: the elements of a listed row are stored when its slot is
+        // needed again (the last rows' when there are no more).
+        const int64_t last = a.p.rows + NL * step;
+        uint32_t parity = 1;  // of the slot's row before
+        int slot = w;
+        bool again = false;   // there is one
+        for (int64_t r = first + w * step; r < last; r += kListWarps * step) {
+            const TopList L = list_of(slot);
+            if (again) {
+                if (!wait(&unlisted[slot], parity)) break;
+                const ListInfo in = linfo[slot];
+                T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
+#pragma unroll 1
+                for (int e = lane; e < a.K; e += 32) {
+                    const int j = L.j[e];
+                    if (j >= in.lo && j < in.hi)
+                        VT::store1(drow, j, fmaf(in.u1, ex2((L.x[e] - in.m) * a.c), -in.x * L.qs[e]));
+                }
+                __syncwarp();
+            }
+            if (r < a.p.rows) {
+                ListInfo in = {};
+                const int64_t t = load_index(a.index, a.idx64, r * a.K);
+                if (t >= 0 && t < a.p.V) top_list<T>(a, r, X + a.p.at(r), L, mine, in, lane);
+                if (lane == 0) linfo[slot] = in;
+                arrive(&listed[slot]);
+                ahead(r + kListWarps * step);
+            }
+            slot += kListWarps;
+            if (slot >= NL) {
+                slot -= NL;
+                parity ^= 1u;
+                again = true;
+            }
         }
-        if (ok && any) (void)store_listed();
     } else if (warp == NW + 1) {
         // ---------------------------------------------------------- a row's statistics from the CTA's
         // warps, and on to every CTA of the cluster
@@ -836,10 +841,9 @@ rows_kernel(const __grid_constant__ RowArgs a) {
 
 template <typename T, int OP, bool ENT>
 const void* rows_threads(int nt) {
-    return nt == 32    ? (const void*)&rows_kernel<T, OP, ENT, 32>
-           : nt == 64  ? (const void*)&rows_kernel<T, OP, ENT, 64>
-           : nt == 128 ? (const void*)&rows_kernel<T, OP, ENT, 128>
-                       : (const void*)&rows_kernel<T, OP, ENT, 256>;
+    return nt == 32   ? (const void*)&rows_kernel<T, OP, ENT, 32>
+           : nt == 64 ? (const void*)&rows_kernel<T, OP, ENT, 64>
+                      : (const void*)&rows_kernel<T, OP, ENT, 256>;
 }
 
 template <typename T>
