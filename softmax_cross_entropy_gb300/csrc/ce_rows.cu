@@ -2,10 +2,7 @@
 // the kernel (ce_rows_kernel.cuh).
 #include <algorithm>
 #include <cstdlib>
-#include <map>
 #include <mutex>
-#include <string>
-#include <tuple>
 
 #include "ce_rows.cuh"
 #include "gbce.h"
@@ -18,24 +15,34 @@ const void* rows_kernel_f16(int op, bool ent, int nt);
 
 namespace {
 
-// dynamic shared memory that leaves room for a second CTA on the SM
-constexpr size_t kHalfSm = 109 * 1000;
+// Dynamic shared memory that leaves room for a second CTA on the SM, and for
+// one alone.
+constexpr size_t kHalfSm = 109 * 1000, kWholeSm = 200 * 1024;
 constexpr int64_t kKeepBytes = int64_t{96} << 20;  // of the 129 MB L2
 
-// How many clusters of C CTAs fit the device at once.
+// How many clusters of C CTAs fit the device at once: asked of the runtime
+// once for each kernel and layout (some microseconds) and kept.
+struct Fit {
+    int dev, C;
+    const void* fn;
+    size_t smem;
+    int clusters;
+};
 std::mutex g_fit_mu;
-std::map<std::tuple<int, const void*, int, size_t>, int> g_fit;
+Fit g_fit[256];
+int g_fits = 0;
 
 ce_status clusters_that_fit(const void* fn, int C, int threads, size_t smem, int sms, int* out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return record_cuda_failure(e, "token loss device");
     std::lock_guard<std::mutex> lock(g_fit_mu);
-    const auto key = std::make_tuple(dev, fn, C, smem);
-    const auto it = g_fit.find(key);
-    if (it != g_fit.end()) {
-        *out = it->second;
-        return CE_OK;
+    for (int i = 0; i < std::min(g_fits, 256); ++i) {
+        const Fit& f = g_fit[i];
+        if (f.dev == dev && f.C == C && f.fn == fn && f.smem == smem) {
+            *out = f.clusters;
+            return CE_OK;
+        }
     }
     int most = 0;
     e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
@@ -64,7 +71,8 @@ ce_status clusters_that_fit(const void* fn, int C, int threads, size_t smem, int
         e = cudaOccupancyMaxActiveClusters(&fit, fn, &lc);
     }
     if (e != cudaSuccess) return record_cuda_failure(e, "token loss occupancy");
-    g_fit[key] = *out = std::max(fit, 1);
+    *out = std::max(fit, 1);
+    g_fit[g_fits++ % 256] = Fit{dev, C, fn, smem, *out};
     return CE_OK;
 }
 
@@ -85,21 +93,36 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
     const bool whole = (reinterpret_cast<uintptr_t>(a.p.x) | static_cast<uintptr_t>(a.p.step * esz) |
                         static_cast<uintptr_t>(a.p.outer * esz)) % 16 == 0;
     const int64_t nv = (a.p.V * esz + (whole ? 15 : 30)) / 16;
-    const int64_t most = env_int("GBCE_ROWS_SLICE", 36864) / 16;
+    // CTAs a row: as few as hold it in slices of 36 KB, three of which (one of
+    // a row in its second pass, one in its first, one on its way) leave room for
+    // a second CTA on the SM. 2048 rows of 131072 bf16, policy loss: 8 CTAs of
+    // 32 KB 174 us, 16 of 16 KB 212, 4 of 64 KB 164 (with entropies 177, 207 and
+    // 183; distillation 202, 350 and 215). More where rows are too few for
+    // every SM.
+    constexpr int64_t kSlice = 36864 / 16;
     int C = 1;
     auto slice = [&]() { return ((nv + C - 1) / C + 7) / 8 * 8; };
-    while (C < kMaxRowCluster && slice() > most) C *= 2;
+    while (C < kMaxRowCluster && slice() > kSlice) C *= 2;
     while (C < kMaxRowCluster && a.p.rows * C * 2 <= sms && slice() > 256) C *= 2;
-    if (const int forced = env_int("GBCE_ROWS_CLUSTER", 0)) C = forced;
+    // (the tests' way to every cluster size: GBCE_ROWS_CLUSTER=n)
+    const int forced = env_int("GBCE_ROWS_CLUSTER", 0);
+    if (forced >= 1 && forced <= kMaxRowCluster && nv * 16 <= static_cast<int64_t>(kWholeSm) / 2) C = forced;
     a.cluster = C;
     a.slice_vec = static_cast<int>(slice());
     a.buf_bytes = static_cast<uint32_t>((a.slice_vec * 16 + 127) / 128 * 128);
-    const int nt = env_int("GBCE_ROWS_THREADS", a.slice_vec > 1152 ? 256
-                                                : a.slice_vec > 576 || op == kRowDistill ? 64
-                                                                                         : 32);
-    a.nbuf = env_int("GBCE_ROWS_BUFFERS", kMaxBuf);
-    while (a.nbuf > 1 && a.nbuf * a.buf_bytes > 200 * 1024) --a.nbuf;
+    // consumers: 256 threads for slices above 18 KB; one warp for up to 9 KB,
+    // where what a row costs besides its elements counts (16384 rows of 4096 bf16,
+    // policy loss: 32 threads 58 us, 64 63, 256 94; of 8192: 102, 93 and 103;
+    // distillation of 4099: 118, 112 and 167)
+    const int nt = a.slice_vec > 1152 ? 256 : a.slice_vec > 576 || op == kRowDistill ? 64 : 32;
+    // what the backward finds in L2 when it begins: the last rows, where there is one
+    a.keep_from = a.kept ? std::max<int64_t>(0, a.p.rows - kKeepBytes / (a.p.V * esz)) : a.p.rows;
+    a.test_stall = env_int("GBCE_TEST_STALL_COPY", 0) != 0 ? 1 : 0;
+    a.nbuf = kMaxBuf;
+    while (a.nbuf > 1 && a.nbuf * a.buf_bytes > kWholeSm) --a.nbuf;
     const size_t list = op == kRowDistill ? 4 * kListWords * static_cast<size_t>(a.K) : 0;
+    // lists: six, or what leaves the second CTA its room (2048 x 131072 bf16, 64 entries: three
+    // lists 224 us, four 205, six 201)
     a.nlist = kMaxLists;
     while (a.nlist > kListWarps && a.nbuf * a.buf_bytes + a.nlist * list > kHalfSm) --a.nlist;
     const size_t smem = a.nbuf * a.buf_bytes + (op == kRowDistill ? a.nlist : 0) * list;

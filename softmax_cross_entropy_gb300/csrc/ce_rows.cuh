@@ -90,6 +90,7 @@ struct RowArgs {
     // layout: CTAs a row, 16-byte vectors of a CTA's slice, its buffers, its lists, a buffer's bytes
     int cluster, slice_vec, nbuf, nlist;
     uint32_t buf_bytes;
+    int test_stall;  // test hook: CTA 0 leaves its first copy out, so that the waits for it run out
 };
 
 __device__ __forceinline__ int64_t load_index(const void* p, int is64, int64_t i) {

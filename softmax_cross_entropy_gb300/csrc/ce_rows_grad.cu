@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kGradThreads) rows_grad(const __grid_constant_
         const bool owner = ti >= 0 && ti / VE >= v0 && ti / VE < v1 &&
                            (static_cast<int>(ti / VE) - v0) % kGradThreads == tid;
         const float xt = owner ? VT::load1(x, g.t) : 0.f;
-        if (fabsf(g.m) < kFarLogit)
+        if (near_zero(g.m, a.c))
             vectors(std::true_type{});
         else
             vectors(std::false_type{});

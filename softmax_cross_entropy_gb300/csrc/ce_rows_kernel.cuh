@@ -186,7 +186,7 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
 #pragma unroll
     for (int u = 0; u < U; ++u) acc = VT::max_fold(acc, q[u]);
     st.m = VT::max_value(acc);
-    if (fabsf(st.m) < kFarLogit) {
+    if (near_zero(st.m, c)) {
         const float B = st.m * c;
         const float rho = c_low / c;
         const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), rho2 = make_float2(rho, rho);
@@ -481,7 +481,8 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                         const uint32_t dst = smem_u32(buf) + static_cast<uint32_t>(in.w0) * 16u;
                         const char* src = reinterpret_cast<const char*>(row + in.first + in.w0 * VE);
                         mbar_arrive_expect_tx(bar, bytes);
-                        for (uint32_t o = 0; o < bytes; o += kBulk)
+                        const bool stall = a.test_stall && blockIdx.x == 0 && r == first;
+                        for (uint32_t o = stall ? bytes : 0; o < bytes; o += kBulk)
                             bulk_g2s(dst + o, src + o, min(kBulk, bytes - o), bar, r < a.keep_from ? once : again);
                     } else {
                         mbar_arrive(bar);
@@ -730,7 +731,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             const int w0 = in.w0, w1 = in.w1, slice0 = in.first, t = in.t;
             T* drow = reinterpret_cast<T*>(a.p.dx) + in.at;
             uint4* dvec = reinterpret_cast<uint4*>(drow + slice0);
-            if (fabsf(kc.m) < kFarLogit)
+            if (near_zero(kc.m, a.c))
                 slice_gradient<T, ENT, NT, U, true>(vec, dvec, w0, w1, tid, a.c, kc);
             else
                 slice_gradient<T, ENT, NT, U, false>(vec, dvec, w0, w1, tid, a.c, kc);

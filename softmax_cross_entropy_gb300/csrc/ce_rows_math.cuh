@@ -7,9 +7,12 @@
 
 namespace gbce {
 
-// Logits beyond this (masks of a type's lowest value, mostly) take the
-// careful forms below: times log2(e) / T they could overflow.
-constexpr float kFarLogit = 1e18f;
+// Whether arguments may be formed as x c - B with B = m c rounded: B's error,
+// at most 2^-13 here, is put right to first order (what is left is below
+// 2^-27), and no finite product overflows that matters. Larger maxima (masks
+// of a type's lowest value, mostly) take the careful forms, differences before
+// products.
+__device__ __forceinline__ bool near_zero(float m, float c) { return fabsf(m) * c < 2048.f; }
 
 // Products with an element's argument where 2^argument is 0: the logits are
 // cut at -1e30 (bf16 pairs in one instruction), or, where -inf is not far from
@@ -51,8 +54,8 @@ __device__ __forceinline__ float2 cut_argument(float2 g) {
     return kCutLogits<T> ? g : make_float2(fmaxf(g.x, -256.f), fmaxf(g.y, -256.f));
 }
 
-// The constants of a vector's gradient 2^a (u0 + u1 a), a = (x - m) c; NEAR (m
-// below kFarLogit): a as x c - B, B = m c rounded, whose error goes into u0
+// The constants of a vector's gradient 2^a (u0 + u1 a), a = (x - m) c; NEAR
+// (near_zero(m, c)): a as x c - B, B = m c rounded, whose error goes into u0
 // and u1.
 template <bool NEAR>
 struct GradTerms {

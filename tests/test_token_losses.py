@@ -361,11 +361,13 @@ def grad_tol(g, p, size, dtype, V):
     """size [rows]: the coefficients' magnitude. The element p_j has the relative error of S's
     (logp_tol), of the kept maximum's difference times c (2^-22 of arg <= 40) and ex2: below
     2^-17 in all, and its coefficient one of 2^-17 more (a ratio's exponent is lp's error). Then
-    one rounding to the type."""
+    one rounding to the type. ex2 gives 0 for results below 2^-126, fp32's smallest normal: an
+    element that small is off by up to 2^-126 times its coefficient (bf16 and fp32, which have
+    subnormals below it, show that)."""
     eps = torch.finfo(DT[dtype]).eps / 2
     tiny = torch.finfo(DT[dtype]).smallest_normal * eps
     rel = 2.0 ** -16 + V / 128 * 2.0 ** -24
-    return np.abs(g) * eps + size[:, None] * (p * rel + (p > 2) * 0) + tiny
+    return np.abs(g) * eps + size[:, None] * (p * rel + 2.0 ** -126) + tiny
 
 
 def tokens_for(rng, B, T, V, skip=0.2):
@@ -870,9 +872,80 @@ def test_factors_on_the_loss(name, dtype):
 @pytest.mark.parametrize("entropy", [False, True])
 @pytest.mark.parametrize("B,T,V,dtype", [(8, 700, 1000, "bf16"), (6, 601, 4099, "f16"),
                                          (4, 600, 9000, "f32"), (2, 700, 40000, "bf16"),
-                                         (2, 300, 70001, "f32"), (2, 250, 131072, "bf16")])
+                                         (2, 300, 70001, "f32"), (2, 250, 131072, "bf16"),
+                                         (2, 9, 524288, "f32")])
 def test_runs_of_rows_that_do_not_count(B, T, V, dtype, entropy):
-    """Many rows a CTA, prompts and padding among them in runs: every loss against 64 bits."""
+    """Many rows a CTA, prompts and padding among them in runs."""
+    check_all(B, T, V, dtype, entropy)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 2, 3, 4, 5, 7, 8, 11, 16])
+@pytest.mark.parametrize("B,T,V,dtype", [(4, 333, 1500, "bf16"), (2, 400, 9001, "f32")])
+def test_every_cluster_size(C, B, T, V, dtype, monkeypatch):
+    """One to sixteen CTAs a row, the last of them with little or nothing of it."""
+    monkeypatch.setenv("GBCE_ROWS_CLUSTER", str(C))
+    check_all(B, T, V, dtype, C % 2 == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("spread,T", [(300.0, 1.0), (3000.0, 1.0), (20000.0, 50.0), (4.0, 1e-3),
+                                      (60000.0, 1000.0), (2.0, 100.0)])
+def test_large_logits_and_extreme_temperatures(dtype, spread, T):
+    import softmax_cross_entropy_gb300 as gbce
+    rng = np.random.default_rng(int(spread))
+    V = 5000
+    x64 = np.clip(rng.normal(size=(1, 6, V)) * spread, -65000, 65000)
+    x64[0, 1] -= x64[0, 1].max() + spread  # every logit far below zero
+    x64 = np.clip(x64, -65000, 65000)
+    x, held = put(x64, dtype)
+    tok = held.argmax(1)
+    tok[2] = 17
+    x.requires_grad_()
+    g = rng.normal(size=6)
+    want = ref.log_probs(held, tok, T, IGN, g, np.zeros(6))
+    lp, h = gbce.token_log_probs(x, cuda(tok).reshape(1, 6), temperature=T, return_entropy=True)
+    close(lp, want[0].reshape(1, 6), logp_tol(want[0], V).reshape(1, 6), "lp")
+    close(h, want[1].reshape(1, 6), 2 * logp_tol(want[1], V).reshape(1, 6), "h")
+    dx, = torch.autograd.grad(lp, x, cuda(g).float().reshape(1, 6))
+    p = probs(held, T)
+    onto = np.zeros_like(p)
+    onto[np.arange(6), tok] = 1.0
+    close(dx.reshape(6, V), want[2], grad_tol(want[2], p + onto * 2.0 ** -6, np.abs(g) / T, dtype, V), "dx")
+    # the losses whose forward forms the gradient: the same rows, coefficients 1
+    loss = gbce.policy_loss(x, cuda(tok).reshape(1, 6), torch.ones(1, 6, device="cuda"),
+                            temperature=T, reduction="sum", entropy_coef=1e-30)
+    dx, = torch.autograd.grad(loss, x)
+    wdx = ref.log_probs(held, tok, T, IGN, -np.ones(6), -1e-30 * np.ones(6))[2]
+    close(dx.reshape(6, V), wdx, grad_tol(wdx, p + onto * 2.0 ** -6, np.ones(6) / T, dtype, V), "policy dx")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["logp", "policy", "pref", "distill"])
+@pytest.mark.parametrize("V", [3000, 70000])
+def test_a_wait_that_runs_out_is_reported(name, V, monkeypatch):
+    """CTA 0 leaves its first copy out: the waits for it give up, nothing else happens, and the next
+    call is right."""
+    import softmax_cross_entropy_gb300 as gbce
+    from softmax_cross_entropy_gb300 import _lib
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    tok = torch.randint(V, (4, 50), generator=g, device="cuda")
+    x = torch.randn(4, 50, V, generator=g, device="cuda").bfloat16().requires_grad_()
+    f = _four(x, tok)[name]
+    want = f(x)
+    monkeypatch.setenv("GBCE_WAIT_TIMEOUT_MS", "20")
+    monkeypatch.setenv("GBCE_TEST_STALL_COPY", "1")
+    f(x)
+    assert gbce.device_status() == _lib.CE_ERR_TIMEOUT
+    monkeypatch.delenv("GBCE_TEST_STALL_COPY")
+    got = f(x)
+    assert gbce.device_status() == _lib.CE_OK and torch.equal(got, want)
+
+
+def check_all(B, T, V, dtype, entropy):
+    """Every loss on one batch against 64 bits."""
     import softmax_cross_entropy_gb300 as gbce
     g = torch.Generator(device="cuda")
     g.manual_seed(V)
