@@ -17,7 +17,7 @@ namespace {
 
 // Dynamic shared memory that leaves room for a second CTA on the SM, and for
 // one alone.
-constexpr size_t kHalfSm = 109 * 1000, kWholeSm = 200 * 1024;
+constexpr size_t kHalfSm = 109 * 1000, kWholeSm = 216 * 1000;
 constexpr int64_t kKeepBytes = int64_t{96} << 20;  // of the 129 MB L2
 
 // How many clusters of C CTAs fit the device at once: asked of the runtime
@@ -93,13 +93,12 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
     const bool whole = (reinterpret_cast<uintptr_t>(a.p.x) | static_cast<uintptr_t>(a.p.step * esz) |
                         static_cast<uintptr_t>(a.p.outer * esz)) % 16 == 0;
     const int64_t nv = (a.p.V * esz + (whole ? 15 : 30)) / 16;
-    // CTAs a row: as few as hold it in slices of 36 KB, three of which (one of
-    // a row in its second pass, one in its first, one on its way) leave room for
-    // a second CTA on the SM. 2048 rows of 131072 bf16, policy loss: 8 CTAs of
-    // 32 KB 174 us, 16 of 16 KB 212, 4 of 64 KB 164 (with entropies 177, 207 and
-    // 183; distillation 202, 350 and 215). More where rows are too few for
-    // every SM.
-    constexpr int64_t kSlice = 36864 / 16;
+    // CTAs a row: as few as hold it in slices of 66 KB, three of which (one of
+    // a row in its second pass, one in its first, one on its way) fill an SM's
+    // shared memory. 2048 rows of 131072 bf16, policy loss: 4 CTAs of 64 KB, one
+    // an SM, 169 us, 8 of 32 KB, two an SM, 175 (with entropies 174 and 182,
+    // distillation 184 and 209). More where rows are too few for every SM.
+    constexpr int64_t kSlice = 67584 / 16;
     int C = 1;
     auto slice = [&]() { return ((nv + C - 1) / C + 7) / 8 * 8; };
     while (C < kMaxRowCluster && slice() > kSlice) C *= 2;
@@ -110,26 +109,31 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
     a.cluster = C;
     a.slice_vec = static_cast<int>(slice());
     a.buf_bytes = static_cast<uint32_t>((a.slice_vec * 16 + 127) / 128 * 128);
-    // consumers: 256 threads for slices above 18 KB; one warp for up to 9 KB,
-    // where what a row costs besides its elements counts (16384 rows of 4096 bf16,
-    // policy loss: 32 threads 58 us, 64 63, 256 94; of 8192: 102, 93 and 103;
-    // distillation of 4099: 118, 112 and 167)
-    const int nt = a.slice_vec > 1152 ? 256 : a.slice_vec > 576 || op == kRowDistill ? 64 : 32;
+    // consumers: 512 threads for slices above 36 KB, 256 above 18 KB; one warp
+    // for up to 9 KB, where what a row costs besides its elements counts (2048
+    // rows of 64 KB slices, log-probabilities with entropies: 512 threads 86 us,
+    // 256 93; 16384 rows of 4096 bf16, policy loss: 32 threads 58 us, 64 63, 256
+    // 94; of 8192: 102, 93 and 103; distillation of 4099: 118, 112 and 167)
+    const int nt = a.slice_vec > 2304 ? 512 : a.slice_vec > 1152 ? 256
+                   : a.slice_vec > 576 || op == kRowDistill      ? 64
+                                                                 : 32;
     // what the backward finds in L2 when it begins: the last rows, where there is one
     a.keep_from = a.kept ? std::max<int64_t>(0, a.p.rows - kKeepBytes / (a.p.V * esz)) : a.p.rows;
     a.test_stall = env_int("GBCE_TEST_STALL_COPY", 0) != 0 ? 1 : 0;
+    // buffers, and lists: two a list warp, or what leaves the second CTA (or this
+    // one) its room (2048 x 131072 bf16 in 32 KB slices, 64 entries, three warps:
+    // three lists 224 us, six 201)
+    const int lw = op == kRowDistill ? list_warps(nt) : 0;
+    const size_t list = 4 * kListWords * static_cast<size_t>(a.K);
     a.nbuf = kMaxBuf;
-    while (a.nbuf > 1 && a.nbuf * a.buf_bytes > kWholeSm) --a.nbuf;
-    const size_t list = op == kRowDistill ? 4 * kListWords * static_cast<size_t>(a.K) : 0;
-    // lists: six, or what leaves the second CTA its room (2048 x 131072 bf16, 64 entries: three
-    // lists 224 us, four 205, six 201)
-    a.nlist = kMaxLists;
-    while (a.nlist > kListWarps && a.nbuf * a.buf_bytes + a.nlist * list > kHalfSm) --a.nlist;
-    const size_t smem = a.nbuf * a.buf_bytes + (op == kRowDistill ? a.nlist : 0) * list;
+    while (a.nbuf > 1 && a.nbuf * a.buf_bytes + lw * list > kWholeSm) --a.nbuf;
+    a.nlist = 2 * lw;
+    while (a.nlist > lw && a.nbuf * a.buf_bytes + a.nlist * list > (nt == 512 ? kWholeSm : kHalfSm)) --a.nlist;
+    const size_t smem = a.nbuf * a.buf_bytes + a.nlist * list;
     const void* fn = dtype == CE_F32    ? rows_kernel_f32(op, ent, nt)
                      : dtype == CE_BF16 ? rows_kernel_bf16(op, ent, nt)
                                         : rows_kernel_f16(op, ent, nt);
-    const int threads = nt + 96 + (op == kRowDistill ? 32 * kListWarps : 0);
+    const int threads = nt + 96 + 32 * lw;
     int fit = 0;
     ce_status rc = clusters_that_fit(fn, C, threads, smem, sms, &fit);
     if (rc != CE_OK) return rc;
@@ -149,7 +153,10 @@ ce_status rows_launch(int op, bool ent, int dtype, const RowArgs& args, int sms,
         attr[n].val.clusterDim.z = 1;
         ++n;
     }
-    if (after_count) {
+    // (begun while the count still runs, the clusters of four and more CTAs, two
+    // an SM, find the SMs partly taken and are placed so that not all fit at
+    // once: 2048 x 131072 in 8 CTAs 187-251 us, after the count 175)
+    if (after_count && (C <= 2 || (C == 4 && nt == 512))) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;

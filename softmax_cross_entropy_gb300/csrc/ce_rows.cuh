@@ -47,8 +47,9 @@ struct TopList {
     int* j;     // the class; -1: padding, or not the first of its class
 };
 constexpr int kListWords = 5;
-constexpr int kMaxLists = 6;   // of a CTA at once
-constexpr int kListWarps = 3;  // that build them, each every third row's
+constexpr int kMaxLists = 12;  // of a CTA at once
+constexpr int kListWarps = 3;  // that build them (of a CTA that has the SM to itself: twice as many)
+constexpr int list_warps(int nt) { return nt == 512 ? 2 * kListWarps : kListWarps; }
 
 struct RowArgs {
     RowPlace p;

@@ -57,13 +57,14 @@ struct __align__(16) RowConst {
 
 // CTAs of an SM that a kernel's registers are to leave room for.
 constexpr int rows_ctas(int op, int nt) {
+    if (nt == 512) return 1;
     if (op == kRowDistill) return nt <= 64 ? 4 : 2;
     return nt == 32 ? 7 : nt == 64 ? 6 : 2;
 }
 
 // A CTA's threads: the consumers, the producer warp, the two warps that bring
 // a row's statistics together, distillation's list warps.
-constexpr int rows_threads_of(int op, int nt) { return nt + 96 + (op == kRowDistill ? 32 * kListWarps : 0); }
+constexpr int rows_threads_of(int op, int nt) { return nt + 96 + (op == kRowDistill ? 32 * list_warps(nt) : 0); }
 
 // Of lanes 0-7 the vector that the row's start shares with what is before it,
 // of lanes 8-15 the one that its end shares; -1: there is none.
@@ -171,43 +172,55 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
     constexpr int VE = VT::N;
     RowPart st = {-INFINITY, 0.f, 0.f, -INFINITY};
     if (tid >= n) return st;
+    // U vectors at once while there are more than two, then two
     uint4 q[U];
     auto load = [&](int v) {
+        const bool wide = v + 2 * NT < n;
         if (v + (U - 1) * NT < n) {
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
         } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = v + u * NT < n ? vec[v + u * NT] : lowest4<T>();
+            for (int u = 0; u < U; ++u)
+                if (wide || u < 2) q[u] = v + u * NT < n ? vec[v + u * NT] : lowest4<T>();
         }
+        return wide;
     };
-    load(tid);
+    bool wide = load(tid);
     typename VT::MaxAcc acc = VT::max_init();
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = VT::max_fold(acc, q[u]);
+    for (int u = 0; u < U; ++u)
+        if (wide || u < 2) acc = VT::max_fold(acc, q[u]);
     st.m = VT::max_value(acc);
     if (near_zero(st.m, c)) {
         const float B = st.m * c;
         const float rho = c_low / c;
         const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), rho2 = make_float2(rho, rho);
         float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
-        for (int v = tid;;) {
+        auto add = [&](const uint4& v) {
+            float f[VE];
+            unpack_cut<T, ENT>(v, f);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float f[VE];
-                unpack_cut<T, ENT>(q[u], f);
-#pragma unroll
-                for (int i = 0; i < VE; i += 2) {
-                    float2 g = ffma2(make_float2(f[i], f[i + 1]), c2, nb2);
-                    g = ffma2(g, rho2, g);
-                    const float2 e = make_float2(ex2(g.x), ex2(g.y));
-                    s2 = fadd2(s2, e);
-                    if (ENT) q2 = ffma2(e, cut_argument<T>(g), q2);
-                }
+            for (int i = 0; i < VE; i += 2) {
+                float2 g = ffma2(make_float2(f[i], f[i + 1]), c2, nb2);
+                g = ffma2(g, rho2, g);
+                const float2 e = make_float2(ex2(g.x), ex2(g.y));
+                s2 = fadd2(s2, e);
+                if (ENT) q2 = ffma2(e, cut_argument<T>(g), q2);
             }
-            v += NT * U;
+        };
+        for (int v = tid;;) {
+            if (wide) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) add(q[u]);
+                v += NT * U;
+            } else {
+                add(q[0]);
+                add(q[1]);
+                v += NT * 2;
+            }
             if (v >= n) break;
-            load(v);
+            wide = load(v);
         }
         st.S = s2.x + s2.y;
         st.Q = q2.x + q2.y;
@@ -240,6 +253,12 @@ __device__ __forceinline__ void slice_gradient(const uint4* vec, uint4* dvec, in
             for (int u = 0; u < U; ++u) q[u] = vec[v + u * NT];
 #pragma unroll
             for (int u = 0; u < U; ++u) dvec[v + u * NT] = grad(q[u]);
+        }
+        if (v + NT < w1) {
+            const uint4 q0 = vec[v], q1 = vec[v + NT];
+            dvec[v] = grad(q0);
+            dvec[v + NT] = grad(q1);
+            v += 2 * NT;
         }
     }
 #pragma unroll 1
@@ -348,6 +367,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     constexpr int VE = VT::N;
     constexpr int NW = NT / 32;
     constexpr int U = 4;  // vectors a thread takes at once
+    constexpr int LW = NT == 512 ? 2 * kListWarps : kListWarps;
     extern __shared__ __align__(128) unsigned char smem[];  // buffers, then the lists
     // a buffer's mbarriers: filled; given back; its row's statistics are all
     // there; its row's constants are there
@@ -360,8 +380,8 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     __shared__ RowInfo info[kMaxBuf];
     __shared__ RowConst consts[kMaxBuf];
     __shared__ ListInfo linfo[OP == kRowDistill ? kMaxLists : 1];
-    __shared__ uint32_t seen[OP == kRowDistill ? kListWarps * 2 * kSeenWords : 1];
-    __shared__ double s_sum, red_d[NW + 3 + kListWarps];
+    __shared__ uint32_t seen[OP == kRowDistill ? LW * 2 * kSeenWords : 1];
+    __shared__ double s_sum, red_d[NW + 3 + LW];
     __shared__ int s_flag;
 
     pdl_launch_dependents();
@@ -370,7 +390,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t first = C > 1 ? cluster_id_x() : blockIdx.x;
     const int64_t step = gridDim.x / static_cast<unsigned>(C);
-    const int NB = a.nbuf, NL = a.nlist;
+    const int NB = a.nbuf, NL = a.nlist;  // (no list: 0)
     auto list_of = [&](int kb) {
         float* w = reinterpret_cast<float*>(smem + static_cast<size_t>(NB) * a.buf_bytes) +
                    static_cast<size_t>(kb) * kListWords * a.K;
@@ -396,7 +416,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
         s_sum = 0.0;
     }
     if (OP == kRowDistill)
-        for (int i = tid; i < kListWarps * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
+        for (int i = tid; i < LW * 2 * kSeenWords; i += static_cast<int>(blockDim.x)) seen[i] = 0u;
     __syncthreads();
     if (C > 1) cluster_sync();
 
@@ -420,7 +440,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
     int l = 0;                // the next row's list
     uint32_t list_phase = 0;  // how often the lists' ring came round, modulo 2
     auto next = [&]() {
-        if (++l == NL) {
+        if (OP == kRowDistill && ++l == NL) {
             l = 0;
             list_phase ^= 1u;
         }
@@ -530,7 +550,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
         uint32_t parity = 1;  // of the slot's row before
         int slot = w;
         bool again = false;   // there is one
-        for (int64_t r = first + w * step; r < last; r += kListWarps * step) {
+        for (int64_t r = first + w * step; r < last; r += LW * step) {
             const TopList L = list_of(slot);
             if (again) {
                 if (!wait(&unlisted[slot], parity)) break;
@@ -550,9 +570,9 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 if (t >= 0 && t < a.p.V) top_list<T>(a, r, X + a.p.at(r), L, mine, in, lane);
                 if (lane == 0) linfo[slot] = in;
                 arrive(&listed[slot]);
-                ahead(r + kListWarps * step);
+                ahead(r + LW * step);
             }
-            slot += kListWarps;
+            slot += LW;
             if (slot >= NL) {
                 slot -= NL;
                 parity ^= 1u;
@@ -842,9 +862,10 @@ rows_kernel(const __grid_constant__ RowArgs a) {
 
 template <typename T, int OP, bool ENT>
 const void* rows_threads(int nt) {
-    return nt == 32   ? (const void*)&rows_kernel<T, OP, ENT, 32>
-           : nt == 64 ? (const void*)&rows_kernel<T, OP, ENT, 64>
-                      : (const void*)&rows_kernel<T, OP, ENT, 256>;
+    return nt == 32    ? (const void*)&rows_kernel<T, OP, ENT, 32>
+           : nt == 64  ? (const void*)&rows_kernel<T, OP, ENT, 64>
+           : nt == 256 ? (const void*)&rows_kernel<T, OP, ENT, 256>
+                       : (const void*)&rows_kernel<T, OP, ENT, 512>;
 }
 
 template <typename T>
