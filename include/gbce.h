@@ -611,7 +611,7 @@ typedef struct {
     void* grad;           /* their gradient, or NULL: the same strides, and the same
                              address modulo 16 bytes; may be data itself */
     int dtype;
-    float temperature;    /* T, in [1e-6, 1e6] */
+    double temperature;   /* T, in [1e-6, 1e6] */
     int64_t rows, V;      /* V at most 2^19 (CE_ERR_UNSUPPORTED above) */
     int64_t inner, outer_stride, row_stride; /* row r starts at element
                              (r / inner) outer_stride + (r % inner) row_stride;

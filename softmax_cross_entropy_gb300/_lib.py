@@ -31,7 +31,7 @@ class BeamState(ctypes.Structure):
 
 class Rows(ctypes.Structure):
     """ce_rows."""
-    _fields_ = [("data", _P), ("grad", _P), ("dtype", _I), ("temperature", _F), ("rows", _I64),
+    _fields_ = [("data", _P), ("grad", _P), ("dtype", _I), ("temperature", _D), ("rows", _I64),
                 ("V", _I64), ("inner", _I64), ("outer_stride", _I64), ("row_stride", _I64)]
 
 

@@ -130,11 +130,14 @@ struct __align__(16) RowPart {
     float m, S, Q, x;
 };
 
+// d (c + c_low), rounded once (c_low > 0: -inf stays -inf).
+__device__ __forceinline__ float argument(float d, float c, float c_low) { return fmaf(d, c, d * c_low); }
+
 // The factor and shift that bring statistics with maximum m to the maximum M
 // (m <= M; an empty part has S = Q = 0 and any factor).
-__device__ __forceinline__ void part_raise(RowPart& v, float M, float c, bool ent) {
+__device__ __forceinline__ void part_raise(RowPart& v, float M, float c, float c_low, bool ent) {
     const float base = M == -INFINITY ? 0.f : M;
-    const float d = fmaxf((v.m - base) * c, -256.f), f = ex2(d);
+    const float d = fmaxf(argument(v.m - base, c, c_low), -256.f), f = ex2(d);
     if (ent) v.Q = f * fmaf(d, v.S, v.Q);
     v.S *= f;
     v.m = M;
@@ -142,8 +145,8 @@ __device__ __forceinline__ void part_raise(RowPart& v, float M, float c, bool en
 
 // The statistics of a warp's parts together, the same bits in every lane.
 template <bool ENT, bool TOKEN>
-__device__ __forceinline__ void part_warp(RowPart& v, float c) {
-    part_raise(v, warp_max_f32(v.m), c, ENT);
+__device__ __forceinline__ void part_warp(RowPart& v, float c, float c_low) {
+    part_raise(v, warp_max_f32(v.m), c, c_low, ENT);
     v.S = warp_sum(v.S);
     if (ENT) v.Q = warp_sum(v.Q);
     if (TOKEN) v.x = warp_max_f32(v.x);

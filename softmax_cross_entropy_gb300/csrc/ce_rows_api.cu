@@ -42,7 +42,7 @@ ce_status check_rows(const ce_rows* x, bool need_grad) {
     if (!x) return CE_ERR_INVALID_ARG;
     if (x->dtype != CE_F32 && x->dtype != CE_BF16 && x->dtype != CE_F16) return CE_ERR_INVALID_ARG;
     if (x->rows < 0 || x->V < 1 || x->inner < 1) return CE_ERR_INVALID_ARG;
-    if (!(x->temperature >= 1e-6f && x->temperature <= 1e6f)) return CE_ERR_INVALID_ARG;
+    if (!(x->temperature >= 1e-6 && x->temperature <= 1e6)) return CE_ERR_INVALID_ARG;
     if (x->V > kMaxVocabulary || x->rows > (int64_t{1} << 40)) {
         record_message("the token losses take up to 2^19 classes and 2^40 rows");
         return CE_ERR_UNSUPPORTED;
@@ -73,7 +73,7 @@ RowPlace place_of(const ce_rows* x) {
 
 void fill_rows(RowArgs* a, const ce_rows* x, const Device& d) {
     a->p = place_of(x);
-    const double inv = 1.0 / static_cast<double>(x->temperature);
+    const double inv = 1.0 / x->temperature;
     a->invT = static_cast<float>(inv);
     a->invT_low = static_cast<float>(inv - static_cast<double>(a->invT));
     const double c = 1.4426950408889634 * inv;
@@ -138,8 +138,8 @@ extern "C" ce_status ce_token_logp_bwd(const ce_rows* x, const void* tokens, int
     if ((rc = device_of(st, &d)) != CE_OK) return rc;
     GradArgs a = {};
     a.p = place_of(x);
-    a.invT = static_cast<float>(1.0 / static_cast<double>(x->temperature));
-    a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(x->temperature));
+    a.invT = static_cast<float>(1.0 / x->temperature);
+    a.c = static_cast<float>(1.4426950408889634 / x->temperature);
     a.tokens = tokens;
     a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
     a.ignore_index = ignore_index;
@@ -324,8 +324,8 @@ extern "C" ce_status ce_preference_loss_bwd(const ce_rows* x, const void* tokens
     if ((rc = device_of(st, &d)) != CE_OK) return rc;
     GradArgs a = {};
     a.p = place_of(x);
-    a.invT = static_cast<float>(1.0 / static_cast<double>(x->temperature));
-    a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(x->temperature));
+    a.invT = static_cast<float>(1.0 / x->temperature);
+    a.c = static_cast<float>(1.4426950408889634 / x->temperature);
     a.tokens = tokens;
     a.tok64 = (flags & CE_FLAG_TARGET_I64) ? 1 : 0;
     a.ignore_index = ignore_index;

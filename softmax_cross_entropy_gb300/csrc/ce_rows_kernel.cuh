@@ -145,7 +145,7 @@ __device__ __noinline__ RowPart slice_stats_careful(const uint4* vec, int n, int
     for (int v = tid; v < n; v += NT) {
         const uint4 q = vec[v];
         const float top = VT::max_value(VT::max_fold(VT::max_init(), q));
-        if (top > st.m) part_raise(st, top, c, ENT);
+        if (top > st.m) part_raise(st, top, c, c_low, ENT);
         const float base = st.m == -INFINITY ? 0.f : st.m;
         float f[VT::N];
         VT::unpack(q, f);
@@ -197,17 +197,24 @@ __device__ __forceinline__ RowPart slice_stats(const uint4* vec, int n, int tid,
         const float rho = c_low / c;
         const float2 c2 = make_float2(c, c), nb2 = make_float2(-B, -B), rho2 = make_float2(rho, rho);
         float2 s2 = make_float2(0.f, 0.f), q2 = make_float2(0.f, 0.f);
+        // (a vector's sum before it is added: a quarter of the roundings at the sum's size)
         auto add = [&](const uint4& v) {
             float f[VE];
             unpack_cut<T, ENT>(v, f);
+            float2 e[VE / 2], w = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < VE; i += 2) {
-                float2 g = ffma2(make_float2(f[i], f[i + 1]), c2, nb2);
+            for (int i = 0; i < VE / 2; ++i) {
+                float2 g = ffma2(make_float2(f[2 * i], f[2 * i + 1]), c2, nb2);
                 g = ffma2(g, rho2, g);
-                const float2 e = make_float2(ex2(g.x), ex2(g.y));
-                s2 = fadd2(s2, e);
-                if (ENT) q2 = ffma2(e, cut_argument<T>(g), q2);
+                e[i] = make_float2(ex2(g.x), ex2(g.y));
+                if (ENT) w = i == 0 ? fmul2(e[i], cut_argument<T>(g)) : ffma2(e[i], cut_argument<T>(g), w);
             }
+#pragma unroll
+            for (int o = VE / 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < o; ++i) e[i] = fadd2(e[i], e[i + o]);
+            s2 = fadd2(s2, e[0]);
+            if (ENT) q2 = fadd2(q2, w);
         };
         for (int v = tid;;) {
             if (wide) {
@@ -592,7 +599,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             if (!wait(&together[k], phase)) break;
             RowPart st = lane < NW ? red[k][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
             arrive(&empty[k]);
-            part_warp<ENT, OP != kRowDistill>(st, a.c);
+            part_warp<ENT, OP != kRowDistill>(st, a.c, a.c_low);
             if (C > 1) {
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(&met[slot]), 16u * C);
                 __syncwarp();
@@ -636,7 +643,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
             }
             if (timed_out(mbar_wait_cluster(smem_u32(&met[slot]), met_phase, a.timeout_ns))) break;
             RowPart st = lane < C ? parts[slot][lane] : RowPart{-INFINITY, 0.f, 0.f, -INFINITY};
-            part_warp<ENT, OP != kRowDistill>(st, a.c);
+            part_warp<ENT, OP != kRowDistill>(st, a.c, a.c_low);
             if (++slot == kMeetings) {
                 slot = 0;
                 met_phase ^= 1u;
@@ -655,12 +662,12 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 if (tail) {
                     // both sums by the row's maximum, that of the list included
                     kc.m = fmaxf(st.m, li.top);
-                    part_raise(st, kc.m, a.c, false);
+                    part_raise(st, kc.m, a.c, a.c_low, false);
                     left = st.S;
                     float inside = 0.f;
 #pragma unroll 1
                     for (int e = lane; e < a.K; e += 32)
-                        if (L.j[e] >= 0) inside += ex2((L.x[e] - kc.m) * a.c);
+                        if (L.j[e] >= 0) inside += ex2(argument(L.x[e] - kc.m, a.c, a.c_low));
                     S = left + warp_sum(inside);
                 }
                 if (two) {
@@ -806,7 +813,7 @@ rows_kernel(const __grid_constant__ RowArgs a) {
                 RowPart st =
                     slice_stats<T, ENT, NT, U>(reinterpret_cast<const uint4*>(buf), n, tid, a.c, a.c_low);
                 __syncwarp();
-                part_warp<ENT, false>(st, a.c);
+                part_warp<ENT, false>(st, a.c, a.c_low);
                 if (OP != kRowDistill && warp == 0) {
                     const int tj = t - slice0;  // the token's place in the slice
                     if (tj >= 0 && tj < n * VE) st.x = VT::load1(buf, tj);
