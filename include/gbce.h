@@ -602,9 +602,12 @@ ce_status ce_beam_reorder(const ce_beam_state* states, int n, const int64_t* bea
  *   lp = z_t - lse          H = -sum_j p_j log p_j  (p log p = 0 where p = 0)
  *
  * Logits of -inf have p = 0 and a gradient of 0. A counted row without a
- * finite logit, or with a NaN or +inf among them, gives NaN. Arithmetic is in
- * fp32 (the sums over rows, sequences and teachers' lists in fp64); gradients
- * are rounded once into the logits' type.
+ * finite logit, or with a NaN or +inf among them, gives NaN, and so does a
+ * teacher's list without a finite value. Arithmetic is in fp32 (the sums over
+ * rows and sequences in two parts or fp64); probabilities below 2^-126 of the
+ * row's largest come out 0; gradients are rounded once into the logits' type.
+ * Results do not depend on the order in which CTAs run; a row's last bits may
+ * depend on how many rows a call has, by which its share of CTAs is chosen.
  */
 typedef struct {
     const void* data;     /* logits, elements of dtype (CE_F32, CE_BF16, CE_F16) */
@@ -784,9 +787,10 @@ ce_status ce_bwd(const float* grad_output, int grad_per_row, void* dlogits,
  * Environment read at each call: GBCE_WAIT_TIMEOUT_MS (default 2000) bounds
  * every device wait of a launch in wall time; GBCE_TEST_STALL_COPY=1 is a
  * test hook that makes CTA 0 of the streaming or register-resident forward
- * kernel leave its first bulk copy out, so that one wait runs out and the
- * call records CE_ERR_TIMEOUT (its outputs are then invalid; nothing
- * faults).
+ * kernel, or of the token losses' forward, leave its first bulk copy out, so
+ * that one wait runs out and the call records CE_ERR_TIMEOUT (its outputs are
+ * then invalid; nothing faults). GBCE_ROWS_CLUSTER=n (1..16) makes the token
+ * losses share a row of up to 100 KB among n CTAs.
  */
 ce_status ce_device_status(ce_stream_t stream);
 

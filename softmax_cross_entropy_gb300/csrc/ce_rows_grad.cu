@@ -18,8 +18,8 @@ constexpr int kCountCtas = 8;  // one cluster
 
 // D = the sum of the counted rows' weights; clears the ticket of the sum that
 // follows. One cluster; a thread adds its rows' weights in two fp32 parts
-// (the fp64 pipe is narrow: a sum in fp64 from the start took 16 us for 16384
-// rows, this takes 4), a fixed butterfly and order in fp64 the rest.
+// (the fp64 pipe is narrow: one CTA that added in fp64 from the start took 17 us
+// for 16384 rows under ncu, this takes 7), a fixed butterfly and order in fp64 the rest.
 __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThreadsRows)
 rows_count(const __grid_constant__ RowArgs a) {
     __shared__ double red[kCountThreadsRows / 32];
@@ -320,21 +320,25 @@ __global__ void __launch_bounds__(kGradThreads) rows_scale(const __grid_constant
     const int tid = threadIdx.x;
     const bool per_row = a.per_pair != 0;
     if (!per_row && __ldg(a.grad_output) == 1.f) return;
-    for (int64_t r = blockIdx.x; r < a.p.rows; r += gridDim.x) {
+    const int64_t units = a.p.rows * a.parts;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t r = u / a.parts;
+        const int part = static_cast<int>(u - r * a.parts);
         const float g = __ldg(a.grad_output + (per_row ? r : 0));
         if (g == 1.f) continue;
         T* dx = reinterpret_cast<T*>(a.p.dx) + a.p.at(r);
         const RowSpan sp = row_span<T>(dx, a.p.V);
         uint4* dv = reinterpret_cast<uint4*>(dx + sp.head);
+        const int v1 = min(sp.nvec, (part + 1) * a.part_vec);
 #pragma unroll 4
-        for (int v = tid; v < sp.nvec; v += kGradThreads) {
+        for (int v = part * a.part_vec + tid; v < v1; v += kGradThreads) {
             float f[VE];
             VT::unpack(dv[v], f);
 #pragma unroll
             for (int e = 0; e < VE; ++e) f[e] *= g;
             dv[v] = VT::pack(f);
         }
-        if (tid < sp.head + sp.tail) {
+        if (part == 0 && tid < sp.head + sp.tail) {
             const int64_t edge = tid < sp.head ? tid : a.p.V - sp.tail + (tid - sp.head);
             VT::store1(dx, edge, VT::load1(dx, edge) * g);
         }
@@ -364,6 +368,15 @@ ce_status launch(const void* fn, int64_t grid, int threads, void* arg, cudaStrea
     return e == cudaSuccess ? CE_OK : record_cuda_failure(e, what);
 }
 
+// A row a CTA; rows are split while there are few of them.
+void split_rows(GradArgs* a, int dtype, int sms) {
+    const int64_t vecs = a->p.V * (dtype == CE_F32 ? 4 : 2) / 16 + 1;
+    constexpr int64_t kPart = int64_t{kGradThreads} * kGradVec;
+    a->parts = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((vecs + kPart - 1) / kPart, (16L * sms + a->p.rows - 1) / a->p.rows)));
+    a->part_vec = static_cast<int>((vecs + a->parts - 1) / a->parts);
+}
+
 }  // namespace
 
 ce_status rows_count_launch(const RowArgs& args, cudaStream_t st) {
@@ -379,12 +392,7 @@ ce_status pair_launch(const PairArgs& args, cudaStream_t st) {
 
 ce_status rows_grad_launch(const GradArgs& args, int dtype, int sms, cudaStream_t st) {
     GradArgs a = args;
-    // a row a CTA; rows are split while there are few of them
-    const int64_t vecs = a.p.V * (dtype == CE_F32 ? 4 : 2) / 16 + 1;
-    constexpr int64_t kPart = int64_t{kGradThreads} * kGradVec;
-    a.parts = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>((vecs + kPart - 1) / kPart, (16L * sms + a.p.rows - 1) / a.p.rows)));
-    a.part_vec = static_cast<int>((vecs + a.parts - 1) / a.parts);
+    split_rows(&a, dtype, sms);
     const int64_t grid = std::min<int64_t>(a.p.rows * a.parts, 8L * sms);
     return launch(a.g_entropy ? grad_fn<true>(dtype) : grad_fn<false>(dtype), grid, kGradThreads, &a, st,
                   false, "log-probability gradient launch");
@@ -395,7 +403,8 @@ ce_status rows_scale_launch(const GradArgs& args, int dtype, int sms, cudaStream
     const void* fn = dtype == CE_F32    ? (const void*)&rows_scale<float>
                      : dtype == CE_BF16 ? (const void*)&rows_scale<__nv_bfloat16>
                                         : (const void*)&rows_scale<__half>;
-    return launch(fn, std::min<int64_t>(a.p.rows, 8L * sms), kGradThreads, &a, st, true,
+    split_rows(&a, dtype, sms);
+    return launch(fn, std::min<int64_t>(a.p.rows * a.parts, 8L * sms), kGradThreads, &a, st, true,
                   "gradient scaling launch");
 }
 

@@ -1114,7 +1114,9 @@ def test_offsets_past_32_bits(name):
     rows = 2 ** 31 // V + 8
     x = torch.zeros(4, rows // 4, V, dtype=torch.bfloat16, device="cuda")
     tok = torch.full((4, rows // 4), IGN, device="cuda")
-    last = torch.randn(2, V, device="cuda").bfloat16()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12)
+    last = torch.randn(2, V, generator=gen, device="cuda").bfloat16()
     x[3, -2:] = last
     tok[3, -2:] = torch.tensor([5, V - 1], device="cuda")
     x.requires_grad_()
@@ -1145,7 +1147,35 @@ def test_offsets_past_32_bits(name):
             assert abs(k) > 0 and float((a - k * b).norm() / a.norm()) < 2.0 ** -8
         return
     wdx, = torch.autograd.grad(want, leaf)
-    assert torch.equal(loss, want) and torch.equal(dx[3:, -2:], wdx)
+    # two rows are shared by more CTAs than many are, whose sums add up in another order (2^-20 of
+    # each); the gradients of the two are then at most a step apart
+    assert torch.allclose(loss, want, rtol=2.0 ** -20)
+    assert torch.allclose(dx[3:, -2:].float(), wdx.float(), rtol=2.0 ** -7, atol=2.0 ** -126)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [777, 5431, 41003, 90001])
+def test_first_call_of_a_size_may_be_captured(V):
+    """Sizes that no call has had, captured at once (whatever a layout needs is asked for then)."""
+    import softmax_cross_entropy_gb300 as gbce
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    x = torch.randn(2, 5, V, generator=g, device="cuda").half()
+    tok = torch.randint(V, (2, 5), generator=g, device="cuda")
+    adv = torch.randn(2, 5, generator=g, device="cuda")
+    idx = torch.randint(V, (2, 5, 6), generator=g, device="cuda")
+    val = torch.randn(2, 5, 6, generator=g, device="cuda")
+    calls = [lambda: gbce.token_log_probs(x, tok), lambda: gbce.policy_loss(x, tok, adv),
+             lambda: gbce.preference_loss(x, tok), lambda: gbce.distillation_loss(x, val, idx)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs, graph = [], torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = [f() for f in calls]
+    graph.replay()
+    torch.cuda.synchronize()
+    for f, got in zip(calls, outs):
+        assert torch.equal(f(), got)
 
 
 @pytest.mark.gpu
