@@ -90,6 +90,16 @@ def _logits(logits, inplace):
     return logits, layout
 
 
+def _saved(t):
+    """A saved tensor and its layout (hooks on saved tensors may have given it
+    other strides)."""
+    layout = _rows_of(t)
+    if layout is None:
+        t = plain(t)
+        layout = _rows_of(t)
+    return t, layout
+
+
 def _tokens(tokens, shape, device, name="tokens"):
     if not isinstance(tokens, torch.Tensor) or tokens.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
@@ -192,7 +202,7 @@ def _overwritten(logits):
 def _log_probs(logits, layout, tokens, temperature, ignore_index, want_entropy, keep):
     dev = logits.device
     logp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    entropy = torch.empty(tokens.shape, dtype=torch.float32, device=dev) if want_entropy else None
+    entropy = torch.empty_like(logp) if want_entropy else None
     kept = torch.empty((tokens.numel(), 4), dtype=torch.float32, device=dev) if keep else None
     with on(dev):
         check(_lib.ce_token_logp(_table(logits, None, layout, temperature), ptr(tokens), ignore_index,
@@ -213,7 +223,7 @@ class TokenLogProbsFunction(torch.autograd.Function):
                                          want_entropy, grad)
         if grad:
             ctx.save_for_backward(logits, tokens, kept)
-            ctx.args = layout, temperature, ignore_index, inplace
+            ctx.args = temperature, ignore_index, inplace
         return logp, entropy
 
     @staticmethod
@@ -225,7 +235,8 @@ class TokenLogProbsFunction(torch.autograd.Function):
         if not given or not ctx.needs_input_grad[0]:
             return None, *none
         logits, tokens, kept = ctx.saved_tensors
-        layout, temperature, ignore_index, inplace = ctx.args
+        temperature, ignore_index, inplace = ctx.args
+        logits, layout = _saved(logits)
         d_logp, d_entropy = (None if d is None else plain(d.float()) for d in (d_logp, d_entropy))
         dx = logits.detach() if inplace else _gradient_like(logits, layout)
         dev = logits.device
@@ -273,7 +284,7 @@ def _forward_gradient(ctx, logits, layout, call, args, inplace):
     if inplace:
         _overwritten(logits)
     ctx.save_for_backward(dx)
-    ctx.layout = layout
+    ctx.spent = False
     return out
 
 
@@ -283,9 +294,10 @@ def _scaled_gradient(ctx, d_loss, name):
         return None
     once(name, d_loss)
     (dx,) = ctx.saved_tensors
-    layout, ctx.layout = ctx.layout, None
-    if layout is None:
+    if ctx.spent:
         raise RuntimeError(f"{name}'s gradient was given to an earlier backward")
+    ctx.spent = True
+    dx, layout = _saved(dx)
     g, dev = plain(d_loss), dx.device
     with on(dev):
         check(_lib.ce_rows_scale(_table(dx, dx, layout), g.data_ptr(), 1 if g.dim() else 0,
@@ -302,7 +314,8 @@ def _policy(logits, dx, layout, tokens, advantages, advantage_rows, old, ref, we
     loss = torch.empty(shape if red == _lib.CE_RED_NONE else (), **f32)
     logp = entropy = kl = clipped = None
     if stats:
-        logp, entropy, kl = (torch.empty(shape, **f32) for _ in range(3))
+        logp = torch.empty(shape, **f32)
+        entropy, kl = torch.empty_like(logp), torch.empty_like(logp)
         clipped = torch.empty(shape, dtype=torch.bool, device=dev)
     with on(dev):
         ws, nbytes = _workspace(dev)
@@ -462,7 +475,7 @@ def _preference(logits, layout, tokens, offsets, ref, ignore_index, pairs, kind,
     f32 = dict(dtype=torch.float32, device=dev)
     loss = torch.empty((pairs,) if red == _lib.CE_RED_NONE else (), **f32)
     scores = torch.empty(2 * pairs, **f32)
-    dscore = torch.empty(2 * pairs, **f32) if grad else None
+    dscore = torch.empty_like(scores) if grad else None
     kept = torch.empty((tokens.numel(), 4), **f32)
     with on(dev):
         ws, nbytes = _workspace(dev)
@@ -486,7 +499,7 @@ class PreferenceLossFunction(torch.autograd.Function):
                                                  grad)
         if grad:
             ctx.save_for_backward(logits, tokens, offsets, kept, dscore)
-            ctx.args = layout, args[0], args[1], inplace
+            ctx.args = args[0], args[1], inplace
         ctx.mark_non_differentiable(scores)
         return loss, scores
 
@@ -496,7 +509,8 @@ class PreferenceLossFunction(torch.autograd.Function):
             return (None,) * 7
         once("preference_loss", d_loss)
         logits, tokens, offsets, kept, dscore = ctx.saved_tensors
-        layout, ignore_index, pairs, inplace = ctx.args
+        ignore_index, pairs, inplace = ctx.args
+        logits, layout = _saved(logits)
         g, dev = plain(d_loss), logits.device
         dx = logits.detach() if inplace else _gradient_like(logits, layout)
         with on(dev):

@@ -1154,6 +1154,35 @@ def test_offsets_past_32_bits(name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name", ALL)
+def test_saved_tensors_with_other_strides(name):
+    """Hooks on saved tensors (here: kept on the host meanwhile) give back contiguous copies of the
+    logits, or of the gradient, whose rows were apart."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    tok = torch.randint(999, (4, 6), generator=g, device="cuda")
+    full = torch.randn(4, 8, 1003, generator=g, device="cuda").bfloat16()
+    x = full[:, 1:-1, :999].detach().requires_grad_()
+    f = _four(x, tok)[name]
+    want, = torch.autograd.grad(f(x) * 2.0, x)
+    with torch.autograd.graph.save_on_cpu():
+        loss = f(x) * 2.0
+    got, = torch.autograd.grad(loss, x)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_sequences_without_rows():
+    import softmax_cross_entropy_gb300 as gbce
+    x = torch.zeros(4, 0, 50, device="cuda", requires_grad=True)
+    out = gbce.preference_loss(x, torch.zeros(4, 0, dtype=torch.int64, device="cuda"),
+                               return_scores=True)
+    g, = torch.autograd.grad(out.loss, x)
+    assert np.isclose(float(out.loss), np.log(2), rtol=1e-6) and (out.scores == 0).all()
+    assert g.shape == x.shape
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V", [777, 5431, 41003, 90001])
 def test_first_call_of_a_size_may_be_captured(V):
     """Sizes that no call has had, captured at once (whatever a layout needs is asked for then)."""
