@@ -31,7 +31,7 @@
 // Bound by the memory for long rows: at 2048 x 131072 bf16 the policy loss takes
 // 169 us (0.95 of the rate of a copy), with entropies 174, distillation from 64
 // entries 187 (0.86), log-probabilities of 2048 x 128256 79 us (1.0 of that rate,
-// which they only read at), with entropies 91 (the instructions: about 6 an
+// which they only read at), with entropies 91 (the instructions: about 8 an
 // element); fp32 of half the length 169 and 82. Rows of 8 KB take 59 us for 40
 // of memory time: what a row costs besides its elements. What came before, policy
 // loss: two passes of plain loads, the second from L2, 0.55 of the rate; the
